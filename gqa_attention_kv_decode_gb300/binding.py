@@ -34,12 +34,17 @@ GQA_DEV_KVLEN_CLAMPED = 1
 GQA_DEV_EMPTY_REQUEST = 2
 GQA_DEV_WAIT_TIMEOUT = 4
 GQA_DEV_BAD_BLOCK = 8
+GQA_DEV_OUT_OF_BLOCKS = 16
+GQA_DEV_BAD_SLOT = 32
+GQA_DEV_BAD_POSITION = 64
 
 EXPORTED = (
     "gqa_attn_decode_workspace_size",
     "gqa_attn_decode",
     "gqa_attn_decode_noalloc",
     "gqa_attn_decode_paged",
+    "gqa_attn_step_tables",
+    "gqa_attn_rope_append",
     "gqa_attn_decode_layers_workspace_size",
     "gqa_attn_decode_layers",
     "gqa_attn_quantize_q4",
@@ -98,6 +103,11 @@ def lib() -> ctypes.CDLL:
                                          sz, vp]
     L.gqa_attn_decode_layers.restype = i32
     i64 = ctypes.c_int64
+    L.gqa_attn_step_tables.argtypes = [vp] * 12 + [i32] * 6 + [vp, sz, vp]
+    L.gqa_attn_step_tables.restype = i32
+    L.gqa_attn_rope_append.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, f32, vp, vp, vp, vp, vp, vp, vp] \
+        + [i32] * 12 + [vp, sz, vp]
+    L.gqa_attn_rope_append.restype = i32
     L.gqa_attn_quantize_q4.argtypes = [vp, i64, vp, vp, vp, i64, i64, i32, i32, i32, i32, vp]
     L.gqa_attn_quantize_q4.restype = i32
     L.gqa_attn_decode_q4_residual_workspace_size.argtypes = [i32, i32, i32, i32, i32]
@@ -155,6 +165,21 @@ def _ptr(t):
     if not t.is_contiguous():
         raise ValueError("tensors passed to libgqa_attn must be contiguous")
     return t.data_ptr()
+
+
+def _heads(t):
+    """Pointer and token stride (elements) of a [T, H, D] tensor whose heads
+    are dense; the tokens may be further apart (views of one projection)."""
+    T, H, D = t.shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError("the heads of a token must be contiguous")
+    return t.data_ptr(), (t.stride(0) if T > 1 else H * D)
+
+
+def _int32(*tensors):
+    for t in tensors:
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError("lengths, tables, positions and slots are int32")
 
 
 def _stream(stream):
@@ -273,6 +298,72 @@ def gqa_attn_decode_paged(q, k_new, v_new, k_pool, v_pool, block_table, kv_lens,
                                      float(scale), _dtype_code(q), _ptr(workspace),
                                      workspace.numel() * workspace.element_size(), _stream(stream))
     _check(rc, "gqa_attn_decode_paged")
+
+
+def gqa_attn_step_tables(prior_lens, new_lens, block_table, free_blocks, free_count, kv_lens, q_lens, q_starts,
+                         positions, slots, q_slots, free_count_out, block_size, q_rows, workspace, stream=None):
+    """One step's tables from the lengths (all int32): block_table [B,max_blocks]
+    grown in place from the stack free_blocks [num_blocks] (or both, and the
+    counts, None for a dense cache of block_size rows a request); writes
+    kv_lens, q_lens [B], q_starts [B+1], positions, slots, q_slots [T]."""
+    _int32(prior_lens, new_lens, block_table, free_blocks, free_count, kv_lens, q_lens, q_starts, positions, slots,
+           q_slots, free_count_out)
+    B, T = prior_lens.shape[0], positions.shape[0]
+    if new_lens.shape[0] != B or kv_lens.shape[0] != B or q_lens.shape[0] != B or q_starts.shape[0] != B + 1:
+        raise ValueError("new_lens, kv_lens and q_lens have B entries, q_starts B + 1")
+    if slots.shape[0] != T or (q_slots is not None and q_slots.shape[0] != T):
+        raise ValueError("positions, slots and q_slots have T entries")
+    max_blocks = num_blocks = 0
+    if block_table is not None:
+        if block_table.shape[0] != B:
+            raise ValueError("block_table has a row per request")
+        max_blocks, num_blocks = block_table.shape[1], free_blocks.shape[0]
+    rc = lib().gqa_attn_step_tables(_ptr(prior_lens), _ptr(new_lens), _ptr(block_table), _ptr(free_blocks),
+                                    _ptr(free_count), _ptr(kv_lens), _ptr(q_lens), _ptr(q_starts), _ptr(positions),
+                                    _ptr(slots), _ptr(q_slots), _ptr(free_count_out), B, T, int(block_size),
+                                    num_blocks, max_blocks, int(q_rows), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "gqa_attn_step_tables")
+
+
+def gqa_attn_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, slots, q_slots, q_out, k_cache,
+                         v_cache, adjacent, workspace, stream=None):
+    """q [T,Hq,D], k, v [T,Hkv,D] (token strides allowed) normed (q_weight,
+    k_weight [D] or None) and rotated (cos_sin fp32 [max_pos,rot_dim] or None)
+    into q_out [q_groups,Hq,q_rows,D] rows q_slots (None: row t) and k_cache,
+    v_cache [num_blocks,Hkv,block_size,D] rows slots; negative slots: padding."""
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
+        raise ValueError("k and v are [T, Hkv, D]")
+    if q_out.shape[1] != Hq or q_out.shape[3] != D or v_cache.shape != k_cache.shape \
+            or k_cache.shape[1] != Hkv or k_cache.shape[3] != D:
+        raise ValueError("q_out is [groups, Hq, q_rows, D], k_cache and v_cache [blocks, Hkv, block_size, D]")
+    dt = q.dtype
+    for t in (k, v, q_weight, k_weight, q_out, k_cache, v_cache):
+        if t is not None and t.dtype != dt:
+            raise TypeError("q, k, v, the weights, q_out and the caches have one dtype")
+    for w in (q_weight, k_weight):
+        if w is not None and w.shape != (D,):
+            raise ValueError("the norm weights have D entries")
+    _int32(positions, slots, q_slots)
+    if slots.shape[0] != T or (q_slots is not None and q_slots.shape[0] != T):
+        raise ValueError("slots and q_slots have T entries")
+    max_pos = rot_dim = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or positions is None or positions.shape[0] != T:
+            raise TypeError("cos_sin is float32 and needs T positions")
+        max_pos, rot_dim = cos_sin.shape
+    elif positions is not None:
+        positions = None  # nothing rotates
+    (qp, qs), (kp, ks), (vp, vs) = _heads(q), _heads(k), _heads(v)
+    rc = lib().gqa_attn_rope_append(qp, kp, vp, qs, ks, vs, _ptr(q_weight), _ptr(k_weight), float(eps),
+                                    _ptr(cos_sin), _ptr(positions), _ptr(slots), _ptr(q_slots), _ptr(q_out),
+                                    _ptr(k_cache), _ptr(v_cache), T, Hq, Hkv, D, rot_dim, max_pos,
+                                    1 if adjacent else 0, k_cache.shape[0], k_cache.shape[2], q_out.shape[0],
+                                    q_out.shape[2], _dtype_code(q), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "gqa_attn_rope_append")
 
 
 def gqa_attn_quantize_q4(src, codes, scale, bias, dst_row0=0, rows=None, group_size=64, stream=None):
@@ -408,6 +499,16 @@ def gqa_attn_version() -> int:
 
 
 # --- conveniences: allocate outputs / workspaces with torch, then call -------
+
+def rope_table(max_pos, rot_dim, base=10000.0, device="cuda") -> torch.Tensor:
+    """The cos_sin table of gqa_attn_rope_append, fp32 [max_pos, rot_dim]: the
+    angles position * base^(-2 i / rot_dim) and their cosines and sines in 64
+    bits (an fp32 angle of a far position is off by whole steps of it),
+    rounded once."""
+    inv = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    a = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * inv[None, :]
+    return torch.cat([a.cos(), a.sin()], dim=1).float()
+
 
 def decode_workspace(B, Hq, Hkv, D, max_kv_len, dtype, device="cuda") -> torch.Tensor:
     n = gqa_attn_decode_workspace_size(B, Hq, Hkv, D, max_kv_len, dtype)

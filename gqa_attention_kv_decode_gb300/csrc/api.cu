@@ -135,6 +135,13 @@ int check_ptrs(std::initializer_list<const void*> ptrs, int dev, size_t align) {
   return GQA_OK;
 }
 
+// The workspace of a call that uses only the status word at its start.
+int check_status_workspace(const void* workspace, size_t ws_bytes, int dev) {
+  if (workspace == nullptr || ws_bytes < sizeof(uint32_t)) return GQA_ERR_WORKSPACE;
+  const int rc = check_ptrs({workspace}, dev, 256);
+  return rc == GQA_ERR_INVALID_ARG ? GQA_ERR_WORKSPACE : rc;
+}
+
 size_t decode_ws_size(int B, int Hq, int Hkv, int D, int max_kv_len, int tile, int ctas_per_sm = 2) {
   const SplitPlan p = plan_splits(B, Hq, Hkv, max_kv_len, tile, device_sm_count(), ctas_per_sm);
   return workspace_layout(B, Hq, Hkv, p.n_hc, p.n_split, D).total;
@@ -378,6 +385,146 @@ GQA_ATTN_API int gqa_attn_decode_paged(const void* q, const void* k_new, const v
   if (ws_bytes < workspace_layout(B, Hq, Hkv, a.plan.n_hc, a.plan.n_split, D).total)
     return GQA_ERR_WORKSPACE;
   if (launch_decode(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return GQA_ERR_CUDA;
+  return GQA_OK;
+}
+
+GQA_ATTN_API int gqa_attn_step_tables(const int32_t* prior_lens, const int32_t* new_lens,
+                                      int32_t* block_table, int32_t* free_blocks,
+                                      const int32_t* free_count, int32_t* kv_lens, int32_t* q_lens,
+                                      int32_t* q_starts, int32_t* positions, int32_t* slots,
+                                      int32_t* q_slots, int32_t* free_count_out, int B, int T,
+                                      int block_size, int num_blocks, int max_blocks, int q_rows,
+                                      void* workspace, size_t ws_bytes, void* stream) {
+  constexpr long kMax = 0x7fffffffL;
+  if (B < 1 || B > 65535 || T < 1 || block_size < 1 || q_rows < 1) return GQA_ERR_INVALID_ARG;
+  if (long(B) * q_rows > kMax) return GQA_ERR_INVALID_ARG;
+  const bool paged = block_table != nullptr;
+  if (paged) {
+    if (num_blocks < 1 || max_blocks < 1) return GQA_ERR_INVALID_ARG;
+    if (long(B) * max_blocks > kMax || long(num_blocks) * block_size > kMax || long(max_blocks) * block_size > kMax)
+      return GQA_ERR_INVALID_ARG;
+  } else {
+    if (free_blocks != nullptr || free_count != nullptr || free_count_out != nullptr) return GQA_ERR_INVALID_ARG;
+    if (long(B) * block_size > kMax) return GQA_ERR_INVALID_ARG;
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
+  int rc = check_ptrs({prior_lens, new_lens, kv_lens, q_lens, q_starts, positions, slots}, dev, 4);
+  if (rc != GQA_OK) return rc;
+  if (paged) {
+    rc = check_ptrs({block_table, free_blocks, free_count, free_count_out}, dev, 4);
+    if (rc != GQA_OK) return rc;
+  }
+  if (q_slots != nullptr) {
+    rc = check_ptrs({q_slots}, dev, 4);
+    if (rc != GQA_OK) return rc;
+  }
+  rc = check_status_workspace(workspace, ws_bytes, dev);
+  if (rc != GQA_OK) return rc;
+  StepTablesArgs a;
+  a.prior_lens = prior_lens;
+  a.new_lens = new_lens;
+  a.block_table = block_table;
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.kv_lens = kv_lens;
+  a.q_lens = q_lens;
+  a.q_starts = q_starts;
+  a.positions = positions;
+  a.slots = slots;
+  a.q_slots = q_slots;
+  a.free_count_out = free_count_out;
+  a.B = B;
+  a.T = T;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks;
+  a.q_rows = q_rows;
+  a.status = static_cast<uint32_t*>(workspace);
+  if (launch_step_tables(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return GQA_ERR_CUDA;
+  return GQA_OK;
+}
+
+GQA_ATTN_API int gqa_attn_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                                      int64_t k_stride, int64_t v_stride, const void* q_weight,
+                                      const void* k_weight, float eps, const float* cos_sin,
+                                      const int32_t* positions, const int32_t* slots,
+                                      const int32_t* q_slots, void* q_out, void* k_cache,
+                                      void* v_cache, int T, int Hq, int Hkv, int D, int rot_dim,
+                                      int max_pos, int adjacent, int num_blocks, int block_size,
+                                      int q_groups, int q_rows, int dtype, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+  constexpr long kMax = 0x7fffffffL;
+  if (T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return GQA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return GQA_ERR_INVALID_ARG;
+  if (dtype != GQA_F32 && dtype != GQA_BF16) return GQA_ERR_INVALID_ARG;
+  if (long(Hq) + 2L * Hkv > 65535) return GQA_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0) return GQA_ERR_INVALID_ARG;
+  if (rot_dim > 0 && max_pos < 1) return GQA_ERR_INVALID_ARG;
+  if (rot_dim == 0 && (cos_sin != nullptr || positions != nullptr)) return GQA_ERR_INVALID_ARG;
+  if (adjacent != 0 && adjacent != 1) return GQA_ERR_INVALID_ARG;
+  if (!(std::isfinite(eps) && eps >= 0.f)) return GQA_ERR_INVALID_ARG;
+  if (num_blocks < 1 || block_size < 1 || q_groups < 1 || q_rows < 1) return GQA_ERR_INVALID_ARG;
+  if (long(num_blocks) * block_size > kMax || long(q_groups) * q_rows > kMax) return GQA_ERR_INVALID_ARG;
+  if (q_slots == nullptr && T > long(q_groups) * q_rows) return GQA_ERR_INVALID_ARG;
+  const int64_t unit = dtype == GQA_F32 ? 4 : 8;  // elements in 16 bytes
+  if (q_stride < int64_t(Hq) * D || k_stride < int64_t(Hkv) * D || v_stride < int64_t(Hkv) * D)
+    return GQA_ERR_INVALID_ARG;
+  if (q_stride % unit != 0 || k_stride % unit != 0 || v_stride % unit != 0) return GQA_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
+  int rc = check_ptrs({q, k, v, q_out, k_cache, v_cache}, dev, 16);
+  if (rc != GQA_OK) return rc;
+  rc = check_ptrs({slots}, dev, 4);
+  if (rc != GQA_OK) return rc;
+  if (rot_dim > 0) {
+    rc = check_ptrs({cos_sin}, dev, 16);
+    if (rc != GQA_OK) return rc;
+    rc = check_ptrs({positions}, dev, 4);
+    if (rc != GQA_OK) return rc;
+  }
+  for (const void* w : {q_weight, k_weight})
+    if (w != nullptr) {
+      rc = check_ptrs({w}, dev, 16);
+      if (rc != GQA_OK) return rc;
+    }
+  if (q_slots != nullptr) {
+    rc = check_ptrs({q_slots}, dev, 4);
+    if (rc != GQA_OK) return rc;
+  }
+  rc = check_status_workspace(workspace, ws_bytes, dev);
+  if (rc != GQA_OK) return rc;
+  RopeAppendArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.positions = positions;
+  a.slots = slots;
+  a.q_slots = q_slots;
+  a.q_out = q_out;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.rot_dim = rot_dim;
+  a.max_pos = max_pos;
+  a.adjacent = adjacent;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.q_groups = q_groups;
+  a.q_rows = q_rows;
+  a.dtype = dtype;
+  a.status = static_cast<uint32_t*>(workspace);
+  if (launch_rope_append(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return GQA_ERR_CUDA;
   return GQA_OK;
 }
 

@@ -144,6 +144,47 @@ struct PrefillArgs {
 
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 
+// One step's tables (gqa_attn_step_tables); block_table == nullptr: a dense
+// cache of block_size rows per request, without a free stack.
+struct StepTablesArgs {
+  const int32_t* prior_lens;
+  const int32_t* new_lens;
+  int32_t* block_table;
+  int32_t* free_blocks;
+  const int32_t* free_count;
+  int32_t* kv_lens;
+  int32_t* q_lens;
+  int32_t* q_starts;
+  int32_t* positions;
+  int32_t* slots;
+  int32_t* q_slots;  // or nullptr
+  int32_t* free_count_out;
+  int B, T, block_size, num_blocks, max_blocks, q_rows;
+  uint32_t* status;
+};
+cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream);
+
+// New tokens into the cache (gqa_attn_rope_append).
+struct RopeAppendArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
+  const void* q_weight;                  // or nullptr: no norm
+  const void* k_weight;
+  float eps;
+  const float* cos_sin;  // [max_pos][rot_dim]: rot_dim / 2 cosines, then the sines
+  const int32_t* positions;
+  const int32_t* slots;
+  const int32_t* q_slots;  // or nullptr: token t is query row t
+  void* q_out;
+  void* k_cache;
+  void* v_cache;
+  int T, Hq, Hkv, D, rot_dim, max_pos, adjacent, num_blocks, block_size, q_groups, q_rows, dtype;
+  uint32_t* status;
+};
+cudaError_t launch_rope_append(const RopeAppendArgs& a, cudaStream_t stream);
+
 // Upper bound on the time a kernel waits for one of its own tile copies
 // before it records GQA_DEV_WAIT_TIMEOUT and stops (nanoseconds).
 constexpr uint64_t kWaitLimitNs = 1000000000ull;

@@ -1,0 +1,215 @@
+// rope_append.cu -- new tokens on their way from the projections into the
+// attention: per-head RMS norm of Q and K, rotary rotation at the token's
+// position, Q to the layout the attention reads, K and V to the cache rows
+// named by a slot map (a block pool, or a dense cache seen as a pool of B
+// blocks of S_cap rows).
+//
+//   y = x * rsqrt(mean(x^2) + eps) * w                 (where a weight is given)
+//   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)  for each rotated pair
+//
+// The arithmetic is fp32 from the loads to one rounding (RNE) at the store.
+// Every head row is read once and written once, so the kernel is bound by
+// memory; the layout of the work serves that alone.  A lane holds two 16-byte
+// chunks of a head row, chosen so that both members of every rotated pair are
+// in it (chunk i and its partner R/2 dims on; for neighbouring pairs two
+// chunks side by side): no exchange between lanes but the sum of squares.
+// The cos and sin a lane needs are the same for every head of the token and
+// are loaded once.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "gqa_attn.h"
+#include "internal.h"
+#include "merge.cuh"
+#include "ptx.cuh"
+
+namespace gqa {
+namespace {
+
+// 16 bytes of a row as floats (exact) and back (one RNE rounding each).
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<__nv_bfloat16> {
+  static constexpr int E = 8;
+  __device__ static void widen(const uint4& w, float (&x)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = bf16x2_to_float2(u[i]);
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+  __device__ static uint4 narrow(const float (&x)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+template <>
+struct Chunk<float> {
+  static constexpr int E = 4;
+  __device__ static void widen(const uint4& w, float (&x)[4]) {
+    x[0] = __uint_as_float(w.x);
+    x[1] = __uint_as_float(w.y);
+    x[2] = __uint_as_float(w.z);
+    x[3] = __uint_as_float(w.w);
+  }
+  __device__ static uint4 narrow(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
+};
+
+constexpr int NT = 256;
+
+// Each warp takes one token and U passes of HP heads of it.
+template <typename T, int D, int U>
+__global__ void __launch_bounds__(NT) rope_append_kernel(const RopeAppendArgs p, int warps_per_token) {
+  using C = Chunk<T>;
+  constexpr int E = C::E;
+  constexpr int NL = D / (2 * E);  // lanes per head row
+  constexpr int HP = 32 / NL;      // head rows a warp takes at a time
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const long w = (long(blockIdx.x) * NT + threadIdx.x) >> 5;
+  const int t = int(w / warps_per_token), part = int(w % warps_per_token);
+  if (t >= p.T) return;
+  const int lane = threadIdx.x & 31, i = lane % NL;
+
+  // where the token goes: K / V row `slot`, Q row `q_slot`; negative: nowhere
+  int slot = p.slots[t], q_slot = p.q_slots != nullptr ? p.q_slots[t] : t;
+  const int pos = p.rot_dim > 0 ? p.positions[t] : 0;
+  uint32_t bits = 0;
+  if (slot >= p.num_blocks * p.block_size) {
+    bits |= GQA_DEV_BAD_SLOT;
+    slot = -1;
+  }
+  if (q_slot >= p.q_groups * p.q_rows) {
+    bits |= GQA_DEV_BAD_SLOT;
+    q_slot = -1;
+  }
+  if ((slot >= 0 || q_slot >= 0) && p.rot_dim > 0 && (pos < 0 || pos >= p.max_pos)) {
+    bits |= GQA_DEV_BAD_POSITION;
+    slot = q_slot = -1;
+  }
+  if (bits != 0 && lane == 0 && part == 0) atomicOr(p.status, bits);
+  if (slot < 0 && q_slot < 0) return;
+
+  // this lane's chunks, and whether it rotates them
+  const int n_rot = p.rot_dim / (2 * E);  // lanes of a head row that rotate
+  const bool rot = i < n_rot, split = rot && !p.adjacent;
+  const int ca = (split ? i : 2 * i) * E, cb = (split ? i + n_rot : 2 * i + 1) * E;
+  float cs[E], sn[E];
+  if (rot) {
+    const float* row = p.cos_sin + size_t(pos) * p.rot_dim + i * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 4) {
+      const float4 c4 = *reinterpret_cast<const float4*>(row + e);
+      const float4 s4 = *reinterpret_cast<const float4*>(row + p.rot_dim / 2 + e);
+      cs[e] = c4.x, cs[e + 1] = c4.y, cs[e + 2] = c4.z, cs[e + 3] = c4.w;
+      sn[e] = s4.x, sn[e + 1] = s4.y, sn[e + 2] = s4.z, sn[e + 3] = s4.w;
+    }
+  }
+  const int n_heads = p.Hq + 2 * p.Hkv;
+  const T* const q = static_cast<const T*>(p.q) + size_t(t) * p.q_stride;
+  const T* const k = static_cast<const T*>(p.k) + size_t(t) * p.k_stride;
+  const T* const v = static_cast<const T*>(p.v) + size_t(t) * p.v_stride;
+
+  uint4 xa[U], xb[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int h = (part * U + u) * HP + lane / NL;
+    const bool is_q = h < p.Hq;
+    xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (h < n_heads && (is_q ? q_slot : slot) >= 0) {
+      const T* src = is_q ? q + size_t(h) * D
+                          : h < p.Hq + p.Hkv ? k + size_t(h - p.Hq) * D : v + size_t(h - p.Hq - p.Hkv) * D;
+      xa[u] = *reinterpret_cast<const uint4*>(src + ca);
+      xb[u] = *reinterpret_cast<const uint4*>(src + cb);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int h = (part * U + u) * HP + lane / NL;
+    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+    const T* wt = static_cast<const T*>(is_v ? nullptr : is_q ? p.q_weight : p.k_weight);
+    float a[E], b[E];
+    C::widen(xa[u], a);
+    C::widen(xb[u], b);
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+#pragma unroll
+    for (int d = NL / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+    if (wt != nullptr) {
+      const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+      float wa[E], wb[E];
+      C::widen(*reinterpret_cast<const uint4*>(wt + ca), wa);
+      C::widen(*reinterpret_cast<const uint4*>(wt + cb), wb);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        a[e] = a[e] * inv * wa[e];
+        b[e] = b[e] * inv * wb[e];
+      }
+    }
+    if (rot && !is_v) {
+      if (p.adjacent) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float a0 = a[e], b0 = b[e];
+          const float c0 = cs[e / 2], s0 = sn[e / 2], c1 = cs[(E + e) / 2], s1 = sn[(E + e) / 2];
+          a[e] = a0 * c0 - a[e + 1] * s0;
+          a[e + 1] = a[e + 1] * c0 + a0 * s0;
+          b[e] = b0 * c1 - b[e + 1] * s1;
+          b[e + 1] = b[e + 1] * c1 + b0 * s1;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float a0 = a[e];
+          a[e] = a0 * cs[e] - b[e] * sn[e];
+          b[e] = b[e] * cs[e] + a0 * sn[e];
+        }
+      }
+    }
+    if (h < n_heads && (is_q ? q_slot : slot) >= 0) {
+      const int rows = is_q ? p.q_rows : p.block_size, at = is_q ? q_slot : slot;
+      const int hh = is_q ? h : is_v ? h - p.Hq - p.Hkv : h - p.Hq;
+      T* base = static_cast<T*>(is_q ? p.q_out : is_v ? p.v_cache : p.k_cache);
+      T* dst = base + ((size_t(at / rows) * (is_q ? p.Hq : p.Hkv) + hh) * rows + at % rows) * D;
+      // a value that is neither scaled nor rotated comes back bit for bit
+      *reinterpret_cast<uint4*>(dst + ca) = is_v ? xa[u] : C::narrow(a);
+      *reinterpret_cast<uint4*>(dst + cb) = is_v ? xb[u] : C::narrow(b);
+    }
+  }
+}
+
+template <typename T, int D, int U>
+cudaError_t launch_u(const RopeAppendArgs& a, cudaStream_t stream) {
+  constexpr int HP = 32 / (D / (2 * Chunk<T>::E));
+  const int n_heads = a.Hq + 2 * a.Hkv;
+  const int wpt = (n_heads + HP * U - 1) / (HP * U);
+  const long blocks = (long(a.T) * wpt + NT / 32 - 1) / (NT / 32);
+  return launch_pdl(rope_append_kernel<T, D, U>, dim3(unsigned(blocks)), dim3(NT), 0, stream, a, wpt);
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const RopeAppendArgs& a, cudaStream_t stream) {
+  return launch_u<T, D, 1>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(const RopeAppendArgs& a, cudaStream_t stream) {
+  if (a.dtype == GQA_F32) return a.D == 128 ? launch_t<float, 128>(a, stream) : launch_t<float, 64>(a, stream);
+  return a.D == 128 ? launch_t<__nv_bfloat16, 128>(a, stream) : launch_t<__nv_bfloat16, 64>(a, stream);
+}
+
+}  // namespace gqa

@@ -87,6 +87,9 @@ typedef enum gqa_dtype {
 #define GQA_DEV_EMPTY_REQUEST 2u /* some kv_lens[b] == 0: that output is zeros    */
 #define GQA_DEV_WAIT_TIMEOUT 4u  /* a bounded wait on a tile copy gave up          */
 #define GQA_DEV_BAD_BLOCK 8u     /* a paged-cache block id was outside the pool    */
+#define GQA_DEV_OUT_OF_BLOCKS 16u /* too few free blocks: some request got no tokens */
+#define GQA_DEV_BAD_SLOT 32u     /* a slot was past the cache: not written          */
+#define GQA_DEV_BAD_POSITION 64u /* a position outside the angle table: not written */
 
 /* ---------------------------------------------------------------------------
  * Single-token decode (q_len = 1), split-KV with a log-sum-exp combine.
@@ -184,6 +187,122 @@ GQA_ATTN_API int gqa_attn_decode_paged(const void* q, const void* k_new, const v
                                        int D, int block_size, int num_blocks, int max_blocks,
                                        int max_kv_len, float scale, int dtype, void* workspace,
                                        size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The tables of one serving step, built on the GPU from the requests' lengths.
+ *
+ * A step appends new_lens[b] tokens to request b.  This call turns the
+ * lengths into what the calls of the step read: the grown block table of a
+ * paged cache (gqa_attn_decode_paged), the lengths (every attention call),
+ * and for each token its position and its cache and query rows
+ * (gqa_attn_rope_append).  Everything stays on the device, so a captured
+ * graph can be replayed while requests grow across block borders, finish and
+ * start.  The tokens of a step are packed: those of request 0, then those of
+ * request 1, and so on.
+ *
+ *   prior_lens   device int32 [B]: rows of each request in the cache already
+ *   new_lens     device int32 [B]: tokens this step adds; 0: an idle entry;
+ *                negative: the request is finished and gives its blocks back
+ *   block_table  device int32 [B, max_blocks], as for gqa_attn_decode_paged;
+ *                its first ceil(prior_lens[b] / block_size) entries of row b
+ *                are read where needed, the entries of new blocks are written,
+ *                nothing else changes.  NULL: a dense cache
+ *                [B, Hkv, block_size, D] (block_size = S_cap; request b owns
+ *                rows [b * block_size, (b + 1) * block_size) of the slot map;
+ *                free_blocks, free_count and free_count_out are NULL,
+ *                num_blocks and max_blocks are not used)
+ *   free_blocks  device int32 [num_blocks]: a stack of free block ids, the
+ *                first *free_count of them valid, popped from the end.  The
+ *                blocks of finished requests are pushed first, in request
+ *                order, then the other requests pop theirs, in request order.
+ *   free_count,  device int32 [1]: ids on the stack before and after the call
+ *   free_count_out
+ *   kv_lens      device int32 [B] (written): rows after the step (0: finished)
+ *   q_lens       device int32 [B] (written): tokens of the step the request
+ *                really got (see below)
+ *   q_starts     device int32 [B + 1] (written): first token of each request,
+ *                min(sum of the new_lens before it, T)
+ *   positions,   device int32 [T] (written): per token its position (= row in
+ *   slots,       the request), its cache row block * block_size + row (as read
+ *   q_slots      by gqa_attn_rope_append), and its query row b * q_rows + i
+ *                (i: its index among the request's new tokens) for a query
+ *                tensor [B, Hq, q_rows, D]; q_slots may be NULL.  Tokens past
+ *                the last one, and those of a request that got none, have
+ *                position 0 and slots -1.
+ *   T            capacity of the token arrays (a captured graph's fixed size)
+ *   q_rows       most new tokens a request may add (1 for a decode step)
+ * kv_lens may be prior_lens itself, q_lens new_lens and free_count_out
+ * free_count; no other two arrays may overlap.
+ *
+ * A request gets all of its tokens or none.  It gets none (q_lens[b] = 0,
+ * kv_lens[b] = prior_lens[b], no blocks) if its tokens do not fit T, q_rows or
+ * the cache (max_blocks * block_size, or block_size): GQA_DEV_KVLEN_CLAMPED;
+ * or if the stack cannot serve it and every request before it:
+ * GQA_DEV_OUT_OF_BLOCKS (requests after it that need no new block still get
+ * their tokens).  prior_lens out of range are clamped
+ * (GQA_DEV_KVLEN_CLAMPED).  A block id outside [0, num_blocks) on the stack or
+ * in a table entry that is read, a *free_count outside [0, num_blocks]
+ * (clamped) and a push past the stack's end (dropped) set GQA_DEV_BAD_BLOCK;
+ * tokens in such a block have slots -1.
+ *   workspace    at least 4 bytes, 256-byte aligned; only the status word at
+ *                its start is used (a decode workspace will do)
+ * B <= 65535; B * q_rows, B * max_blocks, num_blocks * block_size and
+ * max_blocks * block_size (dense: B * block_size) < 2^31.
+ * ------------------------------------------------------------------------- */
+GQA_ATTN_API int gqa_attn_step_tables(const int32_t* prior_lens, const int32_t* new_lens,
+                                      int32_t* block_table, int32_t* free_blocks,
+                                      const int32_t* free_count, int32_t* kv_lens, int32_t* q_lens,
+                                      int32_t* q_starts, int32_t* positions, int32_t* slots,
+                                      int32_t* q_slots, int32_t* free_count_out, int B, int T,
+                                      int block_size, int num_blocks, int max_blocks, int q_rows,
+                                      void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * New tokens into the cache: per-head RMS norm of Q and K, rotary rotation,
+ * Q to the layout of the attention calls, K and V to their cache rows.
+ *
+ *   q            [T, Hq, D] dtype, q_stride elements from token to token
+ *   k, v         [T, Hkv, D] dtype, k_stride and v_stride (the three may be
+ *                views of one [T, (Hq + 2 Hkv) * D] projection output)
+ *   q_weight,    [D] dtype, or NULL (no norm of Q / of K): every head row x
+ *   k_weight     becomes x * rsqrt(mean(x^2) + eps) * weight
+ *   cos_sin      float32 [max_pos, rot_dim]: the cosines of the rot_dim / 2
+ *                angles of each position, then their sines.  The first rot_dim
+ *                dims of every Q and K head are rotated; NULL with rot_dim 0.
+ *   adjacent     0: dim i < rot_dim / 2 pairs with dim i + rot_dim / 2;
+ *                1: dim 2i pairs with dim 2i + 1
+ *   positions    device int32 [T] (NULL with rot_dim 0)
+ *   slots        device int32 [T]: cache row of the token, block * block_size
+ *                + row in block; negative: a padding token, no K / V written
+ *   q_slots      device int32 [T]: query row of the token, group * q_rows +
+ *                row in group; negative: no Q written.  NULL: token t is row t.
+ *   q_out        [q_groups, Hq, q_rows, D] dtype (written): with q_rows = 1 the
+ *                q of the decode calls, with q_rows = Tq_cap that of the prefill
+ *                calls
+ *   k_cache,     [num_blocks, Hkv, block_size, D] dtype (written): the pools of
+ *   v_cache      a paged cache, or a dense cache [B, Hkv, S_cap, D] with
+ *                num_blocks = B and block_size = S_cap
+ * All arithmetic is fp32 (also for a bf16 dtype, norm and rotation without a
+ * rounding between them), each output rounded once; rows that no token names
+ * keep their contents.  Tokens must name different rows: where two name the
+ * same one it holds some mix of theirs.  Outputs must not overlap inputs.
+ * A slot past the cache sets GQA_DEV_BAD_SLOT and is not written; a position
+ * outside [0, max_pos) of a token with any row to write sets
+ * GQA_DEV_BAD_POSITION, and nothing of that token is written.
+ * D = 64 or 128; rot_dim a multiple of 16, 0 to D; strides multiples of 16
+ * bytes; every pointer 16-byte aligned (positions, slots and q_slots 4-byte).
+ * num_blocks * block_size and q_groups * q_rows < 2^31.
+ *   workspace    as for gqa_attn_step_tables (the status word)
+ * ------------------------------------------------------------------------- */
+GQA_ATTN_API int gqa_attn_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                                      int64_t k_stride, int64_t v_stride, const void* q_weight,
+                                      const void* k_weight, float eps, const float* cos_sin,
+                                      const int32_t* positions, const int32_t* slots,
+                                      const int32_t* q_slots, void* q_out, void* k_cache,
+                                      void* v_cache, int T, int Hq, int Hkv, int D, int rot_dim,
+                                      int max_pos, int adjacent, int num_blocks, int block_size,
+                                      int q_groups, int q_rows, int dtype, void* workspace,
+                                      size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Prefill of a batch of requests with their own lengths (varlen, chunked).

@@ -18,3 +18,10 @@ from .gqa_oracle import (  # noqa: F401
     quantize_q4,
     attention_q4_residual,
 )
+from .step_oracle import (  # noqa: F401
+    step_tables,
+    rms_norm,
+    rotate,
+    rope_append,
+    attention_shared_prefix,
+)
