@@ -43,6 +43,9 @@ EXPORTED = (
     "gqa_attn_decode",
     "gqa_attn_decode_noalloc",
     "gqa_attn_decode_paged",
+    "gqa_attn_decode_shared_prefix_workspace_size",
+    "gqa_attn_decode_shared_prefix",
+    "gqa_attn_decode_shared_prefix_paged",
     "gqa_attn_step_tables",
     "gqa_attn_rope_append",
     "gqa_attn_decode_layers_workspace_size",
@@ -103,6 +106,12 @@ def lib() -> ctypes.CDLL:
                                          sz, vp]
     L.gqa_attn_decode_layers.restype = i32
     i64 = ctypes.c_int64
+    L.gqa_attn_decode_shared_prefix_workspace_size.argtypes = [i32] * 6
+    L.gqa_attn_decode_shared_prefix_workspace_size.restype = sz
+    L.gqa_attn_decode_shared_prefix.argtypes = [vp] * 8 + [i32] * 8 + [f32, i32, vp, sz, vp]
+    L.gqa_attn_decode_shared_prefix.restype = i32
+    L.gqa_attn_decode_shared_prefix_paged.argtypes = [vp] * 8 + [i32] * 10 + [f32, i32, vp, sz, vp]
+    L.gqa_attn_decode_shared_prefix_paged.restype = i32
     L.gqa_attn_step_tables.argtypes = [vp] * 12 + [i32] * 6 + [vp, sz, vp]
     L.gqa_attn_step_tables.restype = i32
     L.gqa_attn_rope_append.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, f32, vp, vp, vp, vp, vp, vp, vp] \
@@ -180,6 +189,12 @@ def _int32(*tensors):
     for t in tensors:
         if t is not None and t.dtype != torch.int32:
             raise TypeError("lengths, tables, positions and slots are int32")
+
+
+def _one_dtype(first, *tensors):
+    for t in tensors:
+        if t is not None and t.dtype != first.dtype:
+            raise TypeError("the tensors of a call have one dtype")
 
 
 def _stream(stream):
@@ -300,6 +315,54 @@ def gqa_attn_decode_paged(q, k_new, v_new, k_pool, v_pool, block_table, kv_lens,
     _check(rc, "gqa_attn_decode_paged")
 
 
+def gqa_attn_decode_shared_prefix_workspace_size(B, Hq, Hkv, D, max_prefix_len, max_kv_len) -> int:
+    return lib().gqa_attn_decode_shared_prefix_workspace_size(B, Hq, Hkv, D, max_prefix_len, max_kv_len)
+
+
+def gqa_attn_decode_shared_prefix(q, k_prefix, v_prefix, prefix_len, k, v, kv_lens, o, scale, workspace,
+                                  max_prefix_len=None, max_kv_len=None, stream=None):
+    """q, o [B,Hq,1,D]; k_prefix, v_prefix [Hkv,P_cap,D] shared by the batch,
+    prefix_len int32 [1] or None; k, v [B,Hkv,S_cap,D] own rows behind them,
+    kv_lens int32 [B] or None."""
+    B, Hq, Tq, D = q.shape
+    Hkv, P_cap = k_prefix.shape[0], k_prefix.shape[1]
+    S_cap = k.shape[2]
+    if Tq != 1:
+        raise ValueError("decode takes one query row per request")
+    if k.shape != (B, Hkv, S_cap, D) or v.shape != k.shape or v_prefix.shape != (Hkv, P_cap, D) \
+            or k_prefix.shape[2] != D or o.shape != q.shape:
+        raise ValueError("k_prefix and v_prefix are [Hkv, P_cap, D], k and v [B, Hkv, S_cap, D], o as q")
+    _one_dtype(q, k_prefix, v_prefix, k, v, o)
+    _int32(prefix_len, kv_lens)
+    rc = lib().gqa_attn_decode_shared_prefix(
+        _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), B, Hq,
+        Hkv, D, P_cap, P_cap if max_prefix_len is None else int(max_prefix_len), S_cap,
+        S_cap if max_kv_len is None else int(max_kv_len), float(scale), _dtype_code(q), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "gqa_attn_decode_shared_prefix")
+
+
+def gqa_attn_decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, prefix_len, block_table, kv_lens, o, scale,
+                                        workspace, max_prefix_len, max_kv_len, stream=None):
+    """q, o [B,Hq,1,D]; k_pool, v_pool [num_blocks,Hkv,block_size,D]; the shared
+    rows' blocks prefix_table int32 [blocks] (prefix_len int32 [1] rows, or
+    None: max_prefix_len), the own rows' block_table int32 [B,max_blocks]."""
+    B, Hq, Tq, D = q.shape
+    num_blocks, Hkv, block_size = k_pool.shape[0], k_pool.shape[1], k_pool.shape[2]
+    if Tq != 1:
+        raise ValueError("decode takes one query row per request")
+    if v_pool.shape != k_pool.shape or k_pool.shape[3] != D or o.shape != q.shape or block_table.shape[0] != B:
+        raise ValueError("k_pool and v_pool are [blocks, Hkv, block_size, D], block_table [B, blocks], o as q")
+    _one_dtype(q, k_pool, v_pool, o)
+    _int32(prefix_table, prefix_len, block_table, kv_lens)
+    rc = lib().gqa_attn_decode_shared_prefix_paged(
+        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(prefix_table), _ptr(prefix_len), _ptr(block_table), _ptr(kv_lens),
+        _ptr(o), B, Hq, Hkv, D, block_size, num_blocks, prefix_table.shape[0], block_table.shape[1],
+        int(max_prefix_len), int(max_kv_len), float(scale), _dtype_code(q), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "gqa_attn_decode_shared_prefix_paged")
+
+
 def gqa_attn_step_tables(prior_lens, new_lens, block_table, free_blocks, free_count, kv_lens, q_lens, q_starts,
                          positions, slots, q_slots, free_count_out, block_size, q_rows, workspace, stream=None):
     """One step's tables from the lengths (all int32): block_table [B,max_blocks]
@@ -339,10 +402,7 @@ def gqa_attn_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, s
     if q_out.shape[1] != Hq or q_out.shape[3] != D or v_cache.shape != k_cache.shape \
             or k_cache.shape[1] != Hkv or k_cache.shape[3] != D:
         raise ValueError("q_out is [groups, Hq, q_rows, D], k_cache and v_cache [blocks, Hkv, block_size, D]")
-    dt = q.dtype
-    for t in (k, v, q_weight, k_weight, q_out, k_cache, v_cache):
-        if t is not None and t.dtype != dt:
-            raise TypeError("q, k, v, the weights, q_out and the caches have one dtype")
+    _one_dtype(q, k, v, q_weight, k_weight, q_out, k_cache, v_cache)
     for w in (q_weight, k_weight):
         if w is not None and w.shape != (D,):
             raise ValueError("the norm weights have D entries")
@@ -517,6 +577,13 @@ def decode_workspace(B, Hq, Hkv, D, max_kv_len, dtype, device="cuda") -> torch.T
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
+def decode_shared_prefix_workspace(B, Hq, Hkv, D, max_prefix_len, max_kv_len, device="cuda") -> torch.Tensor:
+    n = gqa_attn_decode_shared_prefix_workspace_size(B, Hq, Hkv, D, max_prefix_len, max_kv_len)
+    if n == 0:
+        raise ValueError("invalid decode shape")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
 def decode_q4_workspace(B, Hq, Hkv, D, max_kv_len, device="cuda") -> torch.Tensor:
     n = gqa_attn_decode_q4_workspace_size(B, Hq, Hkv, D, max_kv_len)
     if n == 0:
@@ -566,6 +633,36 @@ def decode_paged(q, k_pool, v_pool, block_table, kv_lens, max_kv_len, k_new=None
     o = torch.empty_like(q)
     gqa_attn_decode_paged(q, k_new, v_new, k_pool, v_pool, block_table, kv_lens, o, scale, workspace,
                           max_kv_len, stream)
+    return o
+
+
+def decode_shared_prefix(q, k_prefix, v_prefix, k, v, prefix_len=None, kv_lens=None, scale=None,
+                         max_prefix_len=None, max_kv_len=None, workspace=None, stream=None):
+    B, Hq, _, D = q.shape
+    Hkv = k.shape[1]
+    max_prefix_len = k_prefix.shape[1] if max_prefix_len is None else int(max_prefix_len)
+    max_kv_len = k.shape[2] if max_kv_len is None else int(max_kv_len)
+    if scale is None:
+        scale = D ** -0.5
+    if workspace is None:
+        workspace = decode_shared_prefix_workspace(B, Hq, Hkv, D, max_prefix_len, max_kv_len, q.device)
+    o = torch.empty_like(q)
+    gqa_attn_decode_shared_prefix(q, k_prefix, v_prefix, prefix_len, k, v, kv_lens, o, scale, workspace,
+                                  max_prefix_len, max_kv_len, stream)
+    return o
+
+
+def decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, block_table, kv_lens, max_prefix_len, max_kv_len,
+                               prefix_len=None, scale=None, workspace=None, stream=None):
+    B, Hq, _, D = q.shape
+    Hkv = k_pool.shape[1]
+    if scale is None:
+        scale = D ** -0.5
+    if workspace is None:
+        workspace = decode_shared_prefix_workspace(B, Hq, Hkv, D, max_prefix_len, max_kv_len, q.device)
+    o = torch.empty_like(q)
+    gqa_attn_decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, prefix_len, block_table, kv_lens, o, scale,
+                                        workspace, max_prefix_len, max_kv_len, stream)
     return o
 
 

@@ -142,6 +142,47 @@ int check_status_workspace(const void* workspace, size_t ws_bytes, int dev) {
   return rc == GQA_ERR_INVALID_ARG ? GQA_ERR_WORKSPACE : rc;
 }
 
+// Shapes of a shared-prefix decode; the own rows as in a decode call.
+int check_shared_prefix(int B, int Hq, int Hkv, int D, int max_prefix_len, int S_cap, int max_kv_len, float scale) {
+  const int rc = check_decode_shape(B, Hq, Hkv, D, S_cap, max_kv_len, scale);
+  if (rc != GQA_OK) return rc;
+  if (max_prefix_len < 1 || max_prefix_len > 0x7fffff00) return GQA_ERR_INVALID_ARG;  // (tiles of 128 in 32 bits)
+  if (Hkv > 65535) return GQA_ERR_INVALID_ARG;  // grid z
+  return GQA_OK;
+}
+// bf16, and the query heads of a KV head in one 128-row tile.
+int check_shared_prefix_kernel(int Hq, int Hkv, int dtype) {
+  if (dtype != GQA_F32 && dtype != GQA_BF16) return GQA_ERR_INVALID_ARG;
+  if (dtype != GQA_BF16 || Hq / Hkv > 128) return GQA_ERR_UNSUPPORTED;
+  return GQA_OK;
+}
+
+// The workspace serves the dense and the paged call, whose decode kernels may
+// plan different splits of the own rows.
+size_t shared_prefix_ws_size(int B, int Hq, int Hkv, int D, int max_prefix_len, int max_kv_len) {
+  if (Hq / Hkv > 128) return 0;
+  const PrefixPlan px = prefix_plan(B, Hq, Hkv, D, max_prefix_len, device_sm_count());
+  size_t most = 0;
+  for (const bool paged : {false, true}) {
+    const SplitPlan own = decode_plan(B, Hq, Hkv, D, max_kv_len, GQA_BF16, paged);
+    most = std::max(most, workspace_layout(B, Hq, Hkv, own.n_hc, own.n_split + px.n_split, D).total);
+  }
+  return most;
+}
+
+int run_shared_prefix(SharedPrefixArgs& a, size_t ws_bytes, int dev, void* stream) {
+  DecodeArgs& d = a.own;
+  if (d.workspace == nullptr) return GQA_ERR_WORKSPACE;
+  const int rc = check_ptrs({d.workspace}, dev, 256);
+  if (rc == GQA_ERR_INVALID_ARG) return GQA_ERR_WORKSPACE;
+  if (rc != GQA_OK) return rc;
+  d.plan = decode_plan(d.B, d.Hq, d.Hkv, d.D, d.max_kv_len, d.dtype, d.block_table != nullptr);
+  a.plan = prefix_plan(d.B, d.Hq, d.Hkv, d.D, a.max_prefix, device_sm_count());
+  if (ws_bytes < workspace_layout(d.B, d.Hq, d.Hkv, d.plan.n_hc, d.plan.n_split + a.plan.n_split, d.D).total)
+    return GQA_ERR_WORKSPACE;
+  return launch_shared_prefix(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
 size_t decode_ws_size(int B, int Hq, int Hkv, int D, int max_kv_len, int tile, int ctas_per_sm = 2) {
   const SplitPlan p = plan_splits(B, Hq, Hkv, max_kv_len, tile, device_sm_count(), ctas_per_sm);
   return workspace_layout(B, Hq, Hkv, p.n_hc, p.n_split, D).total;
@@ -386,6 +427,109 @@ GQA_ATTN_API int gqa_attn_decode_paged(const void* q, const void* k_new, const v
     return GQA_ERR_WORKSPACE;
   if (launch_decode(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return GQA_ERR_CUDA;
   return GQA_OK;
+}
+
+GQA_ATTN_API size_t gqa_attn_decode_shared_prefix_workspace_size(int B, int Hq, int Hkv, int D,
+                                                                 int max_prefix_len, int max_kv_len) {
+  if (check_shared_prefix(B, Hq, Hkv, D, max_prefix_len, max_kv_len, max_kv_len, 1.f) != GQA_OK) return 0;
+  return shared_prefix_ws_size(B, Hq, Hkv, D, max_prefix_len, max_kv_len);
+}
+
+GQA_ATTN_API int gqa_attn_decode_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix,
+                                               const int32_t* prefix_len, const void* k, const void* v,
+                                               const int32_t* kv_lens, void* o, int B, int Hq, int Hkv, int D,
+                                               int P_cap, int max_prefix_len, int S_cap, int max_kv_len,
+                                               float scale, int dtype, void* workspace, size_t ws_bytes,
+                                               void* stream) {
+  int rc = check_shared_prefix(B, Hq, Hkv, D, max_prefix_len, S_cap, max_kv_len, scale);
+  if (rc != GQA_OK) return rc;
+  if (max_prefix_len > P_cap) return GQA_ERR_INVALID_ARG;
+  rc = check_shared_prefix_kernel(Hq, Hkv, dtype);
+  if (rc != GQA_OK) return rc;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
+  rc = check_ptrs({q, k_prefix, v_prefix, k, v, o}, dev, 16);
+  if (rc != GQA_OK) return rc;
+  for (const int32_t* n : {prefix_len, kv_lens})
+    if (n != nullptr) {
+      rc = check_ptrs({n}, dev, 4);
+      if (rc != GQA_OK) return rc;
+    }
+  SharedPrefixArgs a;
+  a.own.q = q;
+  a.own.k = k;
+  a.own.v = v;
+  a.own.o = o;
+  a.own.kv_lens = kv_lens;
+  a.own.B = B;
+  a.own.Hq = Hq;
+  a.own.Hkv = Hkv;
+  a.own.D = D;
+  a.own.S_cap = S_cap;
+  a.own.max_kv_len = max_kv_len;
+  a.own.scale = scale;
+  a.own.dtype = dtype;
+  a.own.workspace = workspace;
+  a.k_prefix = k_prefix;
+  a.v_prefix = v_prefix;
+  a.prefix_len = prefix_len;
+  a.prefix_table = nullptr;
+  a.max_prefix = max_prefix_len;
+  a.P_cap = P_cap;
+  return run_shared_prefix(a, ws_bytes, dev, stream);
+}
+
+GQA_ATTN_API int gqa_attn_decode_shared_prefix_paged(
+    const void* q, const void* k_pool, const void* v_pool, const int32_t* prefix_table, const int32_t* prefix_len,
+    const int32_t* block_table, const int32_t* kv_lens, void* o, int B, int Hq, int Hkv, int D, int block_size,
+    int num_blocks, int max_prefix_blocks, int max_blocks, int max_prefix_len, int max_kv_len, float scale,
+    int dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (block_size < 1 || num_blocks < 1 || max_blocks < 1 || max_prefix_blocks < 1) return GQA_ERR_INVALID_ARG;
+  if (long(max_kv_len) > long(max_blocks) * block_size) return GQA_ERR_INVALID_ARG;
+  if (long(max_prefix_len) > long(max_prefix_blocks) * block_size) return GQA_ERR_INVALID_ARG;
+  int rc = check_shared_prefix(B, Hq, Hkv, D, max_prefix_len, max_kv_len, max_kv_len, scale);
+  if (rc != GQA_OK) return rc;
+  if (long(num_blocks) * Hkv > 0x7fffffffL || long(num_blocks) * Hkv * block_size > 0x7fffffffL)
+    return GQA_ERR_INVALID_ARG;
+  rc = check_shared_prefix_kernel(Hq, Hkv, dtype);
+  if (rc != GQA_OK) return rc;
+  if (block_size % 64 != 0) return GQA_ERR_UNSUPPORTED;  // (both kernels copy 64 rows at a time)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
+  rc = check_ptrs({q, k_pool, v_pool, o}, dev, 16);
+  if (rc != GQA_OK) return rc;
+  rc = check_ptrs({prefix_table, block_table, kv_lens}, dev, 4);
+  if (rc != GQA_OK) return rc;
+  if (prefix_len != nullptr) {
+    rc = check_ptrs({prefix_len}, dev, 4);
+    if (rc != GQA_OK) return rc;
+  }
+  SharedPrefixArgs a;
+  a.own.q = q;
+  a.own.k = k_pool;
+  a.own.v = v_pool;
+  a.own.o = o;
+  a.own.kv_lens = kv_lens;
+  a.own.B = B;
+  a.own.Hq = Hq;
+  a.own.Hkv = Hkv;
+  a.own.D = D;
+  a.own.S_cap = block_size;
+  a.own.max_kv_len = max_kv_len;
+  a.own.scale = scale;
+  a.own.dtype = dtype;
+  a.own.workspace = workspace;
+  a.own.block_table = block_table;
+  a.own.block_size = block_size;
+  a.own.max_blocks = max_blocks;
+  a.own.num_blocks = num_blocks;
+  a.k_prefix = k_pool;
+  a.v_prefix = v_pool;
+  a.prefix_len = prefix_len;
+  a.prefix_table = prefix_table;
+  a.max_prefix = max_prefix_len;
+  a.P_cap = 0;
+  return run_shared_prefix(a, ws_bytes, dev, stream);
 }
 
 GQA_ATTN_API int gqa_attn_step_tables(const int32_t* prior_lens, const int32_t* new_lens,

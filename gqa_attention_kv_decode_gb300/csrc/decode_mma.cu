@@ -471,6 +471,8 @@ struct MapEntry {
 };
 constexpr int kMapCache = 128;
 
+}  // namespace
+
 bool kv_map(CUtensorMap* out, const void* base, int D, int S_cap, int heads) {
   static std::mutex mu;
   static MapEntry cache[kMapCache];
@@ -495,6 +497,8 @@ bool kv_map(CUtensorMap* out, const void* base, int D, int S_cap, int heads) {
   *out = m;
   return true;
 }
+
+namespace {
 
 template <int D, int NSTAGE, int NW, bool PAGED>
 cudaError_t launch_mma(const CUtensorMap& tk, const CUtensorMap& tv, const MmaParams& p, dim3 grid,

@@ -144,6 +144,29 @@ struct PrefillArgs {
 
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 
+// Row tiles and key shares of the shared rows of a batch (prefix.cu).
+struct PrefixPlan {
+  int rpt;      // requests per 128-row tile
+  int n_tiles;  // row tiles per KV head
+  int units;    // CTAs per KV head and share: one for a single tile, else one per two tiles
+  int n_split;  // shares of the keys
+};
+PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sms);
+
+// Decode over shared rows followed by each request's own (bf16): `own` is the
+// call over the own rows, its plan included; with a block table both caches
+// are the pools own.k / own.v, the shared rows' blocks in prefix_table.
+struct SharedPrefixArgs {
+  DecodeArgs own;
+  const void* k_prefix;  // [Hkv][P_cap][D], or the pools
+  const void* v_prefix;
+  const int32_t* prefix_len;    // device int32 [1], or null: max_prefix
+  const int32_t* prefix_table;  // or null: dense
+  int max_prefix, P_cap;
+  PrefixPlan plan;
+};
+cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, cudaStream_t stream);
+
 // One step's tables (gqa_attn_step_tables); block_table == nullptr: a dense
 // cache of block_size rows per request, without a free stack.
 struct StepTablesArgs {

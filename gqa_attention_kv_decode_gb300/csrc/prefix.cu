@@ -1,0 +1,688 @@
+// prefix.cu -- single-token decode of a batch whose requests share their
+// first keys: the shared rows are read once for the whole batch, on the
+// tcgen05 tensor cores, and joined with each request's own keys.
+//
+// Over the P shared rows every query of the batch meets the same K and V, so
+// for one KV head the B * n_rep query rows are the M rows of
+//     S = Q K^T,   O = P V          (a product, not B matrix-vector products),
+// which reads K and V once instead of B times.  Three kernels:
+//   prefix_kernel  one CTA takes two 128-row tiles of (request, head) rows --
+//                  or, when a KV head has one tile only, that tile, its KV
+//                  tiles dealt to the two softmax warpgroups in turn -- and a
+//                  contiguous share of the shared keys, and writes the rows'
+//                  partials (max, sum, unnormalised O);
+//   decode_mma     the requests' own keys, as in gqa_attn_decode, partials only;
+//   prefix_merge   log-sum-exp merge of a row's partials of both.
+// Inside the CTA the roles, the tensor-memory layout and the softmax are the
+// prefill kernel's: warp 8 TMA, warp 9 issues S, warps 10 and 11 issue P V,
+// warpgroups 0 and 1 do the softmax of one row per thread with a lazily
+// raised reference.  There is no diagonal: only the last KV tile is masked.
+//
+// What bounds it: a KV tile of 128 keys is 64 KB (D = 128) and two M = 128
+// row tiles on it cost 16.8 MFLOP, 250 FLOP a byte -- about this chip's ratio
+// of tensor rate to memory rate.  Up to 256 rows per KV head (B = 64 with 4
+// heads per KV head) the kernel is bound by the stream of K and V, above by
+// the products and exponentials.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+#include <type_traits>
+
+#include "attn_tile.cuh"
+#include "gqa_attn.h"
+#include "internal.h"
+#include "merge.cuh"
+#include "tc.cuh"
+#include "tmap.cuh"
+
+namespace gqa {
+namespace {
+
+// Tensor memory, shared memory and registers as in the prefill kernel:
+//   HD = 64:  S_A [0,128) S_B [128,256) O_A [256,320) O_B [320,384) P_A [384,448) P_B [448,512)
+//   HD = 128: S_A [0,128) S_B [128,256) O_A [256,384) O_B [384,512), P_t over the first 64 columns of S_t
+//   shared:   Q_A, Q_B, then NST stages of K and of V (161 KB, 193 KB)
+template <int HD_>
+struct PxCfg {
+  static constexpr int HD = HD_;
+  static constexpr int NBOX = HD / 64;
+  static constexpr int TILE_BYTES = NBOX * BOX_BYTES;
+  static constexpr int NST = HD == 64 ? 4 : 2;
+  static constexpr bool P_ALIAS = HD == 128;
+  static constexpr uint32_t TM_S = 0, TM_O = 256, TM_P = P_ALIAS ? 0u : 384u;
+  static constexpr uint32_t P_STRIDE = P_ALIAS ? 128u : 64u;
+  static constexpr int REG_CTRL = 56, REG_SOFTMAX = 224;  // 128 x 56 + 256 x 224 <= 384 x 168
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + 2 * TILE_BYTES;
+  static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_V + NST * TILE_BYTES;
+  static constexpr int OFF_ML = OFF_BAR + 256;              // (m, l) of both slots, [2][128]
+  static constexpr int SMEM_BYTES = OFF_ML + 2048 + 1024;   // + alignment slack
+  // mbarriers, [t] per slot: S_t ready; S_t read (4 warps); P_t halves stored
+  // (4 warps each); P.V of the first half / of all keys done
+  static constexpr int B_Q = 0, B_KF = 1, B_VF = B_KF + NST, B_KE = B_VF + NST, B_S = B_KE + NST, B_SC = B_S + 2,
+                       B_P0 = B_SC + 2, B_P1 = B_P0 + 2, B_O0 = B_P1 + 2, B_O1 = B_O0 + 2, B_DRAIN = B_O1 + 2,
+                       B_STALL = B_DRAIN + 1, N_BARS = B_STALL + 1;
+  static constexpr int OFF_TSLOT = 8 * N_BARS, OFF_ABORT = OFF_TSLOT + 8, OFF_ISSUED = OFF_ABORT + 4;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+  static_assert(OFF_ISSUED + 4 <= 256, "barrier area");
+  static_assert(128 * REG_CTRL + 256 * REG_SOFTMAX <= NTHR * 168, "register split exceeds the launch allocation");
+  // the epilogue stages 32 rows x HD floats for each of the 8 softmax warps
+  static_assert(8 * 32 * HD * 4 <= OFF_BAR - OFF_K, "row staging fits over the K and V stages");
+};
+
+struct PrefixParams {
+  const int32_t* prefix_len;  // or null: max_prefix
+  int max_prefix, B, Hq, Hkv, n_rep;
+  int rpt;      // requests per row tile: 128 / n_rep
+  int n_tiles;  // row tiles per KV head
+  int n_split;  // shares of the keys, at most
+  int slot0, n_slots;  // partial slots of a row: [slot0, slot0 + n_split) of n_slots
+  const int32_t* block_table;  // [blocks of the prefix], or null: rows of a dense [Hkv][P_cap][D]
+  int block_size, num_blocks;
+  float qk_scale_log2;
+  float2* ml;
+  float* part_o;
+  uint32_t* status;
+  uint64_t wait_limit_ns, test_stall_ns;
+};
+
+// The keys are cut into min(n_split, KV tiles) shares.
+__host__ __device__ __forceinline__ int prefix_shares(int n_split, int prefix_len) {
+  const int tiles = (prefix_len + BN - 1) / BN;
+  return tiles < n_split ? tiles : n_split;
+}
+
+// Writes NC columns of this warp's 32 rows, held as 32 columns at a time in
+// registers (a thread owns a row), to global memory: through the warp's
+// staging area in shared memory, 16-byte chunks XOR-ed with the row, so that
+// a store instruction covers whole rows (written directly, each would touch
+// 32 rows 16 bytes at a time).  get(cc, o): the columns [32 cc, 32 cc + 32)
+// of this thread's row.  dst: element offset of the thread's row, < 0: none.
+template <int NC, typename Get>
+__device__ __forceinline__ void store_rows(unsigned char* stage, float* out, long dst, int lane, Get get) {
+#pragma unroll
+  for (int cc = 0; cc < NC / 32; ++cc) {
+    float o[32];
+    get(cc, o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      *reinterpret_cast<float4*>(stage + lane * NC * 4 + (((cc * 8 + e) ^ (lane & 7)) << 4)) =
+          make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+  }
+  __syncwarp();
+  constexpr int LPR = NC / 4;      // lanes per row
+  constexpr int RPI = 32 / LPR;    // rows per instruction
+#pragma unroll 8
+  for (int r0 = 0; r0 < 32; r0 += RPI) {
+    const int r = r0 + lane / LPR, c = lane % LPR;
+    const long d = __shfl_sync(0xffffffffu, dst, r);
+    const float4 v = *reinterpret_cast<const float4*>(stage + r * NC * 4 + ((c ^ (r & 7)) << 4));
+    if (d >= 0) *reinterpret_cast<float4*>(out + d + 4 * c) = v;
+  }
+}
+
+// SINGLE: one row tile per CTA, its even KV tiles in slot 0 and the odd ones
+// in slot 1; otherwise tiles A and B (slots 0 and 1) over the same KV tiles.
+template <int HD, bool SINGLE>
+__global__ void __launch_bounds__(NTHR, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const PrefixParams p) {
+  using C = PxCfg<HD>;
+  constexpr int NBOX = C::NBOX, TILE_BYTES = C::TILE_BYTES, NST = C::NST;
+  constexpr int OFF_Q = C::OFF_Q, OFF_K = C::OFF_K, OFF_V = C::OFF_V, OFF_BAR = C::OFF_BAR;
+  constexpr int B_Q = C::B_Q, B_KF = C::B_KF, B_VF = C::B_VF, B_KE = C::B_KE, B_S = C::B_S, B_SC = C::B_SC,
+                B_P0 = C::B_P0, B_P1 = C::B_P1, B_O0 = C::B_O0, B_O1 = C::B_O1, B_DRAIN = C::B_DRAIN;
+  constexpr uint32_t TM_S = C::TM_S, TM_O = C::TM_O, TM_P = C::TM_P;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = blockIdx.x, g = blockIdx.z;
+  const int tile0 = SINGLE ? int(blockIdx.y) : 2 * int(blockIdx.y);
+  const bool two = !SINGLE && tile0 + 1 < p.n_tiles;  // is there a tile B?
+  const int q_rows = p.n_rep * p.rpt;                 // rows of a tile that are queries
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + OFF_BAR + C::OFF_TSLOT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_BAR + C::OFF_ABORT);
+
+  grid_launch_dependents();  // (the next grid's CTAs wait for this one themselves)
+  if (warp == 9) {
+    tmem_alloc(tslot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (tid == 256) {
+    for (int i = 0; i < C::N_BARS; ++i) {
+      const bool per_warp = (i >= B_SC && i < B_O0);
+      const bool three = (i >= B_KE && i < B_KE + NST) || i == B_DRAIN;
+      mbar_init(&bars[i], per_warp ? 4 : three ? 3 : 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  // the last rows of a tile that hold no query (128 is no multiple of n_rep):
+  // zeros, so that their scores are ordinary numbers
+  if (q_rows < BM) {
+    const int chunks = (BM - q_rows) * 8;
+    for (int i = tid; i < 2 * NBOX * chunks; i += NTHR)
+      *reinterpret_cast<uint4*>(smem + OFF_Q + (i / chunks) * BOX_BYTES + q_rows * 128 + (i % chunks) * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  grid_dependency_wait();
+
+  int P = p.max_prefix;
+  if (p.prefix_len != nullptr) {
+    const int raw = *p.prefix_len;
+    P = min(max(raw, 0), p.max_prefix);
+    if (P != raw && tid == 0 && split == 0 && g == 0 && blockIdx.y == 0) atomicOr(p.status, GQA_DEV_KVLEN_CLAMPED);
+  }
+  const int n_kv = (P + BN - 1) / BN, n_used = prefix_shares(p.n_split, P);
+  if (split >= n_used) {  // no share for this CTA
+    if (warp == 9) tmem_dealloc(tmem, TMEM_COLS);
+    return;
+  }
+  const int j_lo = int(long(n_kv) * split / n_used), j_hi = int(long(n_kv) * (split + 1) / n_used);
+  const int nkv = j_hi - j_lo;  // >= 1
+  const int nkv0 = SINGLE ? (nkv + 1) / 2 : nkv;
+  const int nkv1 = SINGLE ? nkv / 2 : two ? nkv : 0;
+  auto active = [&](int j, int t) -> bool { return SINGLE ? (j & 1) == t : (t == 0 || two); };
+  auto local_it = [&](int j) -> int { return SINGLE ? j >> 1 : j; };
+
+  if (warp >= 8) {
+    set_max_regs_dec<C::REG_CTRL>();
+    if (warp == 8 && lane == 0) {
+      // ---------------- TMA ----------------
+      const int n_q = two ? 2 : 1;
+      int n_issued = 0;
+      if (p.test_stall_ns != 0) stall_test(&bars[C::B_STALL], p.test_stall_ns, abort_flag);
+      mbar_arrive_expect_tx(&bars[B_Q], n_q * NBOX * q_rows * 128);
+      for (int t = 0; t < n_q; ++t)
+#pragma unroll
+        for (int bx = 0; bx < NBOX; ++bx)
+          tma_load_4d(smem + OFF_Q + t * TILE_BYTES + bx * BOX_BYTES, &tmQ, bx * 64, 0, (tile0 + t) * p.rpt, g,
+                      &bars[B_Q]);
+      // (row, head) in the map of the two 64-row halves of KV tile j
+      int row[2], head[2];
+      auto locate = [&](int j) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int r0 = (j_lo + j) * BN + s * 64;
+          row[s] = r0;
+          head[s] = g;
+          if (p.block_table != nullptr) {
+            if (r0 >= P) {  // past the keys: any rows will do (masked, and V cleared)
+              row[s] = row[0];
+              head[s] = head[0];
+              continue;
+            }
+            int blk = p.block_table[r0 / p.block_size];
+            if (blk < 0 || blk >= p.num_blocks) {
+              atomicOr(p.status, GQA_DEV_BAD_BLOCK);
+              blk = 0;
+            }
+            row[s] = r0 % p.block_size;
+            head[s] = blk * p.Hkv + g;
+          }
+        }
+      };
+      locate(0);
+      for (int j = 0; j < nkv; ++j) {
+        const int st = j % NST;
+        if (j >= NST) cta_wait(&bars[B_KE + st], uint32_t(j / NST - 1) & 1u, abort_flag, p.wait_limit_ns);
+        if (*abort_flag) break;
+        mbar_arrive_expect_tx(&bars[B_KF + st], TILE_BYTES);
+#pragma unroll
+        for (int bx = 0; bx < NBOX; ++bx)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            tma_load_3d(smem + OFF_K + st * TILE_BYTES + bx * BOX_BYTES + s * 8192, &tmK, bx * 64, row[s], head[s],
+                        &bars[B_KF + st]);
+        mbar_arrive_expect_tx(&bars[B_VF + st], TILE_BYTES);
+#pragma unroll
+        for (int bx = 0; bx < NBOX; ++bx)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            tma_load_3d(smem + OFF_V + st * TILE_BYTES + bx * BOX_BYTES + s * 8192, &tmV, bx * 64, row[s], head[s],
+                        &bars[B_VF + st]);
+        n_issued = j + 1;
+        if (j + 1 < nkv) locate(j + 1);  // (the table entries arrive while the next stage is waited for)
+      }
+      *reinterpret_cast<volatile int*>(smem + OFF_BAR + C::OFF_ISSUED) = n_issued;
+    } else if (warp == 9) {
+      // ---------------- MMA issue: S_t = Q_t K^T ----------------
+      const uint64_t qdesc = sdesc_sw128(smem_u32(smem + OFF_Q));
+      const uint64_t kdesc = sdesc_sw128(smem_u32(smem + OFF_K));
+      constexpr uint64_t TILE_STEP = TILE_BYTES >> 4, K_KSTEP = 32 >> 4, BOX_STEP = BOX_BYTES >> 4;
+      cta_wait(&bars[B_Q], 0, abort_flag, p.wait_limit_ns);
+      for (int j = 0; j < nkv; ++j) {
+        const int st = j % NST;
+        cta_wait(&bars[B_KF + st], uint32_t(j / NST) & 1u, abort_flag, p.wait_limit_ns);
+        const uint64_t kd = kdesc + st * TILE_STEP;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!active(j, t)) continue;
+          const int li = local_it(j);
+          if (li > 0) {  // S_t(li - 1) read by its softmax and, where P_t lies over it, P_t(li - 1) by its P.V
+            cta_wait(&bars[B_SC + t], uint32_t(li - 1) & 1u, abort_flag, p.wait_limit_ns);
+            if (C::P_ALIAS) cta_wait(&bars[B_O1 + t], uint32_t(li - 1) & 1u, abort_flag, p.wait_limit_ns);
+          }
+          tc_fence_after();
+          const uint64_t qd = qdesc + (SINGLE ? 0 : t) * TILE_STEP;
+          const uint32_t d = tmem + TM_S + t * 128;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint64_t koff = (kk / 4) * BOX_STEP + (kk % 4) * K_KSTEP;
+            mma_bf16_warp(d, qd + koff, kd + koff, IDESC_S, kk > 0 ? 1u : 0u);
+          }
+          mma_commit_warp(&bars[B_S + t]);
+        }
+        mma_commit_warp(&bars[B_KE + st]);
+      }
+    } else if (warp >= 10) {
+      // ---------------- MMA issue: O_t += P_t V, t = warp - 10 ----------------
+      const int t = warp - 10;
+      const uint64_t vdesc = sdesc_sw128(smem_u32(smem + OFF_V));
+      constexpr uint64_t TILE_STEP = TILE_BYTES >> 4, V_KSTEP = 2048 >> 4, BOX_STEP = BOX_BYTES >> 4;
+      const uint32_t d = tmem + TM_O + t * HD, a = tmem + TM_P + t * C::P_STRIDE;
+      // rows past P hold anything (their P is 0, but 0 * NaN is NaN): cleared
+      const int j_zero = P % BN != 0 ? (P - 1) / BN - j_lo : -1;
+      for (int j = 0; j < nkv; ++j) {
+        const int st = j % NST;
+        cta_wait(&bars[B_VF + st], uint32_t(j / NST) & 1u, abort_flag, p.wait_limit_ns);
+        if (j == j_zero) {
+          unsigned char* vt = smem + OFF_V + st * TILE_BYTES;
+          const int r0 = P % BN, per_box = (BN - r0) * 8;
+          for (int i = t * 32 + lane; i < per_box * NBOX; i += 64) {
+            const int bx = i / per_box, k = i % per_box;
+            *reinterpret_cast<uint4*>(vt + bx * BOX_BYTES + (r0 + k / 8) * 128 + (k % 8) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          named_bar_sync(1, 64);  // both P.V warps are done clearing
+        }
+        if (active(j, t)) {
+          const int li = local_it(j);
+          const uint64_t vd = vdesc + st * TILE_STEP;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            cta_wait(&bars[(half ? B_P1 : B_P0) + t], uint32_t(li) & 1u, abort_flag, p.wait_limit_ns);
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+              for (int bx = 0; bx < NBOX; ++bx)
+                mma_bf16_ts_warp(d + bx * 64, a + half * 32 + kk * 8, vd + bx * BOX_STEP + (half * 4 + kk) * V_KSTEP,
+                                 IDESC_O, (li > 0 || half > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_warp(&bars[(half ? B_O1 : B_O0) + t]);
+          }
+        }
+        mma_commit_warp(&bars[B_KE + st]);
+      }
+    }
+  } else {
+    // ---------------- softmax of slot t = warp / 4 ----------------
+    set_max_regs_inc<C::REG_SOFTMAX>();
+    const int t = warp >> 2;
+    const int n_it = t == 0 ? nkv0 : nkv1;
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + TM_S + t * 128 + lane_off;
+    const uint32_t tO = tmem + TM_O + lane_off;  // (of slot 0)
+    const uint32_t tP = tmem + TM_P + t * C::P_STRIDE + lane_off;
+    const float c = p.qk_scale_log2;
+    float m_ref = -INFINITY, lsum = 0.f;
+    // the two warpgroups take turns at the exponentials (see the prefill kernel)
+    const int nmin = min(nkv0, nkv1);
+    if (t == 1 && nmin > 0) named_bar_arrive(BAR_TURN_A, 256);
+    for (int j = 0; j < n_it; ++j) {
+      cta_wait(&bars[B_S + t], uint32_t(j) & 1u, abort_flag, p.wait_limit_ns);
+      tc_fence_after();
+      uint32_t s[BN];
+      float rmx[4];
+      tmem_ld32_max(tS, *reinterpret_cast<uint32_t(*)[32]>(s), rmx[0]);
+      tmem_ld32_max(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32), rmx[1]);
+      tmem_ld32_max(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(s + 64), rmx[2]);
+      tmem_ld32_max(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(s + 96), rmx[3]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_SC + t]);
+      const int left = P - (j_lo + (SINGLE ? 2 * j + t : j)) * BN;  // keys from the tile's first on
+      if (left < BN) {  // the last tile: mask, then take the maximum again
+#pragma unroll
+        for (int e = 0; e < BN; ++e)
+          if (e >= left) s[e] = 0xff800000u;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < BN; e += 8) {
+          mx[0] = max3f(mx[0], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          mx[1] = max3f(mx[1], __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+          mx[2] = max3f(mx[2], __uint_as_float(s[e + 4]), __uint_as_float(s[e + 5]));
+          mx[3] = max3f(mx[3], __uint_as_float(s[e + 6]), __uint_as_float(s[e + 7]));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rmx[i] = mx[i];
+      }
+      const float tmax = max3f(rmx[0], rmx[1], fmaxf(rmx[2], rmx[3])) * c;
+      if (j == 0) {
+        m_ref = tmax;
+      } else {
+        const bool resc = tmax > m_ref + 8.f;
+        if (__any_sync(0xffffffffu, resc)) {
+          cta_wait(&bars[B_O1 + t], uint32_t(j - 1) & 1u, abort_flag, p.wait_limit_ns);
+          tc_fence_after();
+          const float alpha = resc ? fast_exp2(m_ref - tmax) : 1.f;
+          if (resc) m_ref = tmax;
+#pragma unroll
+          for (int cc = 0; cc < HD / 32; ++cc) {
+            uint32_t o[32];
+            tmem_ld32(tO + t * HD + cc * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(tO + t * HD + cc * 32, o);
+          }
+          tmem_wait_st();
+          lsum *= alpha;
+        }
+      }
+      // (-inf: every score of the row so far was; its exponentials use 0)
+      float mu = m_ref == -INFINITY ? 0.f : m_ref;
+      if (j < nmin) named_bar_sync(t == 0 ? BAR_TURN_A : BAR_TURN_B, 256);
+      asm volatile("" : "+f"(mu));  // keeps the exponentials behind the turn
+      const float2 cc2 = make_float2(c, c), mm = make_float2(-mu, -mu);
+      float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pw[32];
+        exp_half(s + half * 64, cc2, mm, pw, acc);
+        if (half == 1 && j < nmin) {
+          asm volatile("" ::"f"(acc[0].x), "f"(acc[0].y), "f"(acc[1].x), "f"(acc[1].y), "f"(acc[2].x),
+                       "f"(acc[2].y), "f"(acc[3].x), "f"(acc[3].y));
+          if (t == 0 || j < nmin - 1) named_bar_arrive(t == 0 ? BAR_TURN_B : BAR_TURN_A, 256);
+        }
+        if (j > 0) cta_wait(&bars[(half ? B_O1 : B_O0) + t], uint32_t(j - 1) & 1u, abort_flag, p.wait_limit_ns);
+        tc_fence_after();
+        tmem_st32(tP + half * 32, pw);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[(half ? B_P1 : B_P0) + t]);
+      }
+      lsum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y) + (acc[2].x + acc[2].y) + (acc[3].x + acc[3].y);
+    }
+    if (n_it > 0) {
+      cta_wait(&bars[B_O1 + t], uint32_t(n_it - 1) & 1u, abort_flag, p.wait_limit_ns);
+      tc_fence_after();
+    }
+
+    // ---- epilogue: the rows' partials ----
+    float2* mlx = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    const int r = tid & (BM - 1);  // row in the tile
+    if (SINGLE) mlx[tid] = make_float2(m_ref, lsum);
+    tc_fence_before();
+    named_bar_sync(BAR_ILV, 256);  // both slots are done: every product has run, the K and V stages are free
+    tc_fence_after();
+    const int b = (tile0 + (SINGLE ? 0 : t)) * p.rpt + r / p.n_rep;
+    const bool row_ok = r < q_rows && b < p.B && n_it > 0 && !*abort_flag;
+    const long prow = (long(b) * p.Hq + g * p.n_rep + r % p.n_rep) * p.n_slots + p.slot0 + split;
+    unsigned char* stage = smem + OFF_K + warp * (32 * HD * 4);
+    if constexpr (SINGLE) {
+      // The row has a state in both slots (slot 1 may have seen no KV tile):
+      //   M = max(m0, m1),  w_s = 2^(m_s - M),  O = w0 O0 + w1 O1,  l = w0 l0 + w1 l1;
+      // warpgroup t writes columns [t HD / 2, (t + 1) HD / 2).
+      const float2 x0 = mlx[r], x1 = mlx[BM + r];
+      const bool has1 = nkv1 > 0;  // (O1 was never written otherwise)
+      const float M = has1 ? fmaxf(x0.x, x1.x) : x0.x;
+      const float w0 = x0.x == -INFINITY ? 0.f : x0.x == M ? 1.f : fast_exp2(x0.x - M);
+      const float w1 = (!has1 || x1.x == -INFINITY) ? 0.f : x1.x == M ? 1.f : fast_exp2(x1.x - M);
+      const bool ok = r < q_rows && b < p.B && !*abort_flag;
+      if (t == 0 && ok) p.ml[prow] = make_float2(M, w0 * x0.y + w1 * x1.y);
+      store_rows<HD / 2>(stage, p.part_o, ok ? prow * HD + t * (HD / 2) : -1L, lane, [&](int cc, float (&o)[32]) {
+        uint32_t a0[32], a1[32];
+        tmem_ld32(tO + t * (HD / 2) + cc * 32, a0);
+        if (has1) tmem_ld32(tO + HD + t * (HD / 2) + cc * 32, a1);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          o[e] = __uint_as_float(a0[e]) * w0;
+          if (has1) o[e] = fmaf(__uint_as_float(a1[e]), w1, o[e]);
+        }
+      });
+    } else if (n_it > 0) {
+      if (row_ok) p.ml[prow] = make_float2(m_ref, lsum);
+      store_rows<HD>(stage, p.part_o, row_ok ? prow * HD : -1L, lane, [&](int cc, float (&o)[32]) {
+        uint32_t a[32];
+        tmem_ld32(tO + t * HD + cc * 32, a);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(a[e]);
+      });
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {  // let the work in flight end before the memories are released (as in prefill)
+    if (warp >= 9 && warp <= 11) {
+      mma_commit_warp(&bars[B_DRAIN]);
+      mbar_wait_bounded(&bars[B_DRAIN], 0, p.wait_limit_ns);
+    }
+    if (warp == 8 && lane == 0)
+      drain_copies<NST>(bars, B_Q, B_KF, B_VF, *reinterpret_cast<volatile int*>(smem + OFF_BAR + C::OFF_ISSUED),
+                        p.wait_limit_ns);
+    if (tid == 0) atomicOr(p.status, GQA_DEV_WAIT_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == 9) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+// ---- merge -------------------------------------------------------------------
+
+struct PrefixMergeParams {
+  __nv_bfloat16* o;
+  const int32_t* prefix_len;  // or null: max_prefix
+  const int32_t* kv_lens;     // or null: max_kv_len
+  int rows, Hq, max_prefix, max_kv_len;
+  int chunk, n_own;           // own keys: slots [0, min(n_own, ceil(L / chunk)))
+  int n_split, n_slots;       // shared keys: slots [n_own, n_own + shares)
+  const float2* ml;
+  const float* part_o;
+  uint32_t* status;
+};
+
+// One warp per (request, query head) row: the maximum of the row's partials
+// over the lanes, then their weighted sum, each partial row one load of the
+// whole warp.  The first PRE partial rows are loaded before the weights are
+// known, so that the two round trips overlap.  The order of the sum is fixed.
+template <int D>
+__global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixMergeParams p) {
+  constexpr int V = D / 32;  // columns per lane
+  constexpr int PRE = 8;
+  using Vec = typename std::conditional<V == 4, float4, float2>::type;
+  const int row = int((blockIdx.x * 256 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  if (row >= p.rows) return;
+  const int b = row / p.Hq;
+  int P = p.prefix_len != nullptr ? *p.prefix_len : p.max_prefix;
+  int L = p.kv_lens != nullptr ? p.kv_lens[b] : p.max_kv_len;
+  P = min(max(P, 0), p.max_prefix);
+  L = min(max(L, 0), p.max_kv_len);
+  const int own = min(p.n_own, (L + p.chunk - 1) / p.chunk), n = own + prefix_shares(p.n_split, P);
+  auto slot = [&](int i) { return i < own ? i : p.n_own + i - own; };
+  __nv_bfloat16* const dst = p.o + size_t(row) * D + lane * V;
+  float acc[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  float den = 1.f;
+  if (n == 0) {  // no key at all: zeros
+    if (lane == 0) atomicOr(p.status, GQA_DEV_EMPTY_REQUEST);
+  } else {
+    const float2* ml = p.ml + size_t(row) * p.n_slots;
+    const float* po = p.part_o + size_t(row) * p.n_slots * D + lane * V;
+    Vec x[PRE];
+#pragma unroll
+    for (int k = 0; k < PRE; ++k)
+      if (k < n) x[k] = __ldcg(reinterpret_cast<const Vec*>(po + size_t(slot(k)) * D));
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(&ml[slot(i)]).x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    den = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float w = 0.f;
+      if (i0 + lane < n) {
+        const float2 s = __ldcg(&ml[slot(i0 + lane)]);
+        w = s.x == -INFINITY ? 0.f : fast_exp2(s.x - M);
+        den += s.y * w;
+      }
+      auto add = [&](int k, const Vec& v) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const float* f = reinterpret_cast<const float*>(&v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(f[e], wk, acc[e]);
+      };
+      int k = 0;
+      if (i0 == 0) {
+#pragma unroll
+        for (; k < PRE; ++k)
+          if (k < n) add(k, x[k]);
+      }
+      const int cnt = min(32, n - i0);
+#pragma unroll 4
+      for (; k < cnt; ++k) add(k, __ldcg(reinterpret_cast<const Vec*>(po + size_t(slot(i0 + k)) * D)));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
+  }
+  const float inv = 1.f / den;
+#pragma unroll
+  for (int e = 0; e < V; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+}
+
+template <int HD>
+cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
+  using C = PxCfg<HD>;
+  const DecodeArgs& d = a.own;
+  const int n_rep = d.Hq / d.Hkv;
+  const bool paged = d.block_table != nullptr;
+  CUtensorMap tq, tk, tv;
+  const int heads = paged ? d.num_blocks * d.Hkv : d.Hkv, rows = paged ? d.block_size : a.P_cap;
+  if (!encode_bf16_query_rows(&tq, d.q, HD, n_rep, d.B, d.Hkv, a.plan.rpt) ||
+      !kv_map(&tk, a.k_prefix, HD, rows, heads) || !kv_map(&tv, a.v_prefix, HD, rows, heads))
+    return cudaErrorInvalidValue;
+  const int n_own = d.plan.n_split, n_slots = n_own + a.plan.n_split;
+  const WorkspaceLayout w = workspace_layout(d.B, d.Hq, d.Hkv, d.plan.n_hc, n_slots, HD);
+  unsigned char* ws = static_cast<unsigned char*>(d.workspace);
+  PrefixParams p;
+  p.prefix_len = a.prefix_len;
+  p.max_prefix = a.max_prefix;
+  p.B = d.B;
+  p.Hq = d.Hq;
+  p.Hkv = d.Hkv;
+  p.n_rep = n_rep;
+  p.rpt = a.plan.rpt;
+  p.n_tiles = a.plan.n_tiles;
+  p.n_split = a.plan.n_split;
+  p.slot0 = n_own;
+  p.n_slots = n_slots;
+  p.block_table = a.prefix_table;
+  p.block_size = d.block_size;
+  p.num_blocks = d.num_blocks;
+  p.qk_scale_log2 = float(double(d.scale) * 1.4426950408889634);
+  p.ml = reinterpret_cast<float2*>(ws + w.off_ml);
+  p.part_o = reinterpret_cast<float*>(ws + w.off_o);
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  p.wait_limit_ns = kWaitLimitNs;
+  p.test_stall_ns = wait_test_ns();
+  static std::once_flag once;
+  static cudaError_t cfg_err = cudaSuccess;
+  std::call_once(once, [&] {
+    for (const void* k : {reinterpret_cast<const void*>(prefix_kernel<HD, false>),
+                          reinterpret_cast<const void*>(prefix_kernel<HD, true>)})
+      if (cfg_err == cudaSuccess)
+        cfg_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  });
+  if (cfg_err != cudaSuccess) return cfg_err;
+  const dim3 grid(a.plan.n_split, a.plan.units, d.Hkv);
+  cudaError_t e = a.plan.units == a.plan.n_tiles
+                      ? launch_pdl(prefix_kernel<HD, true>, grid, dim3(NTHR), C::SMEM_BYTES, stream, tq, tk, tv, p)
+                      : launch_pdl(prefix_kernel<HD, false>, grid, dim3(NTHR), C::SMEM_BYTES, stream, tq, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  DecodeArgs own = d;
+  own.n_slots = n_slots;
+  own.force_partial = 1;
+  e = launch_decode_mma(own, stream);
+  if (e != cudaSuccess) return e;
+  PrefixMergeParams m;
+  m.o = static_cast<__nv_bfloat16*>(d.o);
+  m.prefix_len = a.prefix_len;
+  m.kv_lens = d.kv_lens;
+  m.rows = d.B * d.Hq;
+  m.Hq = d.Hq;
+  m.max_prefix = a.max_prefix;
+  m.max_kv_len = d.max_kv_len;
+  m.chunk = d.plan.chunk;
+  m.n_own = n_own;
+  m.n_split = a.plan.n_split;
+  m.n_slots = n_slots;
+  m.ml = p.ml;
+  m.part_o = p.part_o;
+  m.status = p.status;
+  return launch_pdl(prefix_merge_kernel<HD>, dim3((m.rows + 7) / 8), dim3(256), 0, stream, m);
+}
+
+}  // namespace
+
+// Row tiles and key shares.  A unit (a pair of row tiles, or the one tile of
+// a KV head) times a share is a CTA; one CTA fits an SM.  Of the share counts
+// the planner takes the one with the least estimated time, in iterations
+// (one KV tile of a unit): the waves of the grid times the iterations of a
+// share plus a CTA's set-up and epilogue, and the partial rows' way to memory
+// and back.
+PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sms) {
+  PrefixPlan p;
+  const int n_rep = Hq / Hkv;
+  if (num_sms < 1) num_sms = 1;  // (no device: sizes can still be asked for)
+  p.rpt = BM / n_rep;
+  p.n_tiles = (B + p.rpt - 1) / p.rpt;
+  p.units = p.n_tiles == 1 ? 1 : (p.n_tiles + 1) / 2;
+  const long units = long(p.units) * Hkv;
+  const int tiles = (max_prefix + BN - 1) / BN;
+  constexpr double kSetup = 3.3;
+  // partials written and read, against the KV stream of one iteration
+  const double per_share = 2.0 * B * Hq * D * 4 / (double(num_sms) * 2 * BN * D * 2);
+  double best = 0.0;
+  p.n_split = 1;
+  for (int n = 1; n <= std::min(tiles, 256); ++n) {
+    const long waves = (units * n + num_sms - 1) / num_sms;
+    const double t = double(waves) * (kSetup + (tiles + n - 1) / n) + per_share * n;
+    if (n == 1 || t < best - 1e-9) {
+      best = t;
+      p.n_split = n;
+    }
+  }
+  return p;
+}
+
+cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, cudaStream_t stream) {
+  if (a.own.D == 64) return launch_prefix_hd<64>(a, stream);
+  if (a.own.D == 128) return launch_prefix_hd<128>(a, stream);
+  return cudaErrorNotSupported;
+}
+
+}  // namespace gqa

@@ -189,6 +189,59 @@ GQA_ATTN_API int gqa_attn_decode_paged(const void* q, const void* k_new, const v
                                        size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Single-token decode of a batch whose requests share their first keys.
+ *
+ * Every request attends the same P shared rows (a system prompt, a document,
+ * the prompt of several samples) followed by kv_lens[b] rows of its own:
+ * exactly the output of gqa_attn_decode on caches that begin with a copy of
+ * the shared rows, but these are kept once and read once for the batch, as
+ * a matrix product over all its queries instead of one pass per request.
+ *
+ *   q, o          bf16 [B, Hq, 1, D]
+ *   k_prefix,     bf16 [Hkv, P_cap, D]: the shared rows, without a batch axis
+ *   v_prefix
+ *   prefix_len    device int32 [1]: shared rows P, clamped into
+ *                 [0, max_prefix_len] (GQA_DEV_KVLEN_CLAMPED); NULL means
+ *                 max_prefix_len
+ *   k, v          bf16 [B, Hkv, S_cap, D]: the requests' own rows
+ *   kv_lens       device int32 [B]: own rows of each request, without the
+ *                 shared ones (0 is an ordinary length); clamped into
+ *                 [0, max_kv_len]; NULL means max_kv_len for every request
+ *   max_prefix_len, max_kv_len   host bounds, at least 1 and at most P_cap and
+ *                 S_cap; they size the grids and the workspace
+ * A request with no key at all gets a zero row (GQA_DEV_EMPTY_REQUEST).
+ * Rows past the lengths may hold anything, NaN included.  Three kernels run
+ * (shared rows, own rows, merge).  dtype must be GQA_BF16 and Hq / Hkv at most
+ * 128 (else GQA_ERR_UNSUPPORTED).  Workspace:
+ * gqa_attn_decode_shared_prefix_workspace_size, for both entry points.  Other
+ * arguments and errors as for gqa_attn_decode.
+ *
+ * The paged call reads both kinds of rows from one pair of block pools, as
+ * gqa_attn_decode_paged does: shared row j is row j % block_size of block
+ * prefix_table[j / block_size] (device int32 [max_prefix_blocks]), own row j of
+ * request b that of block_table[b][j / block_size], which starts behind the
+ * shared rows (own row 0 begins a block).  block_size is a multiple of 64;
+ * block ids out of range set GQA_DEV_BAD_BLOCK, and what read them is
+ * unspecified (no read leaves the pool).  kv_lens is required there.
+ * ------------------------------------------------------------------------- */
+GQA_ATTN_API size_t gqa_attn_decode_shared_prefix_workspace_size(int B, int Hq, int Hkv, int D,
+                                                                 int max_prefix_len,
+                                                                 int max_kv_len);
+GQA_ATTN_API int gqa_attn_decode_shared_prefix(const void* q, const void* k_prefix,
+                                               const void* v_prefix, const int32_t* prefix_len,
+                                               const void* k, const void* v, const int32_t* kv_lens,
+                                               void* o, int B, int Hq, int Hkv, int D, int P_cap,
+                                               int max_prefix_len, int S_cap, int max_kv_len,
+                                               float scale, int dtype, void* workspace,
+                                               size_t ws_bytes, void* stream);
+GQA_ATTN_API int gqa_attn_decode_shared_prefix_paged(
+    const void* q, const void* k_pool, const void* v_pool, const int32_t* prefix_table,
+    const int32_t* prefix_len, const int32_t* block_table, const int32_t* kv_lens, void* o, int B,
+    int Hq, int Hkv, int D, int block_size, int num_blocks, int max_prefix_blocks, int max_blocks,
+    int max_prefix_len, int max_kv_len, float scale, int dtype, void* workspace, size_t ws_bytes,
+    void* stream);
+
+/* ---------------------------------------------------------------------------
  * The tables of one serving step, built on the GPU from the requests' lengths.
  *
  * A step appends new_lens[b] tokens to request b.  This call turns the
@@ -434,8 +487,8 @@ GQA_ATTN_API int gqa_attn_set_prefill_interleave_override(int from_pair);
  * GQA_DEV_WAIT_TIMEOUT in the workspace status word, a prefill CTA writes its
  * output rows as NaN and sets GQA_DEV_WAIT_TIMEOUT in the prefill status word.
  * With stall_ns > 0 every later launch of gqa_attn_decode, _decode_paged,
- * _decode_layers, _decode_q4, _decode_q4_residual, _prefill and
- * _prefill_varlen makes the thread that issues a CTA's copies, once it has
+ * _decode_layers, _decode_q4, _decode_q4_residual, _decode_shared_prefix(_paged),
+ * _prefill and _prefill_varlen makes the thread that issues a CTA's copies, once it has
  * issued its first ones, wait stall_ns on a barrier that nothing arrives on
  * and give up, so that this path runs deterministically: the call reports
  * GQA_DEV_WAIT_TIMEOUT and its outputs are unspecified (a prefill CTA whose
