@@ -71,6 +71,7 @@ EXPORTED = (
 )
 
 _lib = None
+_I32 = torch.int32
 
 
 class GqaAttnError(RuntimeError):
@@ -176,30 +177,40 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _heads(t):
+def _heads(t, T, H, D):
     """Pointer and token stride (elements) of a [T, H, D] tensor whose heads
     are dense; the tokens may be further apart (views of one projection)."""
-    T, H, D = t.shape
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+    if t.shape != (T, H, D):
+        raise ValueError("q is [T, Hq, D], k and v are [T, Hkv, D]")
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != D and H > 1):
         raise ValueError("the heads of a token must be contiguous")
-    return t.data_ptr(), (t.stride(0) if T > 1 else H * D)
+    return t.data_ptr(), (st if T > 1 else H * D)
 
 
-def _int32(*tensors):
-    for t in tensors:
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError("lengths, tables, positions and slots are int32")
+def _ints(t, n):
+    """Pointer of a dense int32 tensor of n entries; None stays None."""
+    if t is None:
+        return None
+    if t.dtype is not _I32:
+        raise TypeError("lengths, tables, positions and slots are int32")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"a contiguous int32 tensor of {n} entries is needed, got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _one_dtype(first, *tensors):
+    dt = first.dtype
     for t in tensors:
-        if t is not None and t.dtype != first.dtype:
+        if t is not None and t.dtype is not dt:
             raise TypeError("the tensors of a call have one dtype")
 
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # (the handle alone: torch.cuda.current_stream() builds a Stream
+        # object around it, 2.9 us of a 16 us call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -333,12 +344,11 @@ def gqa_attn_decode_shared_prefix(q, k_prefix, v_prefix, prefix_len, k, v, kv_le
             or k_prefix.shape[2] != D or o.shape != q.shape:
         raise ValueError("k_prefix and v_prefix are [Hkv, P_cap, D], k and v [B, Hkv, S_cap, D], o as q")
     _one_dtype(q, k_prefix, v_prefix, k, v, o)
-    _int32(prefix_len, kv_lens)
     rc = lib().gqa_attn_decode_shared_prefix(
-        _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), B, Hq,
-        Hkv, D, P_cap, P_cap if max_prefix_len is None else int(max_prefix_len), S_cap,
+        _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ints(prefix_len, 1), _ptr(k), _ptr(v), _ints(kv_lens, B), _ptr(o),
+        B, Hq, Hkv, D, P_cap, P_cap if max_prefix_len is None else int(max_prefix_len), S_cap,
         S_cap if max_kv_len is None else int(max_kv_len), float(scale), _dtype_code(q), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        workspace.nbytes, _stream(stream))
     _check(rc, "gqa_attn_decode_shared_prefix")
 
 
@@ -351,15 +361,15 @@ def gqa_attn_decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, prefix_
     num_blocks, Hkv, block_size = k_pool.shape[0], k_pool.shape[1], k_pool.shape[2]
     if Tq != 1:
         raise ValueError("decode takes one query row per request")
-    if v_pool.shape != k_pool.shape or k_pool.shape[3] != D or o.shape != q.shape or block_table.shape[0] != B:
-        raise ValueError("k_pool and v_pool are [blocks, Hkv, block_size, D], block_table [B, blocks], o as q")
+    if v_pool.shape != k_pool.shape or k_pool.shape[3] != D or o.shape != q.shape:
+        raise ValueError("k_pool and v_pool are [blocks, Hkv, block_size, D], o as q")
+    n_prefix, max_blocks = prefix_table.shape[0], block_table.shape[1]
     _one_dtype(q, k_pool, v_pool, o)
-    _int32(prefix_table, prefix_len, block_table, kv_lens)
     rc = lib().gqa_attn_decode_shared_prefix_paged(
-        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(prefix_table), _ptr(prefix_len), _ptr(block_table), _ptr(kv_lens),
-        _ptr(o), B, Hq, Hkv, D, block_size, num_blocks, prefix_table.shape[0], block_table.shape[1],
-        int(max_prefix_len), int(max_kv_len), float(scale), _dtype_code(q), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ints(prefix_table, n_prefix), _ints(prefix_len, 1),
+        _ints(block_table, B * max_blocks), _ints(kv_lens, B), _ptr(o), B, Hq, Hkv, D, block_size, num_blocks,
+        n_prefix, max_blocks, int(max_prefix_len), int(max_kv_len), float(scale), _dtype_code(q), _ptr(workspace),
+        workspace.nbytes, _stream(stream))
     _check(rc, "gqa_attn_decode_shared_prefix_paged")
 
 
@@ -369,23 +379,16 @@ def gqa_attn_step_tables(prior_lens, new_lens, block_table, free_blocks, free_co
     grown in place from the stack free_blocks [num_blocks] (or both, and the
     counts, None for a dense cache of block_size rows a request); writes
     kv_lens, q_lens [B], q_starts [B+1], positions, slots, q_slots [T]."""
-    _int32(prior_lens, new_lens, block_table, free_blocks, free_count, kv_lens, q_lens, q_starts, positions, slots,
-           q_slots, free_count_out)
-    B, T = prior_lens.shape[0], positions.shape[0]
-    if new_lens.shape[0] != B or kv_lens.shape[0] != B or q_lens.shape[0] != B or q_starts.shape[0] != B + 1:
-        raise ValueError("new_lens, kv_lens and q_lens have B entries, q_starts B + 1")
-    if slots.shape[0] != T or (q_slots is not None and q_slots.shape[0] != T):
-        raise ValueError("positions, slots and q_slots have T entries")
+    B, T = prior_lens.numel(), positions.numel()
     max_blocks = num_blocks = 0
     if block_table is not None:
-        if block_table.shape[0] != B:
-            raise ValueError("block_table has a row per request")
-        max_blocks, num_blocks = block_table.shape[1], free_blocks.shape[0]
-    rc = lib().gqa_attn_step_tables(_ptr(prior_lens), _ptr(new_lens), _ptr(block_table), _ptr(free_blocks),
-                                    _ptr(free_count), _ptr(kv_lens), _ptr(q_lens), _ptr(q_starts), _ptr(positions),
-                                    _ptr(slots), _ptr(q_slots), _ptr(free_count_out), B, T, int(block_size),
-                                    num_blocks, max_blocks, int(q_rows), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream))
+        max_blocks = block_table.shape[1]
+        num_blocks = 0 if free_blocks is None else free_blocks.numel()
+    rc = lib().gqa_attn_step_tables(
+        _ints(prior_lens, B), _ints(new_lens, B), _ints(block_table, B * max_blocks), _ints(free_blocks, num_blocks),
+        _ints(free_count, 1), _ints(kv_lens, B), _ints(q_lens, B), _ints(q_starts, B + 1), _ints(positions, T),
+        _ints(slots, T), _ints(q_slots, T), _ints(free_count_out, 1), B, T, int(block_size), num_blocks, max_blocks,
+        int(q_rows), _ptr(workspace), workspace.nbytes, _stream(stream))
     _check(rc, "gqa_attn_step_tables")
 
 
@@ -397,32 +400,27 @@ def gqa_attn_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, s
     v_cache [num_blocks,Hkv,block_size,D] rows slots; negative slots: padding."""
     T, Hq, D = q.shape
     Hkv = k.shape[1]
-    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
-        raise ValueError("k and v are [T, Hkv, D]")
-    if q_out.shape[1] != Hq or q_out.shape[3] != D or v_cache.shape != k_cache.shape \
-            or k_cache.shape[1] != Hkv or k_cache.shape[3] != D:
+    q_groups, hq, q_rows, dq = q_out.shape
+    num_blocks, hk, block_size, dk = k_cache.shape
+    if hq != Hq or dq != D or hk != Hkv or dk != D or v_cache.shape != k_cache.shape:
         raise ValueError("q_out is [groups, Hq, q_rows, D], k_cache and v_cache [blocks, Hkv, block_size, D]")
     _one_dtype(q, k, v, q_weight, k_weight, q_out, k_cache, v_cache)
     for w in (q_weight, k_weight):
-        if w is not None and w.shape != (D,):
+        if w is not None and w.numel() != D:
             raise ValueError("the norm weights have D entries")
-    _int32(positions, slots, q_slots)
-    if slots.shape[0] != T or (q_slots is not None and q_slots.shape[0] != T):
-        raise ValueError("slots and q_slots have T entries")
     max_pos = rot_dim = 0
-    if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or positions is None or positions.shape[0] != T:
-            raise TypeError("cos_sin is float32 and needs T positions")
-        max_pos, rot_dim = cos_sin.shape
-    elif positions is not None:
+    if cos_sin is None:
         positions = None  # nothing rotates
-    (qp, qs), (kp, ks), (vp, vs) = _heads(q), _heads(k), _heads(v)
-    rc = lib().gqa_attn_rope_append(qp, kp, vp, qs, ks, vs, _ptr(q_weight), _ptr(k_weight), float(eps),
-                                    _ptr(cos_sin), _ptr(positions), _ptr(slots), _ptr(q_slots), _ptr(q_out),
-                                    _ptr(k_cache), _ptr(v_cache), T, Hq, Hkv, D, rot_dim, max_pos,
-                                    1 if adjacent else 0, k_cache.shape[0], k_cache.shape[2], q_out.shape[0],
-                                    q_out.shape[2], _dtype_code(q), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream))
+    else:
+        if cos_sin.dtype != torch.float32 or positions is None:
+            raise TypeError("cos_sin is float32 and needs positions")
+        max_pos, rot_dim = cos_sin.shape
+    (qp, qs), (kp, ks), (vp, vs) = _heads(q, T, Hq, D), _heads(k, T, Hkv, D), _heads(v, T, Hkv, D)
+    rc = lib().gqa_attn_rope_append(
+        qp, kp, vp, qs, ks, vs, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), _ints(positions, T),
+        _ints(slots, T), _ints(q_slots, T), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), T, Hq, Hkv, D, rot_dim,
+        max_pos, 1 if adjacent else 0, num_blocks, block_size, q_groups, q_rows, _dtype_code(q), _ptr(workspace),
+        workspace.nbytes, _stream(stream))
     _check(rc, "gqa_attn_rope_append")
 
 

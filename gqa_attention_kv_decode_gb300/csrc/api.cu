@@ -602,7 +602,7 @@ GQA_ATTN_API int gqa_attn_rope_append(const void* q, const void* k, const void* 
   if (T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return GQA_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return GQA_ERR_INVALID_ARG;
   if (dtype != GQA_F32 && dtype != GQA_BF16) return GQA_ERR_INVALID_ARG;
-  if (long(Hq) + 2L * Hkv > 65535) return GQA_ERR_INVALID_ARG;
+  if (long(Hq) + 2L * Hkv > 65535 || T * (long(Hq) + 2L * Hkv) > kMax) return GQA_ERR_INVALID_ARG;
   if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0) return GQA_ERR_INVALID_ARG;
   if (rot_dim > 0 && max_pos < 1) return GQA_ERR_INVALID_ARG;
   if (rot_dim == 0 && (cos_sin != nullptr || positions != nullptr)) return GQA_ERR_INVALID_ARG;

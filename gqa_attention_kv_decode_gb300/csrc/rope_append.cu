@@ -69,23 +69,58 @@ struct Chunk<float> {
 
 constexpr int NT = 256;
 
-// Each warp takes one token and U passes of HP heads of it.
-template <typename T, int D, int U>
-__global__ void __launch_bounds__(NT) rope_append_kernel(const RopeAppendArgs p, int warps_per_token) {
+// 16 bytes that are read once.  (volatile: the compiler would move a load
+// down to its first use, behind the wait for the token's place)
+__device__ __forceinline__ uint4 load_once(const void* src) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(src));
+  return v;
+}
+
+// A warp takes one token and U passes of HP heads each, all loaded before the
+// first is used.  MB: blocks an SM holds (few registers, so that many warps
+// wait on memory at once, count for more than a few spilled ones: U = 3 at
+// 16,384 tokens 95 us with two blocks an SM, 80 with three, 76 with four).
+template <typename T, int D, int U, int MB>
+__global__ void __launch_bounds__(NT, MB) rope_append_kernel(const RopeAppendArgs p, unsigned parts) {
   using C = Chunk<T>;
-  constexpr int E = C::E;
-  constexpr int NL = D / (2 * E);  // lanes per head row
-  constexpr int HP = 32 / NL;      // head rows a warp takes at a time
+  constexpr int E = C::E;             // elements of a chunk
+  constexpr int NL = D / (2 * E);     // lanes per head row
+  constexpr int HP = 32 / NL;         // head rows a warp takes at a time
   grid_launch_dependents();
   grid_dependency_wait();
-  const long w = (long(blockIdx.x) * NT + threadIdx.x) >> 5;
-  const int t = int(w / warps_per_token), part = int(w % warps_per_token);
-  if (t >= p.T) return;
-  const int lane = threadIdx.x & 31, i = lane % NL;
+  const unsigned w = blockIdx.x * unsigned(NT / 32) + (threadIdx.x >> 5);
+  const unsigned t = w / parts, part = w % parts;
+  if (t >= unsigned(p.T)) return;
+  const int lane = threadIdx.x & 31, i = lane % NL, h0 = int(part) * U * HP + lane / NL;
 
   // where the token goes: K / V row `slot`, Q row `q_slot`; negative: nowhere
-  int slot = p.slots[t], q_slot = p.q_slots != nullptr ? p.q_slots[t] : t;
-  const int pos = p.rot_dim > 0 ? p.positions[t] : 0;
+  int slot = p.slots[t], q_slot = p.q_slots != nullptr ? p.q_slots[t] : int(t);
+  int pos = p.rot_dim > 0 ? p.positions[t] : 0;
+
+  // this lane's chunks, and whether it rotates them
+  const int n_rot = p.rot_dim / (2 * E);  // lanes of a head row that rotate
+  const bool rot = i < n_rot, apart = rot && !p.adjacent;
+  const int ca = (apart ? i : 2 * i) * E, cb = (apart ? i + n_rot : 2 * i + 1) * E;
+  const int n_heads = p.Hq + 2 * p.Hkv, h_v = p.Hq + p.Hkv;
+  // the loads do not wait for the places (a padding token's row is there all the same)
+  uint4 xa[U], xb[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int h = h0 + u * HP;
+    if (h < n_heads) {
+      const T* src = h < p.Hq ? static_cast<const T*>(p.q) + t * p.q_stride + h * D
+                     : h < h_v ? static_cast<const T*>(p.k) + t * p.k_stride + (h - p.Hq) * D
+                               : static_cast<const T*>(p.v) + t * p.v_stride + (h - h_v) * D;
+      xa[u] = load_once(src + ca);
+      xb[u] = load_once(src + cb);
+    } else {
+      xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+
   uint32_t bits = 0;
   if (slot >= p.num_blocks * p.block_size) {
     bits |= GQA_DEV_BAD_SLOT;
@@ -102,10 +137,6 @@ __global__ void __launch_bounds__(NT) rope_append_kernel(const RopeAppendArgs p,
   if (bits != 0 && lane == 0 && part == 0) atomicOr(p.status, bits);
   if (slot < 0 && q_slot < 0) return;
 
-  // this lane's chunks, and whether it rotates them
-  const int n_rot = p.rot_dim / (2 * E);  // lanes of a head row that rotate
-  const bool rot = i < n_rot, split = rot && !p.adjacent;
-  const int ca = (split ? i : 2 * i) * E, cb = (split ? i + n_rot : 2 * i + 1) * E;
   float cs[E], sn[E];
   if (rot) {
     const float* row = p.cos_sin + size_t(pos) * p.rot_dim + i * E;
@@ -117,28 +148,15 @@ __global__ void __launch_bounds__(NT) rope_append_kernel(const RopeAppendArgs p,
       sn[e] = s4.x, sn[e + 1] = s4.y, sn[e + 2] = s4.z, sn[e + 3] = s4.w;
     }
   }
-  const int n_heads = p.Hq + 2 * p.Hkv;
-  const T* const q = static_cast<const T*>(p.q) + size_t(t) * p.q_stride;
-  const T* const k = static_cast<const T*>(p.k) + size_t(t) * p.k_stride;
-  const T* const v = static_cast<const T*>(p.v) + size_t(t) * p.v_stride;
+  // head 0's row of the token in the cache and in q_out, rows of D elements
+  const unsigned us = unsigned(max(slot, 0)), uq = unsigned(max(q_slot, 0));
+  const size_t kv_row = size_t(us / unsigned(p.block_size)) * p.Hkv * p.block_size + us % unsigned(p.block_size);
+  const size_t q_row = size_t(uq / unsigned(p.q_rows)) * p.Hq * p.q_rows + uq % unsigned(p.q_rows);
 
-  uint4 xa[U], xb[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int h = (part * U + u) * HP + lane / NL;
-    const bool is_q = h < p.Hq;
-    xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (h < n_heads && (is_q ? q_slot : slot) >= 0) {
-      const T* src = is_q ? q + size_t(h) * D
-                          : h < p.Hq + p.Hkv ? k + size_t(h - p.Hq) * D : v + size_t(h - p.Hq - p.Hkv) * D;
-      xa[u] = *reinterpret_cast<const uint4*>(src + ca);
-      xb[u] = *reinterpret_cast<const uint4*>(src + cb);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = (part * U + u) * HP + lane / NL;
-    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+    const int h = h0 + u * HP;
+    const bool is_q = h < p.Hq, is_v = h >= h_v;
     const T* wt = static_cast<const T*>(is_v ? nullptr : is_q ? p.q_weight : p.k_weight);
     float a[E], b[E];
     C::widen(xa[u], a);
@@ -180,29 +198,32 @@ __global__ void __launch_bounds__(NT) rope_append_kernel(const RopeAppendArgs p,
       }
     }
     if (h < n_heads && (is_q ? q_slot : slot) >= 0) {
-      const int rows = is_q ? p.q_rows : p.block_size, at = is_q ? q_slot : slot;
-      const int hh = is_q ? h : is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-      T* base = static_cast<T*>(is_q ? p.q_out : is_v ? p.v_cache : p.k_cache);
-      T* dst = base + ((size_t(at / rows) * (is_q ? p.Hq : p.Hkv) + hh) * rows + at % rows) * D;
-      // a value that is neither scaled nor rotated comes back bit for bit
+      const size_t row = is_q ? q_row + size_t(h) * p.q_rows
+                              : kv_row + size_t(is_v ? h - h_v : h - p.Hq) * p.block_size;
+      T* dst = static_cast<T*>(is_q ? p.q_out : is_v ? p.v_cache : p.k_cache) + row * D;
+      // (V is copied bit for bit)
       *reinterpret_cast<uint4*>(dst + ca) = is_v ? xa[u] : C::narrow(a);
       *reinterpret_cast<uint4*>(dst + cb) = is_v ? xb[u] : C::narrow(b);
     }
   }
 }
 
-template <typename T, int D, int U>
-cudaError_t launch_u(const RopeAppendArgs& a, cudaStream_t stream) {
-  constexpr int HP = 32 / (D / (2 * Chunk<T>::E));
-  const int n_heads = a.Hq + 2 * a.Hkv;
-  const int wpt = (n_heads + HP * U - 1) / (HP * U);
-  const long blocks = (long(a.T) * wpt + NT / 32 - 1) / (NT / 32);
-  return launch_pdl(rope_append_kernel<T, D, U>, dim3(unsigned(blocks)), dim3(NT), 0, stream, a, wpt);
+// Passes a warp makes: one while that leaves a warp of its own to every pass
+// (a step's latency counts: 64 tokens of 32/8 x 128 bf16 2.5 us, 3.6 with
+// three), three once the grid is two waves or more (16,384 tokens 76.0 us,
+// 114 with one).
+template <typename T, int D, int U, int MB>
+cudaError_t launch_u(const RopeAppendArgs& a, unsigned parts, cudaStream_t stream) {
+  const long blocks = (long(a.T) * parts + NT / 32 - 1) / (NT / 32);
+  return launch_pdl(rope_append_kernel<T, D, U, MB>, dim3(unsigned(blocks)), dim3(NT), 0, stream, a, parts);
 }
 
 template <typename T, int D>
 cudaError_t launch_t(const RopeAppendArgs& a, cudaStream_t stream) {
-  return launch_u<T, D, 1>(a, stream);
+  constexpr int HP = 32 / (D / (2 * Chunk<T>::E));
+  const unsigned passes = unsigned((a.Hq + 2 * a.Hkv + HP - 1) / HP);
+  if (long(a.T) * passes < 2L * 32 * device_sm_count()) return launch_u<T, D, 1, 1>(a, passes, stream);
+  return launch_u<T, D, 3, 4>(a, (passes + 2) / 3, stream);
 }
 
 }  // namespace

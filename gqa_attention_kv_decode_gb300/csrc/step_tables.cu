@@ -11,7 +11,8 @@
 //      which are pushed on the stack;
 //   2. prefix sum of the blocks the requests need, which are popped.
 // The tokens are then independent: each finds its request by bisection of
-// q_starts and reads one table entry.
+// q_starts and reads one table entry.  Up to kInlineTokens of them the same
+// block does it, one token a thread; more get a grid of their own.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,30 +27,58 @@ namespace {
 
 constexpr int NT = 1024;          // threads of the scanning block
 constexpr int NWARP = NT / 32;
+constexpr int kInlineTokens = NT;    // tokens the scanning block emits itself
+constexpr int NT_TOK = 256;          // threads, and tokens per thread, of the token grid
+constexpr int kTokPerThread = 4;
+constexpr int kStagedStarts = 8192;  // starts the token grid stages in shared memory (32 KB)
 
-// Inclusive sum of v over the block's threads; total: over all of them.
-// `part` (NWARP entries) may be reused after the caller's next __syncthreads.
-template <typename T>
-__device__ __forceinline__ T block_scan(T v, T* part, T& total) {
+// Inclusive sums of n and r over the block's threads, and their totals.  The
+// parts may be reused after the caller's next __syncthreads.
+struct Scan {
+  unsigned long long n, n_total;
+  int r, r_total;
+};
+__device__ __forceinline__ Scan block_scan(unsigned long long n, int r, unsigned long long* part_n, int* part_r) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto warp_scan = [&](unsigned long long& a, int& b) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const T u = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += u;
-  }
-  if (lane == 31) part[warp] = v;
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned long long u = __shfl_up_sync(0xffffffffu, a, d);
+      const int v = __shfl_up_sync(0xffffffffu, b, d);
+      if (lane >= d) a += u, b += v;
+    }
+  };
+  warp_scan(n, r);
+  if (lane == 31) part_n[warp] = n, part_r[warp] = r;
   __syncthreads();
-  T s = part[lane];  // (NWARP == 32: every lane has one warp's sum)
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const T u = __shfl_up_sync(0xffffffffu, s, d);
-    if (lane >= d) s += u;
-  }
-  total = __shfl_sync(0xffffffffu, s, 31);
-  const T before = __shfl_sync(0xffffffffu, s, (warp + 31) & 31);
-  return warp > 0 ? v + before : v;
+  unsigned long long sn = part_n[lane];  // (NWARP == 32: every lane has one warp's sums)
+  int sr = part_r[lane];
+  warp_scan(sn, sr);
+  Scan s;
+  s.n_total = __shfl_sync(0xffffffffu, sn, 31);
+  s.r_total = __shfl_sync(0xffffffffu, sr, 31);
+  const unsigned long long bn = __shfl_sync(0xffffffffu, sn, (warp + 31) & 31);
+  const int br = __shfl_sync(0xffffffffu, sr, (warp + 31) & 31);
+  s.n = warp > 0 ? n + bn : n;
+  s.r = warp > 0 ? r + br : r;
+  return s;
 }
-static_assert(NWARP == 32, "block_scan reads one warp sum per lane");
+static_assert(NWARP == 32, "block_scan reads one warp's sums per lane");
+
+// The first of the NT inclusive sums that is above k.
+__device__ __forceinline__ int owner_of(const int* ends, int k) {
+  int lo = 0, hi = NT - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] > k) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Blocks of `rows` rows (rows + block_size may pass 2^31, not 2^32).
+__device__ __forceinline__ int blocks_of(int rows, int block_size) {
+  return int((unsigned(rows) + unsigned(block_size) - 1u) / unsigned(block_size));
+}
 
 // What a request asks for, with its lengths clamped (bits: what was wrong).
 struct Ask {
@@ -64,7 +93,7 @@ __device__ __forceinline__ Ask read_ask(const StepTablesArgs& p, int b, int cap,
   const int n = p.new_lens[b];
   a.release = n < 0;
   a.n = max(n, 0);
-  a.have = (a.prior + p.block_size - 1) / p.block_size;
+  a.have = blocks_of(a.prior, p.block_size);
   a.fits = !a.release && a.n <= p.q_rows && a.n <= cap - a.prior;
   return a;
 }
@@ -72,8 +101,8 @@ __device__ __forceinline__ Ask read_ask(const StepTablesArgs& p, int b, int cap,
 // Token t of the step: positions, slots and q_slots.  starts: q_starts (in
 // shared or global memory); the entries of p.block_table, p.kv_lens and
 // p.q_lens this reads were written before.
-__device__ __forceinline__ void emit_token(const StepTablesArgs& p, const int* starts, int lo, int hi, int t,
-                                           uint32_t& bits) {
+__device__ __forceinline__ void emit_token(const StepTablesArgs& p, const int* starts, int t, uint32_t& bits) {
+  int lo = 0, hi = p.B;
   int pos = 0, slot = -1, q_slot = -1;
   if (t < starts[p.B]) {
     // the last request in [lo, hi) that starts at or before t
@@ -106,12 +135,17 @@ __device__ __forceinline__ void emit_token(const StepTablesArgs& p, const int* s
 }
 
 __global__ void __launch_bounds__(NT, 1) step_tables_kernel(const StepTablesArgs p) {
-  __shared__ unsigned long long part64[NWARP];
-  __shared__ int part32[NWARP];
-  const int tid = threadIdx.x, lane = tid & 31;
+  __shared__ unsigned long long part_n[NWARP];
+  __shared__ int part_r[NWARP];
+  __shared__ int starts_s[NT + 1];  // q_starts of the last tile of requests
+  __shared__ int ends_s[NT];        // sums of the blocks given back, then of those needed
+  __shared__ int have_s[NT];
+  __shared__ int taken_s;
+  const int tid = threadIdx.x;
   const bool paged = p.block_table != nullptr;
   const int cap = paged ? p.max_blocks * p.block_size : p.block_size;
   uint32_t bits = 0;
+  if (tid == 0) taken_s = 0;
   grid_launch_dependents();
   grid_dependency_wait();
 
@@ -123,71 +157,74 @@ __global__ void __launch_bounds__(NT, 1) step_tables_kernel(const StepTablesArgs
   }
 
   // ---- pass 1: where each request's tokens start; released blocks -> stack ----
-  unsigned long long start0 = 0;  // tokens before this tile of requests (may exceed 32 bits)
-  int freed0 = 0;
+  Ask a{0, 0, 0, false, false};
+  unsigned long long start0 = 0, end = 0;  // tokens before this tile of requests (may exceed 32 bits)
+  int freed = 0;
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     const int b = b0 + tid;
-    Ask a{0, 0, 0, false, false};
+    a = Ask{0, 0, 0, false, false};
     if (b < p.B) a = read_ask(p, b, cap, bits);
-    unsigned long long tot64;
-    const unsigned long long end = start0 + block_scan<unsigned long long>((unsigned long long)a.n, part64, tot64);
-    if (b < p.B) p.q_starts[b + 1] = int(min(end, (unsigned long long)p.T));
-    start0 += tot64;
-    if (paged) {
-      int tot;
-      const int r = a.release ? a.have : 0;
-      const int at = count + freed0 + block_scan<int>(r, part32, tot) - r;
-      freed0 += tot;
-      // a warp copies the rows of its released requests one after another
-      for (unsigned m = __ballot_sync(0xffffffffu, r > 0); m != 0; m &= m - 1) {
-        const int src = __ffs(m) - 1;
-        const int nb = __shfl_sync(0xffffffffu, r, src), to = __shfl_sync(0xffffffffu, at, src);
-        const int* row = p.block_table + size_t(b0 + (tid & ~31) + src) * p.max_blocks;
-        for (int i = lane; i < nb; i += 32) {
-          const int id = row[i];
-          if (id < 0 || id >= p.num_blocks || to + i >= p.num_blocks) bits |= GQA_DEV_BAD_BLOCK;
-          if (to + i < p.num_blocks) p.free_blocks[to + i] = id;
-        }
+    const int r = paged && a.release ? a.have : 0;
+    const Scan s = block_scan((unsigned long long)a.n, r, part_n, part_r);
+    end = start0 + s.n;
+    start0 += s.n_total;
+    if (b < p.B) p.q_starts[b + 1] = starts_s[tid + 1] = int(min(end, (unsigned long long)p.T));
+    if (s.r_total > 0) {  // one block id a thread
+      ends_s[tid] = s.r;
+      __syncthreads();
+      for (int k = tid; k < s.r_total; k += NT) {
+        const int o = owner_of(ends_s, k), i = k - (o > 0 ? ends_s[o - 1] : 0);
+        const int id = p.block_table[size_t(b0 + o) * p.max_blocks + i];
+        const long to = long(count) + freed + k;
+        if (id < 0 || id >= p.num_blocks || to >= p.num_blocks) bits |= GQA_DEV_BAD_BLOCK;
+        if (to < p.num_blocks) p.free_blocks[to] = id;
       }
+      freed += s.r_total;
     }
-    __syncthreads();  // (part arrays are reused; the stack is complete after the last tile)
+    __syncthreads();  // (shared arrays are reused; the stack is complete after the last tile)
   }
-  if (tid == 0) p.q_starts[0] = 0;
-  const int avail = min(count + freed0, p.num_blocks);
+  if (tid == 0) p.q_starts[0] = starts_s[0] = 0;
+  const int avail = int(min(long(count) + freed, long(p.num_blocks)));
 
   // ---- pass 2: the blocks each request needs <- stack ----
-  unsigned long long s0 = 0;
-  int need0 = 0, taken = 0;
+  start0 = 0;
+  int need0 = 0;
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     const int b = b0 + tid;
-    Ask a{0, 0, 0, false, false};
-    uint32_t again = 0;  // (reported in pass 1)
-    if (b < p.B) a = read_ask(p, b, cap, again);
-    unsigned long long tot64;
-    const unsigned long long end = s0 + block_scan<unsigned long long>((unsigned long long)a.n, part64, tot64);
-    s0 += tot64;
+    if (p.B > NT) {  // (else a and end are still those of the only tile)
+      uint32_t again = 0;  // (reported in pass 1)
+      a = Ask{0, 0, 0, false, false};
+      if (b < p.B) a = read_ask(p, b, cap, again);
+      const Scan s = block_scan((unsigned long long)a.n, 0, part_n, part_r);
+      end = start0 + s.n;
+      start0 += s.n_total;
+      __syncthreads();
+    }
     const bool fits = a.fits && end <= (unsigned long long)p.T;
     if (b < p.B && !a.release && !fits) bits |= GQA_DEV_KVLEN_CLAMPED;
     bool granted = fits;
     if (paged) {
-      const int need = fits ? (a.prior + a.n + p.block_size - 1) / p.block_size - a.have : 0;
-      int tot;
-      const int upto = need0 + block_scan<int>(need, part32, tot);
-      need0 += tot;
+      const int need = fits && b < p.B ? blocks_of(a.prior + a.n, p.block_size) - a.have : 0;
+      const Scan s = block_scan(0ull, need, part_n, part_r);
+      const int upto = need0 + s.r;
       granted = fits && (need == 0 || upto <= avail);
       if (fits && !granted) bits |= GQA_DEV_OUT_OF_BLOCKS;
-      const int take = granted ? need : 0;
-      if (take > 0) taken = max(taken, upto);
-      for (unsigned m = __ballot_sync(0xffffffffu, take > 0); m != 0; m &= m - 1) {
-        const int src = __ffs(m) - 1;
-        const int nb = __shfl_sync(0xffffffffu, take, src), first = __shfl_sync(0xffffffffu, upto - need, src);
-        const int have = __shfl_sync(0xffffffffu, a.have, src);
-        int* row = p.block_table + size_t(b0 + (tid & ~31) + src) * p.max_blocks + have;
-        for (int i = lane; i < nb; i += 32) {
-          const int id = p.free_blocks[avail - 1 - (first + i)];
+      // the requests that take blocks are the first ones that need any, so
+      // the largest of their sums is what is taken
+      if (granted && need > 0) atomicMax(&taken_s, upto);
+      if (s.r_total > 0) {
+        ends_s[tid] = s.r;
+        have_s[tid] = a.have;
+        __syncthreads();
+        for (int k = tid; k < s.r_total; k += NT) {
+          const int o = owner_of(ends_s, k);
+          if (need0 + ends_s[o] > avail) break;  // this request and all after it go without
+          const int i = k - (o > 0 ? ends_s[o - 1] : 0);
+          const int id = p.free_blocks[avail - 1 - (need0 + k)];
           if (id < 0 || id >= p.num_blocks) bits |= GQA_DEV_BAD_BLOCK;
-          row[i] = id;
+          p.block_table[size_t(b0 + o) * p.max_blocks + have_s[o] + i] = id;
         }
+        need0 += s.r_total;
       }
     }
     if (b < p.B) {
@@ -197,28 +234,40 @@ __global__ void __launch_bounds__(NT, 1) step_tables_kernel(const StepTablesArgs
     }
     __syncthreads();
   }
-  if (paged) {
-    // the granted requests that took blocks are the first ones, so the
-    // largest running sum among them is what was taken
-    taken = __reduce_max_sync(0xffffffffu, taken);
-    if (lane == 0) part32[tid >> 5] = taken;
-    __syncthreads();
-    if (tid < 32) {
-      taken = __reduce_max_sync(0xffffffffu, part32[tid]);
-      if (tid == 0) *p.free_count_out = avail - taken;
-    }
+  if (paged && tid == 0) *p.free_count_out = avail - taken_s;
+  if (p.T <= kInlineTokens) {
+    // one tile of requests: their starts are also in shared memory
+    if (tid < p.T) emit_token(p, p.B <= NT ? starts_s : p.q_starts, tid, bits);
   }
-  __syncthreads();
+  if (bits != 0) atomicOr(p.status, bits);
+}
 
-  // ---- the tokens ----
-  for (int t = tid; t < p.T; t += NT) emit_token(p, p.q_starts, 0, p.B, t, bits);
+// The tokens of a large step, one a thread.
+__global__ void __launch_bounds__(NT_TOK) step_tokens_kernel(const StepTablesArgs p) {
+  __shared__ int starts_s[kStagedStarts];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int* starts = p.q_starts;
+  if (p.B < kStagedStarts) {
+    for (int i = threadIdx.x; i <= p.B; i += NT_TOK) starts_s[i] = p.q_starts[i];
+    __syncthreads();
+    starts = starts_s;
+  }
+  uint32_t bits = 0;
+  const long t0 = long(blockIdx.x) * (NT_TOK * kTokPerThread) + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < kTokPerThread; ++k)
+    if (t0 + k * NT_TOK < p.T) emit_token(p, starts, int(t0) + k * NT_TOK, bits);
   if (bits != 0) atomicOr(p.status, bits);
 }
 
 }  // namespace
 
 cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream) {
-  return launch_pdl(step_tables_kernel, dim3(1), dim3(NT), 0, stream, a);
+  const cudaError_t e = launch_pdl(step_tables_kernel, dim3(1), dim3(NT), 0, stream, a);
+  if (e != cudaSuccess || a.T <= kInlineTokens) return e;
+  constexpr int per = NT_TOK * kTokPerThread;
+  return launch_pdl(step_tokens_kernel, dim3((a.T - 1) / per + 1), dim3(NT_TOK), 0, stream, a);
 }
 
 }  // namespace gqa

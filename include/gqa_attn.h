@@ -344,7 +344,7 @@ GQA_ATTN_API int gqa_attn_step_tables(const int32_t* prior_lens, const int32_t* 
  * GQA_DEV_BAD_POSITION, and nothing of that token is written.
  * D = 64 or 128; rot_dim a multiple of 16, 0 to D; strides multiples of 16
  * bytes; every pointer 16-byte aligned (positions, slots and q_slots 4-byte).
- * num_blocks * block_size and q_groups * q_rows < 2^31.
+ * num_blocks * block_size, q_groups * q_rows and T * (Hq + 2 Hkv) < 2^31.
  *   workspace    as for gqa_attn_step_tables (the status word)
  * ------------------------------------------------------------------------- */
 GQA_ATTN_API int gqa_attn_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,

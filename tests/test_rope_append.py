@@ -90,7 +90,7 @@ def call(lib, **change):
     dict(T=0), dict(Hq=0), dict(Hkv=0), dict(Hq=3), dict(D=96), dict(dtype=2), dict(rot=8), dict(rot=80),
     dict(rot=-16), dict(max_pos=0), dict(adjacent=2), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")),
     dict(nb=0), dict(bs=0), dict(qg=0), dict(qr=0), dict(nb=1 << 20, bs=1 << 12), dict(qg=1 << 20, qr=1 << 12),
-    dict(q_slots=None, T=4), dict(qs=248), dict(ks=120), dict(vs=120), dict(qs=260), dict(ks=132), dict(vs=132),
+    dict(q_slots=None, T=4), dict(T=1 << 28), dict(qs=248), dict(ks=120), dict(vs=120), dict(qs=260), dict(ks=132), dict(vs=132),
     dict(rot=0), dict(rot=0, cs=None), dict(rot=0, pos=None),
 ])
 def test_arguments_are_checked_on_the_host(lib, bad):
