@@ -157,29 +157,44 @@ int check_shared_prefix_kernel(int Hq, int Hkv, int dtype) {
   return GQA_OK;
 }
 
-// The workspace serves the dense and the paged call, whose decode kernels may
-// plan different splits of the own rows.
+// The plans of a shared-prefix call whose shape is checked.
+void plan_shared_prefix(SharedPrefixArgs& a) {
+  DecodeArgs& d = a.own;
+  const int sms = device_sm_count();
+  a.plan = prefix_plan(d.B, d.Hq, d.Hkv, d.D, a.max_prefix, sms);
+  a.own_plan = own_rows_plan(d.B, d.Hq, d.Hkv, d.max_kv_len, sms);
+  d.plan = decode_plan(d.B, d.Hq, d.Hkv, d.D, d.max_kv_len, GQA_BF16, d.block_table != nullptr);
+}
+
+// The workspace serves the dense and the paged call (whose decode kernels may
+// plan different splits of the own rows).
 size_t shared_prefix_ws_size(int B, int Hq, int Hkv, int D, int max_prefix_len, int max_kv_len) {
   if (Hq / Hkv > 128) return 0;
-  const PrefixPlan px = prefix_plan(B, Hq, Hkv, D, max_prefix_len, device_sm_count());
+  static const int32_t some_table = 0;
   size_t most = 0;
-  for (const bool paged : {false, true}) {
-    const SplitPlan own = decode_plan(B, Hq, Hkv, D, max_kv_len, GQA_BF16, paged);
-    most = std::max(most, workspace_layout(B, Hq, Hkv, own.n_hc, own.n_split + px.n_split, D).total);
+  for (const int32_t* table : {static_cast<const int32_t*>(nullptr), &some_table}) {
+    SharedPrefixArgs a;
+    a.own.B = B;
+    a.own.Hq = Hq;
+    a.own.Hkv = Hkv;
+    a.own.D = D;
+    a.own.max_kv_len = max_kv_len;
+    a.own.block_table = table;
+    a.max_prefix = max_prefix_len;
+    plan_shared_prefix(a);
+    most = std::max(most, shared_prefix_layout(a).total);
   }
   return most;
 }
 
 int run_shared_prefix(SharedPrefixArgs& a, size_t ws_bytes, int dev, void* stream) {
-  DecodeArgs& d = a.own;
-  if (d.workspace == nullptr) return GQA_ERR_WORKSPACE;
-  const int rc = check_ptrs({d.workspace}, dev, 256);
+  const void* const ws = a.own.workspace;
+  if (ws == nullptr) return GQA_ERR_WORKSPACE;
+  const int rc = check_ptrs({ws}, dev, 256);
   if (rc == GQA_ERR_INVALID_ARG) return GQA_ERR_WORKSPACE;
   if (rc != GQA_OK) return rc;
-  d.plan = decode_plan(d.B, d.Hq, d.Hkv, d.D, d.max_kv_len, d.dtype, d.block_table != nullptr);
-  a.plan = prefix_plan(d.B, d.Hq, d.Hkv, d.D, a.max_prefix, device_sm_count());
-  if (ws_bytes < workspace_layout(d.B, d.Hq, d.Hkv, d.plan.n_hc, d.plan.n_split + a.plan.n_split, d.D).total)
-    return GQA_ERR_WORKSPACE;
+  plan_shared_prefix(a);
+  if (ws_bytes < shared_prefix_layout(a).total) return GQA_ERR_WORKSPACE;
   return launch_shared_prefix(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 

@@ -30,6 +30,7 @@
 #include "gqa_attn.h"
 #include "internal.h"
 #include "merge.cuh"
+#include "mma_tile.cuh"
 #include "ptx.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
@@ -102,37 +103,6 @@ struct MmaCfg {
   static_assert(D == 64 || D == 128, "head dimension");
   static_assert(MERGE_FLOATS * 4 <= NSTAGE * STAGEB, "warp-merge scratch fits in the stages");
 };
-
-// Byte offset of 16-byte chunk `chunk` (0..7) of key row `row` inside a
-// 128-byte-swizzled box: the chunk index is XOR-ed with the row index mod 8.
-__device__ __forceinline__ uint32_t swz(int row, int chunk) {
-  return uint32_t(row * 128 + ((chunk ^ (row & 7)) << 4));
-}
-
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
-                                          uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr));
-}
-// D (+)= A B with A rows 8..15 zero (only 8 query heads per CTA): the A
-// registers a1, a3 of those rows are passed as zero.
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 
 // PAGED: K and V tiles come from block pools through the block table (a tile
 // never crosses a block); with k_new the CTA that owns row kv_len - 1 writes
@@ -461,36 +431,39 @@ __global__ void __launch_bounds__(MmaCfg<D, NSTAGE, NW>::NTHR, 8 / NW)
 }
 
 // Tensor maps of the K and V caches, [B*Hkv][S_cap][D] bf16 as a 3-D tensor
-// with 64-row x 64-dim boxes and 128-byte swizzle.  Encoding one costs about
+// with 64-dim x box_rows boxes (64 rows here) and 128-byte swizzle.  Encoding one costs about
 // a microsecond of host time, so the maps of recently used caches are kept
 // (keyed by base address and shape; a map holds no data, only the layout).
 struct MapEntry {
   const void* base;
-  int D, S_cap, heads;
+  int D, S_cap, heads, box_rows;
   CUtensorMap map;
 };
 constexpr int kMapCache = 128;
 
 }  // namespace
 
-bool kv_map(CUtensorMap* out, const void* base, int D, int S_cap, int heads) {
+bool kv_map(CUtensorMap* out, const void* base, int D, int S_cap, int heads, int box_rows) {
   static std::mutex mu;
   static MapEntry cache[kMapCache];
   static int used = 0, next = 0;
   std::lock_guard<std::mutex> lock(mu);
   for (int i = 0; i < used; ++i)
-    if (cache[i].base == base && cache[i].D == D && cache[i].S_cap == S_cap && cache[i].heads == heads) {
+    if (cache[i].base == base && cache[i].D == D && cache[i].S_cap == S_cap && cache[i].heads == heads &&
+        cache[i].box_rows == box_rows) {
       *out = cache[i].map;
       return true;
     }
   CUtensorMap m;
-  if (!encode_bf16_rows(&m, base, uint64_t(D), uint64_t(S_cap), uint64_t(S_cap), uint64_t(heads), 64, 64))
+  if (!encode_bf16_rows(&m, base, uint64_t(D), uint64_t(S_cap), uint64_t(S_cap), uint64_t(heads), 64,
+                        uint32_t(box_rows)))
     return false;
   MapEntry& e = cache[next];
   e.base = base;
   e.D = D;
   e.S_cap = S_cap;
   e.heads = heads;
+  e.box_rows = box_rows;
   e.map = m;
   next = (next + 1) % kMapCache;
   if (used < kMapCache) ++used;

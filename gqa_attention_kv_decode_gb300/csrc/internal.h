@@ -153,6 +153,19 @@ struct PrefixPlan {
 };
 PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sms);
 
+// The own rows behind the shared ones (own_rows.cu), for up to 1,024 requests.
+struct OwnRowsPlan {
+  bool fits;            // else the decode kernel takes them
+  int n_hc, nrep_cta;   // query-head chunks per KV head, heads of a chunk
+  int units;            // (KV head, chunk) pairs of a request
+  int blocks;           // grid
+  int min_tiles;        // tiles per warp, at least
+  int n_slots;          // partials of a row, at most
+};
+OwnRowsPlan own_rows_plan(int B, int Hq, int Hkv, int max_kv_len, int num_sms);
+cudaError_t launch_own_rows(const DecodeArgs& a, const OwnRowsPlan& plan, int n_slots, float2* ml, float* part_o,
+                            int32_t* counts, cudaStream_t stream);
+
 // Decode over shared rows followed by each request's own (bf16): `own` is the
 // call over the own rows, its plan included; with a block table both caches
 // are the pools own.k / own.v, the shared rows' blocks in prefix_table.
@@ -164,7 +177,15 @@ struct SharedPrefixArgs {
   const int32_t* prefix_table;  // or null: dense
   int max_prefix, P_cap;
   PrefixPlan plan;
+  OwnRowsPlan own_plan;  // own.plan is used where this one does not fit
 };
+// Partial slots of a row (the own rows' first), and the workspace: the decode
+// layout, then how many partials each unit of own rows has.
+struct SharedPrefixLayout {
+  int n_own, n_slots;
+  size_t off_counts, total;
+};
+SharedPrefixLayout shared_prefix_layout(const SharedPrefixArgs& a);
 cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, cudaStream_t stream);
 
 // One step's tables (gqa_attn_step_tables); block_table == nullptr: a dense

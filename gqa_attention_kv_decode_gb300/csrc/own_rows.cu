@@ -1,0 +1,398 @@
+// own_rows.cu -- the requests' own keys of a shared-prefix decode: split-KV
+// partials of a ragged batch of short contexts.
+//
+// A batch behind a shared prefix has many (request, KV head) units of a few
+// hundred keys.  One CTA per unit (gqa_attn_decode) spends as long on getting
+// started, on its last wave and on joining its warps as on its keys: 64
+// requests of up to 1,024 keys took 31 us, 256 of up to 512 56 us, against 20
+// and 39 us for their bytes.  Here the work is one list: the 16-key tiles of
+// all units, request by request, cut into equal contiguous ranges, one for
+// every warp of a grid that fills the GPU once.  A warp
+//   - streams its range through stages of its own (TMA, 128-byte swizzle),
+//     across unit borders, so that copies are always in flight;
+//   - shares nothing with other warps: no block barrier after the start, no
+//     join of warps; a unit that two or more warps touch has a partial of each;
+//   - computes as the bf16 decode kernel does (mma.sync m16n8k16, up to 8
+//     query heads of one KV head as rows, online softmax in base 2).
+// The cut depends on the lengths alone, so the result is deterministic.  A
+// unit's partials take its first slots in order; the warp with the unit's
+// first tile leaves their number for the merge.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "gqa_attn.h"
+#include "internal.h"
+#include "merge.cuh"
+#include "mma_tile.cuh"
+#include "own_rows.cuh"
+#include "ptx.cuh"
+#include "tc.cuh"
+#include "tmap.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int NW = 8;            // warps, one block an SM
+constexpr int NTHR = 32 * NW;
+constexpr int TILE = kOwnTile;   // keys per tile
+constexpr int kMaxB = kOwnMaxRequests;
+
+template <int D>
+struct OwnCfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int BOX = TILE * 128;           // 16 rows x 128 bytes
+  static constexpr int TILEB = HALVES * BOX;       // K (or V) tile
+  static constexpr int STAGEB = 2 * TILEB;
+  static constexpr int NSTAGE = D == 128 ? 3 : 6;  // 24 KB a warp
+  static constexpr int WARPB = NSTAGE * STAGEB;
+  static constexpr int OFF_BAR = NW * WARPB;
+  static constexpr int OFF_STARTS = OFF_BAR + NW * (NSTAGE + 1) * 8;
+  static constexpr int SMEM = OFF_STARTS + (kMaxB + 1) * 4 + 1024;
+  static constexpr int KSTEPS = D / 16, NT_O = D / 8;
+  static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+};
+
+// A place in the list of tiles: tile k of nt of unit u of request b; the first
+// kOwnLead tiles of a unit hold no keys.
+struct Cursor {
+  int b, u, k, nt, x;  // x: its number in the list
+};
+
+template <int D>
+__global__ void __launch_bounds__(NTHR, 1)
+    own_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const OwnRowsParams p) {
+  using C = OwnCfg<D>;
+  constexpr int NS = C::NSTAGE;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ int warp_sum[NW];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * (NS + 1);
+  int* starts = reinterpret_cast<int*>(smem + C::OFF_STARTS);
+  grid_launch_dependents();
+  if (lane == 0) {
+    for (int s = 0; s <= NS; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+  }
+  if (tid == 0) {
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  grid_dependency_wait();
+
+  // ---- the list: starts[b] = tiles before request b ----
+  {
+    const int per = (p.B + NTHR - 1) / NTHR;  // consecutive requests a thread sums
+    int sum = 0;
+    bool clamped = false;
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b >= p.B) break;
+      const int raw = p.kv_lens != nullptr ? p.kv_lens[b] : p.max_kv_len;
+      const int L = min(max(raw, 0), p.max_kv_len);
+      clamped |= L != raw;
+      sum += L > 0 ? ((L + TILE - 1) / TILE + kOwnLead) * p.units : 0;
+      starts[b + 1] = sum;
+    }
+    if (clamped && blockIdx.x == 0) atomicOr(p.status, GQA_DEV_KVLEN_CLAMPED);
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int before = incl - sum;
+    for (int i = 0; i < warp; ++i) before += warp_sum[i];
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b >= p.B) break;
+      starts[b + 1] += before;
+    }
+    if (tid == 0) starts[0] = 0;
+    __syncthreads();
+  }
+  const int N = starts[p.B];
+  const int n_work = own_workers(N, p.warps, p.min_tiles);
+  const int w = warp * int(gridDim.x) + int(blockIdx.x);  // neighbours in the list run on different SMs
+  if (w >= n_work || N == 0) return;
+  const OwnCut cut = own_cut(N, n_work);
+  const int x0 = own_range_start(cut, w), x1 = own_range_start(cut, w + 1);
+
+  auto units_tiles = [&](int b) { return (starts[b + 1] - starts[b]) / p.units; };
+  Cursor at;  // the tile computed next
+  {
+    int lo = 0, hi = p.B;  // the last request that starts at or before x0 (empty ones share its start: the last has tiles)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= x0) lo = mid; else hi = mid;
+    }
+    at.b = lo;
+    at.nt = units_tiles(lo);
+    at.u = (x0 - starts[lo]) / at.nt;
+    at.k = (x0 - starts[lo]) % at.nt;
+    at.x = x0;
+  }
+  auto next_unit = [&](Cursor& c) {
+    c.k = kOwnLead;
+    c.x += kOwnLead;
+    if (++c.u == p.units) {
+      c.u = 0;
+      do ++c.b; while (c.b < p.B && starts[c.b + 1] == starts[c.b]);
+      if (c.b < p.B) c.nt = units_tiles(c.b);
+    }
+  };
+  if (at.k < kOwnLead) {
+    at.x += kOwnLead - at.k;
+    at.k = kOwnLead;
+  }
+  if (at.x >= x1) return;  // the range holds nothing but leading tiles
+
+  // ---- copies ----
+  unsigned char* const stage0 = smem + warp * C::WARPB;
+  Cursor ic = at;  // the tile copied next, and where it is in the maps
+  int irow = 0, ihead = 0;
+  // (a block's id is asked for once, with its first tile: the copies of a
+  // range would wait for one table entry after the other)
+  auto locate = [&](bool first) {
+    const int g = ic.u / p.n_hc, row0 = (ic.k - kOwnLead) * TILE;
+    if (p.block_table == nullptr) {
+      irow = row0;
+      ihead = ic.b * p.Hkv + g;
+      return;
+    }
+    irow = first ? row0 % p.block_size : irow + TILE;
+    if (irow == p.block_size) irow = 0;
+    if (row0 == 0) irow = 0;
+    if (!first && irow != 0) return;
+    int blk = p.block_table[size_t(ic.b) * p.max_blocks + row0 / p.block_size];
+    if (blk < 0 || blk >= p.num_blocks) {
+      atomicOr(p.status, GQA_DEV_BAD_BLOCK);
+      blk = 0;
+    }
+    ihead = blk * p.Hkv + g;
+  };
+  int issued = 0;  // tiles of this range copied so far (all lanes count, lane 0 copies)
+  auto issue = [&]() {
+    if (lane == 0) {
+      const int st = issued % NS;
+      unsigned char* dst = stage0 + st * C::STAGEB;
+      mbar_arrive_expect_tx(&full[st], C::STAGEB);
+#pragma unroll
+      for (int hf = 0; hf < C::HALVES; ++hf) {
+        tma_load_3d(dst + hf * C::BOX, &tmK, hf * 64, irow, ihead, &full[st]);
+        tma_load_3d(dst + C::TILEB + hf * C::BOX, &tmV, hf * 64, irow, ihead, &full[st]);
+      }
+    }
+    ++issued;
+    ++ic.x;
+    if (++ic.k == ic.nt) next_unit(ic);
+    // (a table entry asked for here has a tile's time to arrive)
+    if (lane == 0 && ic.x < x1) locate(false);
+  };
+  if (lane == 0) locate(true);
+  __syncwarp();
+  for (int s = 0; s < NS && ic.x < x1; ++s) issue();
+  bool ok = true;
+  if (p.test_stall_ns != 0) ok = mbar_wait_bounded(&full[NS], 0u, p.test_stall_ns);  // tests: nothing arrives on it
+
+  // ---- the tiles ----
+  const int r = lane >> 2, c = lane & 3, mi = lane >> 3, rr = lane & 7;
+  uint32_t qa[C::KSTEPS][2], qn[C::KSTEPS][2];  // Q of this unit, and of the next
+  auto heads_of = [&](int u, int& h0) {
+    const int g = u / p.n_hc, hc = u % p.n_hc;
+    h0 = g * p.n_rep + hc * p.nrep_cta;
+    return min(p.nrep_cta, p.n_rep - hc * p.nrep_cta);
+  };
+  auto load_q = [&](const Cursor& cu, uint32_t (&qq)[C::KSTEPS][2]) {
+    int h0;
+    const int nh = heads_of(cu.u, h0);
+    const uint32_t* row = reinterpret_cast<const uint32_t*>(p.q + (size_t(cu.b) * p.Hq + h0 + min(r, nh - 1)) * D);
+#pragma unroll
+    for (int ks = 0; ks < C::KSTEPS; ++ks) {
+      qq[ks][0] = r < nh ? row[(16 * ks + 2 * c) / 2] : 0u;
+      qq[ks][1] = r < nh ? row[(16 * ks + 8 + 2 * c) / 2] : 0u;
+    }
+  };
+  load_q(at, qn);
+  int t = 0;
+  while (ok && at.x < x1) {
+    // one unit, or what of it is in the range
+    const Cursor un = at;
+    const int n_here = min(un.nt - un.k, x1 - un.x);
+    const int raw_len = p.kv_lens != nullptr ? p.kv_lens[un.b] : p.max_kv_len;
+    const int L = min(max(raw_len, 0), p.max_kv_len);
+#pragma unroll
+    for (int ks = 0; ks < C::KSTEPS; ++ks) qa[ks][0] = qn[ks][0], qa[ks][1] = qn[ks][1];
+    at.x += n_here;
+    next_unit(at);
+    if (at.x < x1) load_q(at, qn);
+    float m_ref = -INFINITY, lsum = 0.f;
+    float oacc[C::NT_O][4];
+#pragma unroll
+    for (int j = 0; j < C::NT_O; ++j) oacc[j][0] = oacc[j][1] = oacc[j][2] = oacc[j][3] = 0.f;
+    for (int k = 0; k < n_here; ++k, ++t) {
+      const int st = t % NS;
+      ok = mbar_wait_bounded(&full[st], uint32_t(t / NS) & 1u, p.wait_limit_ns);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      unsigned char* const stage = stage0 + st * C::STAGEB;
+      const uint32_t kaddr = smem_u32(stage), vaddr = kaddr + C::TILEB;
+      const int valid = L - (un.k - kOwnLead + k) * TILE;  // keys of the tile, if below 16
+      if (valid < TILE) {
+        // V rows past the length may hold anything: zeroed (their P is 0, but 0 x NaN is NaN)
+        const int n_chunk = (TILE - valid) * 8;
+#pragma unroll
+        for (int hf = 0; hf < C::HALVES; ++hf)
+          for (int i = lane; i < n_chunk; i += 32)
+            *reinterpret_cast<uint4*>(stage + C::TILEB + hf * C::BOX + valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();  // before the stage can be refilled by TMA
+        __syncwarp();
+      }
+      // ---- S = Q K^T: two n-tiles of 8 keys ----
+      float sacc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int ks = 0; ks < C::KSTEPS; ++ks) {
+        const int key = 8 * (mi >> 1) + rr, d = 16 * ks + 8 * (mi & 1);
+        uint32_t b00, b01, b10, b11;
+        ldsm_x4(kaddr + (d / 64) * C::BOX + swz(key, (d % 64) / 8), b00, b01, b10, b11);
+        mma_16816(sacc[0], qa[ks][0], qa[ks][1], b00, b01);
+        mma_16816(sacc[1], qa[ks][0], qa[ks][1], b10, b11);
+      }
+      float sv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        sv[i] = 8 * (i >> 1) + 2 * c + (i & 1) < valid ? sacc[i >> 1][i & 1] * p.qscale : -INFINITY;
+      float mx = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const bool resc = mx > m_ref + 8.f;  // lazy reference, as in decode
+      if (__any_sync(0xffffffffu, resc)) {
+        const float alpha = resc ? fast_exp2(m_ref - mx) : 1.f;
+        if (resc) m_ref = mx;
+        lsum *= alpha;
+#pragma unroll
+        for (int j = 0; j < C::NT_O; ++j) {
+          oacc[j][0] *= alpha;
+          oacc[j][1] *= alpha;
+        }
+      }
+      const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+      float pv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pv[i] = fast_exp2(sv[i] - m_use);
+      lsum += (pv[0] + pv[1]) + (pv[2] + pv[3]);
+      const uint32_t pa0 = pack_bf16(pv[0], pv[1]), pa2 = pack_bf16(pv[2], pv[3]);
+      // ---- O += P V: pairs of 8-dim n-tiles ----
+#pragma unroll
+      for (int jj = 0; jj < C::NT_O / 2; ++jj) {
+        const int key = 8 * (mi & 1) + rr, d = 16 * jj + 8 * (mi >> 1);
+        uint32_t v0, v1, v2, v3;
+        ldsm_x4_t(vaddr + (d / 64) * C::BOX + swz(key, (d % 64) / 8), v0, v1, v2, v3);
+        mma_16816(oacc[2 * jj], pa0, pa2, v0, v1);
+        mma_16816(oacc[2 * jj + 1], pa0, pa2, v2, v3);
+      }
+      __syncwarp();  // every lane has read the stage
+      if (ic.x < x1) issue();
+    }
+    if (!ok) break;
+    lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
+    lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
+    // this warp's partial of the unit
+    const int end = un.x - un.k + un.nt, slot = w - own_worker_of(cut, end - un.nt + kOwnLead);
+    if (un.k == kOwnLead && lane == 0) p.counts[un.b * p.units + un.u] = own_worker_of(cut, end - 1) - w + 1;
+    int h0;
+    const int nh = heads_of(un.u, h0);
+    if (r < nh) {
+      const size_t prow = (size_t(un.b) * p.Hq + h0 + r) * p.n_slots + slot;
+      float* dst = p.part_o + prow * D + 2 * c;
+#pragma unroll
+      for (int j = 0; j < C::NT_O; ++j)
+        *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(oacc[j][0], oacc[j][1]);
+      if (c == 0) p.ml[prow] = make_float2(m_ref, lsum);
+    }
+  }
+  if (!ok) {  // a copy did not arrive in time: report, and let those in flight land
+    if (lane == 0) {
+      atomicOr(p.status, GQA_DEV_WAIT_TIMEOUT);
+      for (int i = t; i < issued; ++i) mbar_wait_bounded(&full[i % NS], uint32_t(i / NS) & 1u, p.wait_limit_ns);
+    }
+    __syncwarp();
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const DecodeArgs& a, const OwnRowsParams& p, int blocks, cudaStream_t stream) {
+  using C = OwnCfg<D>;
+  const bool paged = a.block_table != nullptr;
+  CUtensorMap tk, tv;
+  const int heads = paged ? a.num_blocks * a.Hkv : a.B * a.Hkv, rows = paged ? a.block_size : a.S_cap;
+  if (!kv_map(&tk, a.k, D, rows, heads, TILE) || !kv_map(&tv, a.v, D, rows, heads, TILE)) return cudaErrorInvalidValue;
+  static std::once_flag once;
+  static cudaError_t cfg_err = cudaSuccess;
+  std::call_once(once, [&] {
+    cfg_err = cudaFuncSetAttribute(own_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
+  if (cfg_err != cudaSuccess) return cfg_err;
+  return launch_pdl(own_rows_kernel<D>, dim3(blocks), dim3(NTHR), C::SMEM, stream, tk, tv, p);
+}
+
+}  // namespace
+
+OwnRowsPlan own_rows_plan(int B, int Hq, int Hkv, int max_kv_len, int num_sms) {
+  OwnRowsPlan p;
+  const int n_rep = Hq / Hkv;
+  p.n_hc = (n_rep + 7) / 8;
+  p.nrep_cta = (n_rep + p.n_hc - 1) / p.n_hc;
+  p.units = Hkv * p.n_hc;
+  const int tiles = (max_kv_len - 1) / TILE + 1;
+  p.fits = B <= kMaxB && long(B) * p.units * (long(tiles) + kOwnLead) <= 0x7fffffffL;
+  p.blocks = num_sms > 0 ? num_sms : 1;
+  // A warp's range holds at least min_tiles tiles, so that a unit has at most
+  // (tiles - 2) / min_tiles + 2 partials: 33 or fewer.
+  p.min_tiles = (tiles + 31) / 32;
+  p.n_slots = tiles < 2 ? 1 : (tiles - 2) / p.min_tiles + 2;
+  return p;
+}
+
+cudaError_t launch_own_rows(const DecodeArgs& a, const OwnRowsPlan& plan, int n_slots, float2* ml, float* part_o,
+                            int32_t* counts, cudaStream_t stream) {
+  OwnRowsParams p;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.kv_lens = a.kv_lens;
+  p.block_table = a.block_table;
+  p.block_size = a.block_size;
+  p.max_blocks = a.max_blocks;
+  p.num_blocks = a.num_blocks;
+  p.B = a.B;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.n_rep = a.Hq / a.Hkv;
+  p.n_hc = plan.n_hc;
+  p.nrep_cta = plan.nrep_cta;
+  p.units = plan.units;
+  p.max_kv_len = a.max_kv_len;
+  p.warps = plan.blocks * NW;
+  p.min_tiles = plan.min_tiles;
+  p.n_slots = n_slots;
+  p.qscale = float(double(a.scale) * 1.4426950408889634);
+  p.status = static_cast<uint32_t*>(a.workspace);
+  p.ml = ml;
+  p.part_o = part_o;
+  p.counts = counts;
+  p.wait_limit_ns = kWaitLimitNs;
+  p.test_stall_ns = wait_test_ns();
+  if (a.D == 128) return launch_d<128>(a, p, plan.blocks, stream);
+  return launch_d<64>(a, p, plan.blocks, stream);
+}
+
+}  // namespace gqa

@@ -11,7 +11,8 @@
 //                  tiles dealt to the two softmax warpgroups in turn -- and a
 //                  contiguous share of the shared keys, and writes the rows'
 //                  partials (max, sum, unnormalised O);
-//   decode_mma     the requests' own keys, as in gqa_attn_decode, partials only;
+//   own_rows       the requests' own keys, partials only (more than 1,024
+//                  requests: the decode kernel);
 //   prefix_merge   log-sum-exp merge of a row's partials of both.
 // Inside the CTA the roles, the tensor-memory layout and the softmax are the
 // prefill kernel's: warp 8 TMA, warp 9 issues S, warps 10 and 11 issue P V,
@@ -36,6 +37,7 @@
 #include "gqa_attn.h"
 #include "internal.h"
 #include "merge.cuh"
+#include "own_rows.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
 
@@ -55,21 +57,23 @@ struct PxCfg {
   static constexpr bool P_ALIAS = HD == 128;
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_P = P_ALIAS ? 0u : 384u;
   static constexpr uint32_t P_STRIDE = P_ALIAS ? 128u : 64u;
-  static constexpr int REG_CTRL = 56, REG_SOFTMAX = 224;  // 128 x 56 + 256 x 224 <= 384 x 168
+  // (the warps that issue the copies and products of two boxes a tile spill with 56)
+  static constexpr int REG_CTRL = HD == 64 ? 56 : 80, REG_SOFTMAX = HD == 64 ? 224 : 208;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + 2 * TILE_BYTES;
   static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
   static constexpr int OFF_BAR = OFF_V + NST * TILE_BYTES;
-  static constexpr int OFF_ML = OFF_BAR + 256;              // (m, l) of both slots, [2][128]
+  static constexpr int OFF_ML = OFF_BAR + 512;              // (m, l) of both slots, [2][128]
   static constexpr int SMEM_BYTES = OFF_ML + 2048 + 1024;   // + alignment slack
   // mbarriers, [t] per slot: S_t ready; S_t read (4 warps); P_t halves stored
   // (4 warps each); P.V of the first half / of all keys done
-  static constexpr int B_Q = 0, B_KF = 1, B_VF = B_KF + NST, B_KE = B_VF + NST, B_S = B_KE + NST, B_SC = B_S + 2,
+  static constexpr int B_Q = 0, B_KF = 1, B_VF = B_KF + NST, B_KE = B_VF + NST, B_VE = B_KE + NST, B_S = B_VE + NST,
+                       B_SC = B_S + 2,
                        B_P0 = B_SC + 2, B_P1 = B_P0 + 2, B_O0 = B_P1 + 2, B_O1 = B_O0 + 2, B_DRAIN = B_O1 + 2,
                        B_STALL = B_DRAIN + 1, N_BARS = B_STALL + 1;
   static constexpr int OFF_TSLOT = 8 * N_BARS, OFF_ABORT = OFF_TSLOT + 8, OFF_ISSUED = OFF_ABORT + 4;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
-  static_assert(OFF_ISSUED + 4 <= 256, "barrier area");
+  static_assert(OFF_ISSUED + 4 <= 512, "barrier area");
   static_assert(128 * REG_CTRL + 256 * REG_SOFTMAX <= NTHR * 168, "register split exceeds the launch allocation");
   // the epilogue stages 32 rows x HD floats for each of the 8 softmax warps
   static_assert(8 * 32 * HD * 4 <= OFF_BAR - OFF_K, "row staging fits over the K and V stages");
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   using C = PxCfg<HD>;
   constexpr int NBOX = C::NBOX, TILE_BYTES = C::TILE_BYTES, NST = C::NST;
   constexpr int OFF_Q = C::OFF_Q, OFF_K = C::OFF_K, OFF_V = C::OFF_V, OFF_BAR = C::OFF_BAR;
-  constexpr int B_Q = C::B_Q, B_KF = C::B_KF, B_VF = C::B_VF, B_KE = C::B_KE, B_S = C::B_S, B_SC = C::B_SC,
+  constexpr int B_Q = C::B_Q, B_KF = C::B_KF, B_VF = C::B_VF, B_KE = C::B_KE, B_VE = C::B_VE, B_S = C::B_S, B_SC = C::B_SC,
                 B_P0 = C::B_P0, B_P1 = C::B_P1, B_O0 = C::B_O0, B_O1 = C::B_O1, B_DRAIN = C::B_DRAIN;
   constexpr uint32_t TM_S = C::TM_S, TM_O = C::TM_O, TM_P = C::TM_P;
   extern __shared__ unsigned char smem_raw[];
@@ -159,8 +163,8 @@ __global__ void __launch_bounds__(NTHR, 1)
   if (tid == 256) {
     for (int i = 0; i < C::N_BARS; ++i) {
       const bool per_warp = (i >= B_SC && i < B_O0);
-      const bool three = (i >= B_KE && i < B_KE + NST) || i == B_DRAIN;
-      mbar_init(&bars[i], per_warp ? 4 : three ? 3 : 1);
+      const bool both_pv = i >= B_VE && i < B_VE + NST;  // the two P.V warps
+      mbar_init(&bars[i], per_warp ? 4 : i == B_DRAIN ? 3 : both_pv ? 2 : 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -214,51 +218,44 @@ __global__ void __launch_bounds__(NTHR, 1)
         for (int bx = 0; bx < NBOX; ++bx)
           tma_load_4d(smem + OFF_Q + t * TILE_BYTES + bx * BOX_BYTES, &tmQ, bx * 64, 0, (tile0 + t) * p.rpt, g,
                       &bars[B_Q]);
-      // (row, head) in the map of the two 64-row halves of KV tile j
-      int row[2], head[2];
-      auto locate = [&](int j) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int r0 = (j_lo + j) * BN + s * 64;
-          row[s] = r0;
-          head[s] = g;
-          if (p.block_table != nullptr) {
-            if (r0 >= P) {  // past the keys: any rows will do (masked, and V cleared)
-              row[s] = row[0];
-              head[s] = head[0];
-              continue;
-            }
-            int blk = p.block_table[r0 / p.block_size];
-            if (blk < 0 || blk >= p.num_blocks) {
-              atomicOr(p.status, GQA_DEV_BAD_BLOCK);
-              blk = 0;
-            }
-            row[s] = r0 % p.block_size;
-            head[s] = blk * p.Hkv + g;
-          }
+      // 64-row half s of KV tile j: its row in the map (and head, by reference)
+      auto locate = [&](int j, int s, int& head) -> int {
+        int r0 = (j_lo + j) * BN + s * 64;
+        head = g;
+        if (p.block_table == nullptr) return r0;
+        if (r0 >= P) r0 -= 64;  // past the keys: any rows will do (masked, and V cleared)
+        int blk = p.block_table[r0 / p.block_size];
+        if (blk < 0 || blk >= p.num_blocks) {
+          atomicOr(p.status, GQA_DEV_BAD_BLOCK);
+          blk = 0;
         }
+        head = blk * p.Hkv + g;
+        return r0 % p.block_size;
       };
-      locate(0);
+      int head0, head1, row0 = locate(0, 0, head0), row1 = locate(0, 1, head1);
+#pragma unroll 1
       for (int j = 0; j < nkv; ++j) {
         const int st = j % NST;
-        if (j >= NST) cta_wait(&bars[B_KE + st], uint32_t(j / NST - 1) & 1u, abort_flag, p.wait_limit_ns);
+        auto copy = [&](int off, const CUtensorMap* map, uint64_t* bar) {
+          mbar_arrive_expect_tx(bar, TILE_BYTES);
+          unsigned char* dst = smem + off + st * TILE_BYTES;
+#pragma unroll
+          for (int bx = 0; bx < NBOX; ++bx) {
+            tma_load_3d(dst + bx * BOX_BYTES, map, bx * 64, row0, head0, bar);
+            tma_load_3d(dst + bx * BOX_BYTES + 8192, map, bx * 64, row1, head1, bar);
+          }
+        };
+        const uint32_t freed = uint32_t(j / NST - 1) & 1u;
+        if (j >= NST) cta_wait(&bars[B_KE + st], freed, abort_flag, p.wait_limit_ns);
         if (*abort_flag) break;
-        mbar_arrive_expect_tx(&bars[B_KF + st], TILE_BYTES);
-#pragma unroll
-        for (int bx = 0; bx < NBOX; ++bx)
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-            tma_load_3d(smem + OFF_K + st * TILE_BYTES + bx * BOX_BYTES + s * 8192, &tmK, bx * 64, row[s], head[s],
-                        &bars[B_KF + st]);
-        mbar_arrive_expect_tx(&bars[B_VF + st], TILE_BYTES);
-#pragma unroll
-        for (int bx = 0; bx < NBOX; ++bx)
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-            tma_load_3d(smem + OFF_V + st * TILE_BYTES + bx * BOX_BYTES + s * 8192, &tmV, bx * 64, row[s], head[s],
-                        &bars[B_VF + st]);
+        copy(OFF_K, &tmK, &bars[B_KF + st]);
+        if (j >= NST) cta_wait(&bars[B_VE + st], freed, abort_flag, p.wait_limit_ns);
+        copy(OFF_V, &tmV, &bars[B_VF + st]);
         n_issued = j + 1;
-        if (j + 1 < nkv) locate(j + 1);  // (the table entries arrive while the next stage is waited for)
+        if (j + 1 < nkv) {
+          row0 = locate(j + 1, 0, head0);
+          row1 = locate(j + 1, 1, head1);
+        }
       }
       *reinterpret_cast<volatile int*>(smem + OFF_BAR + C::OFF_ISSUED) = n_issued;
     } else if (warp == 9) {
@@ -329,7 +326,7 @@ __global__ void __launch_bounds__(NTHR, 1)
             mma_commit_warp(&bars[(half ? B_O1 : B_O0) + t]);
           }
         }
-        mma_commit_warp(&bars[B_KE + st]);
+        mma_commit_warp(&bars[B_VE + st]);
       }
     }
   } else {
@@ -496,83 +493,112 @@ struct PrefixMergeParams {
   const int32_t* prefix_len;  // or null: max_prefix
   const int32_t* kv_lens;     // or null: max_kv_len
   int rows, Hq, max_prefix, max_kv_len;
-  int chunk, n_own;           // own keys: slots [0, min(n_own, ceil(L / chunk)))
+  // own keys, slots [0, n_own): counts[b][unit] of them, or (null)
+  // min(n_own, ceil(L / chunk)) splits
+  const int32_t* counts;
+  int n_rep, n_hc, nrep_cta, units;
+  int chunk, n_own;
   int n_split, n_slots;       // shared keys: slots [n_own, n_own + shares)
   const float2* ml;
   const float* part_o;
   uint32_t* status;
 };
 
-// One warp per (request, query head) row: the maximum of the row's partials
-// over the lanes, then their weighted sum, each partial row one load of the
-// whole warp.  The first PRE partial rows are loaded before the weights are
-// known, so that the two round trips overlap.  The order of the sum is fixed.
-template <int D>
+// WPR warps per (request, query head) row.  Every warp finds the maximum of
+// the row's partials over its lanes and takes every WPR-th partial row, one
+// load of the whole warp each; the first PRE of them are loaded before the
+// weights are known, so that the two round trips overlap.  The order of the
+// sums is fixed.
+template <int D, int WPR>
 __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixMergeParams p) {
   constexpr int V = D / 32;  // columns per lane
   constexpr int PRE = 8;
   using Vec = typename std::conditional<V == 4, float4, float2>::type;
-  const int row = int((blockIdx.x * 256 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+  __shared__ float acc_s[WPR > 1 ? 8 : 1][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = int(blockIdx.x) * (8 / WPR) + warp / WPR, part = warp % WPR;
   grid_launch_dependents();
   grid_dependency_wait();
-  if (row >= p.rows) return;
-  const int b = row / p.Hq;
-  int P = p.prefix_len != nullptr ? *p.prefix_len : p.max_prefix;
-  int L = p.kv_lens != nullptr ? p.kv_lens[b] : p.max_kv_len;
-  P = min(max(P, 0), p.max_prefix);
-  L = min(max(L, 0), p.max_kv_len);
-  const int own = min(p.n_own, (L + p.chunk - 1) / p.chunk), n = own + prefix_shares(p.n_split, P);
-  auto slot = [&](int i) { return i < own ? i : p.n_own + i - own; };
-  __nv_bfloat16* const dst = p.o + size_t(row) * D + lane * V;
   float acc[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
   float den = 1.f;
-  if (n == 0) {  // no key at all: zeros
-    if (lane == 0) atomicOr(p.status, GQA_DEV_EMPTY_REQUEST);
-  } else {
-    const float2* ml = p.ml + size_t(row) * p.n_slots;
-    const float* po = p.part_o + size_t(row) * p.n_slots * D + lane * V;
-    Vec x[PRE];
-#pragma unroll
-    for (int k = 0; k < PRE; ++k)
-      if (k < n) x[k] = __ldcg(reinterpret_cast<const Vec*>(po + size_t(slot(k)) * D));
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(&ml[slot(i)]).x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    den = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      float w = 0.f;
-      if (i0 + lane < n) {
-        const float2 s = __ldcg(&ml[slot(i0 + lane)]);
-        w = s.x == -INFINITY ? 0.f : fast_exp2(s.x - M);
-        den += s.y * w;
-      }
-      auto add = [&](int k, const Vec& v) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float* f = reinterpret_cast<const float*>(&v);
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(f[e], wk, acc[e]);
-      };
-      int k = 0;
-      if (i0 == 0) {
-#pragma unroll
-        for (; k < PRE; ++k)
-          if (k < n) add(k, x[k]);
-      }
-      const int cnt = min(32, n - i0);
-#pragma unroll 4
-      for (; k < cnt; ++k) add(k, __ldcg(reinterpret_cast<const Vec*>(po + size_t(slot(i0 + k)) * D)));
+  if (row < p.rows) {
+    const int b = row / p.Hq, h = row % p.Hq;
+    int P = p.prefix_len != nullptr ? *p.prefix_len : p.max_prefix;
+    P = min(max(P, 0), p.max_prefix);
+    const int raw = p.kv_lens != nullptr ? p.kv_lens[b] : p.max_kv_len, L = min(max(raw, 0), p.max_kv_len);
+    int own;
+    if (p.counts != nullptr) {
+      const int u = h / p.n_rep * p.n_hc + h % p.n_rep / p.nrep_cta, count = p.counts[b * p.units + u];
+      own = L > 0 ? count : 0;  // (a unit without keys has no count written)
+    } else {
+      own = min(p.n_own, (L + p.chunk - 1) / p.chunk);
     }
+    const int n = own + prefix_shares(p.n_split, P);
+    auto slot = [&](int i) { return i < own ? i : p.n_own + i - own; };
+    if (n == 0) {  // no key at all: zeros
+      if (lane == 0 && part == 0) atomicOr(p.status, GQA_DEV_EMPTY_REQUEST);
+    } else {
+      const float2* ml = p.ml + size_t(row) * p.n_slots;
+      const float* po = p.part_o + size_t(row) * p.n_slots * D + lane * V;
+      Vec x[PRE];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
+      for (int k = 0; k < PRE; ++k)
+        if (part + k * WPR < n) x[k] = __ldcg(reinterpret_cast<const Vec*>(po + size_t(slot(part + k * WPR)) * D));
+      // lane l has the (max, sum) of partials l, l + 32, ...
+      const float2 s0 = lane < n ? __ldcg(&ml[slot(lane)]) : make_float2(-INFINITY, 0.f);
+      float M = s0.x;
+      for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, __ldcg(&ml[slot(i)]).x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      den = 0.f;
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const float2 s = i0 == 0 ? s0 : i0 + lane < n ? __ldcg(&ml[slot(i0 + lane)]) : make_float2(-INFINITY, 0.f);
+        const float w = s.x == -INFINITY ? 0.f : fast_exp2(s.x - M);
+        den += s.y * w;
+        auto add = [&](int i, const Vec& v) {
+          const float wi = __shfl_sync(0xffffffffu, w, i - i0);
+          const float* f = reinterpret_cast<const float*>(&v);
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[e] = fmaf(f[e], wi, acc[e]);
+        };
+        const int end = min(n, i0 + 32);
+        int i = i0 + part;  // (32 is a multiple of WPR)
+#pragma unroll
+        for (int k = 0; k < PRE; ++k) {
+          const int ik = part + k * WPR;
+          if (ik >= i0 && ik < end) {
+            add(ik, x[k]);
+            i = ik + WPR;
+          }
+        }
+#pragma unroll 4
+        for (; i < end; i += WPR) add(i, __ldcg(reinterpret_cast<const Vec*>(po + size_t(slot(i)) * D)));
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
+    }
   }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc_s[warp][lane * V + e] = acc[e];
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += acc_s[warp + k][lane * V + e];
+  }
+  if (row >= p.rows) return;
+  __nv_bfloat16* const dst = p.o + size_t(row) * D + lane * V;
   const float inv = 1.f / den;
 #pragma unroll
   for (int e = 0; e < V; e += 2)
     *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
 }
+
+constexpr int kMergeWideRows = 4096;  // rows from which one warp takes a row
 
 template <int HD>
 cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
@@ -585,7 +611,8 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   if (!encode_bf16_query_rows(&tq, d.q, HD, n_rep, d.B, d.Hkv, a.plan.rpt) ||
       !kv_map(&tk, a.k_prefix, HD, rows, heads) || !kv_map(&tv, a.v_prefix, HD, rows, heads))
     return cudaErrorInvalidValue;
-  const int n_own = d.plan.n_split, n_slots = n_own + a.plan.n_split;
+  const SharedPrefixLayout lay = shared_prefix_layout(a);
+  const int n_own = lay.n_own, n_slots = lay.n_slots;
   const WorkspaceLayout w = workspace_layout(d.B, d.Hq, d.Hkv, d.plan.n_hc, n_slots, HD);
   unsigned char* ws = static_cast<unsigned char*>(d.workspace);
   PrefixParams p;
@@ -623,10 +650,15 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
                       ? launch_pdl(prefix_kernel<HD, true>, grid, dim3(NTHR), C::SMEM_BYTES, stream, tq, tk, tv, p)
                       : launch_pdl(prefix_kernel<HD, false>, grid, dim3(NTHR), C::SMEM_BYTES, stream, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
-  DecodeArgs own = d;
-  own.n_slots = n_slots;
-  own.force_partial = 1;
-  e = launch_decode_mma(own, stream);
+  int32_t* const counts = a.own_plan.fits ? reinterpret_cast<int32_t*>(ws + lay.off_counts) : nullptr;
+  if (a.own_plan.fits) {
+    e = launch_own_rows(d, a.own_plan, n_slots, p.ml, p.part_o, counts, stream);
+  } else {
+    DecodeArgs own = d;
+    own.n_slots = n_slots;
+    own.force_partial = 1;
+    e = launch_decode_mma(own, stream);
+  }
   if (e != cudaSuccess) return e;
   PrefixMergeParams m;
   m.o = static_cast<__nv_bfloat16*>(d.o);
@@ -636,6 +668,11 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   m.Hq = d.Hq;
   m.max_prefix = a.max_prefix;
   m.max_kv_len = d.max_kv_len;
+  m.counts = counts;
+  m.n_rep = n_rep;
+  m.n_hc = a.own_plan.n_hc;
+  m.nrep_cta = a.own_plan.nrep_cta;
+  m.units = a.own_plan.units;
   m.chunk = d.plan.chunk;
   m.n_own = n_own;
   m.n_split = a.plan.n_split;
@@ -643,7 +680,9 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   m.ml = p.ml;
   m.part_o = p.part_o;
   m.status = p.status;
-  return launch_pdl(prefix_merge_kernel<HD>, dim3((m.rows + 7) / 8), dim3(256), 0, stream, m);
+  if (m.rows >= kMergeWideRows)
+    return launch_pdl(prefix_merge_kernel<HD, 1>, dim3((m.rows + 7) / 8), dim3(256), 0, stream, m);
+  return launch_pdl(prefix_merge_kernel<HD, 4>, dim3((m.rows + 1) / 2), dim3(256), 0, stream, m);
 }
 
 }  // namespace
@@ -677,6 +716,16 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sm
     }
   }
   return p;
+}
+
+SharedPrefixLayout shared_prefix_layout(const SharedPrefixArgs& a) {
+  SharedPrefixLayout l;
+  const DecodeArgs& d = a.own;
+  l.n_own = a.own_plan.fits ? a.own_plan.n_slots : d.plan.n_split;
+  l.n_slots = l.n_own + a.plan.n_split;
+  l.off_counts = workspace_layout(d.B, d.Hq, d.Hkv, d.plan.n_hc, l.n_slots, d.D).total;
+  l.total = l.off_counts + (a.own_plan.fits ? align256(sizeof(int32_t) * size_t(d.B) * a.own_plan.units) : 0);
+  return l;
 }
 
 cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, cudaStream_t stream) {

@@ -73,8 +73,8 @@ inline bool encode_bf16_query_rows(CUtensorMap* map, const void* base, int cols,
   return encode_bf16(map, base, 4, dims, strides, box);
 }
 
-// The map of a K or V cache [heads][rows][D] with 64-row boxes, kept for
-// recently used caches (decode_mma.cu).
-bool kv_map(CUtensorMap* out, const void* base, int D, int rows, int heads);
+// The map of a K or V cache [heads][rows][D] with boxes of box_rows rows, kept
+// for recently used caches (decode_mma.cu).
+bool kv_map(CUtensorMap* out, const void* base, int D, int rows, int heads, int box_rows = 64);
 
 }  // namespace gqa

@@ -142,6 +142,36 @@ def test_empty_parts(P, lens, Hq, Hkv, D):
     parity.check(f64(c.paged(64, max_prefix=300)), c.oracle(), "bf16", "paged")
 
 
+@pytest.mark.parametrize("seed", range(6))
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (14, 2, 64), (24, 1, 64), (17, 1, 128)])
+def test_ragged_own_rows(Hq, Hkv, D, seed):
+    """Runs of empty requests, single rows and long ones: ranges that begin and
+    end anywhere in the list of tiles."""
+    r = np.random.default_rng(seed)
+    B = int(r.integers(1, 90))
+    lens = np.where(r.random(B) < 0.3, 0, np.where(r.random(B) < 0.3, r.integers(1, 18, B), r.integers(1, 900, B)))
+    lens[int(r.integers(0, B))] = 900
+    c = Case(B, Hq, Hkv, D, int(r.integers(1, 300)), lens, seed=seed)
+    ref = c.oracle()
+    parity.check(f64(c.dense()), ref, "bf16", "dense")
+    parity.check(f64(c.paged(64)), ref, "bf16", "paged")
+
+
+@pytest.mark.parametrize("lens", [[5000], [4096, 3], [0, 16, 0, 5000]])
+def test_long_own_rows_of_few_requests(lens):
+    c = Case(len(lens), 28, 4, 128, 200, lens, seed=2)
+    parity.check(f64(c.dense()), c.oracle(), "bf16")
+
+
+@pytest.mark.parametrize("B", [1023, 1024, 1025, 1500])
+def test_many_requests(B):
+    """Up to 1,024 requests the own rows are one list, past that the decode kernel's."""
+    c = Case(B, 4, 2, 64, 150, lens_of(B, 40), seed=1)
+    ref = c.oracle()
+    parity.check(f64(c.dense()), ref, "bf16", "dense")
+    parity.check(f64(c.paged(64)), ref, "bf16", "paged")
+
+
 def test_lengths_default_to_the_bounds():
     c = Case(5, 8, 2, 64, 333, [40] * 5)
     parity.check(f64(binding.decode_shared_prefix(c.q, c.kp, c.vp, c.k, c.v)), c.oracle(), "bf16")
