@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
     ihead = blk * p.Hkv + g;
   };
+  const uint64_t once = l2_policy_evict_first();  // (the partials of both kernels are to stay in L2 for the merge)
   int issued = 0;  // tiles of this range copied so far (all lanes count, lane 0 copies)
   auto issue = [&]() {
     if (lane == 0) {
@@ -187,8 +188,8 @@ __global__ void __launch_bounds__(NTHR, 1)
       mbar_arrive_expect_tx(&full[st], C::STAGEB);
 #pragma unroll
       for (int hf = 0; hf < C::HALVES; ++hf) {
-        tma_load_3d(dst + hf * C::BOX, &tmK, hf * 64, irow, ihead, &full[st]);
-        tma_load_3d(dst + C::TILEB + hf * C::BOX, &tmV, hf * 64, irow, ihead, &full[st]);
+        tma_load_3d(dst + hf * C::BOX, &tmK, hf * 64, irow, ihead, &full[st], once);
+        tma_load_3d(dst + C::TILEB + hf * C::BOX, &tmV, hf * 64, irow, ihead, &full[st], once);
       }
     }
     ++issued;

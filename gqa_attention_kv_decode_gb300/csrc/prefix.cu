@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         head = blk * p.Hkv + g;
         return r0 % p.block_size;
       };
+      const uint64_t once = l2_policy_evict_first();
       int head0, head1, row0 = locate(0, 0, head0), row1 = locate(0, 1, head1);
 #pragma unroll 1
       for (int j = 0; j < nkv; ++j) {
@@ -241,8 +242,13 @@ __global__ void __launch_bounds__(NTHR, 1)
           unsigned char* dst = smem + off + st * TILE_BYTES;
 #pragma unroll
           for (int bx = 0; bx < NBOX; ++bx) {
-            tma_load_3d(dst + bx * BOX_BYTES, map, bx * 64, row0, head0, bar);
-            tma_load_3d(dst + bx * BOX_BYTES + 8192, map, bx * 64, row1, head1, bar);
+            if (gridDim.y == 1) {  // read by this CTA alone
+              tma_load_3d(dst + bx * BOX_BYTES, map, bx * 64, row0, head0, bar, once);
+              tma_load_3d(dst + bx * BOX_BYTES + 8192, map, bx * 64, row1, head1, bar, once);
+            } else {
+              tma_load_3d(dst + bx * BOX_BYTES, map, bx * 64, row0, head0, bar);
+              tma_load_3d(dst + bx * BOX_BYTES + 8192, map, bx * 64, row1, head1, bar);
+            }
           }
         };
         const uint32_t freed = uint32_t(j / NST - 1) & 1u;
@@ -504,15 +510,18 @@ struct PrefixMergeParams {
   uint32_t* status;
 };
 
-// WPR warps per (request, query head) row.  Every warp finds the maximum of
-// the row's partials over its lanes and takes every WPR-th partial row, one
-// load of the whole warp each; the first PRE of them are loaded before the
-// weights are known, so that the two round trips overlap.  The order of the
+// WPR warps per (request, query head) row; warp `part` takes every WPR-th
+// partial row of the shared and of the own keys, one load of the whole warp
+// each.  The time is round trips to L2, so everything that can be asked for at
+// once is: the lengths and counts, the (max, sum) of the partials (a lane
+// each), and the first PS + PO partial rows, before it is known which of these
+// slots the row uses (the others are left out of the sums).  The order of the
 // sums is fixed.
 template <int D, int WPR>
 __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixMergeParams p) {
   constexpr int V = D / 32;  // columns per lane
-  constexpr int PRE = 8;
+  constexpr int PS = WPR < 8 ? 8 : 4, PO = 4;  // (within the first 32 partials, whose weights the lanes hold)
+  static_assert(PS * WPR <= 32 && PO * WPR <= 32, "preloaded partials");
   using Vec = typename std::conditional<V == 4, float4, float2>::type;
   __shared__ float acc_s[WPR > 1 ? 8 : 1][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -525,8 +534,21 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixMergePara
   float den = 1.f;
   if (row < p.rows) {
     const int b = row / p.Hq, h = row % p.Hq;
+    const float2* const ml_own = p.ml + size_t(row) * p.n_slots;
+    const float2* const ml_sh = ml_own + p.n_own;
+    const float* const po_own = p.part_o + size_t(row) * p.n_slots * D + lane * V;
+    const float* const po_sh = po_own + size_t(p.n_own) * D;
+    auto load = [&](const float* base, int s) { return __ldcg(reinterpret_cast<const Vec*>(base + size_t(s) * D)); };
+    Vec xs[PS], xo[PO];
+#pragma unroll
+    for (int k = 0; k < PS; ++k)
+      if (part + k * WPR < p.n_split) xs[k] = load(po_sh, part + k * WPR);
+#pragma unroll
+    for (int k = 0; k < PO; ++k)
+      if (part + k * WPR < p.n_own) xo[k] = load(po_own, part + k * WPR);
+    const float2 none = make_float2(-INFINITY, 0.f);
+    float2 ms = lane < p.n_split ? __ldcg(&ml_sh[lane]) : none, mo = lane < p.n_own ? __ldcg(&ml_own[lane]) : none;
     int P = p.prefix_len != nullptr ? *p.prefix_len : p.max_prefix;
-    P = min(max(P, 0), p.max_prefix);
     const int raw = p.kv_lens != nullptr ? p.kv_lens[b] : p.max_kv_len, L = min(max(raw, 0), p.max_kv_len);
     int own;
     if (p.counts != nullptr) {
@@ -535,47 +557,49 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixMergePara
     } else {
       own = min(p.n_own, (L + p.chunk - 1) / p.chunk);
     }
-    const int n = own + prefix_shares(p.n_split, P);
-    auto slot = [&](int i) { return i < own ? i : p.n_own + i - own; };
-    if (n == 0) {  // no key at all: zeros
+    P = min(max(P, 0), p.max_prefix);
+    const int shares = prefix_shares(p.n_split, P);
+    if (own + shares == 0) {  // no key at all: zeros
       if (lane == 0 && part == 0) atomicOr(p.status, GQA_DEV_EMPTY_REQUEST);
     } else {
-      const float2* ml = p.ml + size_t(row) * p.n_slots;
-      const float* po = p.part_o + size_t(row) * p.n_slots * D + lane * V;
-      Vec x[PRE];
-#pragma unroll
-      for (int k = 0; k < PRE; ++k)
-        if (part + k * WPR < n) x[k] = __ldcg(reinterpret_cast<const Vec*>(po + size_t(slot(part + k * WPR)) * D));
-      // lane l has the (max, sum) of partials l, l + 32, ...
-      const float2 s0 = lane < n ? __ldcg(&ml[slot(lane)]) : make_float2(-INFINITY, 0.f);
-      float M = s0.x;
-      for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, __ldcg(&ml[slot(i)]).x);
+      if (lane >= shares) ms = none;
+      if (lane >= own) mo = none;
+      // the row's maximum; lane l has partials l, l + 32, ... of either kind
+      float M = fmaxf(ms.x, mo.x);
+      for (int i = lane + 32; i < shares; i += 32) M = fmaxf(M, __ldcg(&ml_sh[i]).x);
+      for (int i = lane + 32; i < own; i += 32) M = fmaxf(M, __ldcg(&ml_own[i]).x);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
       den = 0.f;
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const float2 s = i0 == 0 ? s0 : i0 + lane < n ? __ldcg(&ml[slot(i0 + lane)]) : make_float2(-INFINITY, 0.f);
+      auto weight = [&](const float2& s) {
         const float w = s.x == -INFINITY ? 0.f : fast_exp2(s.x - M);
         den += s.y * w;
+        return w;
+      };
+      // adds this warp's share of n partials; the first NP are in x, the first
+      // 32 weights in w
+      auto add_all = [&](int n, const float2* ml, const float* po, float w, const Vec* x, auto np) {
+        constexpr int NP = decltype(np)::value;
         auto add = [&](int i, const Vec& v) {
-          const float wi = __shfl_sync(0xffffffffu, w, i - i0);
+          const float wi = __shfl_sync(0xffffffffu, w, i & 31);
           const float* f = reinterpret_cast<const float*>(&v);
 #pragma unroll
           for (int e = 0; e < V; ++e) acc[e] = fmaf(f[e], wi, acc[e]);
         };
-        const int end = min(n, i0 + 32);
-        int i = i0 + part;  // (32 is a multiple of WPR)
 #pragma unroll
-        for (int k = 0; k < PRE; ++k) {
-          const int ik = part + k * WPR;
-          if (ik >= i0 && ik < end) {
-            add(ik, x[k]);
-            i = ik + WPR;
-          }
+        for (int k = 0; k < NP; ++k)
+          if (part + k * WPR < n) add(part + k * WPR, x[k]);
+        int i = part + NP * WPR;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+          if (i0 > 0) w = weight(i0 + lane < n ? __ldcg(&ml[i0 + lane]) : none);
+          const int end = min(n, i0 + 32);
+#pragma unroll 8
+          for (; i < end; i += WPR) add(i, load(po, i));
         }
-#pragma unroll 4
-        for (; i < end; i += WPR) add(i, __ldcg(reinterpret_cast<const Vec*>(po + size_t(slot(i)) * D)));
-      }
+      };
+      const float ws = weight(ms), wo = weight(mo);
+      add_all(shares, ml_sh, po_sh, ws, xs, std::integral_constant<int, PS>());
+      add_all(own, ml_own, po_own, wo, xo, std::integral_constant<int, PO>());
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
     }
@@ -598,7 +622,19 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixMergePara
     *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
 }
 
-constexpr int kMergeWideRows = 4096;  // rows from which one warp takes a row
+// As many warps a row as keep the grid within a wave (about 20 warps of the
+// merge on an SM), up to eight.
+template <int HD>
+cudaError_t launch_prefix_merge(const PrefixMergeParams& m, cudaStream_t stream) {
+  const long room = 20L * device_sm_count() / m.rows;
+  auto go = [&](auto kern, int wpr) {
+    return launch_pdl(kern, dim3((m.rows * wpr + 7) / 8), dim3(256), 0, stream, m);
+  };
+  if (room >= 8) return go(prefix_merge_kernel<HD, 8>, 8);
+  if (room >= 4) return go(prefix_merge_kernel<HD, 4>, 4);
+  if (room >= 2) return go(prefix_merge_kernel<HD, 2>, 2);
+  return go(prefix_merge_kernel<HD, 1>, 1);
+}
 
 template <int HD>
 cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
@@ -680,9 +716,7 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   m.ml = p.ml;
   m.part_o = p.part_o;
   m.status = p.status;
-  if (m.rows >= kMergeWideRows)
-    return launch_pdl(prefix_merge_kernel<HD, 1>, dim3((m.rows + 7) / 8), dim3(256), 0, stream, m);
-  return launch_pdl(prefix_merge_kernel<HD, 4>, dim3((m.rows + 1) / 2), dim3(256), 0, stream, m);
+  return launch_prefix_merge<HD>(m, stream);
 }
 
 }  // namespace
