@@ -147,7 +147,7 @@ int check_shared_prefix(int B, int Hq, int Hkv, int D, int max_prefix_len, int S
   const int rc = check_decode_shape(B, Hq, Hkv, D, S_cap, max_kv_len, scale);
   if (rc != GQA_OK) return rc;
   if (max_prefix_len < 1 || max_prefix_len > 0x7fffff00) return GQA_ERR_INVALID_ARG;  // (tiles of 128 in 32 bits)
-  if (Hkv > 65535) return GQA_ERR_INVALID_ARG;  // grid z
+  if (long(B) * Hq > (1L << 22)) return GQA_ERR_INVALID_ARG;  // (rows, and their partials, in 32 bits)
   return GQA_OK;
 }
 // bf16, and the query heads of a KV head in one 128-row tile.
@@ -162,7 +162,7 @@ void plan_shared_prefix(SharedPrefixArgs& a) {
   DecodeArgs& d = a.own;
   const int sms = device_sm_count();
   a.plan = prefix_plan(d.B, d.Hq, d.Hkv, d.D, a.max_prefix, sms);
-  a.own_plan = own_rows_plan(d.B, d.Hq, d.Hkv, d.max_kv_len, sms);
+  a.own_plan = own_rows_plan(d.B, d.Hq, d.Hkv, d.max_kv_len);
   d.plan = decode_plan(d.B, d.Hq, d.Hkv, d.D, d.max_kv_len, GQA_BF16, d.block_table != nullptr);
 }
 

@@ -150,21 +150,19 @@ struct PrefixPlan {
   int n_tiles;  // row tiles per KV head
   int units;    // CTAs per KV head and share: one for a single tile, else one per two tiles
   int n_split;  // shares of the keys
+  double share_us;  // a share's time, estimated
 };
 PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sms);
 
-// The own rows behind the shared ones (own_rows.cu), for up to 1,024 requests.
+// The own rows behind the shared ones (own_rows.cuh), for up to 1,024 requests.
 struct OwnRowsPlan {
   bool fits;            // else the decode kernel takes them
   int n_hc, nrep_cta;   // query-head chunks per KV head, heads of a chunk
   int units;            // (KV head, chunk) pairs of a request
-  int blocks;           // grid
-  int min_tiles;        // tiles per warp, at least
+  int min_tiles;        // tiles of a warp's range of the list, at least
   int n_slots;          // partials of a row, at most
 };
-OwnRowsPlan own_rows_plan(int B, int Hq, int Hkv, int max_kv_len, int num_sms);
-cudaError_t launch_own_rows(const DecodeArgs& a, const OwnRowsPlan& plan, int n_slots, float2* ml, float* part_o,
-                            int32_t* counts, cudaStream_t stream);
+OwnRowsPlan own_rows_plan(int B, int Hq, int Hkv, int max_kv_len);
 
 // Decode over shared rows followed by each request's own (bf16): `own` is the
 // call over the own rows, its plan included; with a block table both caches

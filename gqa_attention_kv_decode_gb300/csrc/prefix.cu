@@ -5,16 +5,19 @@
 // Over the P shared rows every query of the batch meets the same K and V, so
 // for one KV head the B * n_rep query rows are the M rows of
 //     S = Q K^T,   O = P V          (a product, not B matrix-vector products),
-// which reads K and V once instead of B times.  Three kernels:
-//   prefix_kernel  one CTA takes two 128-row tiles of (request, head) rows --
-//                  or, when a KV head has one tile only, that tile, its KV
-//                  tiles dealt to the two softmax warpgroups in turn -- and a
-//                  contiguous share of the shared keys, and writes the rows'
-//                  partials (max, sum, unnormalised O);
-//   own_rows       the requests' own keys, partials only (more than 1,024
-//                  requests: the decode kernel);
+// which reads K and V once instead of B times.  Two kernels:
+//   shared_prefix_kernel  its first CTAs work on the shared rows: each takes
+//                  two 128-row tiles of (request, head) rows -- or, when a KV
+//                  head has one tile only, that tile, its KV tiles dealt to the
+//                  two softmax warpgroups in turn -- and a contiguous share of
+//                  the shared keys, and writes the rows' partials (max, sum,
+//                  unnormalised O).  The other CTAs, one an SM, work on the
+//                  requests' own rows (own_rows.cuh), at once on the SMs that
+//                  the shared rows leave free, otherwise as those end (more
+//                  than 1,024 requests: the decode kernel takes the own rows,
+//                  in a launch of its own);
 //   prefix_merge   log-sum-exp merge of a row's partials of both.
-// Inside the CTA the roles, the tensor-memory layout and the softmax are the
+// Inside a CTA of the shared rows the roles, the tensor-memory layout and the softmax are the
 // prefill kernel's: warp 8 TMA, warp 9 issues S, warps 10 and 11 issue P V,
 // warpgroups 0 and 1 do the softmax of one row per thread with a lazily
 // raised reference.  There is no diagonal: only the last KV tile is masked.
@@ -130,24 +133,55 @@ __device__ __forceinline__ void store_rows(unsigned char* stage, float* out, lon
   }
 }
 
+// Which CTA of the grid this is: the first n_shared ones work on the shared
+// rows, (split, unit, KV head) with the split fastest, the rest on the own rows.
+// (CTAs of the shared rows that went on with the own ones themselves saved a
+// start, but the code behind the softmax loop made that loop 10 % slower.)
+struct GridPlan {
+  int n_shared, units;
+};
+
+template <int HD>
+constexpr int kSmemBytes = PxCfg<HD>::SMEM_BYTES > OwnCfg<HD>::SMEM ? PxCfg<HD>::SMEM_BYTES : OwnCfg<HD>::SMEM;
+
 // SINGLE: one row tile per CTA, its even KV tiles in slot 0 and the odd ones
 // in slot 1; otherwise tiles A and B (slots 0 and 1) over the same KV tiles.
 template <int HD, bool SINGLE>
 __global__ void __launch_bounds__(NTHR, 1)
-    prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                  const __grid_constant__ CUtensorMap tmV, const PrefixParams p) {
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKo,
+                         const __grid_constant__ CUtensorMap tmVo, const PrefixParams p, const OwnRowsParams own,
+                         const GridPlan grid) {
   using C = PxCfg<HD>;
   constexpr int NBOX = C::NBOX, TILE_BYTES = C::TILE_BYTES, NST = C::NST;
   constexpr int OFF_Q = C::OFF_Q, OFF_K = C::OFF_K, OFF_V = C::OFF_V, OFF_BAR = C::OFF_BAR;
-  constexpr int B_Q = C::B_Q, B_KF = C::B_KF, B_VF = C::B_VF, B_KE = C::B_KE, B_VE = C::B_VE, B_S = C::B_S, B_SC = C::B_SC,
-                B_P0 = C::B_P0, B_P1 = C::B_P1, B_O0 = C::B_O0, B_O1 = C::B_O1, B_DRAIN = C::B_DRAIN;
+  constexpr int B_Q = C::B_Q, B_KF = C::B_KF, B_VF = C::B_VF, B_KE = C::B_KE, B_VE = C::B_VE, B_S = C::B_S,
+                B_SC = C::B_SC, B_P0 = C::B_P0, B_P1 = C::B_P1, B_O0 = C::B_O0, B_O1 = C::B_O1,
+                B_DRAIN = C::B_DRAIN;
   constexpr uint32_t TM_S = C::TM_S, TM_O = C::TM_O, TM_P = C::TM_P;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = blockIdx.x, g = blockIdx.z;
-  const int tile0 = SINGLE ? int(blockIdx.y) : 2 * int(blockIdx.y);
+  grid_launch_dependents();  // (the next grid's CTAs wait for this one themselves)
+  if (int(blockIdx.x) >= grid.n_shared) {
+    if (tid == 0) {
+      prefetch_tmap(&tmKo);
+      prefetch_tmap(&tmVo);
+    }
+    if (warp >= kOwnWarps) {  // gives its registers to the eight warps that work
+      set_max_regs_dec<C::REG_CTRL>();
+      return;
+    }
+    set_max_regs_inc<C::REG_SOFTMAX>();
+    grid_dependency_wait();
+    own_scan<HD>(smem, own, int(blockIdx.x) == grid.n_shared);
+    own_rows<HD>(smem, &tmKo, &tmVo, own, int(blockIdx.x) - grid.n_shared);
+    return;
+  }
+  const int split = int(blockIdx.x) % p.n_split, unit = int(blockIdx.x) / p.n_split % grid.units,
+            g = int(blockIdx.x) / p.n_split / grid.units;
+  const int tile0 = SINGLE ? unit : 2 * unit;
   const bool two = !SINGLE && tile0 + 1 < p.n_tiles;  // is there a tile B?
   const int q_rows = p.n_rep * p.rpt;                 // rows of a tile that are queries
 
@@ -155,7 +189,6 @@ __global__ void __launch_bounds__(NTHR, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + OFF_BAR + C::OFF_TSLOT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_BAR + C::OFF_ABORT);
 
-  grid_launch_dependents();  // (the next grid's CTAs wait for this one themselves)
   if (warp == 9) {
     tmem_alloc(tslot, TMEM_COLS);
     tmem_relinquish();
@@ -191,7 +224,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   if (p.prefix_len != nullptr) {
     const int raw = *p.prefix_len;
     P = min(max(raw, 0), p.max_prefix);
-    if (P != raw && tid == 0 && split == 0 && g == 0 && blockIdx.y == 0) atomicOr(p.status, GQA_DEV_KVLEN_CLAMPED);
+    if (P != raw && tid == 0 && blockIdx.x == 0) atomicOr(p.status, GQA_DEV_KVLEN_CLAMPED);
   }
   const int n_kv = (P + BN - 1) / BN, n_used = prefix_shares(p.n_split, P);
   if (split >= n_used) {  // no share for this CTA
@@ -242,7 +275,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           unsigned char* dst = smem + off + st * TILE_BYTES;
 #pragma unroll
           for (int bx = 0; bx < NBOX; ++bx) {
-            if (gridDim.y == 1) {  // read by this CTA alone
+            if (grid.units == 1) {  // read by this CTA alone
               tma_load_3d(dst + bx * BOX_BYTES, map, bx * 64, row0, head0, bar, once);
               tma_load_3d(dst + bx * BOX_BYTES + 8192, map, bx * 64, row1, head1, bar, once);
             } else {
@@ -636,6 +669,9 @@ cudaError_t launch_prefix_merge(const PrefixMergeParams& m, cudaStream_t stream)
   return go(prefix_merge_kernel<HD, 1>, 1);
 }
 
+// A 16-key tile's time for one warp of the own rows when all SMs are at it.
+double own_tile_us(int D) { return D == 64 ? 0.75 : 1.45; }
+
 template <int HD>
 cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   using C = PxCfg<HD>;
@@ -646,6 +682,11 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   const int heads = paged ? d.num_blocks * d.Hkv : d.Hkv, rows = paged ? d.block_size : a.P_cap;
   if (!encode_bf16_query_rows(&tq, d.q, HD, n_rep, d.B, d.Hkv, a.plan.rpt) ||
       !kv_map(&tk, a.k_prefix, HD, rows, heads) || !kv_map(&tv, a.v_prefix, HD, rows, heads))
+    return cudaErrorInvalidValue;
+  CUtensorMap tko = tk, tvo = tv;  // the own rows, in boxes of their tile
+  const bool listed = a.own_plan.fits;
+  if (listed && (!kv_map(&tko, d.k, HD, paged ? d.block_size : d.S_cap, paged ? heads : d.B * d.Hkv, kOwnTile) ||
+                 !kv_map(&tvo, d.v, HD, paged ? d.block_size : d.S_cap, paged ? heads : d.B * d.Hkv, kOwnTile)))
     return cudaErrorInvalidValue;
   const SharedPrefixLayout lay = shared_prefix_layout(a);
   const int n_own = lay.n_own, n_slots = lay.n_slots;
@@ -672,24 +713,52 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   p.status = reinterpret_cast<uint32_t*>(ws);
   p.wait_limit_ns = kWaitLimitNs;
   p.test_stall_ns = wait_test_ns();
+  OwnRowsParams o = {};
+  o.q = static_cast<const __nv_bfloat16*>(d.q);
+  o.kv_lens = d.kv_lens;
+  o.block_table = d.block_table;
+  o.block_size = d.block_size;
+  o.max_blocks = d.max_blocks;
+  o.num_blocks = d.num_blocks;
+  o.B = d.B;
+  o.Hq = d.Hq;
+  o.Hkv = d.Hkv;
+  o.n_rep = n_rep;
+  o.n_hc = a.own_plan.n_hc;
+  o.nrep_cta = a.own_plan.nrep_cta;
+  o.units = a.own_plan.units;
+  o.max_kv_len = d.max_kv_len;
+  o.min_tiles = a.own_plan.min_tiles;
+  o.n_slots = n_slots;
+  o.qscale = p.qk_scale_log2;
+  o.status = p.status;
+  o.ml = p.ml;
+  o.part_o = p.part_o;
+  o.counts = listed ? reinterpret_cast<int32_t*>(ws + lay.off_counts) : nullptr;
+  o.wait_limit_ns = p.wait_limit_ns;
+  o.test_stall_ns = p.test_stall_ns;
+  GridPlan gp;
+  gp.units = a.plan.units;
+  gp.n_shared = a.plan.n_split * a.plan.units * d.Hkv;
+  // CTAs of the own rows: one for each SM that the last wave of the shared
+  // rows' CTAs leaves free, which begin a share's time ahead of the others
+  const int sms = std::max(1, device_sm_count()), own_ctas = listed ? sms : 0;
+  o.early = listed ? (sms - gp.n_shared % sms) % sms : 0;
+  o.late = own_ctas - o.early;
+  o.head_start = float(a.plan.share_us / own_tile_us(HD));
   static std::once_flag once;
   static cudaError_t cfg_err = cudaSuccess;
   std::call_once(once, [&] {
-    for (const void* k : {reinterpret_cast<const void*>(prefix_kernel<HD, false>),
-                          reinterpret_cast<const void*>(prefix_kernel<HD, true>)})
+    for (const void* k : {reinterpret_cast<const void*>(shared_prefix_kernel<HD, false>),
+                          reinterpret_cast<const void*>(shared_prefix_kernel<HD, true>)})
       if (cfg_err == cudaSuccess)
-        cfg_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+        cfg_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<HD>);
   });
   if (cfg_err != cudaSuccess) return cfg_err;
-  const dim3 grid(a.plan.n_split, a.plan.units, d.Hkv);
-  cudaError_t e = a.plan.units == a.plan.n_tiles
-                      ? launch_pdl(prefix_kernel<HD, true>, grid, dim3(NTHR), C::SMEM_BYTES, stream, tq, tk, tv, p)
-                      : launch_pdl(prefix_kernel<HD, false>, grid, dim3(NTHR), C::SMEM_BYTES, stream, tq, tk, tv, p);
-  if (e != cudaSuccess) return e;
-  int32_t* const counts = a.own_plan.fits ? reinterpret_cast<int32_t*>(ws + lay.off_counts) : nullptr;
-  if (a.own_plan.fits) {
-    e = launch_own_rows(d, a.own_plan, n_slots, p.ml, p.part_o, counts, stream);
-  } else {
+  auto kern = a.plan.units == a.plan.n_tiles ? shared_prefix_kernel<HD, true> : shared_prefix_kernel<HD, false>;
+  cudaError_t e = launch_pdl(kern, dim3(gp.n_shared + own_ctas), dim3(NTHR), kSmemBytes<HD>, stream, tq, tk, tv, tko,
+                             tvo, p, o, gp);
+  if (e == cudaSuccess && !listed) {
     DecodeArgs own = d;
     own.n_slots = n_slots;
     own.force_partial = 1;
@@ -704,7 +773,7 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   m.Hq = d.Hq;
   m.max_prefix = a.max_prefix;
   m.max_kv_len = d.max_kv_len;
-  m.counts = counts;
+  m.counts = o.counts;
   m.n_rep = n_rep;
   m.n_hc = a.own_plan.n_hc;
   m.nrep_cta = a.own_plan.nrep_cta;
@@ -723,10 +792,9 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
 
 // Row tiles and key shares.  A unit (a pair of row tiles, or the one tile of
 // a KV head) times a share is a CTA; one CTA fits an SM.  Of the share counts
-// the planner takes the one with the least estimated time, in iterations
-// (one KV tile of a unit): the waves of the grid times the iterations of a
-// share plus a CTA's set-up and epilogue, and the partial rows' way to memory
-// and back.
+// the planner takes the one with the least estimated time: the waves of the
+// grid times a share's time (start, its KV tiles, epilogue; measured, in us),
+// and the partial rows' way to memory and back.
 PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sms) {
   PrefixPlan p;
   const int n_rep = Hq / Hkv;
@@ -736,17 +804,18 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sm
   p.units = p.n_tiles == 1 ? 1 : (p.n_tiles + 1) / 2;
   const long units = long(p.units) * Hkv;
   const int tiles = (max_prefix + BN - 1) / BN;
-  constexpr double kSetup = 3.3;
-  // partials written and read, against the KV stream of one iteration
-  const double per_share = 2.0 * B * Hq * D * 4 / (double(num_sms) * 2 * BN * D * 2);
+  const double start = p.n_tiles == 1 ? 5.0 : 7.0;
+  const double per_tile = (p.n_tiles == 1 ? 1.5 : 1.65) * (D == 64 ? 0.6 : 1.0);
+  const double per_share = 2.0 * B * Hq * D * 4 / 5e6;  // partials written and read, at 5 TB/s
   double best = 0.0;
   p.n_split = 1;
   for (int n = 1; n <= std::min(tiles, 256); ++n) {
     const long waves = (units * n + num_sms - 1) / num_sms;
-    const double t = double(waves) * (kSetup + (tiles + n - 1) / n) + per_share * n;
+    const double share = start + per_tile * ((tiles + n - 1) / n), t = double(waves) * share + per_share * n;
     if (n == 1 || t < best - 1e-9) {
       best = t;
       p.n_split = n;
+      p.share_us = share;
     }
   }
   return p;
@@ -760,6 +829,22 @@ SharedPrefixLayout shared_prefix_layout(const SharedPrefixArgs& a) {
   l.off_counts = workspace_layout(d.B, d.Hq, d.Hkv, d.plan.n_hc, l.n_slots, d.D).total;
   l.total = l.off_counts + (a.own_plan.fits ? align256(sizeof(int32_t) * size_t(d.B) * a.own_plan.units) : 0);
   return l;
+}
+
+OwnRowsPlan own_rows_plan(int B, int Hq, int Hkv, int max_kv_len) {
+  OwnRowsPlan p;
+  const int n_rep = Hq / Hkv;
+  p.n_hc = (n_rep + 7) / 8;
+  p.nrep_cta = (n_rep + p.n_hc - 1) / p.n_hc;
+  p.units = Hkv * p.n_hc;
+  const int tiles = (max_kv_len - 1) / kOwnTile + 1;
+  p.fits = B <= kOwnMaxRequests && long(B) * p.units * (long(tiles) + kOwnLead) <= 0x7fffffffL / 5;
+  // A warp's range holds at least min_tiles tiles (but for the early CTAs'
+  // part where that is all of a range), so that a unit has at most
+  // (tiles - 2) / min_tiles + 3 partials: 34 or fewer.
+  p.min_tiles = std::max(2, (tiles + 31) / 32);
+  p.n_slots = tiles < 2 ? 1 : (tiles - 2) / p.min_tiles + 3;
+  return p;
 }
 
 cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, cudaStream_t stream) {

@@ -212,7 +212,7 @@ GQA_ATTN_API int gqa_attn_decode_paged(const void* q, const void* k_new, const v
  * A request with no key at all gets a zero row (GQA_DEV_EMPTY_REQUEST).
  * Rows past the lengths may hold anything, NaN included.  Three kernels run
  * (shared rows, own rows, merge).  dtype must be GQA_BF16 and Hq / Hkv at most
- * 128 (else GQA_ERR_UNSUPPORTED).  Workspace:
+ * 128 (else GQA_ERR_UNSUPPORTED); B * Hq <= 2^22.  Workspace:
  * gqa_attn_decode_shared_prefix_workspace_size, for both entry points.  Other
  * arguments and errors as for gqa_attn_decode.
  *

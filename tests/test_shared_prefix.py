@@ -49,7 +49,8 @@ GOOD = dict(B=2, Hq=8, Hkv=2, D=64, P_cap=100, maxp=100, S=50, L=50, scale=0.1, 
 @pytest.mark.parametrize("bad,rc", [
     (dict(B=0), -1), (dict(B=65536), -1), (dict(Hkv=3), -1), (dict(D=96), -1), (dict(maxp=0), -1), (dict(maxp=101), -1),
     (dict(L=0), -1), (dict(L=51), -1), (dict(scale=0.0), -1), (dict(scale=float("inf")), -1), (dict(dtype=5), -1),
-    (dict(P_cap=2 ** 31 - 1, maxp=2 ** 31 - 1), -1), (dict(dtype=0), -2), (dict(Hq=258, Hkv=2), -2),
+    (dict(P_cap=2 ** 31 - 1, maxp=2 ** 31 - 1), -1), (dict(B=65535, Hq=128, Hkv=64), -1),
+    (dict(dtype=0), -2), (dict(Hq=258, Hkv=2), -2),
 ])
 def test_dense_arguments_are_checked_on_the_host(lib, bad, rc):
     a = GOOD | bad
