@@ -24,6 +24,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include <array>
 #include <cmath>
 #include <mutex>
 
@@ -430,45 +431,56 @@ __global__ void __launch_bounds__(MmaCfg<D, NSTAGE, NW>::NTHR, 8 / NW)
   }
 }
 
-// Tensor maps of the K and V caches, [B*Hkv][S_cap][D] bf16 as a 3-D tensor
-// with 64-dim x box_rows boxes (64 rows here) and 128-byte swizzle.  Encoding one costs about
-// a microsecond of host time, so the maps of recently used caches are kept
-// (keyed by base address and shape; a map holds no data, only the layout).
-struct MapEntry {
-  const void* base;
-  int D, S_cap, heads, box_rows;
-  CUtensorMap map;
+// Encoding a tensor map costs about a microsecond of host time, so the maps of
+// recently used tensors are kept (keyed by base address and shape; a map holds
+// no data, only the layout).
+template <int N>
+struct MapCache {
+  struct Entry {
+    const void* base;
+    std::array<int, N> shape;
+    CUtensorMap map;
+  };
+  static constexpr int kEntries = 128;
+  std::mutex mu;
+  Entry entries[kEntries];
+  int used = 0, next = 0;
+
+  template <typename Encode>
+  bool get(CUtensorMap* out, const void* base, const std::array<int, N>& shape, Encode encode) {
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < used; ++i)
+      if (entries[i].base == base && entries[i].shape == shape) {
+        *out = entries[i].map;
+        return true;
+      }
+    CUtensorMap m;
+    if (!encode(&m)) return false;
+    entries[next] = Entry{base, shape, m};
+    next = (next + 1) % kEntries;
+    if (used < kEntries) ++used;
+    *out = m;
+    return true;
+  }
 };
-constexpr int kMapCache = 128;
 
 }  // namespace
 
-bool kv_map(CUtensorMap* out, const void* base, int D, int S_cap, int heads, int box_rows) {
-  static std::mutex mu;
-  static MapEntry cache[kMapCache];
-  static int used = 0, next = 0;
-  std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < used; ++i)
-    if (cache[i].base == base && cache[i].D == D && cache[i].S_cap == S_cap && cache[i].heads == heads &&
-        cache[i].box_rows == box_rows) {
-      *out = cache[i].map;
-      return true;
-    }
-  CUtensorMap m;
-  if (!encode_bf16_rows(&m, base, uint64_t(D), uint64_t(S_cap), uint64_t(S_cap), uint64_t(heads), 64,
-                        uint32_t(box_rows)))
-    return false;
-  MapEntry& e = cache[next];
-  e.base = base;
-  e.D = D;
-  e.S_cap = S_cap;
-  e.heads = heads;
-  e.box_rows = box_rows;
-  e.map = m;
-  next = (next + 1) % kMapCache;
-  if (used < kMapCache) ++used;
-  *out = m;
-  return true;
+// K and V caches, [heads][rows][D] bf16 as a 3-D tensor with 64-dim x box_rows
+// boxes (64 rows in the decode kernel) and 128-byte swizzle.
+bool kv_map(CUtensorMap* out, const void* base, int D, int rows, int heads, int box_rows) {
+  static MapCache<4> cache;
+  return cache.get(out, base, {D, rows, heads, box_rows}, [&](CUtensorMap* m) {
+    return encode_bf16_rows(m, base, uint64_t(D), uint64_t(rows), uint64_t(rows), uint64_t(heads), 64,
+                            uint32_t(box_rows));
+  });
+}
+
+bool query_map(CUtensorMap* out, const void* base, int D, int n_rep, int B, int Hkv, int rpt) {
+  static MapCache<5> cache;
+  return cache.get(out, base, {D, n_rep, B, Hkv, rpt}, [&](CUtensorMap* m) {
+    return encode_bf16_query_rows(m, base, D, n_rep, B, Hkv, rpt);
+  });
 }
 
 namespace {

@@ -173,19 +173,30 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const MergeParams p) 
 // once every CTA of the preceding grid in the stream has called
 // griddepcontrol.launch_dependents (or exited), and must itself call
 // griddepcontrol.wait before it touches memory that grid may write.
+// cluster > 1: blocks in clusters of that many along x (of which grid.x is a
+// multiple).
 template <typename Kern, typename... Args>
-cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const Args&... args) {
+cudaError_t launch_pdl_cluster(Kern kern, unsigned cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                               const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+template <typename Kern, typename... Args>
+cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const Args&... args) {
+  return launch_pdl_cluster(kern, 1u, grid, block, smem, stream, args...);
 }
 
 // The merge grid (one CTA per request and query head) overlaps the split

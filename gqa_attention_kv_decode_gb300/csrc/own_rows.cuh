@@ -53,8 +53,6 @@ struct OwnRowsParams {
   const int32_t* block_table;  // or null: dense [B][Hkv][S_cap][D]
   int block_size, max_blocks, num_blocks;
   int B, Hq, Hkv, n_rep, n_hc, nrep_cta, units, max_kv_len;
-  int early, late;  // CTAs that work on the own rows from the start; and after the shared rows
-  float head_start; // the former's lead, in tiles of a warp
   int min_tiles;    // tiles of a warp's range, at least
   int n_slots;    // partial slots of a row (the first ones are the own rows')
   float qscale;   // scale * log2(e)
@@ -114,7 +112,9 @@ struct OwnCfg {
   static constexpr int STAGEB = 2 * TILEB;
   static constexpr int NSTAGE = D == 128 ? 3 : 6;  // 24 KB a warp
   static constexpr int WARPB = NSTAGE * STAGEB;
-  static constexpr int OFF_BAR = kOwnWarps * WARPB;
+  // (behind the barriers of the shared rows' work, which a CTA may have set up
+  // before it learns that it has no part in it)
+  static constexpr int OFF_BAR = kOwnWarps * WARPB + 3072;
   static constexpr int OFF_SUM = OFF_BAR + kOwnWarps * (NSTAGE + 1) * 8;
   static constexpr int OFF_STARTS = OFF_SUM + kOwnWarps * 4;
   static constexpr int SMEM = OFF_STARTS + (kOwnMaxRequests + 1) * 4 + 1024;
@@ -172,11 +172,31 @@ __device__ __forceinline__ void own_scan(unsigned char* smem, const OwnRowsParam
   named_bar_sync(BAR_OWN, NTHREADS);
 }
 
-// The work of CTA `cta` of the p.early + p.late (the first p.early of them
-// early) on the own rows, by its first 256 threads, after own_scan.
+// Who works on the own rows: this is CTA `cta` of early + late ones, the first
+// of which begin with the grid, the others head_start later (in tiles of a warp).
+struct OwnRole {
+  int cta, early, late;
+  float head_start;
+};
+
+// Tiles of the whole list, by one warp.
+__device__ __forceinline__ int own_total(const OwnRowsParams& p) {
+  int sum = 0;
+#pragma unroll 4
+  for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+    const int raw = p.kv_lens != nullptr ? p.kv_lens[b] : p.max_kv_len, L = min(max(raw, 0), p.max_kv_len);
+    sum += L > 0 ? (L + kOwnTile - 1) / kOwnTile + kOwnLead : 0;
+  }
+  return __reduce_add_sync(0xffffffffu, sum) * p.units;
+}
+
+// The work of a CTA on the own rows, by its first 256 threads, after own_scan.
+// (CTAs of the shared rows that go on with this themselves were tried: inlined
+// behind the softmax loop it made that loop 10 % slower, out of line it got too
+// few registers.)
 template <int D>
 __device__ __forceinline__ void own_rows(unsigned char* smem, const CUtensorMap* tmK, const CUtensorMap* tmV,
-                                         const OwnRowsParams& p, int cta) {
+                                         const OwnRowsParams& p, const OwnRole& role) {
   using C = OwnCfg<D>;
   constexpr int NS = C::NSTAGE, TILE = C::TILE;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -188,12 +208,13 @@ __device__ __forceinline__ void own_rows(unsigned char* smem, const CUtensorMap*
   }
   const int N = starts[p.B];
   if (N == 0) return;
-  const OwnCut cut = OwnCut::of(unsigned(N), unsigned(p.early * kOwnWarps), unsigned(p.late * kOwnWarps), p.head_start,
+  const OwnCut cut = OwnCut::of(unsigned(N), unsigned(role.early * kOwnWarps), unsigned(role.late * kOwnWarps), role.head_start,
                                 unsigned(p.min_tiles));
   // this warp's range: neighbours in the list run on different SMs
-  const bool is_early = cta < p.early;
+  const bool is_early = role.cta < role.early;
   const OwnRanges& part = is_early ? cut.a : cut.b;
-  const unsigned w = is_early ? unsigned(warp * p.early + cta) : unsigned(warp * p.late + cta - p.early);
+  const unsigned w = is_early ? unsigned(warp * role.early + role.cta)
+                               : unsigned(warp * role.late + role.cta - role.early);
   if (w >= part.n) return;
   const int base = is_early ? 0 : int(cut.head);
   const int x0 = base + int(part.start(w)), x1 = base + int(part.start(w + 1));

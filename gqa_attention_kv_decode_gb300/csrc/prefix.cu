@@ -61,7 +61,7 @@ struct PxCfg {
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_P = P_ALIAS ? 0u : 384u;
   static constexpr uint32_t P_STRIDE = P_ALIAS ? 128u : 64u;
   // (the warps that issue the copies and products of two boxes a tile spill with 56)
-  static constexpr int REG_CTRL = HD == 64 ? 56 : 80, REG_SOFTMAX = HD == 64 ? 224 : 208;
+  static constexpr int REG_CTRL = HD == 64 ? 64 : 80, REG_SOFTMAX = HD == 64 ? 216 : 208;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + 2 * TILE_BYTES;
   static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
@@ -88,6 +88,7 @@ struct PrefixParams {
   int rpt;      // requests per row tile: 128 / n_rep
   int n_tiles;  // row tiles per KV head
   int n_split;  // shares of the keys, at most
+  int32_t* shares;  // (written) shares used, for the merge
   int slot0, n_slots;  // partial slots of a row: [slot0, slot0 + n_split) of n_slots
   const int32_t* block_table;  // [blocks of the prefix], or null: rows of a dense [Hkv][P_cap][D]
   int block_size, num_blocks;
@@ -97,12 +98,6 @@ struct PrefixParams {
   uint32_t* status;
   uint64_t wait_limit_ns, test_stall_ns;
 };
-
-// The keys are cut into min(n_split, KV tiles) shares.
-__host__ __device__ __forceinline__ int prefix_shares(int n_split, int prefix_len) {
-  const int tiles = (prefix_len + BN - 1) / BN;
-  return tiles < n_split ? tiles : n_split;
-}
 
 // Writes NC columns of this warp's 32 rows, held as 32 columns at a time in
 // registers (a thread owns a row), to global memory: through the warp's
@@ -133,13 +128,54 @@ __device__ __forceinline__ void store_rows(unsigned char* stage, float* out, lon
   }
 }
 
-// Which CTA of the grid this is: the first n_shared ones work on the shared
-// rows, (split, unit, KV head) with the split fastest, the rest on the own rows.
-// (CTAs of the shared rows that went on with the own ones themselves saved a
-// start, but the code behind the softmax loop made that loop 10 % slower.)
+// How the grid is shared out.  CTA x < n_cand may work on the shared rows:
+// (KV head, unit) = x % per_share, share x / per_share.  The own rows are cut
+// for sms CTAs: early ones, which begin with the grid, and late ones, which
+// follow on the SMs of the shared rows.
+//   adaptive   the kernel chooses the number of shares from the lengths.  The
+//              grid is sms CTAs, of which those without a share are early, and
+//              n_cand more for the late ones.
+//   otherwise  all shares are used (there are as many KV tiles); the grid is
+//              n_cand CTAs and, with own rows in the list, sms more, the first
+//              of them early, on SMs that (the last wave of) the former leaves.
 struct GridPlan {
-  int n_shared, units;
+  int n_cand, per_share, units, sms, early;
+  bool adaptive, listed;
+  // estimated times in us: a share's start and epilogue, its KV tile, a share's
+  // partials to the merge and back, an own-row tile on one SM's eight warps,
+  // the start of a CTA of own rows, and the same behind one of shared rows
+  float start, kv_tile, merge, own_tile, lead_in, follow;
 };
+
+// The time of the shared rows in n shares, and of everything: the SMs without
+// a share are at the own rows meanwhile, all of them afterwards.  (With a few
+// shares fewer than there are SMs both kinds of work run throughout, and HBM
+// has no idle time at the starts and ends of the shares: 64 requests behind
+// 32,768 rows, up to 1,024 own, 65.6 us with all SMs on the shared rows first.)
+__device__ __forceinline__ float share_time(const GridPlan& g, int n_kv, int n) {
+  return g.start + g.kv_tile * float((n_kv + n - 1) / n);
+}
+constexpr int kMaxShares = 1023;  // of an adaptive grid
+constexpr uint32_t kShareMask = 1023u;
+__device__ __forceinline__ int choose_shares(const GridPlan& g, int n_split, int P, int own_tiles) {
+  const int n_kv = (P + BN - 1) / BN, most = min(n_split, n_kv);
+  if (most <= 1) return most;
+  // The least time, of equal ones the fewest shares: positive floats order like
+  // their bits, of which the low ones make room for n.  (One integer reduction,
+  // whose result the compiler knows to be the same in all lanes: what follows
+  // from it stays in uniform registers, or the softmax loop spills.)
+  uint32_t best = 0xffffffffu;
+  for (int n = 1 + int(threadIdx.x & 31); n <= most; n += 32) {
+    const float share = share_time(g, n_kv, n), ctas = float(n * g.per_share);
+    const float own = own_tiles * g.own_tile, room = (share - g.lead_in) * (float(g.sms) - ctas);
+    // what of the own rows the free SMs do not get done follows on all
+    const float rest = own > room ? (own - room) / float(g.sms) + g.follow : 0.f;
+    // (a share is drawn out by its neighbours' traffic now and then: 1.1)
+    const float t = 1.1f * share + rest + g.merge * float(n);
+    best = min(best, (__float_as_uint(t) & ~kShareMask) | uint32_t(n));
+  }
+  return int(__reduce_min_sync(0xffffffffu, best) & kShareMask);
+}
 
 template <int HD>
 constexpr int kSmemBytes = PxCfg<HD>::SMEM_BYTES > OwnCfg<HD>::SMEM ? PxCfg<HD>::SMEM_BYTES : OwnCfg<HD>::SMEM;
@@ -150,8 +186,8 @@ template <int HD, bool SINGLE>
 __global__ void __launch_bounds__(NTHR, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKo,
-                         const __grid_constant__ CUtensorMap tmVo, const PrefixParams p, const OwnRowsParams own,
-                         const GridPlan grid) {
+                         const __grid_constant__ CUtensorMap tmVo, const PrefixParams p,
+                         const OwnRowsParams own, const GridPlan grid) {
   using C = PxCfg<HD>;
   constexpr int NBOX = C::NBOX, TILE_BYTES = C::TILE_BYTES, NST = C::NST;
   constexpr int OFF_Q = C::OFF_Q, OFF_K = C::OFF_K, OFF_V = C::OFF_V, OFF_BAR = C::OFF_BAR;
@@ -164,23 +200,10 @@ __global__ void __launch_bounds__(NTHR, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_launch_dependents();  // (the next grid's CTAs wait for this one themselves)
-  if (int(blockIdx.x) >= grid.n_shared) {
-    if (tid == 0) {
-      prefetch_tmap(&tmKo);
-      prefetch_tmap(&tmVo);
-    }
-    if (warp >= kOwnWarps) {  // gives its registers to the eight warps that work
-      set_max_regs_dec<C::REG_CTRL>();
-      return;
-    }
-    set_max_regs_inc<C::REG_SOFTMAX>();
-    grid_dependency_wait();
-    own_scan<HD>(smem, own, int(blockIdx.x) == grid.n_shared);
-    own_rows<HD>(smem, &tmKo, &tmVo, own, int(blockIdx.x) - grid.n_shared);
-    return;
-  }
-  const int split = int(blockIdx.x) % p.n_split, unit = int(blockIdx.x) / p.n_split % grid.units,
-            g = int(blockIdx.x) / p.n_split / grid.units;
+  const int cta = blockIdx.x;
+  const bool cand = cta < grid.n_cand;  // may have a share of the shared rows
+  const int split = cta / grid.per_share, unit = cta % grid.per_share % grid.units,
+            g = cta % grid.per_share / grid.units;
   const int tile0 = SINGLE ? unit : 2 * unit;
   const bool two = !SINGLE && tile0 + 1 < p.n_tiles;  // is there a tile B?
   const int q_rows = p.n_rep * p.rpt;                 // rows of a tile that are queries
@@ -189,11 +212,11 @@ __global__ void __launch_bounds__(NTHR, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + OFF_BAR + C::OFF_TSLOT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_BAR + C::OFF_ABORT);
 
-  if (warp == 9) {
+  if (cand && warp == 9) {
     tmem_alloc(tslot, TMEM_COLS);
     tmem_relinquish();
   }
-  if (tid == 256) {
+  if (cand && tid == 256) {
     for (int i = 0; i < C::N_BARS; ++i) {
       const bool per_warp = (i >= B_SC && i < B_O0);
       const bool both_pv = i >= B_VE && i < B_VE + NST;  // the two P.V warps
@@ -205,9 +228,13 @@ __global__ void __launch_bounds__(NTHR, 1)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
+  if (!cand && tid == 0) {
+    prefetch_tmap(&tmKo);
+    prefetch_tmap(&tmVo);
+  }
   // the last rows of a tile that hold no query (128 is no multiple of n_rep):
   // zeros, so that their scores are ordinary numbers
-  if (q_rows < BM) {
+  if (cand && q_rows < BM) {
     const int chunks = (BM - q_rows) * 8;
     for (int i = tid; i < 2 * NBOX * chunks; i += NTHR)
       *reinterpret_cast<uint4*>(smem + OFF_Q + (i / chunks) * BOX_BYTES + q_rows * 128 + (i % chunks) * 16) =
@@ -217,18 +244,52 @@ __global__ void __launch_bounds__(NTHR, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = cand ? *tslot : 0u;
   grid_dependency_wait();
 
-  int P = p.max_prefix;
-  if (p.prefix_len != nullptr) {
-    const int raw = *p.prefix_len;
-    P = min(max(raw, 0), p.max_prefix);
-    if (P != raw && tid == 0 && blockIdx.x == 0) atomicOr(p.status, GQA_DEV_KVLEN_CLAMPED);
+  // The length is asked for here, but a CTA that has no share whatever it is
+  // does not wait for it before its own first loads (volatile: the load stays
+  // where it is, its uses below).
+  int raw_prefix = p.max_prefix;
+  if (p.prefix_len != nullptr) asm volatile("ld.global.b32 %0, [%1];" : "=r"(raw_prefix) : "l"(p.prefix_len));
+  const bool direct = !cand && !grid.adaptive;
+  int P = 0, n_kv = 0, n_used = 0;
+  auto use_length = [&] {
+    P = min(max(raw_prefix, 0), p.max_prefix);
+    n_kv = (P + BN - 1) / BN;
+    n_used = min(p.n_split, n_kv);
+  };
+  if (!direct) {
+    use_length();
+    if (cta == 0 && tid == 0 && P != raw_prefix) atomicOr(p.status, GQA_DEV_KVLEN_CLAMPED);
+    if (grid.adaptive) n_used = choose_shares(grid, p.n_split, P, own_total(own));
+    if (cta == 0 && tid == 0) *p.shares = n_used;  // for the merge
   }
-  const int n_kv = (P + BN - 1) / BN, n_used = prefix_shares(p.n_split, P);
-  if (split >= n_used) {  // no share for this CTA
-    if (warp == 9) tmem_dealloc(tmem, TMEM_COLS);
+  bool at_own = !cand;
+  if (cand) at_own = split >= n_used;
+  if (at_own) {  // no share for this CTA: the own rows, if it has a part in them
+    if (cand && warp == 9) tmem_dealloc(tmem, TMEM_COLS);
+    OwnRole r;
+    if (grid.adaptive) {
+      r.late = n_used * grid.per_share;  // the CTAs at the shared rows
+      r.early = grid.sms - r.late;
+      r.cta = cta < grid.sms ? cta - r.late : r.early + cta - grid.sms;
+    } else {
+      r.early = grid.early;
+      r.late = grid.listed ? grid.sms - grid.early : 0;
+      r.cta = cand ? r.early + r.late : cta - grid.n_cand;
+    }
+    if (r.cta >= r.early + r.late) return;
+    if (warp >= kOwnWarps) {  // gives its registers to the eight warps that work
+      set_max_regs_dec<C::REG_CTRL>();
+      return;
+    }
+    set_max_regs_inc<C::REG_SOFTMAX>();
+    own_scan<HD>(smem, own, r.cta == 0);
+    if (direct) use_length();
+    r.head_start =
+        n_used > 0 ? (share_time(grid, n_kv, n_used) + grid.follow) / (grid.own_tile * kOwnWarps) : 0.f;
+    own_rows<HD>(smem, &tmKo, &tmVo, own, r);
     return;
   }
   const int j_lo = int(long(n_kv) * split / n_used), j_hi = int(long(n_kv) * (split + 1) / n_used);
@@ -340,12 +401,10 @@ __global__ void __launch_bounds__(NTHR, 1)
         cta_wait(&bars[B_VF + st], uint32_t(j / NST) & 1u, abort_flag, p.wait_limit_ns);
         if (j == j_zero) {
           unsigned char* vt = smem + OFF_V + st * TILE_BYTES;
-          const int r0 = P % BN, per_box = (BN - r0) * 8;
-          for (int i = t * 32 + lane; i < per_box * NBOX; i += 64) {
-            const int bx = i / per_box, k = i % per_box;
-            *reinterpret_cast<uint4*>(vt + bx * BOX_BYTES + (r0 + k / 8) * 128 + (k % 8) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
+#pragma unroll
+          for (int bx = 0; bx < NBOX; ++bx)  // (whole 128-byte rows: the swizzle stays inside a row)
+            for (int at = (P % BN) * 128 + (t * 32 + lane) * 16; at < BOX_BYTES; at += 64 * 16)
+              *reinterpret_cast<uint4*>(vt + bx * BOX_BYTES + at) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
           named_bar_sync(1, 64);  // both P.V warps are done clearing
         }
@@ -471,9 +530,15 @@ __global__ void __launch_bounds__(NTHR, 1)
     tc_fence_before();
     named_bar_sync(BAR_ILV, 256);  // both slots are done: every product has run, the K and V stages are free
     tc_fence_after();
-    const int b = (tile0 + (SINGLE ? 0 : t)) * p.rpt + r / p.n_rep;
-    const bool row_ok = r < q_rows && b < p.B && n_it > 0 && !*abort_flag;
-    const long prow = (long(b) * p.Hq + g * p.n_rep + r % p.n_rep) * p.n_slots + p.slot0 + split;
+    // (which rows these are is worked out again: kept through the loop, which
+    // uses nearly all of this warpgroup's registers, it would be spilled)
+    int cta_e;
+    asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(cta_e));
+    const int split_e = cta_e / grid.per_share, unit_e = cta_e % grid.per_share % grid.units,
+              g_e = cta_e % grid.per_share / grid.units, rows_e = p.n_rep * p.rpt;
+    const int b = (SINGLE ? unit_e : 2 * unit_e + t) * p.rpt + r / p.n_rep;
+    const bool row_ok = r < rows_e && b < p.B && n_it > 0 && !*abort_flag;
+    const long prow = (long(b) * p.Hq + g_e * p.n_rep + r % p.n_rep) * p.n_slots + p.slot0 + split_e;
     unsigned char* stage = smem + OFF_K + warp * (32 * HD * 4);
     if constexpr (SINGLE) {
       // The row has a state in both slots (slot 1 may have seen no KV tile):
@@ -484,7 +549,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       const float M = has1 ? fmaxf(x0.x, x1.x) : x0.x;
       const float w0 = x0.x == -INFINITY ? 0.f : x0.x == M ? 1.f : fast_exp2(x0.x - M);
       const float w1 = (!has1 || x1.x == -INFINITY) ? 0.f : x1.x == M ? 1.f : fast_exp2(x1.x - M);
-      const bool ok = r < q_rows && b < p.B && !*abort_flag;
+      const bool ok = r < rows_e && b < p.B && !*abort_flag;
       if (t == 0 && ok) p.ml[prow] = make_float2(M, w0 * x0.y + w1 * x1.y);
       store_rows<HD / 2>(stage, p.part_o, ok ? prow * HD + t * (HD / 2) : -1L, lane, [&](int cc, float (&o)[32]) {
         uint32_t a0[32], a1[32];
@@ -529,9 +594,9 @@ __global__ void __launch_bounds__(NTHR, 1)
 
 struct PrefixMergeParams {
   __nv_bfloat16* o;
-  const int32_t* prefix_len;  // or null: max_prefix
-  const int32_t* kv_lens;     // or null: max_kv_len
-  int rows, Hq, max_prefix, max_kv_len;
+  const int32_t* shares;   // shares of the shared keys
+  const int32_t* kv_lens;  // or null: max_kv_len
+  int rows, Hq, max_kv_len;
   // own keys, slots [0, n_own): counts[b][unit] of them, or (null)
   // min(n_own, ceil(L / chunk)) splits
   const int32_t* counts;
@@ -550,10 +615,10 @@ struct PrefixMergeParams {
 // each), and the first PS + PO partial rows, before it is known which of these
 // slots the row uses (the others are left out of the sums).  The order of the
 // sums is fixed.
-template <int D, int WPR>
-__global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixMergeParams p) {
+template <int D, int WPR, int PS, int PO, int MB>
+__global__ void __launch_bounds__(256, MB) prefix_merge_kernel(const PrefixMergeParams p) {
   constexpr int V = D / 32;  // columns per lane
-  constexpr int PS = WPR < 8 ? 8 : 4, PO = 4;  // (within the first 32 partials, whose weights the lanes hold)
+  // (PS and PO are within the first 32 partials, whose weights the lanes hold)
   static_assert(PS * WPR <= 32 && PO * WPR <= 32, "preloaded partials");
   using Vec = typename std::conditional<V == 4, float4, float2>::type;
   __shared__ float acc_s[WPR > 1 ? 8 : 1][D];
@@ -581,7 +646,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixMergePara
       if (part + k * WPR < p.n_own) xo[k] = load(po_own, part + k * WPR);
     const float2 none = make_float2(-INFINITY, 0.f);
     float2 ms = lane < p.n_split ? __ldcg(&ml_sh[lane]) : none, mo = lane < p.n_own ? __ldcg(&ml_own[lane]) : none;
-    int P = p.prefix_len != nullptr ? *p.prefix_len : p.max_prefix;
+    const int shares = *p.shares;
     const int raw = p.kv_lens != nullptr ? p.kv_lens[b] : p.max_kv_len, L = min(max(raw, 0), p.max_kv_len);
     int own;
     if (p.counts != nullptr) {
@@ -590,8 +655,6 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixMergePara
     } else {
       own = min(p.n_own, (L + p.chunk - 1) / p.chunk);
     }
-    P = min(max(P, 0), p.max_prefix);
-    const int shares = prefix_shares(p.n_split, P);
     if (own + shares == 0) {  // no key at all: zeros
       if (lane == 0 && part == 0) atomicOr(p.status, GQA_DEV_EMPTY_REQUEST);
     } else {
@@ -663,14 +726,17 @@ cudaError_t launch_prefix_merge(const PrefixMergeParams& m, cudaStream_t stream)
   auto go = [&](auto kern, int wpr) {
     return launch_pdl(kern, dim3((m.rows * wpr + 7) / 8), dim3(256), 0, stream, m);
   };
-  if (room >= 8) return go(prefix_merge_kernel<HD, 8>, 8);
-  if (room >= 4) return go(prefix_merge_kernel<HD, 4>, 4);
-  if (room >= 2) return go(prefix_merge_kernel<HD, 2>, 2);
-  return go(prefix_merge_kernel<HD, 1>, 1);
+  if (room >= 8) return go(prefix_merge_kernel<HD, 8, 4, 4, 1>, 8);
+  if (room >= 4) return go(prefix_merge_kernel<HD, 4, 8, 4, 1>, 4);
+  if (room >= 2) return go(prefix_merge_kernel<HD, 2, 8, 4, 1>, 2);
+  if (m.n_split > 4) return go(prefix_merge_kernel<HD, 1, 8, 4, 1>, 1);
+  // many rows, few partials each: as many warps as fit an SM
+  return go(prefix_merge_kernel<HD, 1, 4, 2, 4>, 1);
 }
 
-// A 16-key tile's time for one warp of the own rows when all SMs are at it.
-double own_tile_us(int D) { return D == 64 ? 0.75 : 1.45; }
+// A 16-key tile's time for one warp of the own rows while most SMs are at the
+// shared ones: an SM's copies take 54 GB/s then (1.4 us when all SMs copy).
+double own_tile_us(int D) { return D == 64 ? 0.6 : 1.0; }
 
 template <int HD>
 cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
@@ -680,7 +746,7 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   const bool paged = d.block_table != nullptr;
   CUtensorMap tq, tk, tv;
   const int heads = paged ? d.num_blocks * d.Hkv : d.Hkv, rows = paged ? d.block_size : a.P_cap;
-  if (!encode_bf16_query_rows(&tq, d.q, HD, n_rep, d.B, d.Hkv, a.plan.rpt) ||
+  if (!query_map(&tq, d.q, HD, n_rep, d.B, d.Hkv, a.plan.rpt) ||
       !kv_map(&tk, a.k_prefix, HD, rows, heads) || !kv_map(&tv, a.v_prefix, HD, rows, heads))
     return cudaErrorInvalidValue;
   CUtensorMap tko = tk, tvo = tv;  // the own rows, in boxes of their tile
@@ -702,6 +768,7 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   p.rpt = a.plan.rpt;
   p.n_tiles = a.plan.n_tiles;
   p.n_split = a.plan.n_split;
+  p.shares = reinterpret_cast<int32_t*>(ws + lay.off_counts);
   p.slot0 = n_own;
   p.n_slots = n_slots;
   p.block_table = a.prefix_table;
@@ -734,18 +801,24 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   o.status = p.status;
   o.ml = p.ml;
   o.part_o = p.part_o;
-  o.counts = listed ? reinterpret_cast<int32_t*>(ws + lay.off_counts) : nullptr;
+  o.counts = listed ? p.shares + 1 : nullptr;
   o.wait_limit_ns = p.wait_limit_ns;
   o.test_stall_ns = p.test_stall_ns;
-  GridPlan gp;
+  GridPlan gp = {};
   gp.units = a.plan.units;
-  gp.n_shared = a.plan.n_split * a.plan.units * d.Hkv;
-  // CTAs of the own rows: one for each SM that the last wave of the shared
-  // rows' CTAs leaves free, which begin a share's time ahead of the others
-  const int sms = std::max(1, device_sm_count()), own_ctas = listed ? sms : 0;
-  o.early = listed ? (sms - gp.n_shared % sms) % sms : 0;
-  o.late = own_ctas - o.early;
-  o.head_start = float(a.plan.share_us / own_tile_us(HD));
+  gp.per_share = a.plan.units * d.Hkv;
+  gp.n_cand = a.plan.n_split * gp.per_share;
+  gp.sms = std::max(1, device_sm_count());
+  gp.listed = listed;
+  gp.adaptive = listed && a.plan.adaptive;
+  gp.early = listed ? (gp.sms - gp.n_cand % gp.sms) % gp.sms : 0;
+  gp.start = float(a.plan.start_us);
+  gp.kv_tile = float(a.plan.tile_us);
+  gp.merge = float(a.plan.merge_us);
+  gp.own_tile = float(own_tile_us(HD)) / kOwnWarps;
+  gp.lead_in = 4.f;
+  gp.follow = 8.f;
+  const int n_ctas = gp.adaptive ? gp.sms + gp.n_cand : gp.n_cand + (listed ? gp.sms : 0);
   static std::once_flag once;
   static cudaError_t cfg_err = cudaSuccess;
   std::call_once(once, [&] {
@@ -756,8 +829,12 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   });
   if (cfg_err != cudaSuccess) return cfg_err;
   auto kern = a.plan.units == a.plan.n_tiles ? shared_prefix_kernel<HD, true> : shared_prefix_kernel<HD, false>;
-  cudaError_t e = launch_pdl(kern, dim3(gp.n_shared + own_ctas), dim3(NTHR), kSmemBytes<HD>, stream, tq, tk, tv, tko,
-                             tvo, p, o, gp);
+  // In clusters of two, which share a TPC: CTAs of the shared and of the own
+  // rows side by side compete for its way to L2 (96 CTAs with a share, 64
+  // requests behind 32,768 rows: those with such a neighbour took up to 60 us,
+  // the others 46).
+  cudaError_t e = launch_pdl_cluster(kern, 2u, dim3((n_ctas + 1) / 2 * 2), dim3(NTHR), kSmemBytes<HD>, stream, tq, tk,
+                                     tv, tko, tvo, p, o, gp);
   if (e == cudaSuccess && !listed) {
     DecodeArgs own = d;
     own.n_slots = n_slots;
@@ -767,11 +844,10 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   PrefixMergeParams m;
   m.o = static_cast<__nv_bfloat16*>(d.o);
-  m.prefix_len = a.prefix_len;
+  m.shares = p.shares;
   m.kv_lens = d.kv_lens;
   m.rows = d.B * d.Hq;
   m.Hq = d.Hq;
-  m.max_prefix = a.max_prefix;
   m.max_kv_len = d.max_kv_len;
   m.counts = o.counts;
   m.n_rep = n_rep;
@@ -791,10 +867,11 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
 }  // namespace
 
 // Row tiles and key shares.  A unit (a pair of row tiles, or the one tile of
-// a KV head) times a share is a CTA; one CTA fits an SM.  Of the share counts
-// the planner takes the one with the least estimated time: the waves of the
-// grid times a share's time (start, its KV tiles, epilogue; measured, in us),
-// and the partial rows' way to memory and back.
+// a KV head) times a share is a CTA; one CTA fits an SM.  A share's time is
+// its start and epilogue and its KV tiles (measured, in us); the partials of
+// every share go to memory and back (at 5 TB/s).  One wave of shares is cut by
+// the kernel (choose_shares) where it fills most SMs; more waves only where the units alone leave many
+// SMs without one and the waves' estimate is well below that of one.
 PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sms) {
   PrefixPlan p;
   const int n_rep = Hq / Hkv;
@@ -804,20 +881,31 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sm
   p.units = p.n_tiles == 1 ? 1 : (p.n_tiles + 1) / 2;
   const long units = long(p.units) * Hkv;
   const int tiles = (max_prefix + BN - 1) / BN;
-  const double start = p.n_tiles == 1 ? 5.0 : 7.0;
-  const double per_tile = (p.n_tiles == 1 ? 1.5 : 1.65) * (D == 64 ? 0.6 : 1.0);
-  const double per_share = 2.0 * B * Hq * D * 4 / 5e6;  // partials written and read, at 5 TB/s
-  double best = 0.0;
-  p.n_split = 1;
-  for (int n = 1; n <= std::min(tiles, 256); ++n) {
+  p.start_us = p.n_tiles == 1 ? 5.0 : 7.0;
+  p.tile_us = (p.n_tiles == 1 ? 1.5 : 1.8) * (D == 64 ? 0.6 : 1.0);
+  p.merge_us = 2.0 * B * Hq * D * 4 / 5e6;
+  auto time_of = [&](int n) {
     const long waves = (units * n + num_sms - 1) / num_sms;
-    const double share = start + per_tile * ((tiles + n - 1) / n), t = double(waves) * share + per_share * n;
-    if (n == 1 || t < best - 1e-9) {
-      best = t;
+    return double(waves) * (p.start_us + p.tile_us * ((tiles + n - 1) / n)) + p.merge_us * n;
+  };
+  const int one_wave = int(std::max(1L, std::min<long>({long(tiles), num_sms / units, long(kMaxShares)})));
+  p.n_split = 1;
+  double best = time_of(1);
+  for (int n = 2; n <= one_wave; ++n)
+    if (time_of(n) < best - 1e-9) {
+      best = time_of(n);
       p.n_split = n;
-      p.share_us = share;
     }
-  }
+  // Few CTAs: the own rows have most SMs to themselves, and the shares stay as
+  // planned (working them out again costs a microsecond at the start).
+  p.adaptive = units <= num_sms && 2 * units * p.n_split > num_sms;
+  best *= 0.85;
+  for (int n = one_wave + 1; n <= std::min(tiles, 256); ++n)
+    if (time_of(n) < best) {
+      best = time_of(n);
+      p.n_split = n;
+      p.adaptive = false;
+    }
   return p;
 }
 
@@ -827,7 +915,7 @@ SharedPrefixLayout shared_prefix_layout(const SharedPrefixArgs& a) {
   l.n_own = a.own_plan.fits ? a.own_plan.n_slots : d.plan.n_split;
   l.n_slots = l.n_own + a.plan.n_split;
   l.off_counts = workspace_layout(d.B, d.Hq, d.Hkv, d.plan.n_hc, l.n_slots, d.D).total;
-  l.total = l.off_counts + (a.own_plan.fits ? align256(sizeof(int32_t) * size_t(d.B) * a.own_plan.units) : 0);
+  l.total = l.off_counts + align256(sizeof(int32_t) * (1 + (a.own_plan.fits ? size_t(d.B) * a.own_plan.units : 0)));
   return l;
 }
 

@@ -76,5 +76,7 @@ inline bool encode_bf16_query_rows(CUtensorMap* map, const void* base, int cols,
 // The map of a K or V cache [heads][rows][D] with boxes of box_rows rows, kept
 // for recently used caches (decode_mma.cu).
 bool kv_map(CUtensorMap* out, const void* base, int D, int rows, int heads, int box_rows = 64);
+// The map of a step's queries (encode_bf16_query_rows), kept alike.
+bool query_map(CUtensorMap* out, const void* base, int D, int n_rep, int B, int Hkv, int rpt);
 
 }  // namespace gqa
