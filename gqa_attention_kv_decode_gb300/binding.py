@@ -3,7 +3,8 @@
 The functions named like the C entry points take torch tensors, check that
 they are dense (the C ABI cannot see strides), pass ``data_ptr()`` values,
 sizes and the CUDA stream handle, and raise ``GqaAttnError`` on a non-zero
-status.  Every step of the computation runs in the library's kernels; there
+status.  The calls of a serving step around the attention, which pass many
+small tensors, do this natively (``csrc/torch_call.cpp``).  Every step of the computation runs in the library's kernels; there
 is no Python or CPU implementation behind these names.  If the library has
 not been built, the first call raises instead of falling back to anything.
 """
@@ -71,7 +72,6 @@ EXPORTED = (
 )
 
 _lib = None
-_I32 = torch.int32
 
 
 class GqaAttnError(RuntimeError):
@@ -177,33 +177,22 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _heads(t, T, H, D):
-    """Pointer and token stride (elements) of a [T, H, D] tensor whose heads
-    are dense; the tokens may be further apart (views of one projection)."""
-    if t.shape != (T, H, D):
-        raise ValueError("q is [T, Hq, D], k and v are [T, Hkv, D]")
-    st, sh, sd = t.stride()
-    if sd != 1 or (sh != D and H > 1):
-        raise ValueError("the heads of a token must be contiguous")
-    return t.data_ptr(), (st if T > 1 else H * D)
+_call_mod = None
 
 
-def _ints(t, n):
-    """Pointer of a dense int32 tensor of n entries; None stays None."""
-    if t is None:
-        return None
-    if t.dtype is not _I32:
-        raise TypeError("lengths, tables, positions and slots are int32")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"a contiguous int32 tensor of {n} entries is needed, got {tuple(t.shape)}")
-    return t.data_ptr()
+def _call():
+    """The native half of this module (csrc/torch_call.cpp): checks the tensors
+    of the serving-step calls and passes them on."""
+    global _call_mod
+    if _call_mod is None:
+        lib()  # (raises if nothing has been built)
+        from . import _torch_call
+        _call_mod = _torch_call
+    return _call_mod
 
 
-def _one_dtype(first, *tensors):
-    dt = first.dtype
-    for t in tensors:
-        if t is not None and t.dtype is not dt:
-            raise TypeError("the tensors of a call have one dtype")
+def _handle(stream):
+    return None if stream is None else _stream(stream)  # None: the current stream, read natively
 
 
 def _stream(stream):
@@ -335,20 +324,8 @@ def gqa_attn_decode_shared_prefix(q, k_prefix, v_prefix, prefix_len, k, v, kv_le
     """q, o [B,Hq,1,D]; k_prefix, v_prefix [Hkv,P_cap,D] shared by the batch,
     prefix_len int32 [1] or None; k, v [B,Hkv,S_cap,D] own rows behind them,
     kv_lens int32 [B] or None."""
-    B, Hq, Tq, D = q.shape
-    Hkv, P_cap = k_prefix.shape[0], k_prefix.shape[1]
-    S_cap = k.shape[2]
-    if Tq != 1:
-        raise ValueError("decode takes one query row per request")
-    if k.shape != (B, Hkv, S_cap, D) or v.shape != k.shape or v_prefix.shape != (Hkv, P_cap, D) \
-            or k_prefix.shape[2] != D or o.shape != q.shape:
-        raise ValueError("k_prefix and v_prefix are [Hkv, P_cap, D], k and v [B, Hkv, S_cap, D], o as q")
-    _one_dtype(q, k_prefix, v_prefix, k, v, o)
-    rc = lib().gqa_attn_decode_shared_prefix(
-        _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ints(prefix_len, 1), _ptr(k), _ptr(v), _ints(kv_lens, B), _ptr(o),
-        B, Hq, Hkv, D, P_cap, P_cap if max_prefix_len is None else int(max_prefix_len), S_cap,
-        S_cap if max_kv_len is None else int(max_kv_len), float(scale), _dtype_code(q), _ptr(workspace),
-        workspace.nbytes, _stream(stream))
+    rc = _call().decode_shared_prefix(q, k_prefix, v_prefix, prefix_len, k, v, kv_lens, o, scale, workspace,
+                                      max_prefix_len, max_kv_len, _handle(stream))
     _check(rc, "gqa_attn_decode_shared_prefix")
 
 
@@ -357,19 +334,8 @@ def gqa_attn_decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, prefix_
     """q, o [B,Hq,1,D]; k_pool, v_pool [num_blocks,Hkv,block_size,D]; the shared
     rows' blocks prefix_table int32 [blocks] (prefix_len int32 [1] rows, or
     None: max_prefix_len), the own rows' block_table int32 [B,max_blocks]."""
-    B, Hq, Tq, D = q.shape
-    num_blocks, Hkv, block_size = k_pool.shape[0], k_pool.shape[1], k_pool.shape[2]
-    if Tq != 1:
-        raise ValueError("decode takes one query row per request")
-    if v_pool.shape != k_pool.shape or k_pool.shape[3] != D or o.shape != q.shape:
-        raise ValueError("k_pool and v_pool are [blocks, Hkv, block_size, D], o as q")
-    n_prefix, max_blocks = prefix_table.shape[0], block_table.shape[1]
-    _one_dtype(q, k_pool, v_pool, o)
-    rc = lib().gqa_attn_decode_shared_prefix_paged(
-        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ints(prefix_table, n_prefix), _ints(prefix_len, 1),
-        _ints(block_table, B * max_blocks), _ints(kv_lens, B), _ptr(o), B, Hq, Hkv, D, block_size, num_blocks,
-        n_prefix, max_blocks, int(max_prefix_len), int(max_kv_len), float(scale), _dtype_code(q), _ptr(workspace),
-        workspace.nbytes, _stream(stream))
+    rc = _call().decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, prefix_len, block_table, kv_lens, o, scale,
+                                            workspace, max_prefix_len, max_kv_len, _handle(stream))
     _check(rc, "gqa_attn_decode_shared_prefix_paged")
 
 
@@ -379,16 +345,9 @@ def gqa_attn_step_tables(prior_lens, new_lens, block_table, free_blocks, free_co
     grown in place from the stack free_blocks [num_blocks] (or both, and the
     counts, None for a dense cache of block_size rows a request); writes
     kv_lens, q_lens [B], q_starts [B+1], positions, slots, q_slots [T]."""
-    B, T = prior_lens.numel(), positions.numel()
-    max_blocks = num_blocks = 0
-    if block_table is not None:
-        max_blocks = block_table.shape[1]
-        num_blocks = 0 if free_blocks is None else free_blocks.numel()
-    rc = lib().gqa_attn_step_tables(
-        _ints(prior_lens, B), _ints(new_lens, B), _ints(block_table, B * max_blocks), _ints(free_blocks, num_blocks),
-        _ints(free_count, 1), _ints(kv_lens, B), _ints(q_lens, B), _ints(q_starts, B + 1), _ints(positions, T),
-        _ints(slots, T), _ints(q_slots, T), _ints(free_count_out, 1), B, T, int(block_size), num_blocks, max_blocks,
-        int(q_rows), _ptr(workspace), workspace.nbytes, _stream(stream))
+    rc = _call().step_tables(prior_lens, new_lens, block_table, free_blocks, free_count, kv_lens, q_lens, q_starts,
+                             positions, slots, q_slots, free_count_out, block_size, q_rows, workspace,
+                             _handle(stream))
     _check(rc, "gqa_attn_step_tables")
 
 
@@ -398,29 +357,8 @@ def gqa_attn_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, s
     k_weight [D] or None) and rotated (cos_sin fp32 [max_pos,rot_dim] or None)
     into q_out [q_groups,Hq,q_rows,D] rows q_slots (None: row t) and k_cache,
     v_cache [num_blocks,Hkv,block_size,D] rows slots; negative slots: padding."""
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    q_groups, hq, q_rows, dq = q_out.shape
-    num_blocks, hk, block_size, dk = k_cache.shape
-    if hq != Hq or dq != D or hk != Hkv or dk != D or v_cache.shape != k_cache.shape:
-        raise ValueError("q_out is [groups, Hq, q_rows, D], k_cache and v_cache [blocks, Hkv, block_size, D]")
-    _one_dtype(q, k, v, q_weight, k_weight, q_out, k_cache, v_cache)
-    for w in (q_weight, k_weight):
-        if w is not None and w.numel() != D:
-            raise ValueError("the norm weights have D entries")
-    max_pos = rot_dim = 0
-    if cos_sin is None:
-        positions = None  # nothing rotates
-    else:
-        if cos_sin.dtype != torch.float32 or positions is None:
-            raise TypeError("cos_sin is float32 and needs positions")
-        max_pos, rot_dim = cos_sin.shape
-    (qp, qs), (kp, ks), (vp, vs) = _heads(q, T, Hq, D), _heads(k, T, Hkv, D), _heads(v, T, Hkv, D)
-    rc = lib().gqa_attn_rope_append(
-        qp, kp, vp, qs, ks, vs, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), _ints(positions, T),
-        _ints(slots, T), _ints(q_slots, T), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), T, Hq, Hkv, D, rot_dim,
-        max_pos, 1 if adjacent else 0, num_blocks, block_size, q_groups, q_rows, _dtype_code(q), _ptr(workspace),
-        workspace.nbytes, _stream(stream))
+    rc = _call().rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, slots, q_slots, q_out, k_cache,
+                             v_cache, adjacent, workspace, _handle(stream))
     _check(rc, "gqa_attn_rope_append")
 
 

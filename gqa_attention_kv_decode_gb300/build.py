@@ -1,8 +1,10 @@
-"""Builds libgqa_attn.so in-tree with nvcc for sm_103a.
+"""Builds libgqa_attn.so in-tree with nvcc for sm_103a, and the native half of
+the Python binding.
 
-Each translation unit under csrc/ is compiled by its own nvcc process (in
+Each CUDA translation unit under csrc/ is compiled by its own nvcc process (in
 parallel) and the objects are linked into ``libgqa_attn.so`` next to this
-file.  Nothing is installed anywhere else.
+file; ``csrc/torch_call.cpp`` becomes the extension module ``_torch_call.so``
+beside it.  Nothing is installed anywhere else.
 
     python -m gqa_attention_kv_decode_gb300.build [--force] [--verbose]
 """
@@ -15,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgqa_attn.so")
+CALL = os.path.join(PKG, "_torch_call.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -39,15 +43,34 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _host_compile(obj):
+    """The command that compiles csrc/torch_call.cpp (host code, torch headers)."""
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-isystem", inc, "-isystem",
+            os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
+            "-isystem", cuda, "-c", os.path.join(CSRC, "torch_call.cpp"), "-o", obj]
+
+
+def _host_link(obj, out):
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-shared", "-o", out, obj, "-L", PKG, "-lgqa_attn", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10",
+            "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
+    return _sources() + [os.path.join(CSRC, "torch_call.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
         + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -67,6 +90,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    call_obj = os.path.join(BUILD, "torch_call.o")
+    cmd = _host_compile(call_obj)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    procs.append(("torch_call.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                                                     text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -75,13 +104,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError("nvcc failed on: " + ", ".join(os.path.basename(f) for f in failed))
+        raise RuntimeError("the compiler failed on: " + ", ".join(os.path.basename(f) for f in failed))
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    tmp = CALL + ".tmp"
+    cmd = _host_link(call_obj, tmp)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, CALL)
     return LIB
 
 
