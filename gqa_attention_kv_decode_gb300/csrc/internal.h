@@ -204,6 +204,7 @@ struct StepTablesArgs {
   int32_t* free_count_out;
   int B, T, block_size, num_blocks, max_blocks, q_rows;
   uint32_t* status;
+  bool tokens_apart = false;  // the tokens are another kernel's
 };
 cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream);
 
