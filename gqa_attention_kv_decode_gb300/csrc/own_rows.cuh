@@ -114,7 +114,7 @@ struct OwnCfg {
   static constexpr int WARPB = NSTAGE * STAGEB;
   // (behind the barriers of the shared rows' work, which a CTA may have set up
   // before it learns that it has no part in it)
-  static constexpr int OFF_BAR = kOwnWarps * WARPB + 3072;
+  static constexpr int OFF_BAR = kOwnWarps * WARPB + 4096;
   static constexpr int OFF_SUM = OFF_BAR + kOwnWarps * (NSTAGE + 1) * 8;
   static constexpr int OFF_STARTS = OFF_SUM + kOwnWarps * 4;
   static constexpr int SMEM = OFF_STARTS + (kOwnMaxRequests + 1) * 4 + 1024;

@@ -179,6 +179,8 @@ __device__ __forceinline__ int choose_shares(const GridPlan& g, int n_split, int
 
 template <int HD>
 constexpr int kSmemBytes = PxCfg<HD>::SMEM_BYTES > OwnCfg<HD>::SMEM ? PxCfg<HD>::SMEM_BYTES : OwnCfg<HD>::SMEM;
+static_assert(PxCfg<64>::OFF_ML + 2048 <= OwnCfg<64>::OFF_BAR && PxCfg<128>::OFF_ML + 2048 <= OwnCfg<128>::OFF_BAR,
+              "the own rows' barriers lie behind those of the shared rows");
 
 // SINGLE: one row tile per CTA, its even KV tiles in slot 0 and the odd ones
 // in slot 1; otherwise tiles A and B (slots 0 and 1) over the same KV tiles.

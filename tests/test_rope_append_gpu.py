@@ -163,6 +163,37 @@ def test_many_tokens_of_wide_heads():
     check(Case(2001, 32, 8, 128, torch.bfloat16, q_rows=512, bs=64, seed=4, pad=17))
 
 
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,T", [(torch.bfloat16, 32, 8, 128, 1500), (torch.bfloat16, 14, 2, 64, 4001),
+                                              (torch.float32, 28, 4, 128, 1300), (torch.float32, 9, 3, 64, 3000),
+                                              (torch.bfloat16, 7, 7, 64, 4000), (torch.bfloat16, 16, 1, 128, 2500),
+                                              (torch.float32, 64, 16, 128, 600), (torch.bfloat16, 96, 96, 128, 200)])
+@pytest.mark.parametrize("kind", ["half", "adjacent", "part", "plain", "one-norm"])
+def test_many_tokens_of_every_kind(dtype, Hq, Hkv, D, T, kind):
+    """Steps of several waves of blocks, and, at the smallest head counts, of one
+    pass of heads a warp."""
+    kw = {"half": {}, "adjacent": dict(adjacent=True), "part": dict(rot=48, pad=T // 3, gap=64, q_rows=100),
+          "plain": dict(rot=0, norm="", identity_q=True), "one-norm": dict(norm="k", rot=D - 16, adjacent=True)}[kind]
+    check(Case(T, Hq, Hkv, D, dtype, bs=64, seed=20, **kw))
+
+
+def test_many_tokens_with_bad_places():
+    c = Case(3000, 14, 2, 64, torch.bfloat16, bs=64, seed=21, pad=100)
+    c.pos[5], c.pos[2999], c.slots[700], c.q_slots[701] = -1, 5000, 2 ** 31 - 1, c.q_out.shape[0] * c.q_out.shape[2]
+    check(c)
+
+
+def test_many_padding_tokens():
+    """Runs of padding that leave whole blocks with nothing to do."""
+    c = Case(40000, 2, 2, 64, torch.bfloat16, bs=64, seed=22)
+    c.slots[100:39000] = -1
+    c.q_slots[90:39500] = -1
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    qo, kc, vc, _ = c.oracle()
+    c.call(ws)
+    np.testing.assert_array_equal(f64(c.vc), vc)
+    assert np.abs(f64(c.q_out) - qo).max() <= 2.0 ** -8 * np.abs(qo).max() + 76 * U * 20
+
+
 @pytest.mark.parametrize("gap", [8, 64])
 def test_token_strides(gap):
     check(Case(33, 14, 2, 64, torch.bfloat16, gap=gap, seed=5))
