@@ -4,9 +4,10 @@ The functions named like the C entry points take torch tensors, check that
 they are dense (the C ABI cannot see strides), pass ``data_ptr()`` values,
 sizes and the CUDA stream handle, and raise ``GqaAttnError`` on a non-zero
 status.  The calls of a serving step around the attention, which pass many
-small tensors, do this natively (``csrc/torch_call.cpp``).  Every step of the computation runs in the library's kernels; there
-is no Python or CPU implementation behind these names.  If the library has
-not been built, the first call raises instead of falling back to anything.
+small tensors, do this natively (``csrc/torch_call.cpp``).  Every step of the
+computation runs in the library's kernels; there is no Python or CPU
+implementation behind these names.  If the library has not been built, the
+first call raises instead of falling back to anything.
 """
 
 from __future__ import annotations

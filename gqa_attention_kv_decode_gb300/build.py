@@ -63,7 +63,8 @@ def _host_link(obj, out):
 
 
 def _deps():
-    return _sources() + [os.path.join(CSRC, "torch_call.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
+    return _sources() + [os.path.join(CSRC, "torch_call.cpp")] \
+        + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
         + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 

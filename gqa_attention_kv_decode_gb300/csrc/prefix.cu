@@ -17,10 +17,10 @@
 //                  than 1,024 requests: the decode kernel takes the own rows,
 //                  in a launch of its own);
 //   prefix_merge   log-sum-exp merge of a row's partials of both.
-// Inside a CTA of the shared rows the roles, the tensor-memory layout and the softmax are the
-// prefill kernel's: warp 8 TMA, warp 9 issues S, warps 10 and 11 issue P V,
-// warpgroups 0 and 1 do the softmax of one row per thread with a lazily
-// raised reference.  There is no diagonal: only the last KV tile is masked.
+// Inside a CTA of the shared rows the roles, the tensor-memory layout and the
+// softmax are the prefill kernel's: warp 8 TMA, warp 9 issues S, warps 10 and
+// 11 issue P V, warpgroups 0 and 1 do the softmax of one row per thread with a
+// lazily raised reference.  There is no diagonal: only the last KV tile is masked.
 //
 // What bounds it: a KV tile of 128 keys is 64 KB (D = 128) and two M = 128
 // row tiles on it cost 16.8 MFLOP, 250 FLOP a byte -- about this chip's ratio
@@ -648,12 +648,14 @@ __global__ void __launch_bounds__(256, MB) prefix_merge_kernel(const PrefixMerge
       if (part + k * WPR < p.n_own) xo[k] = load(po_own, part + k * WPR);
     const float2 none = make_float2(-INFINITY, 0.f);
     float2 ms = lane < p.n_split ? __ldcg(&ml_sh[lane]) : none, mo = lane < p.n_own ? __ldcg(&ml_own[lane]) : none;
-    const int shares = *p.shares;
+    const int shares = min(max(*p.shares, 0), p.n_split);
     const int raw = p.kv_lens != nullptr ? p.kv_lens[b] : p.max_kv_len, L = min(max(raw, 0), p.max_kv_len);
     int own;
     if (p.counts != nullptr) {
       const int u = h / p.n_rep * p.n_hc + h % p.n_rep / p.nrep_cta, count = p.counts[b * p.units + u];
-      own = L > 0 ? count : 0;  // (a unit without keys has no count written)
+      // (a unit without keys has no count written; nor has one whose warp gave
+      // up on a copy: whatever stands there, no slot past the row's is read)
+      own = L > 0 ? min(max(count, 0), p.n_own) : 0;
     } else {
       own = min(p.n_own, (L + p.chunk - 1) / p.chunk);
     }
@@ -872,8 +874,9 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
 // a KV head) times a share is a CTA; one CTA fits an SM.  A share's time is
 // its start and epilogue and its KV tiles (measured, in us); the partials of
 // every share go to memory and back (at 5 TB/s).  One wave of shares is cut by
-// the kernel (choose_shares) where it fills most SMs; more waves only where the units alone leave many
-// SMs without one and the waves' estimate is well below that of one.
+// the kernel (choose_shares) where it fills most SMs; more waves only where the
+// units alone leave many SMs without one and the waves' estimate is well below
+// that of one.
 PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sms) {
   PrefixPlan p;
   const int n_rep = Hq / Hkv;

@@ -210,8 +210,10 @@ GQA_ATTN_API int gqa_attn_decode_paged(const void* q, const void* k_new, const v
  *   max_prefix_len, max_kv_len   host bounds, at least 1 and at most P_cap and
  *                 S_cap; they size the grids and the workspace
  * A request with no key at all gets a zero row (GQA_DEV_EMPTY_REQUEST).
- * Rows past the lengths may hold anything, NaN included.  Three kernels run
- * (shared rows, own rows, merge).  dtype must be GQA_BF16 and Hq / Hkv at most
+ * Rows past the lengths may hold anything, NaN included.  Two kernels run
+ * (shared and own rows, then a merge; three for more than 1,024 requests).
+ * With rotated keys an own row's position counts the shared rows before it:
+ * P + its row.  dtype must be GQA_BF16 and Hq / Hkv at most
  * 128 (else GQA_ERR_UNSUPPORTED); B * Hq <= 2^22.  Workspace:
  * gqa_attn_decode_shared_prefix_workspace_size, for both entry points.  Other
  * arguments and errors as for gqa_attn_decode.

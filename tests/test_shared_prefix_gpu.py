@@ -346,6 +346,25 @@ def test_a_lost_copy_is_reported_and_the_next_call_is_right(Hq, Hkv, D, B, paged
     assert binding.gqa_attn_read_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("fill", [0x7F, 0xFF])
+@pytest.mark.parametrize("Hq,Hkv,D,B", [(14, 2, 64, 4), (32, 8, 128, 80)])
+def test_a_lost_copy_in_a_workspace_that_held_something_else(Hq, Hkv, D, B, fill):
+    """The counts of partials that a lost copy leaves unwritten are not trusted."""
+    c = Case(B, Hq, Hkv, D, 300, lens_of(B, 100))
+    ws = binding.decode_shared_prefix_workspace(B, Hq, Hkv, D, 300, 100)
+    ws[256:] = fill
+    binding.gqa_attn_set_wait_test(200_000)
+    try:
+        c.dense(workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        binding.gqa_attn_set_wait_test(0)
+    assert binding.gqa_attn_read_device_status(ws) & binding.GQA_DEV_WAIT_TIMEOUT
+    binding.gqa_attn_clear_device_status(ws)
+    parity.check(f64(c.dense(workspace=ws)), c.oracle(), "bf16")
+    assert binding.gqa_attn_read_device_status(ws) == 0
+
+
 # ------------------------------------------------ refusals
 
 @pytest.mark.parametrize("name", ["q", "k_prefix", "v_prefix", "prefix_len", "k", "v", "kv_lens", "o", "workspace"])
