@@ -889,6 +889,50 @@ def _case_inputs(name, device):
         nbytes = NL * metrics.decode_bytes(HQ, HKV, D, [S_HEAD], 4)
         return (lambda st: binding_mod().gqa_attn_decode_layers(q, k, v, o, None, D ** -0.5, ws, max_kv_len=S_HEAD,
                                                                 stream=st)), nbytes, "bytes"
+    if name.startswith("decode-shared-prefix-"):
+        # a shared prompt, and own rows of lengths up to 1,024 (B = 64) or 512
+        n, p_len = (int(x[1:]) for x in name.split("-")[3:])
+        own = 1024 if n == 64 else 512
+        lens = inputs.ragged_kv_lens(n, 1, own, seed=inputs.BASE_SEED + n)
+        lens_t = torch.from_numpy(lens).to(device)
+        q, k, v = inputs.qkv(n, 32, 8, 128, 1, own, torch.bfloat16, device=device)
+        kp = inputs.randn((8, p_len, 128), inputs.tensor_seed(1, 1), torch.bfloat16, device)
+        vp = inputs.randn((8, p_len, 128), inputs.tensor_seed(1, 2), torch.bfloat16, device)
+        o = torch.empty_like(q)
+        ws = binding_mod().decode_shared_prefix_workspace(n, 32, 8, 128, p_len, own, device)
+        nbytes = metrics.decode_bytes(32, 8, 128, lens, 2) + 2 * kp.numel() * 2
+        return (lambda st: binding_mod().gqa_attn_decode_shared_prefix(q, kp, vp, None, k, v, lens_t, o, 128 ** -0.5,
+                                                                       ws, stream=st)), nbytes, "bytes"
+    if name == "prefill-rope-append-T16384":
+        # the projections of 32 chunks of 512 tokens into their queries and a paged cache
+        n, hq, hkv, hd, bs = 16384, 32, 8, 128, 64
+        x = inputs.randn((n, (hq + 2 * hkv) * hd), inputs.tensor_seed(0, 0), torch.bfloat16, device)
+        q, k, v = (y.unflatten(1, (-1, hd)) for y in x.split([hq * hd, hkv * hd, hkv * hd], dim=1))
+        wq, wk = (inputs.randn((hd,), inputs.tensor_seed(0, i), torch.bfloat16, device) for i in (1, 2))
+        blocks = torch.from_numpy(np.random.default_rng(0).permutation(n // bs)).to(device)
+        slots = (blocks[:, None] * bs + torch.arange(bs, device=device)).flatten().int()
+        pos, rows = torch.arange(n, device=device).int() % 512, torch.arange(n, device=device).int()
+        q_out = torch.empty((n // 512, hq, 512, hd), dtype=torch.bfloat16, device=device)
+        kc, vc = (torch.empty((n // bs, hkv, bs, hd), dtype=torch.bfloat16, device=device) for _ in range(2))
+        cs = binding_mod().rope_table(512, hd, device=device)
+        ws = torch.zeros(256, dtype=torch.uint8, device=device)
+        nbytes = 2 * x.numel() * 2 + 512 * hd * 4 + 3 * n * 4
+        return (lambda st: binding_mod().gqa_attn_rope_append(q, k, v, wq, wk, 1e-6, cs, pos, slots, rows, q_out, kc,
+                                                              vc, False, ws, stream=st)), nbytes, "bytes"
+    if name == "decode-step-tables-B256":
+        # a token more for every request, each at the border of a block
+        n, bs, mb = 256, 64, 64
+        lens = torch.full((n,), 640, dtype=torch.int32, device=device)
+        one = torch.ones(n, dtype=torch.int32, device=device)
+        table = torch.arange(n * mb, dtype=torch.int32, device=device).reshape(n, mb)
+        stack = torch.arange(n * mb, dtype=torch.int32, device=device)
+        count = torch.full((1,), n * mb, dtype=torch.int32, device=device)
+        kv, ql, pos, slots, rows = (torch.empty(n, dtype=torch.int32, device=device) for _ in range(5))
+        starts, left = (torch.empty(m, dtype=torch.int32, device=device) for m in (n + 1, 1))
+        ws = torch.zeros(256, dtype=torch.uint8, device=device)
+        nbytes = 4 * (n * 2 + n * 7 + 2)  # (lengths read; six arrays and a block id of each written)
+        return (lambda st: binding_mod().gqa_attn_step_tables(lens, one, table, stack, count, kv, ql, starts, pos, slots,
+                                                              rows, left, bs, 1, ws, stream=st)), nbytes, "bytes"
     if name.startswith("prefill-"):
         # prefill-T4097, prefill-q512-kv4096 (Qwen2.5-0.5B heads, D=64) or
         # prefill-d128-T4097 (Qwen2.5-7B heads, D=128)
@@ -914,7 +958,9 @@ KERNEL_CASES = ("decode-f32-S32768", "decode-bf16-S32768", "decode-bf16-ragged-B
                 "q4-B4-S16384", "quantize-B4-S16384",
                 "prefill-T4097", "prefill-T16384", "prefill-q512-kv4096", "varlen-prefill-B16",
                 "prefill-d128-T4097", "prefill-d128-T16384",
-                "decode-f32-layers8-S32768")
+                "decode-f32-layers8-S32768",
+                "decode-shared-prefix-B64-P32768", "decode-shared-prefix-B256-P16384", "prefill-rope-append-T16384",
+                "decode-step-tables-B256")
 
 
 def binding_mod():
