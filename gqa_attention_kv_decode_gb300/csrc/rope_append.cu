@@ -14,7 +14,11 @@
 // in it (chunk i and its partner R/2 dims on; for neighbouring pairs two
 // chunks side by side): no exchange between lanes but the sum of squares.
 // The cos and sin a lane needs are the same for every head of the token and
-// are loaded once.
+// are loaded once.  16,384 tokens of 32/8 x 128 bf16 take 70.5 us, 5.83 TB/s
+// (a plain copy of as many bytes 61.4); with 290 instructions a pass of 4 KB
+// issue slots come next (68 % used).  Staging the rows through shared memory
+// with bulk copies, so that few warps keep many bytes in flight, was slower
+// (88 us): it left too few warps for those instructions.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -67,8 +71,6 @@ struct Chunk<float> {
   }
 };
 
-constexpr int NT = 256;
-
 // 16 bytes that are read once.  (volatile: the compiler would move a load
 // down to its first use, behind the wait for the token's place)
 __device__ __forceinline__ uint4 load_once(const void* src) {
@@ -80,19 +82,22 @@ __device__ __forceinline__ uint4 load_once(const void* src) {
 }
 
 // A warp takes one token and U passes of HP heads each, all loaded before the
-// first is used.  MB: blocks an SM holds (few registers, so that many warps
-// wait on memory at once, count for more than a few spilled ones: U = 3 at
-// 16,384 tokens 95 us with two blocks an SM, 80 with three, 76 with four).
-template <typename T, int D, int U, int MB>
-__global__ void __launch_bounds__(NT, MB) rope_append_kernel(const RopeAppendArgs p, unsigned parts) {
+// first is used.  A block's W warps take the passes of one token after the
+// other or, TOKENS, the same passes of W tokens.  MB: blocks an SM holds (few
+// registers, so that many warps wait on memory at once, count for more than a
+// few spilled ones: U = 3 at 16,384 tokens 95 us with 16 warps an SM, 80 with
+// 24, 76 with 32; with 40, 115).
+template <typename T, int D, int U, int W, int MB, bool TOKENS, bool PASS_ON>
+__global__ void __launch_bounds__(32 * W, MB) rope_append_kernel(const RopeAppendArgs p, unsigned parts) {
   using C = Chunk<T>;
   constexpr int E = C::E;             // elements of a chunk
   constexpr int NL = D / (2 * E);     // lanes per head row
   constexpr int HP = 32 / NL;         // head rows a warp takes at a time
   grid_launch_dependents();
   grid_dependency_wait();
-  const unsigned w = blockIdx.x * unsigned(NT / 32) + (threadIdx.x >> 5);
-  const unsigned t = w / parts, part = w % parts;
+  const unsigned warp = threadIdx.x >> 5, w = blockIdx.x * unsigned(W) + warp;
+  const unsigned t = TOKENS ? blockIdx.x / parts * unsigned(W) + warp : w / parts;
+  const unsigned part = TOKENS ? blockIdx.x % parts : w % parts;
   if (t >= unsigned(p.T)) return;
   const int lane = threadIdx.x & 31, i = lane % NL, h0 = int(part) * U * HP + lane / NL;
 
@@ -151,79 +156,106 @@ __global__ void __launch_bounds__(NT, MB) rope_append_kernel(const RopeAppendArg
   // head 0's row of the token in the cache and in q_out, rows of D elements
   const unsigned us = unsigned(max(slot, 0)), uq = unsigned(max(q_slot, 0));
   const size_t kv_row = size_t(us / unsigned(p.block_size)) * p.Hkv * p.block_size + us % unsigned(p.block_size);
+  const bool normed = p.q_weight != nullptr || p.k_weight != nullptr;
   const size_t q_row = size_t(uq / unsigned(p.q_rows)) * p.Hq * p.q_rows + uq % unsigned(p.q_rows);
 
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * HP;
+    const int first = int(part) * U * HP + u * HP, h = first + lane / NL;  // (first: the same in all lanes)
     const bool is_q = h < p.Hq, is_v = h >= h_v;
-    const T* wt = static_cast<const T*>(is_v ? nullptr : is_q ? p.q_weight : p.k_weight);
-    float a[E], b[E];
-    C::widen(xa[u], a);
-    C::widen(xb[u], b);
-    float ss = 0.f;
+    uint4 ya = xa[u], yb = xb[u];
+    if (first < h_v) {  // (else V heads alone: copied bit for bit)
+      const T* wt = static_cast<const T*>(is_v ? nullptr : is_q ? p.q_weight : p.k_weight);
+      float a[E], b[E];
+      C::widen(ya, a);
+      C::widen(yb, b);
+      if (normed) {
+        float ss = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+        for (int e = 0; e < E; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
 #pragma unroll
-    for (int d = NL / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-    if (wt != nullptr) {
-      const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-      float wa[E], wb[E];
-      C::widen(*reinterpret_cast<const uint4*>(wt + ca), wa);
-      C::widen(*reinterpret_cast<const uint4*>(wt + cb), wb);
+        for (int d = NL / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+        if (wt != nullptr) {
+          const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+          float wa[E], wb[E];
+          C::widen(*reinterpret_cast<const uint4*>(wt + ca), wa);
+          C::widen(*reinterpret_cast<const uint4*>(wt + cb), wb);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        a[e] = a[e] * inv * wa[e];
-        b[e] = b[e] * inv * wb[e];
+          for (int e = 0; e < E; ++e) {
+            a[e] = a[e] * inv * wa[e];
+            b[e] = b[e] * inv * wb[e];
+          }
+        }
       }
-    }
-    if (rot && !is_v) {
-      if (p.adjacent) {
+      if (rot) {
+        if (p.adjacent) {
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float a0 = a[e], b0 = b[e];
-          const float c0 = cs[e / 2], s0 = sn[e / 2], c1 = cs[(E + e) / 2], s1 = sn[(E + e) / 2];
-          a[e] = a0 * c0 - a[e + 1] * s0;
-          a[e + 1] = a[e + 1] * c0 + a0 * s0;
-          b[e] = b0 * c1 - b[e + 1] * s1;
-          b[e + 1] = b[e + 1] * c1 + b0 * s1;
-        }
-      } else {
+          for (int e = 0; e < E; e += 2) {
+            const float a0 = a[e], b0 = b[e];
+            const float c0 = cs[e / 2], s0 = sn[e / 2], c1 = cs[(E + e) / 2], s1 = sn[(E + e) / 2];
+            a[e] = a0 * c0 - a[e + 1] * s0;
+            a[e + 1] = a[e + 1] * c0 + a0 * s0;
+            b[e] = b0 * c1 - b[e + 1] * s1;
+            b[e + 1] = b[e + 1] * c1 + b0 * s1;
+          }
+        } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float a0 = a[e];
-          a[e] = a0 * cs[e] - b[e] * sn[e];
-          b[e] = b[e] * cs[e] + a0 * sn[e];
+          for (int e = 0; e < E; ++e) {
+            const float a0 = a[e];
+            a[e] = a0 * cs[e] - b[e] * sn[e];
+            b[e] = b[e] * cs[e] + a0 * sn[e];
+          }
         }
+      }
+      if (!is_v) {
+        ya = C::narrow(a);
+        yb = C::narrow(b);
       }
     }
     if (h < n_heads && (is_q ? q_slot : slot) >= 0) {
       const size_t row = is_q ? q_row + size_t(h) * p.q_rows
                               : kv_row + size_t(is_v ? h - h_v : h - p.Hq) * p.block_size;
       T* dst = static_cast<T*>(is_q ? p.q_out : is_v ? p.v_cache : p.k_cache) + row * D;
-      // (V is copied bit for bit)
-      *reinterpret_cast<uint4*>(dst + ca) = is_v ? xa[u] : C::narrow(a);
-      *reinterpret_cast<uint4*>(dst + cb) = is_v ? xb[u] : C::narrow(b);
+      if constexpr (PASS_ON) {
+        __stcs(reinterpret_cast<uint4*>(dst + ca), ya);
+        __stcs(reinterpret_cast<uint4*>(dst + cb), yb);
+      } else {
+        *reinterpret_cast<uint4*>(dst + ca) = ya;
+        *reinterpret_cast<uint4*>(dst + cb) = yb;
+      }
     }
   }
 }
 
 // Passes a warp makes: one while that leaves a warp of its own to every pass
-// (a step's latency counts: 64 tokens of 32/8 x 128 bf16 2.5 us, 3.6 with
-// three), three once the grid is two waves or more (16,384 tokens 76.0 us,
-// 114 with one).
-template <typename T, int D, int U, int MB>
-cudaError_t launch_u(const RopeAppendArgs& a, unsigned parts, cudaStream_t stream) {
-  const long blocks = (long(a.T) * parts + NT / 32 - 1) / (NT / 32);
-  return launch_pdl(rope_append_kernel<T, D, U, MB>, dim3(unsigned(blocks)), dim3(NT), 0, stream, a, parts);
+// (a step's latency counts: 64 tokens of 32/8 x 128 bf16 2.6 us, 3.6 with
+// three), three once the grid is two waves or more (16,384 tokens 73 us, 114
+// with one).  Blocks of eight warps while those of three passes are one wave
+// (2,049 tokens of 14/2 x 64 fp32: 5.1 us, 5.5 with two warps); beyond it two
+// warps, which leave their places to others sooner, two tokens side by side,
+// so that what a block writes is twice as long (4,097 tokens of 28/4 x 128 bf16
+// 15.9 us, 16.4 with eight warps; 16,384 of 32/8 73, 80).
+// Outputs of more than half of L2 (PASS_ON) will not be there for the
+// attention anyway: they are written to leave it first (70.5 us).
+constexpr long kHalfL2 = 64L << 20;
+template <typename T, int D, int U, int W, int MB, bool TOKENS, bool PASS_ON>
+cudaError_t launch_u(const RopeAppendArgs& a, unsigned passes, cudaStream_t stream) {
+  const unsigned parts = (passes + U - 1) / U;
+  const long blocks = TOKENS ? (long(a.T) + W - 1) / W * parts : (long(a.T) * parts + W - 1) / W;
+  return launch_pdl(rope_append_kernel<T, D, U, W, MB, TOKENS, PASS_ON>, dim3(unsigned(blocks)), dim3(32 * W), 0,
+                    stream, a, parts);
 }
 
 template <typename T, int D>
 cudaError_t launch_t(const RopeAppendArgs& a, cudaStream_t stream) {
   constexpr int HP = 32 / (D / (2 * Chunk<T>::E));
   const unsigned passes = unsigned((a.Hq + 2 * a.Hkv + HP - 1) / HP);
-  if (long(a.T) * passes < 2L * 32 * device_sm_count()) return launch_u<T, D, 1, 1>(a, passes, stream);
-  return launch_u<T, D, 3, 4>(a, (passes + 2) / 3, stream);
+  const long wave = 32L * device_sm_count();  // warps
+  if (long(a.T) * passes < 2 * wave) return launch_u<T, D, 1, 8, 1, false, false>(a, passes, stream);
+  if (long(a.T) * ((passes + 2) / 3) <= wave) return launch_u<T, D, 3, 8, 4, false, false>(a, passes, stream);
+  if (long(a.T) * (a.Hq + 2 * a.Hkv) * D * long(sizeof(T)) <= kHalfL2)
+    return launch_u<T, D, 3, 2, 16, true, false>(a, passes, stream);
+  return launch_u<T, D, 3, 2, 16, true, true>(a, passes, stream);
 }
 
 }  // namespace

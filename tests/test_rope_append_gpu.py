@@ -176,6 +176,11 @@ def test_many_tokens_of_every_kind(dtype, Hq, Hkv, D, T, kind):
     check(Case(T, Hq, Hkv, D, dtype, bs=64, seed=20, **kw))
 
 
+@pytest.mark.parametrize("dtype,T", [(torch.bfloat16, 5501), (torch.float32, 2751)], ids=["bf16", "f32"])
+def test_outputs_of_more_than_half_of_l2(dtype, T):
+    check(Case(T, 32, 8, 128, dtype, q_rows=512, bs=64, seed=24, pad=99, gap=64))
+
+
 def test_many_tokens_with_bad_places():
     c = Case(3000, 14, 2, 64, torch.bfloat16, bs=64, seed=21, pad=100)
     c.pos[5], c.pos[2999], c.slots[700], c.q_slots[701] = -1, 5000, 2 ** 31 - 1, c.q_out.shape[0] * c.q_out.shape[2]
