@@ -476,6 +476,12 @@ bool kv_map(CUtensorMap* out, const void* base, int D, int rows, int heads, int 
   });
 }
 
+bool kv_tile_map(CUtensorMap* out, const void* base, int D, int rows, int heads, int box_rows) {
+  static MapCache<4> cache;
+  return cache.get(out, base, {D, rows, heads, box_rows}, [&](CUtensorMap* m) {
+    return encode_bf16_tiles(m, base, uint64_t(D), uint64_t(rows), uint64_t(heads), uint32_t(box_rows));
+  });
+}
 bool query_map(CUtensorMap* out, const void* base, int D, int n_rep, int B, int Hkv, int rpt) {
   static MapCache<5> cache;
   return cache.get(out, base, {D, n_rep, B, Hkv, rpt}, [&](CUtensorMap* m) {

@@ -151,7 +151,6 @@ struct PrefixPlan {
   int units;    // CTAs per KV head and share: one for a single tile, else one per two tiles
   int n_split;  // shares of the keys, at most
   bool adaptive;  // one wave: the kernel chooses the number of shares
-  double start_us, tile_us, merge_us;  // estimates: a share's start and epilogue, its KV tile, its partials
 };
 PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sms);
 

@@ -5,21 +5,28 @@
 // hundred keys.  One CTA per unit (gqa_attn_decode) spends as long on getting
 // started, on its last wave and on joining its warps as on its keys: 64
 // requests of up to 1,024 keys took 31 us, 256 of up to 512 56 us, against 20
-// and 39 us for their bytes.  Here the work is one list: the 16-key tiles of
+// and 39 us for their bytes.  Here the work is one list: the 32-key tiles of
 // all units, request by request, cut into contiguous ranges, one for every
-// warp of resident CTAs.  A warp
-//   - streams its range through stages of its own (TMA, 128-byte swizzle),
-//     across unit borders, so that copies are always in flight;
-//   - shares nothing with other warps after the start: no block barrier, no
-//     join of warps; a unit that several warps touch has a partial of each;
-//   - computes as the bf16 decode kernel does (mma.sync m16n8k16, up to 8
-//     query heads of one KV head as rows, online softmax in base 2).
+// computing warp of the resident CTAs.  Such a warp
+//   - has its range streamed through slots of its own by a lane of a copying
+//     warp (TMA, 128-byte swizzle; K and V of a tile are a slot each), across
+//     unit borders, so that copies are always in flight;
+//   - shares nothing with other computing warps: no block barrier, no join of
+//     warps; a unit that several warps touch has a partial of each;
+//   - multiplies on the tensor cores (mma.sync m16n8k16) with the keys as rows
+//     and up to 8 query heads of one KV head as columns, online softmax in base 2.
+// What bounds it: beside the shared rows few SMs do this work and HBM has
+// bytes to spare, so it is the instructions of a warp, which mostly wait for
+// one another.  24 SMs take 42 GB/s each if one warp copies for all with four
+// copies a tile of K or V, 60 to 65 if the computing warps copy for themselves
+// (567 instructions a tile), and 100 this way; copies alone reach 165.  On all
+// SMs it is HBM: 256 requests of up to 512 keys, D = 128, 268 MB, in 57 us
+// with the launch and the merge.
 // The cut depends on the lengths and the grid alone, so the result does not
 // vary.  A unit's partials take its first slots in order; the warp with the
 // unit's first keys leaves their number for the merge.  (Chunks taken from a
 // queue evened out the ends, but each start of a chunk costs a warp its
-// queries, its place in the list and a partial: 1.56 against 1.45 us a tile,
-// 64 requests 74 against 67 us.)
+// queries, its place in the list and a partial: 64 requests 74 against 67 us.)
 #pragma once
 
 #include <cuda.h>
@@ -38,13 +45,15 @@
 namespace gqa {
 namespace {
 
-constexpr int kOwnTile = 16;   // keys per tile
-constexpr int kOwnWarps = 8;   // warps of a CTA that work
+constexpr int kOwnTile = 32;   // keys per tile
+constexpr int kOwnWarps = 9;   // warps of a CTA that compute
+constexpr int kOwnCopiers = 3; // and that copy for them
+constexpr int kOwnThreads = 32 * (kOwnWarps + kOwnCopiers);
 // A unit costs a warp more than its tiles (its queries, its partial): it counts
-// this many tiles more, without keys, ahead of its own.  (256 requests of up
-// to 512 keys: a warp that got a run of requests of a few keys ended at 60 us,
-// the others at 46.)
-constexpr int kOwnLead = 2;
+// as a tile more, without keys, ahead of its own.  (256 requests of up to 512
+// keys: a warp that got a run of requests of a few keys ended at 60 us, the
+// others at 46.)
+constexpr int kOwnLead = 1;
 constexpr int kOwnMaxRequests = 1024;  // requests whose prefix sums a CTA holds
 
 struct OwnRowsParams {
@@ -107,18 +116,20 @@ template <int D>
 struct OwnCfg {
   static constexpr int TILE = kOwnTile;
   static constexpr int HALVES = D / 64;
-  static constexpr int BOX = TILE * 128;           // 16 rows x 128 bytes
-  static constexpr int TILEB = HALVES * BOX;       // K (or V) tile
-  static constexpr int STAGEB = 2 * TILEB;
-  static constexpr int NSTAGE = D == 128 ? 3 : 6;  // 24 KB a warp
-  static constexpr int WARPB = NSTAGE * STAGEB;
+  static constexpr int HALFB = TILE * 128;           // 64 dims of a tile
+  static constexpr int SLOTB = HALVES * HALFB;       // K, or V, of a tile
+  static constexpr int NSLOT = D == 128 ? 3 : 6;     // 24 KB a warp
+  static constexpr int WARPB = NSLOT * SLOTB;
   // (behind the barriers of the shared rows' work, which a CTA may have set up
   // before it learns that it has no part in it)
-  static constexpr int OFF_BAR = kOwnWarps * WARPB + 4096;
-  static constexpr int OFF_SUM = OFF_BAR + kOwnWarps * (NSTAGE + 1) * 8;
-  static constexpr int OFF_STARTS = OFF_SUM + kOwnWarps * 4;
-  static constexpr int SMEM = OFF_STARTS + (kOwnMaxRequests + 1) * 4 + 1024;
-  static constexpr int KSTEPS = D / 16, NT_O = D / 8;
+  static constexpr int OFF_BAR = kOwnWarps * WARPB + 1024;
+  static constexpr int N_BARS = 2 * NSLOT * kOwnWarps + 1;  // full and empty of each slot; one for the tests
+  static constexpr int OFF_SUM = OFF_BAR + N_BARS * 8;
+  static constexpr int OFF_ABORT = OFF_SUM + kOwnThreads / 32 * 4;
+  static constexpr int OFF_STARTS = OFF_ABORT + 4;
+  static constexpr int OFF_LENS = OFF_STARTS + (kOwnMaxRequests + 1) * 4;
+  static constexpr int SMEM = OFF_LENS + kOwnMaxRequests * 4 + 1024;
+  static constexpr int KSTEPS = D / 16;
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -128,19 +139,25 @@ struct Cursor {
   int b, u, k, nt, x;  // x: its number in the list
 };
 
-constexpr int BAR_OWN = 5;  // named barrier of the 256 threads that work on own rows
+constexpr int BAR_OWN = 5;  // named barrier of a CTA's threads at the own rows
 
-// The prefix sums of the list, starts[b] = tiles before request b, into shared
-// memory (by the CTA's first 256 threads; grid_dependency_wait has returned).
+// The lengths and the prefix sums of the list, starts[b] = tiles before request
+// b, into shared memory (by the whole CTA; grid_dependency_wait has returned), and its barriers.
 // `report`: this CTA reports lengths that had to be clamped.
 template <int D>
 __device__ __forceinline__ void own_scan(unsigned char* smem, const OwnRowsParams& p, bool report) {
   using C = OwnCfg<D>;
-  constexpr int NTHREADS = 32 * kOwnWarps;
+  constexpr int NTHREADS = kOwnThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int* warp_sum = reinterpret_cast<int*>(smem + C::OFF_SUM);
   int* starts = reinterpret_cast<int*>(smem + C::OFF_STARTS);
+  int* lens = reinterpret_cast<int*>(smem + C::OFF_LENS);
   const int per = (p.B + NTHREADS - 1) / NTHREADS;  // consecutive requests a thread sums
+  if (tid < C::N_BARS) {
+    mbar_init(reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + tid, 1);
+    fence_barrier_init();
+  }
+  if (tid == 0) *reinterpret_cast<volatile int*>(smem + C::OFF_ABORT) = 0;
   int sum = 0;
   bool clamped = false;
   for (int i = 0; i < per; ++i) {
@@ -149,6 +166,7 @@ __device__ __forceinline__ void own_scan(unsigned char* smem, const OwnRowsParam
     const int raw = p.kv_lens != nullptr ? p.kv_lens[b] : p.max_kv_len;
     const int L = min(max(raw, 0), p.max_kv_len);
     clamped |= L != raw;
+    lens[b] = L;
     sum += L > 0 ? ((L + kOwnTile - 1) / kOwnTile + kOwnLead) * p.units : 0;
     starts[b + 1] = sum;
   }
@@ -190,7 +208,93 @@ __device__ __forceinline__ int own_total(const OwnRowsParams& p) {
   return __reduce_add_sync(0xffffffffu, sum) * p.units;
 }
 
-// The work of a CTA on the own rows, by its first 256 threads, after own_scan.
+// A copying warp: its lanes copy for a warp each, K and V of a tile an item each,
+// in slots used in turn, from tile `ic` to the end of the range, x1.  It stays
+// until all warps are done; after a wait that ran out it sees to it that the
+// copies still in flight land before the CTA's shared memory is let go.
+template <int D, typename NextUnit>
+__device__ __forceinline__ void own_copies(unsigned char* smem, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                                           const OwnRowsParams& p, int who, Cursor ic, int x1, NextUnit next_unit) {
+  using C = OwnCfg<D>;
+  constexpr int NS = C::NSLOT, TILE = C::TILE;
+  const int lane = threadIdx.x & 31;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
+  uint64_t* const full = bars + min(who, kOwnWarps - 1) * 2 * NS;
+  uint64_t* const empty = full + NS;
+  unsigned char* const slot0 = smem + min(who, kOwnWarps - 1) * C::WARPB;
+  const uint64_t once = l2_policy_evict_first();  // (the partials are to stay in L2 for the merge)
+  // Where tile ic is in the maps: row irow of block (or request) iblk, asked for
+  // once a block, an item's time before it is needed (and looked at only then).
+  int irow = 0, iblk = 0;
+  auto locate = [&](bool first) {
+    const int row0 = (ic.k - kOwnLead) * TILE;
+    if (p.block_table == nullptr) {
+      irow = row0;
+      iblk = ic.b;
+      return;
+    }
+    irow = first ? row0 % p.block_size : irow + TILE;
+    if (irow == p.block_size || row0 == 0) irow = 0;
+    if (first || irow == 0)
+      asm volatile("ld.global.b32 %0, [%1];"
+                   : "=r"(iblk)
+                   : "l"(p.block_table + size_t(ic.b) * p.max_blocks + row0 / p.block_size));
+  };
+  const int n_blk = p.block_table == nullptr ? p.B : p.num_blocks;
+  int issued = 0, slot = 0;  // items copied so far, the next one's slot
+  uint32_t freed = 1;        // and the phase of `empty` that frees it (the first use waits for none)
+  bool is_k = true, more = ic.x < x1;
+  if (more) locate(true);
+  uint64_t since = 0;  // (of the last copy, while none can be made)
+  while (__any_sync(0xffffffffu, more)) {
+    const bool go = more && (issued < NS || mbar_test_wait(&empty[slot], freed));
+    if (go) {
+      unsigned char* dst = slot0 + slot * C::SLOTB;
+      const CUtensorMap* map = is_k ? tmK : tmV;
+      if (iblk < 0 || iblk >= n_blk) {
+        atomicOr(p.status, GQA_DEV_BAD_BLOCK);
+        iblk = 0;
+      }
+      const int ihead = iblk * p.Hkv + ic.u / p.n_hc;
+      mbar_arrive_expect_tx(&full[slot], C::SLOTB);
+      tma_load_4d(dst, map, 0, irow, 0, ihead, &full[slot], once);
+      ++issued;
+      if (++slot == NS) slot = 0, freed ^= 1u;
+      is_k = !is_k;
+      if (is_k) {
+        ++ic.x;
+        if (++ic.k == ic.nt) next_unit(ic);
+        more = ic.x < x1;
+        // (a table entry asked for here has an item's time to arrive)
+        if (more) locate(false);
+      }
+    }
+    if (!__any_sync(0xffffffffu, go)) {
+      if (p.test_stall_ns != 0) break;
+      const uint64_t now = global_timer_ns();
+      if (since == 0) since = now;
+      const bool late = now - since > p.wait_limit_ns;
+      if (late) *abort_flag = 1;
+      if (__any_sync(0xffffffffu, late || *abort_flag != 0)) break;
+      __nanosleep(20);
+    } else {
+      since = 0;
+    }
+  }
+  if (p.test_stall_ns != 0 && lane == 0 &&  // tests: a wait on what nothing arrives on
+      !mbar_wait_bounded(&bars[C::N_BARS - 1], 0u, p.test_stall_ns))
+    *abort_flag = 1;
+  __syncwarp();
+  named_bar_sync(BAR_OWN, kOwnThreads);
+  if (*abort_flag != 0) {
+    if (lane == 0) atomicOr(p.status, GQA_DEV_WAIT_TIMEOUT);
+    for (int i = max(0, issued - NS); i < issued; ++i)
+      mbar_wait_bounded(&full[i % NS], uint32_t(i / NS) & 1u, p.wait_limit_ns);
+  }
+}
+
+// The work of a CTA on the own rows, after own_scan.
 // (CTAs of the shared rows that go on with this themselves were tried: inlined
 // behind the softmax loop it made that loop 10 % slower, out of line it got too
 // few registers.)
@@ -198,27 +302,27 @@ template <int D>
 __device__ __forceinline__ void own_rows(unsigned char* smem, const CUtensorMap* tmK, const CUtensorMap* tmV,
                                          const OwnRowsParams& p, const OwnRole& role) {
   using C = OwnCfg<D>;
-  constexpr int NS = C::NSTAGE, TILE = C::TILE;
+  constexpr int NS = C::NSLOT, TILE = C::TILE;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * (NS + 1);
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
   const int* starts = reinterpret_cast<const int*>(smem + C::OFF_STARTS);
-  if (lane == 0) {
-    for (int s = 0; s <= NS; ++s) mbar_init(&full[s], 1);
-    fence_barrier_init();
-  }
+  const int* lens = reinterpret_cast<const int*>(smem + C::OFF_LENS);
   const int N = starts[p.B];
   if (N == 0) return;
-  const OwnCut cut = OwnCut::of(unsigned(N), unsigned(role.early * kOwnWarps), unsigned(role.late * kOwnWarps), role.head_start,
-                                unsigned(p.min_tiles));
-  // this warp's range: neighbours in the list run on different SMs
+  const OwnCut cut = OwnCut::of(unsigned(N), unsigned(role.early * kOwnWarps), unsigned(role.late * kOwnWarps),
+                                role.head_start, unsigned(p.min_tiles));
+  // warp `who`'s range: neighbours in the list run on different SMs
+  constexpr int PER = (kOwnWarps + kOwnCopiers - 1) / kOwnCopiers;  // warps a copying warp serves
+  const bool copies = warp >= kOwnWarps;
+  const int who = !copies ? warp : lane < PER ? (warp - kOwnWarps) * PER + lane : kOwnWarps;
   const bool is_early = role.cta < role.early;
   const OwnRanges& part = is_early ? cut.a : cut.b;
-  const unsigned w = is_early ? unsigned(warp * role.early + role.cta)
-                               : unsigned(warp * role.late + role.cta - role.early);
-  if (w >= part.n) return;
+  const unsigned w = is_early ? unsigned(who * role.early + role.cta)
+                               : unsigned(who * role.late + role.cta - role.early);
   const int base = is_early ? 0 : int(cut.head);
-  const int x0 = base + int(part.start(w)), x1 = base + int(part.start(w + 1));
-  if (x0 >= x1) return;
+  int x0 = 0, x1 = 0;
+  if (who < kOwnWarps && w < part.n) x0 = base + int(part.start(w)), x1 = base + int(part.start(w + 1));
 
   auto units_tiles = [&](int b) { return (starts[b + 1] - starts[b]) / p.units; };
   auto next_unit = [&](Cursor& c) {
@@ -230,9 +334,10 @@ __device__ __forceinline__ void own_rows(unsigned char* smem, const CUtensorMap*
       if (c.b < p.B) c.nt = units_tiles(c.b);
     }
   };
-  Cursor at;  // the tile computed next
-  {
-    int lo = 0, hi = p.B;  // the last request that starts at or before x0 (of empty ones at the same place the one after)
+  Cursor at{0, 0, 0, 0, x0};  // the tile computed (or copied) next
+  if (x0 < x1) {
+    // the last request that starts at or before x0 (of empty ones at the same place the one after)
+    int lo = 0, hi = p.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (starts[mid] <= x0) lo = mid; else hi = mid;
@@ -241,63 +346,29 @@ __device__ __forceinline__ void own_rows(unsigned char* smem, const CUtensorMap*
     at.nt = units_tiles(lo);
     at.u = (x0 - starts[lo]) / at.nt;
     at.k = (x0 - starts[lo]) - at.u * at.nt;
-    at.x = x0;
-  }
-  if (at.k < kOwnLead) {
-    at.x += kOwnLead - at.k;
-    at.k = kOwnLead;
-  }
-  if (at.x >= x1) return;  // the range holds nothing but leading tiles
+    if (at.k < kOwnLead) {
+      at.x += kOwnLead - at.k;
+      at.k = kOwnLead;
+    }
+  }  // (a range with nothing but leading tiles: at.x >= x1)
 
-  // ---- copies ----
-  unsigned char* const stage0 = smem + warp * C::WARPB;
-  const uint64_t once = l2_policy_evict_first();  // (the partials are to stay in L2 for the merge)
-  Cursor ic = at;  // the tile copied next, and where it is in the maps
-  int irow = 0, ihead = 0;
-  // (a block's id is asked for once, with its first tile: the copies would
-  // wait for one table entry after the other)
-  auto locate = [&](bool first) {
-    const int g = ic.u / p.n_hc, row0 = (ic.k - kOwnLead) * TILE;
-    if (p.block_table == nullptr) {
-      irow = row0;
-      ihead = ic.b * p.Hkv + g;
-      return;
-    }
-    irow = first ? row0 % p.block_size : irow + TILE;
-    if (irow == p.block_size || row0 == 0) irow = 0;
-    if (!first && irow != 0) return;
-    int blk = p.block_table[size_t(ic.b) * p.max_blocks + row0 / p.block_size];
-    if (blk < 0 || blk >= p.num_blocks) {
-      atomicOr(p.status, GQA_DEV_BAD_BLOCK);
-      blk = 0;
-    }
-    ihead = blk * p.Hkv + g;
-  };
-  int issued = 0;  // tiles copied so far (all lanes count, lane 0 copies)
-  auto issue = [&]() {
-    if (lane == 0) {
-      const int st = issued % NS;
-      unsigned char* dst = stage0 + st * C::STAGEB;
-      mbar_arrive_expect_tx(&full[st], C::STAGEB);
-#pragma unroll
-      for (int hf = 0; hf < C::HALVES; ++hf) {
-        tma_load_3d(dst + hf * C::BOX, tmK, hf * 64, irow, ihead, &full[st], once);
-        tma_load_3d(dst + C::TILEB + hf * C::BOX, tmV, hf * 64, irow, ihead, &full[st], once);
-      }
-    }
-    ++issued;
-    ++ic.x;
-    if (++ic.k == ic.nt) next_unit(ic);
-    // (a table entry asked for here has a tile's time to arrive)
-    if (lane == 0 && ic.x < x1) locate(false);
-  };
-  if (lane == 0) locate(true);
-  __syncwarp();
-  for (int s = 0; s < NS && ic.x < x1; ++s) issue();
-  bool ok = true;
-  if (p.test_stall_ns != 0) ok = mbar_wait_bounded(&full[NS], 0u, p.test_stall_ns);  // tests: nothing arrives on it
+  if (copies) {
+    own_copies<D>(smem, tmK, tmV, p, who, at, x1, next_unit);
+    return;
+  }
+  if (at.x >= x1) {
+    named_bar_sync(BAR_OWN, kOwnThreads);  // (see own_copies)
+    return;
+  }
+  uint64_t* const full = bars + warp * 2 * NS;
+  uint64_t* const empty = full + NS;
+  unsigned char* const slot0 = smem + warp * C::WARPB;
 
   // ---- the tiles ----
+  // Keys are the rows of both products' first operand: S^T = K Q^T of 16 keys
+  // by 8 heads, O^T = V^T P^T of 16 dims by 8 heads, so that no row of a
+  // product is empty (with the heads as rows half would be).  A lane has keys
+  // r and r + 8 of heads 2c and 2c + 1, and of O^T dims r and r + 8 of these.
   const int r = lane >> 2, c = lane & 3, mi = lane >> 3, rr = lane & 7;
   uint32_t qa[C::KSTEPS][2], qn[C::KSTEPS][2];  // Q of this unit, and of the next
   auto heads_of = [&](int u, int& h0) {
@@ -316,112 +387,141 @@ __device__ __forceinline__ void own_rows(unsigned char* smem, const CUtensorMap*
     }
   };
   load_q(at, qn);
-  int t = 0;
+  int slot = 0;         // of the item used next
+  uint32_t parity = 0;  // and its barrier's phase
+  auto arrived = [&] {
+    return __all_sync(0xffffffffu, wait_or_abort(&full[slot], parity, abort_flag, p.wait_limit_ns)) != 0;
+  };
+  auto release = [&] {
+    __syncwarp();  // every lane has read the slot
+    if (lane == 0) mbar_arrive(&empty[slot]);
+    if (++slot == NS) slot = 0, parity ^= 1u;
+  };
+  bool ok = true;
   while (ok && at.x < x1) {
     // one unit, or what of it is in the range
     const Cursor un = at;
     const int n_here = min(un.nt - un.k, x1 - un.x);
-    const int raw_len = p.kv_lens != nullptr ? p.kv_lens[un.b] : p.max_kv_len;
-    const int L = min(max(raw_len, 0), p.max_kv_len);
+    const int L = lens[un.b];
 #pragma unroll
     for (int ks = 0; ks < C::KSTEPS; ++ks) qa[ks][0] = qn[ks][0], qa[ks][1] = qn[ks][1];
     at.x += n_here;
     next_unit(at);  // (past the range where it ends inside the unit)
     if (at.x < x1) load_q(at, qn);
-    float m_ref = -INFINITY, lsum = 0.f;
-    float oacc[C::NT_O][4];
+    float m_ref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
+    float oacc[D / 16][4];
 #pragma unroll
-    for (int j = 0; j < C::NT_O; ++j) oacc[j][0] = oacc[j][1] = oacc[j][2] = oacc[j][3] = 0.f;
-    for (int k = 0; k < n_here; ++k, ++t) {
-      const int st = t % NS;
-      ok = mbar_wait_bounded(&full[st], uint32_t(t / NS) & 1u, p.wait_limit_ns);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
+    for (int j = 0; j < D / 16; ++j) oacc[j][0] = oacc[j][1] = oacc[j][2] = oacc[j][3] = 0.f;
+    for (int k = 0; k < n_here; ++k) {
+      const uint32_t kaddr = smem_u32(slot0 + slot * C::SLOTB);
+      ok = arrived();
+      if (!ok) break;
+      const int valid = L - (un.k - kOwnLead + k) * TILE;  // keys of the tile, if below 32
+      // ---- S^T = K Q^T: two tiles of 16 keys ----
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int ks = 0; ks < C::KSTEPS; ++ks) {
+        const int key = 8 * (mi & 1) + rr, d = 16 * ks + 8 * (mi >> 1);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          uint32_t a[4];
+          ldsm_x4(kaddr + (d / 64) * C::HALFB + swz(16 * m + key, (d % 64) / 8), a[0], a[1], a[2], a[3]);
+          mma_16816(s[m], a, qa[ks][0], qa[ks][1]);
+        }
       }
-      unsigned char* const stage = stage0 + st * C::STAGEB;
-      const uint32_t kaddr = smem_u32(stage), vaddr = kaddr + C::TILEB;
-      const int valid = L - (un.k - kOwnLead + k) * TILE;  // keys of the tile, if below 16
+      release();
+      if (valid < TILE) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (16 * m + 8 * (i >> 1) + r >= valid) s[m][i] = -INFINITY;
+      }
+      // ---- softmax, with a lazy reference as in decode: it is raised when a
+      // score passes it by 2^8 ----
+      float mx[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        mx[h] = fmaxf(fmaxf(s[0][h], s[0][2 + h]), fmaxf(s[1][h], s[1][2 + h])) * p.qscale;
+      if (__any_sync(0xffffffffu, mx[0] > m_ref[0] + 8.f || mx[1] > m_ref[1] + 8.f)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], d));
+          if (mx[h] > m_ref[h] + 8.f) {
+            const float alpha = fast_exp2(m_ref[h] - mx[h]);
+            m_ref[h] = mx[h];
+            lsum[h] *= alpha;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) oacc[j][h] *= alpha, oacc[j][2 + h] *= alpha;
+          }
+        }
+      }
+      const float neg[2] = {m_ref[0] == -INFINITY ? 0.f : -m_ref[0], m_ref[1] == -INFINITY ? 0.f : -m_ref[1]};
+      uint32_t pt[2][2];  // P^T of 8 keys each, as the second operand
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[i] = fast_exp2(fmaf(s[m][i], p.qscale, neg[i & 1]));
+          lsum[i & 1] += e[i];
+        }
+        pt[m][0] = transpose_8x8(pack_bf16(e[0], e[1]));
+        pt[m][1] = transpose_8x8(pack_bf16(e[2], e[3]));
+      }
+      unsigned char* const vslot = slot0 + slot * C::SLOTB;
+      const uint32_t vaddr = smem_u32(vslot);
+      ok = arrived();
+      if (!ok) break;
       if (valid < TILE) {
         // V rows past the length may hold anything: zeroed (their P is 0, but 0 x NaN is NaN)
         const int n_chunk = (TILE - valid) * 8;
 #pragma unroll
         for (int hf = 0; hf < C::HALVES; ++hf)
           for (int i = lane; i < n_chunk; i += 32)
-            *reinterpret_cast<uint4*>(stage + C::TILEB + hf * C::BOX + valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();  // before the stage can be refilled by TMA
+            *reinterpret_cast<uint4*>(vslot + hf * C::HALFB + valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();  // before the slot can be refilled by TMA
         __syncwarp();
       }
-      // ---- S = Q K^T: two n-tiles of 8 keys ----
-      float sacc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      // ---- O^T += V^T P^T: 16 dims at a time ----
 #pragma unroll
-      for (int ks = 0; ks < C::KSTEPS; ++ks) {
-        const int key = 8 * (mi >> 1) + rr, d = 16 * ks + 8 * (mi & 1);
-        uint32_t b00, b01, b10, b11;
-        ldsm_x4(kaddr + (d / 64) * C::BOX + swz(key, (d % 64) / 8), b00, b01, b10, b11);
-        mma_16816(sacc[0], qa[ks][0], qa[ks][1], b00, b01);
-        mma_16816(sacc[1], qa[ks][0], qa[ks][1], b10, b11);
-      }
-      float sv[4];
+      for (int j = 0; j < D / 16; ++j) {
+        const int key = 8 * (mi >> 1) + rr, d = 16 * j + 8 * (mi & 1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sv[i] = 8 * (i >> 1) + 2 * c + (i & 1) < valid ? sacc[i >> 1][i & 1] * p.qscale : -INFINITY;
-      float mx = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const bool resc = mx > m_ref + 8.f;  // lazy reference, as in decode
-      if (__any_sync(0xffffffffu, resc)) {
-        const float alpha = resc ? fast_exp2(m_ref - mx) : 1.f;
-        if (resc) m_ref = mx;
-        lsum *= alpha;
-#pragma unroll
-        for (int j = 0; j < C::NT_O; ++j) {
-          oacc[j][0] *= alpha;
-          oacc[j][1] *= alpha;
+        for (int m = 0; m < 2; ++m) {
+          uint32_t a[4];
+          ldsm_x4_t(vaddr + (d / 64) * C::HALFB + swz(16 * m + key, (d % 64) / 8), a[0], a[1], a[2], a[3]);
+          mma_16816(oacc[j], a, pt[m][0], pt[m][1]);
         }
       }
-      const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-      float pv[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) pv[i] = fast_exp2(sv[i] - m_use);
-      lsum += (pv[0] + pv[1]) + (pv[2] + pv[3]);
-      const uint32_t pa0 = pack_bf16(pv[0], pv[1]), pa2 = pack_bf16(pv[2], pv[3]);
-      // ---- O += P V: pairs of 8-dim n-tiles ----
-#pragma unroll
-      for (int jj = 0; jj < C::NT_O / 2; ++jj) {
-        const int key = 8 * (mi & 1) + rr, d = 16 * jj + 8 * (mi >> 1);
-        uint32_t v0, v1, v2, v3;
-        ldsm_x4_t(vaddr + (d / 64) * C::BOX + swz(key, (d % 64) / 8), v0, v1, v2, v3);
-        mma_16816(oacc[2 * jj], pa0, pa2, v0, v1);
-        mma_16816(oacc[2 * jj + 1], pa0, pa2, v2, v3);
-      }
-      __syncwarp();  // every lane has read the stage
-      if (ic.x < x1) issue();
+      release();
     }
     if (!ok) break;
-    lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
-    lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) lsum[h] += __shfl_xor_sync(0xffffffffu, lsum[h], d);
     // this warp's partial of the unit
-    const int end = un.x - un.k + un.nt, first = cut.holder(end - un.nt + kOwnLead), slot = cut.holder(un.x) - first;
+    const int end = un.x - un.k + un.nt, first = cut.holder(end - un.nt + kOwnLead);
+    const int part_slot = cut.holder(un.x) - first;
     if (un.k == kOwnLead && lane == 0) p.counts[un.b * p.units + un.u] = cut.holder(end - 1) - first + 1;
     int h0;
     const int nh = heads_of(un.u, h0);
-    if (r < nh) {
-      const size_t prow = (size_t(un.b) * p.Hq + h0 + r) * p.n_slots + slot;
-      float* dst = p.part_o + prow * D + 2 * c;
 #pragma unroll
-      for (int j = 0; j < C::NT_O; ++j)
-        *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(oacc[j][0], oacc[j][1]);
-      if (c == 0) p.ml[prow] = make_float2(m_ref, lsum);
+    for (int h = 0; h < 2; ++h) {
+      if (2 * c + h < nh) {
+        const size_t prow = (size_t(un.b) * p.Hq + h0 + 2 * c + h) * p.n_slots + part_slot;
+        float* dst = p.part_o + prow * D + r;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) dst[16 * j] = oacc[j][h], dst[16 * j + 8] = oacc[j][2 + h];
+        if (r == 0) p.ml[prow] = make_float2(m_ref[h], lsum[h]);
+      }
     }
   }
-  if (!ok) {  // a copy did not arrive in time: report, and let those in flight land
-    if (lane == 0) {
-      atomicOr(p.status, GQA_DEV_WAIT_TIMEOUT);
-      for (int i = t; i < issued; ++i) mbar_wait_bounded(&full[i % NS], uint32_t(i / NS) & 1u, p.wait_limit_ns);
-    }
-    __syncwarp();
-  }
+  if (!ok && lane == 0) atomicOr(p.status, GQA_DEV_WAIT_TIMEOUT);  // (a copy did not arrive in time)
+  __syncwarp();
+  named_bar_sync(BAR_OWN, kOwnThreads);
 }
 
 }  // namespace

@@ -142,9 +142,11 @@ struct GridPlan {
   int n_cand, per_share, units, sms, early;
   bool adaptive, listed;
   // estimated times in us: a share's start and epilogue, its KV tile, a share's
-  // partials to the merge and back, an own-row tile on one SM's eight warps,
-  // the start of a CTA of own rows, and the same behind one of shared rows
-  float start, kv_tile, merge, own_tile, lead_in, follow;
+  // partials to the merge and back, the start of a CTA of own rows, the same
+  // behind one of shared rows, and how much later all is done where some are
+  float start, kv_tile, merge, lead_in, follow, rest;
+  float own_sm, hbm;  // tiles of own rows that an SM, and that HBM, does in a us
+  int kv_heads;       // (a KV tile of one is as many bytes as four tiles of own rows)
 };
 
 // The time of the shared rows in n shares, and of everything: the SMs without
@@ -153,7 +155,13 @@ struct GridPlan {
 // has no idle time at the starts and ends of the shares: 64 requests behind
 // 32,768 rows, up to 1,024 own, 65.6 us with all SMs on the shared rows first.)
 __device__ __forceinline__ float share_time(const GridPlan& g, int n_kv, int n) {
-  return g.start + g.kv_tile * float((n_kv + n - 1) / n);
+  return g.start + g.kv_tile * ceilf(__fdividef(float(n_kv), float(n)));
+}
+// Tiles of own rows that `early` SMs do in a us beside n shares: what an SM can
+// do, or what the stream of the shared rows leaves of HBM.
+__device__ __forceinline__ float own_rate(const GridPlan& g, int n_kv, float share, float early) {
+  const float shared = float(4 * n_kv * g.kv_heads);
+  return fminf(early * g.own_sm, fmaxf(g.hbm - __fdividef(shared, share), 0.25f * g.hbm));
 }
 constexpr int kMaxShares = 1023;  // of an adaptive grid
 constexpr uint32_t kShareMask = 1023u;
@@ -166,12 +174,16 @@ __device__ __forceinline__ int choose_shares(const GridPlan& g, int n_split, int
   // from it stays in uniform registers, or the softmax loop spills.)
   uint32_t best = 0xffffffffu;
   for (int n = 1 + int(threadIdx.x & 31); n <= most; n += 32) {
-    const float share = share_time(g, n_kv, n), ctas = float(n * g.per_share);
-    const float own = own_tiles * g.own_tile, room = (share - g.lead_in) * (float(g.sms) - ctas);
+    const float ctas = float(n * g.per_share), own = float(own_tiles);
+    float share = share_time(g, n_kv, n);
+    // (shares are drawn out by the traffic of both kinds of work, the more the
+    // nearer it comes to what HBM delivers)
+    const float load = __fdividef(own + float(4 * n_kv * g.kv_heads), g.hbm * share);
+    const float rate = own_rate(g, n_kv, share, float(g.sms) - ctas);
+    share *= 0.83f + 0.34f * fminf(load, 1.1f);
     // what of the own rows the free SMs do not get done follows on all
-    const float rest = own > room ? (own - room) / float(g.sms) + g.follow : 0.f;
-    // (a share is drawn out by its neighbours' traffic now and then: 1.1)
-    const float t = 1.1f * share + rest + g.merge * float(n);
+    const float room = (share - g.lead_in) * rate, rest = own > room ? __fdividef(own - room, g.hbm) + g.rest : 0.f;
+    const float t = share + rest + g.merge * float(n);
     best = min(best, (__float_as_uint(t) & ~kShareMask) | uint32_t(n));
   }
   return int(__reduce_min_sync(0xffffffffu, best) & kShareMask);
@@ -181,6 +193,7 @@ template <int HD>
 constexpr int kSmemBytes = PxCfg<HD>::SMEM_BYTES > OwnCfg<HD>::SMEM ? PxCfg<HD>::SMEM_BYTES : OwnCfg<HD>::SMEM;
 static_assert(PxCfg<64>::OFF_ML + 2048 <= OwnCfg<64>::OFF_BAR && PxCfg<128>::OFF_ML + 2048 <= OwnCfg<128>::OFF_BAR,
               "the own rows' barriers lie behind those of the shared rows");
+static_assert(NTHR == kOwnThreads, "both kinds of work fill the CTA");
 
 // SINGLE: one row tile per CTA, its even KV tiles in slot 0 and the odd ones
 // in slot 1; otherwise tiles A and B (slots 0 and 1) over the same KV tiles.
@@ -282,15 +295,13 @@ __global__ void __launch_bounds__(NTHR, 1)
       r.cta = cand ? r.early + r.late : cta - grid.n_cand;
     }
     if (r.cta >= r.early + r.late) return;
-    if (warp >= kOwnWarps) {  // gives its registers to the eight warps that work
-      set_max_regs_dec<C::REG_CTRL>();
-      return;
-    }
-    set_max_regs_inc<C::REG_SOFTMAX>();
     own_scan<HD>(smem, own, r.cta == 0);
     if (direct) use_length();
-    r.head_start =
-        n_used > 0 ? (share_time(grid, n_kv, n_used) + grid.follow) / (grid.own_tile * kOwnWarps) : 0.f;
+    r.head_start = 0.f;
+    if (n_used > 0 && r.early > 0) {
+      const float share = share_time(grid, n_kv, n_used);
+      r.head_start = (share + grid.follow) * own_rate(grid, n_kv, share, float(r.early)) / float(r.early * kOwnWarps);
+    }
     own_rows<HD>(smem, &tmKo, &tmVo, own, r);
     return;
   }
@@ -738,9 +749,9 @@ cudaError_t launch_prefix_merge(const PrefixMergeParams& m, cudaStream_t stream)
   return go(prefix_merge_kernel<HD, 1, 4, 2, 4>, 1);
 }
 
-// A 16-key tile's time for one warp of the own rows while most SMs are at the
-// shared ones: an SM's copies take 54 GB/s then (1.4 us when all SMs copy).
-double own_tile_us(int D) { return D == 64 ? 0.6 : 1.0; }
+// Bytes of own rows an SM takes in a us where HBM has more (24 SMs alone, 256
+// requests of up to 512 keys, D = 128), and what HBM delivers to all.
+constexpr float kOwnBytesPerUs = 105e3f, kHbmBytesPerUs = 7.8e6f;
 
 template <int HD>
 cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
@@ -755,8 +766,9 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   CUtensorMap tko = tk, tvo = tv;  // the own rows, in boxes of their tile
   const bool listed = a.own_plan.fits;
-  if (listed && (!kv_map(&tko, d.k, HD, paged ? d.block_size : d.S_cap, paged ? heads : d.B * d.Hkv, kOwnTile) ||
-                 !kv_map(&tvo, d.v, HD, paged ? d.block_size : d.S_cap, paged ? heads : d.B * d.Hkv, kOwnTile)))
+  const int own_rows_n = paged ? d.block_size : d.S_cap, own_heads = paged ? heads : d.B * d.Hkv;
+  if (listed && (!kv_tile_map(&tko, d.k, HD, own_rows_n, own_heads, kOwnTile) ||
+                 !kv_tile_map(&tvo, d.v, HD, own_rows_n, own_heads, kOwnTile)))
     return cudaErrorInvalidValue;
   const SharedPrefixLayout lay = shared_prefix_layout(a);
   const int n_own = lay.n_own, n_slots = lay.n_slots;
@@ -816,12 +828,19 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   gp.listed = listed;
   gp.adaptive = listed && a.plan.adaptive;
   gp.early = listed ? (gp.sms - gp.n_cand % gp.sms) % gp.sms : 0;
-  gp.start = float(a.plan.start_us);
-  gp.kv_tile = float(a.plan.tile_us);
-  gp.merge = float(a.plan.merge_us);
-  gp.own_tile = float(own_tile_us(HD)) / kOwnWarps;
-  gp.lead_in = 4.f;
+  // (fitted, with hbm and own_sm, to the times of 12 shapes -- 32 to 512 requests
+  // behind 4,096 to 65,536 rows, D = 64 and 128 -- in 1 to 50 shares: what is
+  // chosen is 3 % slower than the best of these in the mean, 11 % at most)
+  const bool single = a.plan.n_tiles == 1;
+  gp.start = single ? 5.f : 8.5f;
+  gp.kv_tile = (single ? 1.25f : 1.75f) * (HD == 64 ? 0.5f : 1.f);
+  gp.merge = float(2.0 * d.B * d.Hq * HD * 4 / 18e6);
+  gp.own_sm = kOwnBytesPerUs / (kOwnTile * HD * 4);
+  gp.hbm = kHbmBytesPerUs / (kOwnTile * HD * 4);
+  gp.kv_heads = d.Hkv;
+  gp.lead_in = 6.f;
   gp.follow = 8.f;
+  gp.rest = 2.f;
   const int n_ctas = gp.adaptive ? gp.sms + gp.n_cand : gp.n_cand + (listed ? gp.sms : 0);
   static std::once_flag once;
   static cudaError_t cfg_err = cudaSuccess;
@@ -886,12 +905,12 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sm
   p.units = p.n_tiles == 1 ? 1 : (p.n_tiles + 1) / 2;
   const long units = long(p.units) * Hkv;
   const int tiles = (max_prefix + BN - 1) / BN;
-  p.start_us = p.n_tiles == 1 ? 5.0 : 7.0;
-  p.tile_us = (p.n_tiles == 1 ? 1.5 : 1.8) * (D == 64 ? 0.6 : 1.0);
-  p.merge_us = 2.0 * B * Hq * D * 4 / 5e6;
+  const double start_us = p.n_tiles == 1 ? 5.0 : 7.0;
+  const double tile_us = (p.n_tiles == 1 ? 1.5 : 1.8) * (D == 64 ? 0.6 : 1.0);
+  const double merge_us = 2.0 * B * Hq * D * 4 / 5e6;
   auto time_of = [&](int n) {
     const long waves = (units * n + num_sms - 1) / num_sms;
-    return double(waves) * (p.start_us + p.tile_us * ((tiles + n - 1) / n)) + p.merge_us * n;
+    return double(waves) * (start_us + tile_us * ((tiles + n - 1) / n)) + merge_us * n;
   };
   const int one_wave = int(std::max(1L, std::min<long>({long(tiles), num_sms / units, long(kMaxShares)})));
   p.n_split = 1;
@@ -935,7 +954,7 @@ OwnRowsPlan own_rows_plan(int B, int Hq, int Hkv, int max_kv_len) {
   // A warp's range holds at least min_tiles tiles (but for the early CTAs'
   // part where that is all of a range), so that a unit has at most
   // (tiles - 2) / min_tiles + 3 partials: 34 or fewer.
-  p.min_tiles = std::max(2, (tiles + 31) / 32);
+  p.min_tiles = std::max(1, (tiles + 31) / 32);
   p.n_slots = tiles < 2 ? 1 : (tiles - 2) / p.min_tiles + 3;
   return p;
 }

@@ -61,6 +61,16 @@ inline bool encode_bf16_rows(CUtensorMap* map, const void* base, uint64_t cols, 
   return encode_bf16(map, base, 3, dims, strides, box);
 }
 
+// The same tensor with its rows in halves of 64 columns, as a 4-D tensor (column,
+// row, half, head): a box holds box_rows whole rows, one half after the other.
+inline bool encode_bf16_tiles(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t heads,
+                              uint32_t box_rows) {
+  const cuuint64_t dims[4] = {64, rows, cols / 64, heads};
+  const cuuint64_t strides[3] = {cols * 2, 128, rows * cols * 2};
+  const cuuint32_t box[4] = {64, box_rows, uint32_t(cols / 64), 1};
+  return encode_bf16(map, base, 4, dims, strides, box);
+}
+
 // The queries [B][Hkv * n_rep][cols] of one decode step as a 4-D tensor
 // (column, head in its KV head's group, request, KV head): a box holds the
 // n_rep query heads of one KV head for rpt requests, 64 columns wide, as rows
@@ -76,6 +86,8 @@ inline bool encode_bf16_query_rows(CUtensorMap* map, const void* base, int cols,
 // The map of a K or V cache [heads][rows][D] with boxes of box_rows rows, kept
 // for recently used caches (decode_mma.cu).
 bool kv_map(CUtensorMap* out, const void* base, int D, int rows, int heads, int box_rows = 64);
+// The same with boxes of whole rows (encode_bf16_tiles).
+bool kv_tile_map(CUtensorMap* out, const void* base, int D, int rows, int heads, int box_rows);
 // The map of a step's queries (encode_bf16_query_rows), kept alike.
 bool query_map(CUtensorMap* out, const void* base, int D, int n_rep, int B, int Hkv, int rpt);
 
