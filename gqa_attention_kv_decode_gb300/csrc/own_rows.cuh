@@ -120,8 +120,9 @@ struct OwnCfg {
   static constexpr int SLOTB = HALVES * HALFB;       // K, or V, of a tile
   static constexpr int NSLOT = D == 128 ? 3 : 6;     // 24 KB a warp
   static constexpr int WARPB = NSLOT * SLOTB;
-  // (behind the barriers of the shared rows' work, which a CTA may have set up
-  // before it learns that it has no part in it)
+  // (behind what a CTA with a share of the shared rows may have set up before it
+  // learns that it has none: these barriers are initialised while others there
+  // are still being ended)
   static constexpr int OFF_BAR = kOwnWarps * WARPB + 1024;
   static constexpr int N_BARS = 2 * NSLOT * kOwnWarps + 1;  // full and empty of each slot; one for the tests
   static constexpr int OFF_SUM = OFF_BAR + N_BARS * 8;

@@ -284,6 +284,10 @@ __global__ void __launch_bounds__(NTHR, 1)
   if (cand) at_own = split >= n_used;
   if (at_own) {  // no share for this CTA: the own rows, if it has a part in them
     if (cand && warp == 9) tmem_dealloc(tmem, TMEM_COLS);
+    if (cand && tid < C::N_BARS) {  // (slots of the own rows lie over these)
+      mbar_inval(&bars[tid]);
+      fence_proxy_async_smem();
+    }
     OwnRole r;
     if (grid.adaptive) {
       r.late = n_used * grid.per_share;  // the CTAs at the shared rows

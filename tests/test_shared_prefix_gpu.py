@@ -187,6 +187,31 @@ def test_capacity_sized_plans(P):
     parity.check(f64(c.dense()), c.oracle(), "bf16")
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,B", [(32, 8, 128, 80), (14, 2, 64, 150), (40, 2, 128, 64), (16, 1, 64, 130)])
+@pytest.mark.parametrize("P", [0, 129, 2500])
+@pytest.mark.parametrize("own", ["none", "one", "full", "ragged", "last"])
+def test_plans_that_follow_the_lengths(Hq, Hkv, D, B, P, own):
+    """Grids of several SMs' worth of shares, whose number the lengths decide."""
+    S = 300
+    lens = {"none": [0] * B, "one": [1] * B, "full": [S] * B, "ragged": lens_of(B, S, P),
+            "last": [0] * (B - 1) + [S]}[own]
+    c = Case(B, Hq, Hkv, D, P, lens, P_cap=2500, S=S, seed=P + B)
+    ws = binding.decode_shared_prefix_workspace(B, Hq, Hkv, D, 2500, S)
+    ws[256:] = 0xFF
+    parity.check(f64(c.dense(workspace=ws)), c.oracle(), "bf16")
+    empty = P == 0 and min(lens) == 0
+    assert binding.gqa_attn_read_device_status(ws) == (binding.GQA_DEV_EMPTY_REQUEST if empty else 0)
+
+
+@pytest.mark.parametrize("S", [1, 15, 16, 17, 31, 32, 33, 47, 48, 63, 64, 65])
+@pytest.mark.parametrize("D", [64, 128])
+def test_own_rows_of_every_tile_remainder(S, D):
+    c = Case(S + 1, 8, 2, D, 70, range(S + 1), seed=S)
+    ref = c.oracle()
+    parity.check(f64(c.dense()), ref, "bf16")
+    parity.check(f64(c.paged(64)), ref, "bf16", "paged")
+
+
 @pytest.mark.parametrize("raw,P", [(-4, 0), (301, 300), (2 ** 31 - 1, 300), (-2 ** 31, 0)])
 def test_lengths_out_of_range_are_clamped_and_reported(raw, P):
     c = Case(3, 8, 2, 64, P, [20, 7, 0], P_cap=300, S=20)
