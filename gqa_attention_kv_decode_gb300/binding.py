@@ -68,6 +68,7 @@ EXPORTED = (
     "gqa_attn_set_plan_override",
     "gqa_attn_set_prefill_interleave_override",
     "gqa_attn_set_wait_test",
+    "gqa_attn_set_pointer_checks",
     "gqa_attn_read_prefill_status",
     "gqa_attn_clear_prefill_status",
 )
@@ -154,6 +155,8 @@ def lib() -> ctypes.CDLL:
     L.gqa_attn_set_prefill_interleave_override.restype = i32
     L.gqa_attn_set_wait_test.argtypes = [ctypes.c_uint64]
     L.gqa_attn_set_wait_test.restype = i32
+    L.gqa_attn_set_pointer_checks.argtypes = [i32]
+    L.gqa_attn_set_pointer_checks.restype = i32
     L.gqa_attn_read_prefill_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
     L.gqa_attn_read_prefill_status.restype = i32
     L.gqa_attn_clear_prefill_status.argtypes = [vp]
@@ -190,10 +193,6 @@ def _call():
         from . import _torch_call
         _call_mod = _torch_call
     return _call_mod
-
-
-def _handle(stream):
-    return None if stream is None else _stream(stream)  # None: the current stream, read natively
 
 
 def _stream(stream):
@@ -245,6 +244,16 @@ def gqa_attn_set_wait_test(stall_ns=0) -> None:
     that never lands (a wait of stall_ns on a barrier nothing arrives on), so
     they report GQA_DEV_WAIT_TIMEOUT; 0 turns it off."""
     _check(lib().gqa_attn_set_wait_test(int(stall_ns)), "gqa_attn_set_wait_test")
+
+
+def gqa_attn_set_pointer_checks(on=True) -> bool:
+    """Whether this thread's calls look up if their pointers are the current
+    device's (the calls of a serving step see that by the tensors).  Returns
+    the setting before."""
+    before = lib().gqa_attn_set_pointer_checks(int(on))
+    if before < 0:
+        _check(before, "gqa_attn_set_pointer_checks")
+    return bool(before)
 
 
 def gqa_attn_set_prefill_interleave_override(from_pair=-1) -> None:
@@ -325,9 +334,11 @@ def gqa_attn_decode_shared_prefix(q, k_prefix, v_prefix, prefix_len, k, v, kv_le
     """q, o [B,Hq,1,D]; k_prefix, v_prefix [Hkv,P_cap,D] shared by the batch,
     prefix_len int32 [1] or None; k, v [B,Hkv,S_cap,D] own rows behind them,
     kv_lens int32 [B] or None."""
-    rc = _call().decode_shared_prefix(q, k_prefix, v_prefix, prefix_len, k, v, kv_lens, o, scale, workspace,
-                                      max_prefix_len, max_kv_len, _handle(stream))
-    _check(rc, "gqa_attn_decode_shared_prefix")
+    rc = (_call_mod or _call()).decode_shared_prefix(
+        q, k_prefix, v_prefix, prefix_len, k, v, kv_lens, o, scale, workspace, max_prefix_len, max_kv_len,
+        None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "gqa_attn_decode_shared_prefix")
 
 
 def gqa_attn_decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, prefix_len, block_table, kv_lens, o, scale,
@@ -335,9 +346,11 @@ def gqa_attn_decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, prefix_
     """q, o [B,Hq,1,D]; k_pool, v_pool [num_blocks,Hkv,block_size,D]; the shared
     rows' blocks prefix_table int32 [blocks] (prefix_len int32 [1] rows, or
     None: max_prefix_len), the own rows' block_table int32 [B,max_blocks]."""
-    rc = _call().decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, prefix_len, block_table, kv_lens, o, scale,
-                                            workspace, max_prefix_len, max_kv_len, _handle(stream))
-    _check(rc, "gqa_attn_decode_shared_prefix_paged")
+    rc = (_call_mod or _call()).decode_shared_prefix_paged(
+        q, k_pool, v_pool, prefix_table, prefix_len, block_table, kv_lens, o, scale, workspace, max_prefix_len,
+        max_kv_len, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "gqa_attn_decode_shared_prefix_paged")
 
 
 def gqa_attn_step_tables(prior_lens, new_lens, block_table, free_blocks, free_count, kv_lens, q_lens, q_starts,
@@ -346,10 +359,11 @@ def gqa_attn_step_tables(prior_lens, new_lens, block_table, free_blocks, free_co
     grown in place from the stack free_blocks [num_blocks] (or both, and the
     counts, None for a dense cache of block_size rows a request); writes
     kv_lens, q_lens [B], q_starts [B+1], positions, slots, q_slots [T]."""
-    rc = _call().step_tables(prior_lens, new_lens, block_table, free_blocks, free_count, kv_lens, q_lens, q_starts,
-                             positions, slots, q_slots, free_count_out, block_size, q_rows, workspace,
-                             _handle(stream))
-    _check(rc, "gqa_attn_step_tables")
+    rc = (_call_mod or _call()).step_tables(
+        prior_lens, new_lens, block_table, free_blocks, free_count, kv_lens, q_lens, q_starts, positions, slots,
+        q_slots, free_count_out, block_size, q_rows, workspace, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "gqa_attn_step_tables")
 
 
 def gqa_attn_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, slots, q_slots, q_out, k_cache,
@@ -358,9 +372,11 @@ def gqa_attn_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, s
     k_weight [D] or None) and rotated (cos_sin fp32 [max_pos,rot_dim] or None)
     into q_out [q_groups,Hq,q_rows,D] rows q_slots (None: row t) and k_cache,
     v_cache [num_blocks,Hkv,block_size,D] rows slots; negative slots: padding."""
-    rc = _call().rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, slots, q_slots, q_out, k_cache,
-                             v_cache, adjacent, workspace, _handle(stream))
-    _check(rc, "gqa_attn_rope_append")
+    rc = (_call_mod or _call()).rope_append(
+        q, k, v, q_weight, k_weight, eps, cos_sin, positions, slots, q_slots, q_out, k_cache, v_cache, adjacent,
+        workspace, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "gqa_attn_rope_append")
 
 
 def gqa_attn_quantize_q4(src, codes, scale, bias, dst_row0=0, rows=None, group_size=64, stream=None):

@@ -99,7 +99,12 @@ using namespace gqa;
 
 namespace {
 
+// Off while the calling thread's caller vouches for its pointers
+// (gqa_attn_set_pointer_checks).
+thread_local bool t_pointer_checks = true;
+
 bool is_device_ptr(const void* p, int dev) {
+  if (!t_pointer_checks) return true;
   cudaPointerAttributes attr;
   if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
     cudaGetLastError();  // clear the sticky-free error state of this query
@@ -244,6 +249,13 @@ GQA_ATTN_API int gqa_attn_set_wait_test(uint64_t stall_ns) {
   if (stall_ns > kWaitLimitNs) return GQA_ERR_INVALID_ARG;
   g_wait_test_ns.store(stall_ns, std::memory_order_relaxed);
   return GQA_OK;
+}
+
+GQA_ATTN_API int gqa_attn_set_pointer_checks(int on) {
+  if (on != 0 && on != 1) return GQA_ERR_INVALID_ARG;
+  const int before = t_pointer_checks ? 1 : 0;
+  t_pointer_checks = on != 0;
+  return before;
 }
 
 GQA_ATTN_API const char* gqa_attn_status_string(int status) {

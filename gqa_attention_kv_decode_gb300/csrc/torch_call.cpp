@@ -4,13 +4,15 @@
 //
 // A step makes these calls for every layer, and each passes ten to twenty
 // tensors whose checks cost 0.2 us apiece from Python, besides 0.1 us per
-// argument in ctypes: 10.4, 12.5 and 12.7 us a call for the tables, the append
-// and the shared-prefix decode, of which the library and its launches take 3
-// to 5.  The functions return the C entry point's status; what is wrong
-// with a tensor raises TypeError or ValueError.  No exception crosses the C
-// interfaces on either side.
+// argument in ctypes and 0.06 us for each pointer that the library looks up
+// (which the tensors spare it): 10.4, 12.5 and 15.5 us a call for the tables,
+// the append and the shared-prefix decode that way, 3.0, 3.2 and 5.1 this way,
+// of which the launches take 1.5 each.  The functions return the C entry
+// point's status; what is wrong with a tensor raises TypeError or ValueError.
+// No exception crosses the C interfaces on either side.
 #include <Python.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -101,11 +103,32 @@ void* stream_of(PyObject* o) {
   return reinterpret_cast<void*>(static_cast<uintptr_t>(integer(o)));
 }
 
+// Around a library call: no lookup of pointers that are known to be the current
+// device's, as all of them are where the tensors say so.  (Otherwise the
+// library looks them up, and refuses the call with its own error.)
+class Pointers {
+ public:
+  Pointers(std::initializer_list<const Tensor*> all) {
+    const auto device = c10::cuda::current_device();
+    for (const Tensor* t : all)
+      if (t != nullptr && !(t->is_cuda() && t->get_device() == device)) return;
+    before_ = gqa_attn_set_pointer_checks(0);
+  }
+  ~Pointers() {
+    if (before_ > 0) gqa_attn_set_pointer_checks(before_);
+  }
+  Pointers(const Pointers&) = delete;
+
+ private:
+  int before_ = 0;
+};
+
 struct Workspace {
+  const Tensor* t;
   void* p;
   size_t bytes;
   explicit Workspace(PyObject* o) {
-    const Tensor* t = tensor(o);
+    t = tensor(o);
     p = dense(t);
     bytes = size_t(t->numel()) * t->element_size();
   }
@@ -140,6 +163,7 @@ int step_tables(PyObject* const* a) {
             rows = size(integer(a[13]));
   const Workspace ws(a[14]);
   void* const stream = stream_of(a[15]);
+  const Pointers known({prior, fresh, table, stack, count, kv, q_lens, starts, pos, slots, q_slots, count_out, ws.t});
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = gqa_attn_step_tables(p_prior, p_new, p_table, p_stack, p_count, p_kv, p_q, p_starts, p_pos, p_slots, p_qs,
@@ -187,6 +211,7 @@ int rope_append(PyObject* const* a) {
             dt = dtype_code(q);
   const Workspace ws(a[14]);
   void* const stream = stream_of(a[15]);
+  const Pointers known({q, k, v, wq, wk, cs, pos, slots, q_slots, q_out, kc, vc, ws.t});
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = gqa_attn_rope_append(qp, kp, vp, qs, ks, vs, pq, pk, eps, pcs, ppos, pslots, pqs, po, pkc, pvc, t, hq, hkv, d,
@@ -218,6 +243,7 @@ int decode_shared_prefix(PyObject* const* a) {
             mk = bound(a[11], S), dt = dtype_code(q);
   const Workspace ws(a[9]);
   void* const stream = stream_of(a[12]);
+  const Pointers known({q, kp, vp, plen, k, v, lens, o, ws.t});
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = gqa_attn_decode_shared_prefix(pq, pkp, pvp, pp, pk, pv, pl, po, b, hq, hkv, d, p, mp, s, mk, scale, dt, ws.p,
@@ -248,6 +274,7 @@ int decode_shared_prefix_paged(PyObject* const* a) {
             mk = size(integer(a[11])), dt = dtype_code(q);
   const Workspace ws(a[9]);
   void* const stream = stream_of(a[12]);
+  const Pointers known({q, kp, vp, ptable, plen, table, lens, o, ws.t});
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = gqa_attn_decode_shared_prefix_paged(pq, pk, pv, pt, pp, tb, pl, po, b, hq, hkv, d, bs, nb, np, mb, mp, mk,

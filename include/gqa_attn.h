@@ -499,6 +499,15 @@ GQA_ATTN_API int gqa_attn_set_prefill_interleave_override(int from_pair);
  * otherwise GQA_OK.  Same threading rules as gqa_attn_set_plan_override. */
 GQA_ATTN_API int gqa_attn_set_wait_test(uint64_t stall_ns);
 
+/* Whether the calling thread's calls look up if their pointers are memory of
+ * the current device (on = 1, the initial setting of every thread; the lookups
+ * are 0.06 us each, about a fifth of a call with a dozen of them).  A caller
+ * that knows it of all pointers of a call, such as a binding that has the
+ * tensors, may turn it off around that call (on = 0) and put it back behind it;
+ * null and misaligned pointers are refused either way.  Returns the setting
+ * before (0 or 1), or GQA_ERR_INVALID_ARG for another value of `on`. */
+GQA_ATTN_API int gqa_attn_set_pointer_checks(int on);
+
 /* ---------------------------------------------------------------------------
  * Single-token decode without any caller-provided or allocated scratch.
  *
