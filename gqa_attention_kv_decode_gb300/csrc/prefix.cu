@@ -748,9 +748,12 @@ cudaError_t launch_prefix_merge(const PrefixMergeParams& m, cudaStream_t stream)
   if (room >= 8) return go(prefix_merge_kernel<HD, 8, 4, 4, 1>, 8);
   if (room >= 4) return go(prefix_merge_kernel<HD, 4, 8, 4, 1>, 4);
   if (room >= 2) return go(prefix_merge_kernel<HD, 2, 8, 4, 1>, 2);
-  if (m.n_split > 4) return go(prefix_merge_kernel<HD, 1, 8, 4, 1>, 1);
-  // many rows, few partials each: as many warps as fit an SM
-  return go(prefix_merge_kernel<HD, 1, 4, 2, 4>, 1);
+  // Several waves, or few partials: as many warps as fit an SM, each asking for
+  // less at once (159 requests of 32 heads, D = 128, behind 153 of 4,153 rows:
+  // 43.5 us, 46 the other way; 64 behind 32,768: 55.6 the other way, 56.5 with
+  // one block an SM).
+  if ((HD == 128 && room < 1) || m.n_split <= 4) return go(prefix_merge_kernel<HD, 1, 4, 2, 4>, 1);
+  return go(prefix_merge_kernel<HD, 1, 8, 2, 3>, 1);
 }
 
 // Bytes of own rows an SM takes in a us where HBM has more (24 SMs alone, 256
