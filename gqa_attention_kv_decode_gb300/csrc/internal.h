@@ -159,7 +159,6 @@ struct OwnRowsPlan {
   bool fits;            // else the decode kernel takes them
   int n_hc, nrep_cta;   // query-head chunks per KV head, heads of a chunk
   int units;            // (KV head, chunk) pairs of a request
-  int min_tiles;        // tiles of a warp's range of the list, at least
   int n_slots;          // partials of a row, at most
 };
 OwnRowsPlan own_rows_plan(int B, int Hq, int Hkv, int max_kv_len);

@@ -62,8 +62,8 @@ struct OwnRowsParams {
   const int32_t* block_table;  // or null: dense [B][Hkv][S_cap][D]
   int block_size, max_blocks, num_blocks;
   int B, Hq, Hkv, n_rep, n_hc, nrep_cta, units, max_kv_len;
-  int min_tiles;    // tiles of a warp's range, at least
-  int n_slots;    // partial slots of a row (the first ones are the own rows')
+  int n_own;      // partial slots of a row for the own rows
+  int n_slots;    // and of all partials of a row (the own rows' are the first)
   float qscale;   // scale * log2(e)
   uint32_t* status;
   float2* ml;
@@ -126,7 +126,8 @@ struct OwnCfg {
   static constexpr int OFF_BAR = kOwnWarps * WARPB + 1024;
   static constexpr int N_BARS = 2 * NSLOT * kOwnWarps + 1;  // full and empty of each slot; one for the tests
   static constexpr int OFF_SUM = OFF_BAR + N_BARS * 8;
-  static constexpr int OFF_ABORT = OFF_SUM + kOwnThreads / 32 * 4;
+  static constexpr int OFF_MAX = OFF_SUM + kOwnThreads / 32 * 4;
+  static constexpr int OFF_ABORT = OFF_MAX + kOwnThreads / 32 * 4;
   static constexpr int OFF_STARTS = OFF_ABORT + 4;
   static constexpr int OFF_LENS = OFF_STARTS + (kOwnMaxRequests + 1) * 4;
   static constexpr int SMEM = OFF_LENS + kOwnMaxRequests * 4 + 1024;
@@ -142,7 +143,7 @@ struct Cursor {
 
 constexpr int BAR_OWN = 5;  // named barrier of a CTA's threads at the own rows
 
-// The lengths and the prefix sums of the list, starts[b] = tiles before request
+// The lengths, the longest of each warp's, and the prefix sums of the list, starts[b] = tiles before request
 // b, into shared memory (by the whole CTA; grid_dependency_wait has returned), and its barriers.
 // `report`: this CTA reports lengths that had to be clamped.
 template <int D>
@@ -151,6 +152,7 @@ __device__ __forceinline__ void own_scan(unsigned char* smem, const OwnRowsParam
   constexpr int NTHREADS = kOwnThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int* warp_sum = reinterpret_cast<int*>(smem + C::OFF_SUM);
+  int* warp_max = reinterpret_cast<int*>(smem + C::OFF_MAX);
   int* starts = reinterpret_cast<int*>(smem + C::OFF_STARTS);
   int* lens = reinterpret_cast<int*>(smem + C::OFF_LENS);
   const int per = (p.B + NTHREADS - 1) / NTHREADS;  // consecutive requests a thread sums
@@ -159,7 +161,7 @@ __device__ __forceinline__ void own_scan(unsigned char* smem, const OwnRowsParam
     fence_barrier_init();
   }
   if (tid == 0) *reinterpret_cast<volatile int*>(smem + C::OFF_ABORT) = 0;
-  int sum = 0;
+  int sum = 0, longest = 0;
   bool clamped = false;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
@@ -168,6 +170,7 @@ __device__ __forceinline__ void own_scan(unsigned char* smem, const OwnRowsParam
     const int L = min(max(raw, 0), p.max_kv_len);
     clamped |= L != raw;
     lens[b] = L;
+    longest = max(longest, L);
     sum += L > 0 ? ((L + kOwnTile - 1) / kOwnTile + kOwnLead) * p.units : 0;
     starts[b + 1] = sum;
   }
@@ -178,7 +181,8 @@ __device__ __forceinline__ void own_scan(unsigned char* smem, const OwnRowsParam
     const int v = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += v;
   }
-  if (lane == 31) warp_sum[warp] = incl;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) warp_sum[warp] = incl, warp_max[warp] = longest;
   named_bar_sync(BAR_OWN, NTHREADS);
   int before = incl - sum;
   for (int i = 0; i < warp; ++i) before += warp_sum[i];
@@ -311,8 +315,16 @@ __device__ __forceinline__ void own_rows(unsigned char* smem, const CUtensorMap*
   const int* lens = reinterpret_cast<const int*>(smem + C::OFF_LENS);
   const int N = starts[p.B];
   if (N == 0) return;
+  // Tiles of a range, at least: as few as leave the longest unit, with what it
+  // has in both parts of the cut, a slot for each of its partials.
+  const int* warp_max = reinterpret_cast<const int*>(smem + C::OFF_MAX);
+  int longest = 0;
+#pragma unroll
+  for (int i = 0; i < kOwnThreads / 32; ++i) longest = max(longest, warp_max[i]);
+  const int most = (longest + TILE - 1) / TILE;
+  const unsigned min_tiles = most < 2 ? 1u : unsigned(most - 2) / unsigned(p.n_own - 2) + 1u;
   const OwnCut cut = OwnCut::of(unsigned(N), unsigned(role.early * kOwnWarps), unsigned(role.late * kOwnWarps),
-                                role.head_start, unsigned(p.min_tiles));
+                                role.head_start, min_tiles);
   // warp `who`'s range: neighbours in the list run on different SMs
   constexpr int PER = (kOwnWarps + kOwnCopiers - 1) / kOwnCopiers;  // warps a copying warp serves
   const bool copies = warp >= kOwnWarps;

@@ -818,7 +818,7 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   o.nrep_cta = a.own_plan.nrep_cta;
   o.units = a.own_plan.units;
   o.max_kv_len = d.max_kv_len;
-  o.min_tiles = a.own_plan.min_tiles;
+  o.n_own = n_own;
   o.n_slots = n_slots;
   o.qscale = p.qk_scale_log2;
   o.status = p.status;
@@ -958,11 +958,11 @@ OwnRowsPlan own_rows_plan(int B, int Hq, int Hkv, int max_kv_len) {
   p.units = Hkv * p.n_hc;
   const int tiles = (max_kv_len - 1) / kOwnTile + 1;
   p.fits = B <= kOwnMaxRequests && long(B) * p.units * (long(tiles) + kOwnLead) <= 0x7fffffffL / 5;
-  // A warp's range holds at least min_tiles tiles (but for the early CTAs'
-  // part where that is all of a range), so that a unit has at most
-  // (tiles - 2) / min_tiles + 3 partials: 34 or fewer.
-  p.min_tiles = std::max(1, (tiles + 31) / 32);
-  p.n_slots = tiles < 2 ? 1 : (tiles - 2) / p.min_tiles + 3;
+  // A unit of n tiles has at most (n - 2) / m + 3 partials if the ranges have m
+  // tiles (ceil(n1 / m) + ceil(n2 / m) where the cut's two parts share it): 34
+  // slots at most; the kernel takes the m that the longest request leaves.
+  const int min_tiles = std::max(1, (tiles + 31) / 32);
+  p.n_slots = tiles < 2 ? 1 : (tiles - 2) / min_tiles + 3;
   return p;
 }
 

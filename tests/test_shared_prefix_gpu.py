@@ -212,6 +212,15 @@ def test_own_rows_of_every_tile_remainder(S, D):
     parity.check(f64(c.paged(64)), ref, "bf16", "paged")
 
 
+@pytest.mark.parametrize("lens", [[33, 0, 1, 32], [1055, 1056, 1057, 3], [4096, 1, 4095, 0], [1, 1, 1, 1],
+                                  [2100, 31, 64, 700]])
+@pytest.mark.parametrize("Hq,Hkv,D", [(14, 2, 64), (28, 4, 128), (40, 2, 128)])
+def test_capacity_sized_own_rows(Hq, Hkv, D, lens):
+    """Partials of a row are as many as the lengths ask for, in slots planned for 4096 own rows."""
+    c = Case(4, Hq, Hkv, D, 200, lens, P_cap=8192, S=4096, seed=sum(lens))
+    parity.check(f64(c.dense()), c.oracle(), "bf16")
+
+
 @pytest.mark.parametrize("raw,P", [(-4, 0), (301, 300), (2 ** 31 - 1, 300), (-2 ** 31, 0)])
 def test_lengths_out_of_range_are_clamped_and_reported(raw, P):
     c = Case(3, 8, 2, 64, P, [20, 7, 0], P_cap=300, S=20)
