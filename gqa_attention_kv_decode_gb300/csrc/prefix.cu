@@ -837,7 +837,7 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   gp.early = listed ? (gp.sms - gp.n_cand % gp.sms) % gp.sms : 0;
   // (fitted, with hbm and own_sm, to the times of 12 shapes -- 32 to 512 requests
   // behind 4,096 to 65,536 rows, D = 64 and 128 -- in 1 to 50 shares: what is
-  // chosen is 3 % slower than the best of these in the mean, 11 % at most)
+  // chosen is 2 % slower than the best of these in the mean, 9 % at most)
   const bool single = a.plan.n_tiles == 1;
   gp.start = single ? 5.f : 8.5f;
   gp.kv_tile = (single ? 1.25f : 1.75f) * (HD == 64 ? 0.5f : 1.f);
@@ -899,10 +899,12 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
 // Row tiles and key shares.  A unit (a pair of row tiles, or the one tile of
 // a KV head) times a share is a CTA; one CTA fits an SM.  A share's time is
 // its start and epilogue and its KV tiles (measured, in us); the partials of
-// every share go to memory and back (at 5 TB/s).  One wave of shares is cut by
-// the kernel (choose_shares) where it fills most SMs; more waves only where the
-// units alone leave many SMs without one and the waves' estimate is well below
-// that of one.
+// every share go to memory and back (at 5 TB/s); and every CTA takes an SM from
+// the own rows and delays the last one's start (one request of 8/8 x 64 behind
+// 1,321 rows: 10.3 us in 11 shares of a KV tile, 9.0 in four of three).  One
+// wave of shares is cut by the kernel (choose_shares) where it fills most SMs;
+// more waves only where the units alone leave many SMs without one and the
+// waves' estimate is well below that of one.
 PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sms) {
   PrefixPlan p;
   const int n_rep = Hq / Hkv;
@@ -912,12 +914,13 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sm
   p.units = p.n_tiles == 1 ? 1 : (p.n_tiles + 1) / 2;
   const long units = long(p.units) * Hkv;
   const int tiles = (max_prefix + BN - 1) / BN;
-  const double start_us = p.n_tiles == 1 ? 5.0 : 7.0;
-  const double tile_us = (p.n_tiles == 1 ? 1.5 : 1.8) * (D == 64 ? 0.6 : 1.0);
+  const bool single = p.n_tiles == 1;
+  const double start_us = single ? 5.0 : 7.0, cta_us = single ? 0.03 : 0.07;
+  const double tile_us = single ? (D == 64 ? 0.44 : 1.1) : (D == 64 ? 1.1 : 1.8);
   const double merge_us = 2.0 * B * Hq * D * 4 / 5e6;
   auto time_of = [&](int n) {
     const long waves = (units * n + num_sms - 1) / num_sms;
-    return double(waves) * (start_us + tile_us * ((tiles + n - 1) / n)) + merge_us * n;
+    return double(waves) * (start_us + tile_us * ((tiles + n - 1) / n)) + (merge_us + cta_us * units) * n;
   };
   const int one_wave = int(std::max(1L, std::min<long>({long(tiles), num_sms / units, long(kMaxShares)})));
   p.n_split = 1;
@@ -927,9 +930,9 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int max_prefix, int num_sm
       best = time_of(n);
       p.n_split = n;
     }
-  // Few CTAs: the own rows have most SMs to themselves, and the shares stay as
+  // Few CTAs: the own rows have SMs enough to themselves, and the shares stay as
   // planned (working them out again costs a microsecond at the start).
-  p.adaptive = units <= num_sms && 2 * units * p.n_split > num_sms;
+  p.adaptive = units <= num_sms && 4 * units * p.n_split > 3 * num_sms;
   best *= 0.85;
   for (int n = one_wave + 1; n <= std::min(tiles, 256); ++n)
     if (time_of(n) < best) {
