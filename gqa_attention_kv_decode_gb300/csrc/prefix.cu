@@ -738,13 +738,17 @@ __global__ void __launch_bounds__(256, MB) prefix_merge_kernel(const PrefixMerge
 }
 
 // As many warps a row as keep the grid within a wave (about 20 warps of the
-// merge on an SM), up to eight.
+// merge on an SM), up to eight; of few partials four or one, which have less to
+// join (11 requests of 16 heads, D = 128, two partials each: 10.5 us, 11.0 with
+// eight; 39 of 32 heads, 6 each: 12.9, 14.0 with two).
 template <int HD>
 cudaError_t launch_prefix_merge(const PrefixMergeParams& m, cudaStream_t stream) {
   const long room = 20L * device_sm_count() / m.rows;
   auto go = [&](auto kern, int wpr) {
     return launch_pdl(kern, dim3((m.rows * wpr + 7) / 8), dim3(256), 0, stream, m);
   };
+  if (room >= 4 && m.n_split <= 8 && m.n_own <= 8) return go(prefix_merge_kernel<HD, 4, 2, 2, 1>, 4);
+  if (room >= 2 && m.n_split <= 8 && m.n_own <= 4) return go(prefix_merge_kernel<HD, 1, 8, 4, 1>, 1);
   if (room >= 8) return go(prefix_merge_kernel<HD, 8, 4, 4, 1>, 8);
   if (room >= 4) return go(prefix_merge_kernel<HD, 4, 8, 4, 1>, 4);
   if (room >= 2) return go(prefix_merge_kernel<HD, 2, 8, 4, 1>, 2);
