@@ -136,11 +136,12 @@ __device__ __forceinline__ void store_rows(unsigned char* stage, float* out, lon
 //              grid is sms CTAs, of which those without a share are early, and
 //              n_cand more for the late ones.
 //   otherwise  all shares are used (there are as many KV tiles); the grid is
-//              n_cand CTAs and, with own rows in the list, sms more, the first
-//              of them early, on SMs that (the last wave of) the former leaves.
+//              n_cand CTAs and, with own rows in the list, `early` more on the
+//              SMs that (the last wave of) the former leaves, and `late` ones,
+//              which are left out where the early ones are soon done alone.
 struct GridPlan {
-  int n_cand, per_share, units, sms, early;
-  bool adaptive, listed;
+  int n_cand, per_share, units, sms, early, late;
+  bool adaptive;
   // estimated times in us: a share's start and epilogue, its KV tile, a share's
   // partials to the merge and back, the start of a CTA of own rows, the same
   // behind one of shared rows, and how much later all is done where some are
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   int raw_prefix = p.max_prefix;
   if (p.prefix_len != nullptr) asm volatile("ld.global.b32 %0, [%1];" : "=r"(raw_prefix) : "l"(p.prefix_len));
   const bool direct = !cand && !grid.adaptive;
-  int P = 0, n_kv = 0, n_used = 0;
+  int P = 0, n_kv = 0, n_used = 0, own_tiles = 0;
   auto use_length = [&] {
     P = min(max(raw_prefix, 0), p.max_prefix);
     n_kv = (P + BN - 1) / BN;
@@ -277,7 +278,10 @@ __global__ void __launch_bounds__(NTHR, 1)
   if (!direct) {
     use_length();
     if (cta == 0 && tid == 0 && P != raw_prefix) atomicOr(p.status, GQA_DEV_KVLEN_CLAMPED);
-    if (grid.adaptive) n_used = choose_shares(grid, p.n_split, P, own_total(own));
+    if (grid.adaptive) {
+      own_tiles = own_total(own);
+      n_used = choose_shares(grid, p.n_split, P, own_tiles);
+    }
     if (cta == 0 && tid == 0) *p.shares = n_used;  // for the merge
   }
   bool at_own = !cand;
@@ -295,17 +299,25 @@ __global__ void __launch_bounds__(NTHR, 1)
       r.cta = cta < grid.sms ? cta - r.late : r.early + cta - grid.sms;
     } else {
       r.early = grid.early;
-      r.late = grid.listed ? grid.sms - grid.early : 0;
+      r.late = grid.late;
       r.cta = cand ? r.early + r.late : cta - grid.n_cand;
     }
     if (r.cta >= r.early + r.late) return;
+    auto head_start = [&] {
+      if (n_used == 0 || r.early == 0) return 0.f;
+      const float share = share_time(grid, n_kv, n_used);
+      return (share + grid.follow) * own_rate(grid, n_kv, share, float(r.early)) / float(r.early * kOwnWarps);
+    };
+    if (grid.adaptive) {
+      r.head_start = head_start();
+      // (a late CTA for which the early ones leave nothing)
+      if (r.cta >= r.early && OwnCut::of(unsigned(own_tiles), unsigned(r.early * kOwnWarps),
+                                         unsigned(r.late * kOwnWarps), r.head_start, 1u).head == unsigned(own_tiles))
+        return;
+    }
     own_scan<HD>(smem, own, r.cta == 0);
     if (direct) use_length();
-    r.head_start = 0.f;
-    if (n_used > 0 && r.early > 0) {
-      const float share = share_time(grid, n_kv, n_used);
-      r.head_start = (share + grid.follow) * own_rate(grid, n_kv, share, float(r.early)) / float(r.early * kOwnWarps);
-    }
+    if (!grid.adaptive) r.head_start = head_start();
     own_rows<HD>(smem, &tmKo, &tmVo, own, r);
     return;
   }
@@ -641,8 +653,10 @@ __global__ void __launch_bounds__(256, MB) prefix_merge_kernel(const PrefixMerge
   __shared__ float acc_s[WPR > 1 ? 8 : 1][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = int(blockIdx.x) * (8 / WPR) + warp / WPR, part = warp % WPR;
-  grid_launch_dependents();
   grid_dependency_wait();
+  // (not sooner: the next grid's start would take turns with this work; 0.3 to
+  // 0.6 us of a small call)
+  grid_launch_dependents();
   float acc[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
@@ -831,14 +845,15 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   o.counts = listed ? p.shares + 1 : nullptr;
   o.wait_limit_ns = p.wait_limit_ns;
   o.test_stall_ns = p.test_stall_ns;
+  const int n_kv_max = (a.max_prefix + BN - 1) / BN;
   GridPlan gp = {};
   gp.units = a.plan.units;
   gp.per_share = a.plan.units * d.Hkv;
   gp.n_cand = a.plan.n_split * gp.per_share;
   gp.sms = std::max(1, device_sm_count());
-  gp.listed = listed;
   gp.adaptive = listed && a.plan.adaptive;
   gp.early = listed ? (gp.sms - gp.n_cand % gp.sms) % gp.sms : 0;
+  gp.late = listed ? gp.sms - gp.early : 0;
   // (fitted, with hbm and own_sm, to the times of 12 shapes -- 32 to 512 requests
   // behind 4,096 to 65,536 rows, D = 64 and 128 -- in 1 to 50 shares: what is
   // chosen is 2 % slower than the best of these in the mean, 9 % at most)
@@ -852,7 +867,15 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   gp.lead_in = 6.f;
   gp.follow = 8.f;
   gp.rest = 2.f;
-  const int n_ctas = gp.adaptive ? gp.sms + gp.n_cand : gp.n_cand + (listed ? gp.sms : 0);
+  if (listed && !gp.adaptive && gp.early > 0 && gp.n_cand < gp.sms) {
+    // The most own rows there can be, done by the early CTAs alone: if not (3 us)
+    // after the shares, no late ones, whose start there costs 2 us (16 requests
+    // of up to 512 own rows behind 4,097: 13.5 us with them, 12.7 without).
+    const float share = gp.start + gp.kv_tile * float((n_kv_max + a.plan.n_split - 1) / a.plan.n_split);
+    const float most = float(d.B) * float(a.own_plan.units) * float((d.max_kv_len - 1) / kOwnTile + 1 + kOwnLead);
+    if (gp.lead_in + most / std::min(float(gp.early) * gp.own_sm, gp.hbm) <= share + 3.f) gp.late = 0;
+  }
+  const int n_ctas = gp.adaptive ? gp.sms + gp.n_cand : gp.n_cand + gp.early + gp.late;
   static std::once_flag once;
   static cudaError_t cfg_err = cudaSuccess;
   std::call_once(once, [&] {
