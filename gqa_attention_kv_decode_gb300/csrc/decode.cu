@@ -32,8 +32,8 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
-#include <mutex>
 
+#include "device_once.h"
 #include "gqa_attn.h"
 #include "internal.h"
 #include "merge.cuh"
@@ -553,13 +553,13 @@ template <typename T, int D, int NREP, int R, int NSTAGE, bool PAGED>
 cudaError_t launch_one(const DecodeParams& p, dim3 grid, cudaStream_t stream) {
   using C = Cfg<T, D, NREP, R, NSTAGE>;
   auto kern = decode_split_kernel<T, D, NREP, R, NSTAGE, PAGED>;
-  static std::once_flag once;  // per instantiation; the attributes are per function
-  static cudaError_t cfg_err = cudaSuccess;
-  std::call_once(once, [&] {
-    cfg_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (cfg_err == cudaSuccess)  // the largest shared-memory carveout
-      cfg_err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                     cudaSharedmemCarveoutMaxShared);
+  static DeviceOnce once;  // per instantiation; the attributes are per function and device
+  const cudaError_t cfg_err = once.run([&] {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    // the largest shared-memory carveout
+    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                cudaSharedmemCarveoutMaxShared);
   });
   if (cfg_err != cudaSuccess) return cfg_err;
   return launch_pdl(kern, grid, dim3(C::NTHR), C::SMEM, stream, p);

@@ -28,6 +28,7 @@
 #include <cmath>
 #include <mutex>
 
+#include "device_once.h"
 #include "gqa_attn.h"
 #include "internal.h"
 #include "merge.cuh"
@@ -496,13 +497,13 @@ cudaError_t launch_mma(const CUtensorMap& tk, const CUtensorMap& tv, const MmaPa
                        cudaStream_t stream) {
   using C = MmaCfg<D, NSTAGE, NW>;
   auto kern = decode_mma_kernel<D, NSTAGE, NW, PAGED>;
-  static std::once_flag once;
-  static cudaError_t cfg_err = cudaSuccess;
-  std::call_once(once, [&] {
-    cfg_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (cfg_err == cudaSuccess)  // two CTAs per SM need the largest shared-memory carveout
-      cfg_err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                     cudaSharedmemCarveoutMaxShared);
+  static DeviceOnce once;  // per instantiation; the attributes are per function and device
+  const cudaError_t cfg_err = once.run([&] {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    // two CTAs per SM need the largest shared-memory carveout
+    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                cudaSharedmemCarveoutMaxShared);
   });
   if (cfg_err != cudaSuccess) return cfg_err;
   return launch_pdl(kern, grid, dim3(C::NTHR), C::SMEM, stream, tk, tv, p);

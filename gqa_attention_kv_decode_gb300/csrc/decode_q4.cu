@@ -45,9 +45,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <mutex>
 #include <type_traits>
 
+#include "device_once.h"
 #include "gqa_attn.h"
 #include "internal.h"
 #include "merge.cuh"
@@ -634,13 +634,13 @@ template <int D, int NSTAGE>
 cudaError_t launch_q4_mma(const Q4Params& p, dim3 grid, cudaStream_t stream) {
   using C = Q4Cfg<D, NSTAGE>;
   auto kern = decode_q4_mma_kernel<D, NSTAGE>;
-  static std::once_flag once;  // per instantiation; the attributes are per function
-  static cudaError_t cfg_err = cudaSuccess;
-  std::call_once(once, [&] {
-    cfg_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (cfg_err == cudaSuccess)  // four CTAs per SM need the largest shared-memory carveout
-      cfg_err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                     cudaSharedmemCarveoutMaxShared);
+  static DeviceOnce once;  // per instantiation; the attributes are per function and device
+  const cudaError_t cfg_err = once.run([&] {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    // four CTAs per SM need the largest shared-memory carveout
+    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                cudaSharedmemCarveoutMaxShared);
   });
   if (cfg_err != cudaSuccess) return cfg_err;
   return launch_pdl(kern, grid, dim3(C::NTHR), C::SMEM, stream, p);

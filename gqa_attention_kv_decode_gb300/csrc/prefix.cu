@@ -33,10 +33,10 @@
 
 #include <algorithm>
 #include <cmath>
-#include <mutex>
 #include <type_traits>
 
 #include "attn_tile.cuh"
+#include "device_once.h"
 #include "gqa_attn.h"
 #include "internal.h"
 #include "merge.cuh"
@@ -876,13 +876,13 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
     if (gp.lead_in + most / std::min(float(gp.early) * gp.own_sm, gp.hbm) <= share + 3.f) gp.late = 0;
   }
   const int n_ctas = gp.adaptive ? gp.sms + gp.n_cand : gp.n_cand + gp.early + gp.late;
-  static std::once_flag once;
-  static cudaError_t cfg_err = cudaSuccess;
-  std::call_once(once, [&] {
+  static DeviceOnce once;
+  const cudaError_t cfg_err = once.run([&] {
+    cudaError_t e = cudaSuccess;
     for (const void* k : {reinterpret_cast<const void*>(shared_prefix_kernel<HD, false>),
                           reinterpret_cast<const void*>(shared_prefix_kernel<HD, true>)})
-      if (cfg_err == cudaSuccess)
-        cfg_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<HD>);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<HD>);
+    return e;
   });
   if (cfg_err != cudaSuccess) return cfg_err;
   auto kern = a.plan.units == a.plan.n_tiles ? shared_prefix_kernel<HD, true> : shared_prefix_kernel<HD, false>;
