@@ -310,8 +310,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     };
     if (grid.adaptive) {
       r.head_start = head_start();
-      // (a late CTA for which the early ones leave nothing)
-      if (r.cta >= r.early && OwnCut::of(unsigned(own_tiles), unsigned(r.early * kOwnWarps),
+      // (a late CTA for which the early ones leave nothing; the first CTA stays,
+      // which reports the lengths that had to be clamped)
+      if (r.cta >= max(r.early, 1) && OwnCut::of(unsigned(own_tiles), unsigned(r.early * kOwnWarps),
                                          unsigned(r.late * kOwnWarps), r.head_start, 1u).head == unsigned(own_tiles))
         return;
     }
