@@ -152,6 +152,7 @@ int check_shared_prefix(int B, int Hq, int Hkv, int D, int max_prefix_len, int S
   const int rc = check_decode_shape(B, Hq, Hkv, D, S_cap, max_kv_len, scale);
   if (rc != GQA_OK) return rc;
   if (max_prefix_len < 1 || max_prefix_len > 0x7fffff00) return GQA_ERR_INVALID_ARG;  // (tiles of 128 in 32 bits)
+  if (max_kv_len > (1 << 30)) return GQA_ERR_INVALID_ARG;  // (a length and a split's or tile's rows in 32 bits)
   if (long(B) * Hq > (1L << 22)) return GQA_ERR_INVALID_ARG;  // (rows, and their partials, in 32 bits)
   return GQA_OK;
 }

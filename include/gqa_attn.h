@@ -208,7 +208,8 @@ GQA_ATTN_API int gqa_attn_decode_paged(const void* q, const void* k_new, const v
  *                 shared ones (0 is an ordinary length); clamped into
  *                 [0, max_kv_len]; NULL means max_kv_len for every request
  *   max_prefix_len, max_kv_len   host bounds, at least 1 and at most P_cap and
- *                 S_cap; they size the grids and the workspace
+ *                 S_cap, max_prefix_len at most 2^31 - 256, max_kv_len at most
+ *                 2^30 (256 GiB of K and V); they size the grids and the workspace
  * A request with no key at all gets a zero row (GQA_DEV_EMPTY_REQUEST).
  * Rows past the lengths may hold anything, NaN included.  Two kernels run
  * (shared and own rows, then a merge; three for more than 1,024 requests).
