@@ -39,6 +39,7 @@
 #include "gqa_attn.h"
 #include "internal.h"
 #include "mma_tile.cuh"
+#include "own_cut.h"
 #include "ptx.cuh"
 #include "tc.cuh"
 
@@ -72,45 +73,21 @@ struct OwnRowsParams {
   uint64_t wait_limit_ns, test_stall_ns;
 };
 
-// n ranges of `size` tiles, the first `longer` of them one longer.
-struct OwnRanges {
-  unsigned n, size, longer;
-  __device__ __forceinline__ static OwnRanges of(unsigned tiles, unsigned warps, unsigned min_tiles) {
-    OwnRanges r;
-    r.n = min(warps, max(1u, tiles / min_tiles));
-    r.size = tiles / r.n;
-    r.longer = tiles - r.size * r.n;
-    return r;
-  }
-  __device__ __forceinline__ unsigned start(unsigned w) const { return w * size + min(w, longer); }
-  __device__ __forceinline__ unsigned holder(unsigned x) const {  // the range with tile x
-    const unsigned head = longer * (size + 1);
-    return x < head ? x / (size + 1) : longer + (x - head) / size;
-  }
-};
-// The list's first `head` tiles go to the warps of the early CTAs, the rest to
-// those of the late ones: as many to each that all end at about the same time
-// T (in tiles of a warp), the late ones beginning head_start after the early:
+// Tiles of the list's beginning that go to the warps of the early CTAs, the
+// others going to those of the late ones: as many to each that all end at about
+// the same time T (in tiles of a warp), the late ones beginning head_start after
+// the early:
 //   early T + late (T - head_start) = N   (warps of each);
 // nothing is left for the late ones where T would be less than head_start.
-struct OwnCut {
-  unsigned head;
-  OwnRanges a, b;
-  __device__ __forceinline__ static OwnCut of(unsigned N, unsigned early, unsigned late, float head_start,
-                                              unsigned min_tiles) {
-    OwnCut c;
-    const float T = (float(N) + float(late) * head_start) / float(early + late);
-    const bool all = late == 0 || (early > 0 && T <= head_start);
-    c.head = early == 0 ? 0u : all ? N : min(N, unsigned(float(early) * T));
-    c.a = OwnRanges::of(c.head, max(early, 1u), min_tiles);
-    c.b = OwnRanges::of(N - c.head, max(late, 1u), min_tiles);
-    return c;
-  }
-  // The number, among all ranges in order, of the one with tile x.
-  __device__ __forceinline__ int holder(unsigned x) const {
-    return int(x < head ? a.holder(x) : (head > 0 ? a.n : 0u) + b.holder(x - head));
-  }
-};
+// A CTA makes this estimate once, and everything that follows from it is in
+// whole numbers (own_cut.h).  All CTAs have to come to the same: the operations
+// are ones that the compiler does not contract, so that they round alike in
+// whatever copies it makes of this.
+__device__ __forceinline__ unsigned own_head(unsigned N, unsigned early, unsigned late, float head_start) {
+  const float T = __fdiv_rn(__fmaf_rn(float(late), head_start, float(N)), float(early + late));
+  if (late == 0 || (early > 0 && T <= head_start)) return N;
+  return early == 0 ? 0u : min(N, unsigned(__fmul_rn(float(early), T)));
+}
 
 template <int D>
 struct OwnCfg {
@@ -145,9 +122,9 @@ constexpr int BAR_OWN = 5;  // named barrier of a CTA's threads at the own rows
 
 // The lengths, the longest of each warp's, and the prefix sums of the list, starts[b] = tiles before request
 // b, into shared memory (by the whole CTA; grid_dependency_wait has returned), and its barriers.
-// `report`: this CTA reports lengths that had to be clamped.
+// `report`: this CTA reports lengths that had to be clamped.  Returns the tiles of the list.
 template <int D>
-__device__ __forceinline__ void own_scan(unsigned char* smem, const OwnRowsParams& p, bool report) {
+__device__ __forceinline__ int own_scan(unsigned char* smem, const OwnRowsParams& p, bool report) {
   using C = OwnCfg<D>;
   constexpr int NTHREADS = kOwnThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -193,13 +170,15 @@ __device__ __forceinline__ void own_scan(unsigned char* smem, const OwnRowsParam
   }
   if (tid == 0) starts[0] = 0;
   named_bar_sync(BAR_OWN, NTHREADS);
+  return starts[p.B];
 }
 
 // Who works on the own rows: this is CTA `cta` of early + late ones, the first
-// of which begin with the grid, the others head_start later (in tiles of a warp).
+// of which begin with the grid, the others later; the early ones take the first
+// `head` tiles of the list.
 struct OwnRole {
   int cta, early, late;
-  float head_start;
+  unsigned head;
 };
 
 // Tiles of the whole list, by one warp.
@@ -323,8 +302,8 @@ __device__ __forceinline__ void own_rows(unsigned char* smem, const CUtensorMap*
   for (int i = 0; i < kOwnThreads / 32; ++i) longest = max(longest, warp_max[i]);
   const int most = (longest + TILE - 1) / TILE;
   const unsigned min_tiles = most < 2 ? 1u : unsigned(most - 2) / unsigned(p.n_own - 2) + 1u;
-  const OwnCut cut = OwnCut::of(unsigned(N), unsigned(role.early * kOwnWarps), unsigned(role.late * kOwnWarps),
-                                role.head_start, min_tiles);
+  const OwnCut cut = OwnCut::of(unsigned(N), role.head, unsigned(role.early * kOwnWarps),
+                                unsigned(role.late * kOwnWarps), min_tiles);
   // warp `who`'s range: neighbours in the list run on different SMs
   constexpr int PER = (kOwnWarps + kOwnCopiers - 1) / kOwnCopiers;  // warps a copying warp serves
   const bool copies = warp >= kOwnWarps;

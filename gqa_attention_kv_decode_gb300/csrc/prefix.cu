@@ -155,14 +155,17 @@ struct GridPlan {
 // shares fewer than there are SMs both kinds of work run throughout, and HBM
 // has no idle time at the starts and ends of the shares: 64 requests behind
 // 32,768 rows, up to 1,024 own, 65.6 us with all SMs on the shared rows first.)
+// Every CTA makes these estimates for itself and all have to come to the same,
+// so the operations here and in choose_shares are ones that the compiler does
+// not contract (see own_head).
 __device__ __forceinline__ float share_time(const GridPlan& g, int n_kv, int n) {
-  return g.start + g.kv_tile * ceilf(__fdividef(float(n_kv), float(n)));
+  return __fmaf_rn(g.kv_tile, ceilf(__fdividef(float(n_kv), float(n))), g.start);
 }
 // Tiles of own rows that `early` SMs do in a us beside n shares: what an SM can
 // do, or what the stream of the shared rows leaves of HBM.
 __device__ __forceinline__ float own_rate(const GridPlan& g, int n_kv, float share, float early) {
   const float shared = float(4 * n_kv * g.kv_heads);
-  return fminf(early * g.own_sm, fmaxf(g.hbm - __fdividef(shared, share), 0.25f * g.hbm));
+  return fminf(__fmul_rn(early, g.own_sm), fmaxf(__fadd_rn(g.hbm, -__fdividef(shared, share)), 0.25f * g.hbm));
 }
 constexpr int kMaxShares = 1023;  // of an adaptive grid
 constexpr uint32_t kShareMask = 1023u;
@@ -181,10 +184,11 @@ __device__ __forceinline__ int choose_shares(const GridPlan& g, int n_split, int
     // nearer it comes to what HBM delivers)
     const float load = __fdividef(own + float(4 * n_kv * g.kv_heads), g.hbm * share);
     const float rate = own_rate(g, n_kv, share, float(g.sms) - ctas);
-    share *= 0.83f + 0.34f * fminf(load, 1.1f);
+    share = __fmul_rn(share, __fmaf_rn(0.34f, fminf(load, 1.1f), 0.83f));
     // what of the own rows the free SMs do not get done follows on all
-    const float room = (share - g.lead_in) * rate, rest = own > room ? __fdividef(own - room, g.hbm) + g.rest : 0.f;
-    const float t = share + rest + g.merge * float(n);
+    const float room = __fmul_rn(__fadd_rn(share, -g.lead_in), rate);
+    const float rest = own > room ? __fadd_rn(__fdividef(__fadd_rn(own, -room), g.hbm), g.rest) : 0.f;
+    const float t = __fmaf_rn(g.merge, float(n), __fadd_rn(share, rest));
     best = min(best, (__float_as_uint(t) & ~kShareMask) | uint32_t(n));
   }
   return int(__reduce_min_sync(0xffffffffu, best) & kShareMask);
@@ -303,22 +307,24 @@ __global__ void __launch_bounds__(NTHR, 1)
       r.cta = cand ? r.early + r.late : cta - grid.n_cand;
     }
     if (r.cta >= r.early + r.late) return;
-    auto head_start = [&] {
-      if (n_used == 0 || r.early == 0) return 0.f;
-      const float share = share_time(grid, n_kv, n_used);
-      return (share + grid.follow) * own_rate(grid, n_kv, share, float(r.early)) / float(r.early * kOwnWarps);
+    auto head_of = [&](int tiles) {
+      float head_start = 0.f;  // of the early CTAs, in tiles of a warp
+      if (n_used > 0 && r.early > 0) {
+        const float share = share_time(grid, n_kv, n_used);
+        head_start = __fdiv_rn(__fmul_rn(__fadd_rn(share, grid.follow), own_rate(grid, n_kv, share, float(r.early))),
+                               float(r.early * kOwnWarps));
+      }
+      return own_head(unsigned(tiles), unsigned(r.early * kOwnWarps), unsigned(r.late * kOwnWarps), head_start);
     };
     if (grid.adaptive) {
-      r.head_start = head_start();
+      r.head = head_of(own_tiles);
       // (a late CTA for which the early ones leave nothing; the first CTA stays,
       // which reports the lengths that had to be clamped)
-      if (r.cta >= max(r.early, 1) && OwnCut::of(unsigned(own_tiles), unsigned(r.early * kOwnWarps),
-                                         unsigned(r.late * kOwnWarps), r.head_start, 1u).head == unsigned(own_tiles))
-        return;
+      if (r.cta >= max(r.early, 1) && r.head == unsigned(own_tiles)) return;
     }
-    own_scan<HD>(smem, own, r.cta == 0);
+    const int listed = own_scan<HD>(smem, own, r.cta == 0);
     if (direct) use_length();
-    if (!grid.adaptive) r.head_start = head_start();
+    if (!grid.adaptive) r.head = head_of(listed);
     own_rows<HD>(smem, &tmKo, &tmVo, own, r);
     return;
   }
