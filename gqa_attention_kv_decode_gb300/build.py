@@ -4,7 +4,8 @@ the Python binding.
 Each CUDA translation unit under csrc/ is compiled by its own nvcc process (in
 parallel) and the objects are linked into ``libgqa_attn.so`` next to this
 file; ``csrc/torch_call.cpp`` becomes the extension module ``_torch_call.so``
-beside it.  Nothing is installed anywhere else.
+beside it (without torch the library alone is built, which needs none).  Nothing is installed anywhere
+else.
 
     python -m gqa_attention_kv_decode_gb300.build [--force] [--verbose]
 """
@@ -43,81 +44,98 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _host_compile(obj):
-    """The command that compiles csrc/torch_call.cpp (host code, torch headers)."""
-    import torch
+def _torch():
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch
 
+
+def _host_compile(obj, torch):
+    """The command that compiles csrc/torch_call.cpp (host code, torch headers)."""
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
-    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-isystem", inc, "-isystem",
-            os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
-            "-isystem", cuda, "-c", os.path.join(CSRC, "torch_call.cpp"), "-o", obj]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+            "-I", INCLUDE, "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-c",
+            os.path.join(CSRC, "torch_call.cpp"), "-o", obj]
 
 
-def _host_link(obj, out):
-    import torch
-
+def _host_link(obj, out, torch):
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     return ["g++", "-shared", "-o", out, obj, "-L", PKG, "-lgqa_attn", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10",
             "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
-def _deps():
-    return _sources() + [os.path.join(CSRC, "torch_call.cpp")] \
-        + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
-        + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+
+
+def _newer(out, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps)
+
+
+def _lib_up_to_date() -> bool:
+    return _newer(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+                  + _headers())
+
+
+def _call_up_to_date() -> bool:
+    return _newer(CALL, [os.path.join(CSRC, "torch_call.cpp")] + _headers())
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALL):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    torch = _torch()
+    return _lib_up_to_date() and (torch is None or _call_up_to_date())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and up_to_date():
+    torch = _torch()
+    do_lib = force or not _lib_up_to_date()
+    do_call = torch is not None and (force or not _call_up_to_date())
+    if not do_lib and not do_call:
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     procs = []
     objs = []
-    for src in _sources():
-        obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        objs.append(obj)
-        cmd = [nvcc, *ARCH, *CFLAGS, "-c", src, "-o", obj]
-        if ptxas_info:
-            cmd += ["-Xptxas", "-v"]
+
+    def start(name, cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+        procs.append((name, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+
+    def link(cmd, tmp, out):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, out)
+
+    for src in _sources() if do_lib else ():
+        obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
+        objs.append(obj)
+        start(src, [nvcc, *ARCH, *CFLAGS, "-c", src, "-o", obj] + (["-Xptxas", "-v"] if ptxas_info else []))
     call_obj = os.path.join(BUILD, "torch_call.o")
-    cmd = _host_compile(call_obj)
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    procs.append(("torch_call.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
-                                                     text=True)))
+    if do_call:
+        start("torch_call.cpp", _host_compile(call_obj, torch))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
         if out and (verbose or ptxas_info or p.returncode != 0):
             print(out, file=sys.stderr)
         if p.returncode != 0:
-            failed.append(src)
+            failed.append(os.path.basename(src))
+    if failed != [] and failed != ["torch_call.cpp"]:
+        raise RuntimeError("the compiler failed on: " + ", ".join(failed))
+    if do_lib:
+        link([nvcc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs], LIB + ".tmp", LIB)
     if failed:
-        raise RuntimeError("the compiler failed on: " + ", ".join(os.path.basename(f) for f in failed))
-    tmp = LIB + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
-    tmp = CALL + ".tmp"
-    cmd = _host_link(call_obj, tmp)
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, CALL)
+        raise RuntimeError("the compiler failed on: " + ", ".join(failed) + " (the C library is built)")
+    if do_call:
+        link(_host_link(call_obj, CALL + ".tmp", torch), CALL + ".tmp", CALL)
+    elif torch is None:
+        print("no torch: the C library is built, the Python binding's module is not", file=sys.stderr)
     return LIB
 
 
