@@ -190,7 +190,14 @@ def _call():
     global _call_mod
     if _call_mod is None:
         lib()  # (raises if nothing has been built)
-        from . import _torch_call
+        again = "build it with `python -m gqa_attention_kv_decode_gb300.build`"
+        try:
+            from . import _torch_call
+        except ImportError as e:
+            raise RuntimeError(f"_torch_call is missing, or of another Python or torch: {again} ({e})") from e
+        if _torch_call.torch_version != torch.__version__:
+            raise RuntimeError(f"_torch_call was built for torch {_torch_call.torch_version}, this is "
+                               f"{torch.__version__}: {again}")
         _call_mod = _torch_call
     return _call_mod
 

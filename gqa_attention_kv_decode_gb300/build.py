@@ -3,8 +3,9 @@ the Python binding.
 
 Each CUDA translation unit under csrc/ is compiled by its own nvcc process (in
 parallel) and the objects are linked into ``libgqa_attn.so`` next to this
-file; ``csrc/torch_call.cpp`` becomes the extension module ``_torch_call.so``
-beside it (without torch the library alone is built, which needs none).  Nothing is installed anywhere
+file; ``csrc/torch_call.cpp`` becomes the extension module ``_torch_call``
+beside it, for the Python and the torch that are there (without torch the
+library alone is built, which needs neither).  Nothing is installed anywhere
 else.
 
     python -m gqa_attention_kv_decode_gb300.build [--force] [--verbose]
@@ -26,7 +27,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgqa_attn.so")
-CALL = os.path.join(PKG, "_torch_call.so")
+CALL = os.path.join(PKG, "_torch_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -56,7 +57,7 @@ def _host_compile(obj, torch):
     """The command that compiles csrc/torch_call.cpp (host code, torch headers)."""
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
-    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f'-DGQA_TORCH_VERSION="{torch.__version__}"',
             "-I", INCLUDE, "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
             "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-c",
             os.path.join(CSRC, "torch_call.cpp"), "-o", obj]
@@ -81,19 +82,26 @@ def _lib_up_to_date() -> bool:
                   + _headers())
 
 
-def _call_up_to_date() -> bool:
-    return _newer(CALL, [os.path.join(CSRC, "torch_call.cpp")] + _headers())
+def _call_stamp():
+    return os.path.join(BUILD, "torch_call.torch")  # the torch that the module was built for
+
+
+def _call_up_to_date(torch) -> bool:
+    if not _newer(CALL, [os.path.join(CSRC, "torch_call.cpp")] + _headers()) or not os.path.exists(_call_stamp()):
+        return False
+    with open(_call_stamp()) as f:
+        return f.read() == torch.__version__
 
 
 def up_to_date() -> bool:
     torch = _torch()
-    return _lib_up_to_date() and (torch is None or _call_up_to_date())
+    return _lib_up_to_date() and (torch is None or _call_up_to_date(torch))
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     torch = _torch()
     do_lib = force or not _lib_up_to_date()
-    do_call = torch is not None and (force or not _call_up_to_date())
+    do_call = torch is not None and (force or not _call_up_to_date(torch))
     if not do_lib and not do_call:
         return LIB
     nvcc = _nvcc()
@@ -134,6 +142,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         raise RuntimeError("the compiler failed on: " + ", ".join(failed) + " (the C library is built)")
     if do_call:
         link(_host_link(call_obj, CALL + ".tmp", torch), CALL + ".tmp", CALL)
+        with open(_call_stamp(), "w") as f:
+            f.write(torch.__version__)
     elif torch is None:
         print("no torch: the C library is built, the Python binding's module is not", file=sys.stderr)
     return LIB

@@ -311,4 +311,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_call", "Native calls of lib
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__torch_call() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__torch_call() {
+  PyObject* m = PyModule_Create(&module);
+  // (binding.py uses the module with the torch it was built for alone)
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", GQA_TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}

@@ -1,5 +1,5 @@
 """The build's own rules (CPU, with stand-ins for the compilers): the C library
-needs no torch."""
+needs no torch, and the binding's module is built again for another torch."""
 
 import os
 import subprocess
@@ -7,8 +7,11 @@ import sys
 import types
 
 import pytest
+import torch
 
-from gqa_attention_kv_decode_gb300 import build
+import __graft_entry__
+import gqa_attention_kv_decode_gb300 as package
+from gqa_attention_kv_decode_gb300 import binding, build
 
 # writes its output file, and a line about it to $COMPILER_LOG
 COMPILER = """#!/bin/sh
@@ -75,3 +78,32 @@ def test_a_module_that_does_not_compile_leaves_the_library(tree):
     p, _ = tree.run("torch", FAIL_CALL="1")
     assert p.returncode != 0 and "torch_call.cpp" in p.stderr
     assert (tree.path / "libgqa_attn.so").exists()
+
+
+def test_another_torch_makes_the_module_stale(monkeypatch):
+    __graft_entry__.build()
+    assert build.up_to_date()
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert not build.up_to_date()
+
+
+def test_the_module_is_named_for_its_python():
+    assert os.path.basename(build.CALL).startswith("_torch_call.") and "3" in os.path.basename(build.CALL)
+    assert os.path.basename(build.CALL) != "_torch_call.so"
+
+
+@pytest.mark.parametrize("version,text", [("0.0.1", "was built for torch 0.0.1"), (None, "missing")])
+def test_a_module_of_another_torch_is_not_used(monkeypatch, version, text):
+    __graft_entry__.build()
+    fake = None if version is None else types.SimpleNamespace(torch_version=version)
+    name = package.__name__ + "._torch_call"
+    monkeypatch.setitem(sys.modules, name, fake)
+    if hasattr(package, "_torch_call"):
+        monkeypatch.delattr(package, "_torch_call")
+    if fake is not None:
+        monkeypatch.setattr(package, "_torch_call", fake, raising=False)
+    monkeypatch.setattr(binding, "_call_mod", None)
+    with pytest.raises(RuntimeError, match=text):
+        binding._call()
+    monkeypatch.undo()
+    assert binding._call().torch_version == torch.__version__
