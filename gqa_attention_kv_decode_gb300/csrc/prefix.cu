@@ -759,9 +759,20 @@ __global__ void __launch_bounds__(256, MB) prefix_merge_kernel(const PrefixMerge
 }
 
 // As many warps a row as keep the grid within a wave (about 20 warps of the
-// merge on an SM), up to eight; of few partials four or one, which have less to
-// join (11 requests of 16 heads, D = 128, two partials each: 10.5 us, 11.0 with
-// eight; 39 of 32 heads, 6 each: 12.9, 14.0 with two).
+// merge on an SM), up to eight.  Times of whole calls, in us, on both sides of
+// each choice (requests x heads x D, shares + own partials a row):
+//   few partials, four warps  4 x 14 x 64, 5 + 5: 7.7; asking for more at once
+//                             8.0, eight warps 7.9; 11 x 16 x 128, 6 + 3: 9.5;
+//                             10.0, 9.9
+//   few partials, one warp    39 x 32 x 128, 4 + 3: 13.0; two warps 14.6, four
+//                             16.1; 34 x 32 x 128, 4 + 3: 13.4; 13.7, 15.5
+//   eight warps               6 x 28 x 128, 32 + 11: 17.8; four 18.0; 30 x 14 x
+//                             64, 24 + 14: 11.6; 11.8
+//   four warps                16 x 28 x 128, 11 + 17: 13.3; eight 14.5, two 14.2;
+//                             22 x 32 x 64, 9 + 11: 13.1; 14.8, 13.6 (40 x 16 x
+//                             128, 10 + 5, near the border: 16.4; 17.7, 15.1)
+//   two warps                 48 x 16 x 128, 32 + 17: 27.6; four 28.6, one 28.7;
+//                             24 x 32 x 128, 12 + 5: 17.5; 19.2, 18.5
 template <int HD>
 cudaError_t launch_prefix_merge(const PrefixMergeParams& m, cudaStream_t stream) {
   const long room = 20L * device_sm_count() / m.rows;
@@ -773,16 +784,19 @@ cudaError_t launch_prefix_merge(const PrefixMergeParams& m, cudaStream_t stream)
   if (room >= 8) return go(prefix_merge_kernel<HD, 8, 4, 4, 1>, 8);
   if (room >= 4) return go(prefix_merge_kernel<HD, 4, 8, 4, 1>, 4);
   if (room >= 2) return go(prefix_merge_kernel<HD, 2, 8, 4, 1>, 2);
-  // Several waves, or few partials: as many warps as fit an SM, each asking for
-  // less at once (159 requests of 32 heads, D = 128, behind 153 of 4,153 rows:
-  // 43.5 us, 46 the other way; 64 behind 32,768: 55.6 the other way, 56.5 with
-  // one block an SM).
-  if ((HD == 128 && room < 1) || m.n_split <= 4) return go(prefix_merge_kernel<HD, 1, 4, 2, 4>, 1);
+  // Long grids: as many warps as fit an SM, each asking for less at once.  Where
+  // a partial row is 512 bytes and the grid several waves, fewer bytes a warp and
+  // four blocks an SM (256 x 32 x 128, 4 + 17: 89.0, 90.2 the other way; 159 x 32
+  // x 128, 5 + 18: 42.5, 43.5), else more and three (64 x 32 x 128, 19 + 33: 53.2,
+  // 53.2; 100 x 28 x 128, 4 + 11: 20.9, 21.4; 250 x 14 x 64, 10 + 8: 27.2, 28.2).
+  if (HD == 128 && room < 1) return go(prefix_merge_kernel<HD, 1, 4, 2, 4>, 1);
   return go(prefix_merge_kernel<HD, 1, 8, 2, 3>, 1);
 }
 
-// Bytes of own rows an SM takes in a us where HBM has more (24 SMs alone, 256
-// requests of up to 512 keys, D = 128), and what HBM delivers to all.
+// Of the kernel's estimates: bytes of own rows an SM takes in a us where HBM has
+// more (measured: 24 SMs alone, 256 requests of up to 512 keys, D = 128), and
+// what all together take at most.  The latter is a parameter of the fit below,
+// no measured rate: HBM copies 6.7e6 bytes a us.
 constexpr float kOwnBytesPerUs = 105e3f, kHbmBytesPerUs = 7.8e6f;
 
 template <int HD>
@@ -862,8 +876,12 @@ cudaError_t launch_prefix_hd(const SharedPrefixArgs& a, cudaStream_t stream) {
   gp.early = listed ? (gp.sms - gp.n_cand % gp.sms) % gp.sms : 0;
   gp.late = listed ? gp.sms - gp.early : 0;
   // (fitted, with hbm and own_sm, to the times of 12 shapes -- 32 to 512 requests
-  // behind 4,096 to 65,536 rows, D = 64 and 128 -- in 1 to 50 shares: what is
-  // chosen is 2 % slower than the best of these in the mean, 9 % at most)
+  // behind 4,096 to 65,536 rows, D = 64 and 128 -- in 1 to 40 shares: what is
+  // chosen is 1 % slower than the best of these in the mean, 2 % at most; on 14
+  // shapes drawn from the same ranges, 2 % in the mean, 9 % at most.  prefix_plan,
+  // which has to say before the lengths are known how many shares there can be,
+  // has figures of its own, fitted to whole calls without the own rows; the two
+  // need not agree.)
   const bool single = a.plan.n_tiles == 1;
   gp.start = single ? 5.f : 8.5f;
   gp.kv_tile = (single ? 1.25f : 1.75f) * (HD == 64 ? 0.5f : 1.f);
