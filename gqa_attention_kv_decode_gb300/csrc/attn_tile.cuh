@@ -50,7 +50,11 @@ __device__ __forceinline__ void named_bar_arrive(int id, int n) {
 }
 
 // Exponentials of 64 scores s[0..63] of one row against the reference m
-// (P = 2^(s*c - m)), packed as 32 bf16 pairs; their sum is added to acc.
+// (P = 2^(s*c - m)), packed as 32 bf16 pairs; their sum is added to acc.  P is
+// rounded to bf16 (half a step, 2^-8 of it) because the product with V takes
+// operands of V's type; the sum, the reference and the accumulators are fp32.
+// The output's error against 64 bits is 1.3 times that of its own rounding to
+// bf16 (2.2e-3 of its norm against 1.7e-3).
 __device__ __forceinline__ void exp_half(const uint32_t* s, float2 c, float2 mm, uint32_t (&pw)[32],
                                          float2 (&acc)[4]) {
 #pragma unroll

@@ -14,7 +14,9 @@
 //   - shares nothing with other computing warps: no block barrier, no join of
 //     warps; a unit that several warps touch has a partial of each;
 //   - multiplies on the tensor cores (mma.sync m16n8k16) with the keys as rows
-//     and up to 8 query heads of one KV head as columns, online softmax in base 2.
+//     and up to 8 query heads of one KV head as columns, online softmax in base 2;
+//     the probabilities are rounded to bf16 for the product with V, as in the
+//     shared rows (exp_half), and all that is summed or kept is fp32.
 // What bounds it: beside the shared rows few SMs do this work and HBM has
 // bytes to spare, so it is the instructions of a warp, which mostly wait for
 // one another.  24 SMs take 42 GB/s each if one warp copies for all with four

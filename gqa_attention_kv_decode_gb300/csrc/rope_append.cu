@@ -83,10 +83,11 @@ __device__ __forceinline__ uint4 load_once(const void* src) {
 
 // A warp takes one token and U passes of HP heads each, all loaded before the
 // first is used.  A block's W warps take the passes of one token after the
-// other or, TOKENS, the same passes of W tokens.  MB: blocks an SM holds (few
-// registers, so that many warps wait on memory at once, count for more than a
-// few spilled ones: U = 3 at 16,384 tokens 95 us with 16 warps an SM, 80 with
-// 24, 76 with 32; with 40, 115).
+// other or, TOKENS, the same passes of W tokens.  MB: blocks an SM holds.  With
+// three passes of bf16 rows the 64 registers that 32 warps leave do not hold
+// everything: 72 bytes a thread are spilled (112 in blocks of eight warps), fp32
+// rows none.  Many warps that wait on memory at once count for more (U = 3 at
+// 16,384 tokens 95 us with 16 warps an SM, 80 with 24, 76 with 32; with 40, 115).
 template <typename T, int D, int U, int W, int MB, bool TOKENS, bool PASS_ON>
 __global__ void __launch_bounds__(32 * W, MB) rope_append_kernel(const RopeAppendArgs p, unsigned parts) {
   using C = Chunk<T>;

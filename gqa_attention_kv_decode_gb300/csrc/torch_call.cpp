@@ -6,8 +6,9 @@
 // tensors whose checks cost 0.2 us apiece from Python, besides 0.1 us per
 // argument in ctypes and 0.06 us for each pointer that the library looks up
 // (which the tensors spare it): 10.4, 12.5 and 15.5 us a call for the tables,
-// the append and the shared-prefix decode that way, 3.0, 3.2 and 5.1 this way,
-// of which the launches take 1.5 each.  The functions return the C entry
+// the append and the shared-prefix decode that way, 3.1, 3.2 and 5.0 this way,
+// of which the launches take 1.5 each.  (The decode behind 513 shared rows; its
+// plan looks at more numbers of shares the longer they are: 6.1 behind 32,768.)  The functions return the C entry
 // point's status; what is wrong with a tensor raises TypeError or ValueError.
 // No exception crosses the C interfaces on either side.
 #include <Python.h>
