@@ -520,6 +520,19 @@ def gqa_attn_version() -> int:
 
 # --- conveniences: allocate outputs / workspaces with torch, then call -------
 
+def _on(stream):
+    """The workspace that a call on `stream` makes for itself belongs to that
+    stream: one of the current stream would be cleared, and given to the next
+    tensor, in an order that the call's kernels do not follow.  (Outputs belong
+    to the current stream, as whatever the caller makes for the call does.)"""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        # (the handles 0 to 2 name default streams, which wait for one another)
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) > 2 else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def rope_table(max_pos, rot_dim, base=10000.0, device="cuda") -> torch.Tensor:
     """The cos_sin table of gqa_attn_rope_append, fp32 [max_pos, rot_dim]: the
     angles position * base^(-2 i / rot_dim) and their cosines and sines in 64
@@ -558,7 +571,8 @@ def decode(q, k, v, kv_lens=None, scale=None, max_kv_len=None, workspace=None, s
     if scale is None:
         scale = D ** -0.5
     if workspace is None:
-        workspace = decode_workspace(B, Hq, Hkv, D, max_kv_len, _dtype_code(q), q.device)
+        with _on(stream):
+            workspace = decode_workspace(B, Hq, Hkv, D, max_kv_len, _dtype_code(q), q.device)
     o = torch.empty_like(q)
     gqa_attn_decode(q, k, v, o, kv_lens, scale, workspace, max_kv_len, stream)
     return o
@@ -572,10 +586,11 @@ def decode_q4_residual(q, k_codes, k_scale, k_bias, v_codes, v_scale, v_bias, k_
     if scale is None:
         scale = D ** -0.5
     if workspace is None:
-        n = gqa_attn_decode_q4_residual_workspace_size(B, Hq, Hkv, D, max_quant)
-        if n == 0:
-            raise ValueError("invalid decode shape")
-        workspace = torch.zeros(n, dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            n = gqa_attn_decode_q4_residual_workspace_size(B, Hq, Hkv, D, max_quant)
+            if n == 0:
+                raise ValueError("invalid decode shape")
+            workspace = torch.zeros(n, dtype=torch.uint8, device=q.device)
     o = torch.empty_like(q)
     gqa_attn_decode_q4_residual(q, k_codes, k_scale, k_bias, v_codes, v_scale, v_bias, k_res, v_res,
                                 n_quant, kv_lens, o, scale, workspace, max_quant, stream=stream)
@@ -589,7 +604,8 @@ def decode_paged(q, k_pool, v_pool, block_table, kv_lens, max_kv_len, k_new=None
     if scale is None:
         scale = D ** -0.5
     if workspace is None:
-        workspace = decode_workspace(B, Hq, Hkv, D, max_kv_len, _dtype_code(q), q.device)
+        with _on(stream):
+            workspace = decode_workspace(B, Hq, Hkv, D, max_kv_len, _dtype_code(q), q.device)
     o = torch.empty_like(q)
     gqa_attn_decode_paged(q, k_new, v_new, k_pool, v_pool, block_table, kv_lens, o, scale, workspace,
                           max_kv_len, stream)
@@ -605,7 +621,8 @@ def decode_shared_prefix(q, k_prefix, v_prefix, k, v, prefix_len=None, kv_lens=N
     if scale is None:
         scale = D ** -0.5
     if workspace is None:
-        workspace = decode_shared_prefix_workspace(B, Hq, Hkv, D, max_prefix_len, max_kv_len, q.device)
+        with _on(stream):
+            workspace = decode_shared_prefix_workspace(B, Hq, Hkv, D, max_prefix_len, max_kv_len, q.device)
     o = torch.empty_like(q)
     gqa_attn_decode_shared_prefix(q, k_prefix, v_prefix, prefix_len, k, v, kv_lens, o, scale, workspace,
                                   max_prefix_len, max_kv_len, stream)
@@ -619,7 +636,8 @@ def decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, block_table, kv_
     if scale is None:
         scale = D ** -0.5
     if workspace is None:
-        workspace = decode_shared_prefix_workspace(B, Hq, Hkv, D, max_prefix_len, max_kv_len, q.device)
+        with _on(stream):
+            workspace = decode_shared_prefix_workspace(B, Hq, Hkv, D, max_prefix_len, max_kv_len, q.device)
     o = torch.empty_like(q)
     gqa_attn_decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, prefix_len, block_table, kv_lens, o, scale,
                                         workspace, max_prefix_len, max_kv_len, stream)
@@ -634,7 +652,8 @@ def decode_q4(q, k_codes, k_scale, k_bias, v_codes, v_scale, v_bias, kv_lens=Non
     if scale is None:
         scale = D ** -0.5
     if workspace is None:
-        workspace = decode_q4_workspace(B, Hq, Hkv, D, max_kv_len, q.device)
+        with _on(stream):
+            workspace = decode_q4_workspace(B, Hq, Hkv, D, max_kv_len, q.device)
     o = torch.empty_like(q)
     gqa_attn_decode_q4(q, k_codes, k_scale, k_bias, v_codes, v_scale, v_bias, o, kv_lens, scale,
                        workspace, max_kv_len, stream=stream)
