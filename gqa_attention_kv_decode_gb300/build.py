@@ -48,7 +48,7 @@ def _sources():
 def _torch():
     try:
         import torch
-    except ImportError:
+    except (ImportError, OSError):  # (none, or one whose own libraries are missing)
         return None
     return torch
 
