@@ -39,6 +39,7 @@ GQA_DEV_BAD_BLOCK = 8
 GQA_DEV_OUT_OF_BLOCKS = 16
 GQA_DEV_BAD_SLOT = 32
 GQA_DEV_BAD_POSITION = 64
+GQA_DEV_BAD_INDEX = 128
 
 EXPORTED = (
     "gqa_attn_decode_workspace_size",
@@ -49,6 +50,13 @@ EXPORTED = (
     "gqa_attn_decode_shared_prefix",
     "gqa_attn_decode_shared_prefix_paged",
     "gqa_attn_step_tables",
+    "gqa_attn_decode_tree_workspace_size",
+    "gqa_attn_decode_tree",
+    "gqa_attn_decode_tree_paged",
+    "gqa_attn_tree_tables",
+    "gqa_attn_compact_rows",
+    "gqa_attn_fork_tables",
+    "gqa_attn_copy_blocks",
     "gqa_attn_rope_append",
     "gqa_attn_decode_layers_workspace_size",
     "gqa_attn_decode_layers",
@@ -120,6 +128,20 @@ def lib() -> ctypes.CDLL:
     L.gqa_attn_rope_append.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, f32, vp, vp, vp, vp, vp, vp, vp] \
         + [i32] * 12 + [vp, sz, vp]
     L.gqa_attn_rope_append.restype = i32
+    L.gqa_attn_decode_tree_workspace_size.argtypes = [i32] * 6
+    L.gqa_attn_decode_tree_workspace_size.restype = sz
+    L.gqa_attn_decode_tree.argtypes = [vp] * 8 + [i32] * 8 + [f32, i32, vp, sz, vp]
+    L.gqa_attn_decode_tree.restype = i32
+    L.gqa_attn_decode_tree_paged.argtypes = [vp] * 9 + [i32] * 10 + [f32, i32, vp, sz, vp]
+    L.gqa_attn_decode_tree_paged.restype = i32
+    L.gqa_attn_tree_tables.argtypes = [vp] * 7 + [i32] * 5 + [vp, sz, vp]
+    L.gqa_attn_tree_tables.restype = i32
+    L.gqa_attn_compact_rows.argtypes = [vp] * 8 + [i32] * 9 + [vp, sz, vp]
+    L.gqa_attn_compact_rows.restype = i32
+    L.gqa_attn_fork_tables.argtypes = [vp] * 15 + [i32] * 5 + [vp, sz, vp]
+    L.gqa_attn_fork_tables.restype = i32
+    L.gqa_attn_copy_blocks.argtypes = [vp] * 5 + [i32] * 7 + [vp, sz, vp]
+    L.gqa_attn_copy_blocks.restype = i32
     L.gqa_attn_quantize_q4.argtypes = [vp, i64, vp, vp, vp, i64, i64, i32, i32, i32, i32, vp]
     L.gqa_attn_quantize_q4.restype = i32
     L.gqa_attn_decode_q4_residual_workspace_size.argtypes = [i32, i32, i32, i32, i32]
@@ -386,6 +408,78 @@ def gqa_attn_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, s
         _check(rc, "gqa_attn_rope_append")
 
 
+def gqa_attn_decode_tree_workspace_size(B, Hq, Hkv, D, Tq, max_kv_len) -> int:
+    return lib().gqa_attn_decode_tree_workspace_size(B, Hq, Hkv, D, Tq, max_kv_len)
+
+
+def gqa_attn_decode_tree(q, k, v, tree_mask, q_lens, tree_lens, kv_lens, o, scale, workspace, max_kv_len=None,
+                         stream=None):
+    """q, o [B,Hq,Tq,D]: the last q_lens[b] rows of request b (int32 [B], None:
+    Tq) over k, v [B,Hkv,S_cap,D], kv_lens int32 [B] rows; tree_mask int32
+    [B,Tq,words] over the last tree_lens[b] rows (None: q_lens), or None: a chain."""
+    rc = (_call_mod or _call()).decode_tree(
+        q, k, v, tree_mask, q_lens, tree_lens, kv_lens, o, scale, workspace, max_kv_len,
+        None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "gqa_attn_decode_tree")
+
+
+def gqa_attn_decode_tree_paged(q, k_pool, v_pool, block_table, tree_mask, q_lens, tree_lens, kv_lens, o, scale,
+                               workspace, max_kv_len=None, stream=None):
+    """gqa_attn_decode_tree over pools [num_blocks,Hkv,block_size,D] and a
+    block_table int32 [B,max_blocks]."""
+    rc = (_call_mod or _call()).decode_tree_paged(
+        q, k_pool, v_pool, block_table, tree_mask, q_lens, tree_lens, kv_lens, o, scale, workspace, max_kv_len,
+        None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "gqa_attn_decode_tree_paged")
+
+
+def gqa_attn_tree_tables(parents, tree_lens, q_lens, kv_lens, q_starts, tree_mask, positions, workspace, stream=None):
+    """parents int32 [B,N] -> tree_mask int32 [B,Tq,ceil(N/32)] of the last
+    q_lens[b] (None: all) of tree_lens[b] nodes, and positions [T] from
+    q_starts[b] on (or kv_lens, q_starts and positions None)."""
+    rc = (_call_mod or _call()).tree_tables(parents, tree_lens, q_lens, kv_lens, q_starts, tree_mask, positions,
+                                            workspace, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "gqa_attn_tree_tables")
+
+
+def gqa_attn_compact_rows(path, n_keep, tree_lens, kv_lens, block_table, k_cache, v_cache, kv_lens_out, workspace,
+                          stream=None):
+    """The tree's rows path int32 [B,P] (the first n_keep[b]) moved together
+    behind the rows before it, in k_cache, v_cache [num_blocks,Hkv,block_size,D]
+    or [layers,...]; block_table None: a dense cache."""
+    rc = (_call_mod or _call()).compact_rows(path, n_keep, tree_lens, kv_lens, block_table, k_cache, v_cache,
+                                             kv_lens_out, workspace, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "gqa_attn_compact_rows")
+
+
+def gqa_attn_fork_tables(src, keep_lens, held_lens, block_table, shared, free_blocks, free_count, block_table_out,
+                         kv_lens_out, shared_out, free_blocks_out, free_count_out, copy_src, copy_dst, copy_rows,
+                         block_size, workspace, stream=None):
+    """New request b is the first keep_lens[b] rows (None: all) of old request
+    src[b] (int32 [B], negative: none): its table, its length, the holders and
+    the stack afterwards, and the copy it needs (gqa_attn_copy_blocks)."""
+    rc = (_call_mod or _call()).fork_tables(
+        src, keep_lens, held_lens, block_table, shared, free_blocks, free_count, block_table_out, kv_lens_out,
+        shared_out, free_blocks_out, free_count_out, copy_src, copy_dst, copy_rows, block_size, workspace,
+        None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "gqa_attn_fork_tables")
+
+
+def gqa_attn_copy_blocks(src, dst, rows, k_cache, v_cache, workspace, stream=None):
+    """Block src[i] -> block dst[i] (int32 [n], src negative: none), the first
+    rows[i] rows of each head (None: all), in k_cache, v_cache
+    [num_blocks,Hkv,block_size,D] or [layers,...]."""
+    rc = (_call_mod or _call()).copy_blocks(src, dst, rows, k_cache, v_cache, workspace,
+                                            None if stream is None else _stream(stream))
+    if rc:
+        _check(rc, "gqa_attn_copy_blocks")
+
+
 def gqa_attn_quantize_q4(src, codes, scale, bias, dst_row0=0, rows=None, group_size=64, stream=None):
     """src bf16 [B,Hkv,S_src,D]; codes uint8 [B,Hkv,S_cap,D/2]; scale, bias fp16
     [B,Hkv,S_cap,D/64]: rows [0, rows) of src go to rows [dst_row0, dst_row0 + rows)."""
@@ -557,6 +651,13 @@ def decode_shared_prefix_workspace(B, Hq, Hkv, D, max_prefix_len, max_kv_len, de
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
+def decode_tree_workspace(B, Hq, Hkv, D, Tq, max_kv_len, device="cuda") -> torch.Tensor:
+    n = gqa_attn_decode_tree_workspace_size(B, Hq, Hkv, D, Tq, max_kv_len)
+    if n == 0:
+        raise ValueError("invalid decode shape")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
 def decode_q4_workspace(B, Hq, Hkv, D, max_kv_len, device="cuda") -> torch.Tensor:
     n = gqa_attn_decode_q4_workspace_size(B, Hq, Hkv, D, max_kv_len)
     if n == 0:
@@ -641,6 +742,35 @@ def decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, block_table, kv_
     o = torch.empty_like(q)
     gqa_attn_decode_shared_prefix_paged(q, k_pool, v_pool, prefix_table, prefix_len, block_table, kv_lens, o, scale,
                                         workspace, max_prefix_len, max_kv_len, stream)
+    return o
+
+
+def decode_tree(q, k, v, kv_lens, tree_mask=None, q_lens=None, tree_lens=None, scale=None, max_kv_len=None,
+                workspace=None, stream=None):
+    B, Hq, Tq, D = q.shape
+    max_kv_len = k.shape[2] if max_kv_len is None else int(max_kv_len)
+    if scale is None:
+        scale = D ** -0.5
+    if workspace is None:
+        with _on(stream):
+            workspace = decode_tree_workspace(B, Hq, k.shape[1], D, Tq, max_kv_len, q.device)
+    o = torch.empty_like(q)
+    gqa_attn_decode_tree(q, k, v, tree_mask, q_lens, tree_lens, kv_lens, o, scale, workspace, max_kv_len, stream)
+    return o
+
+
+def decode_tree_paged(q, k_pool, v_pool, block_table, kv_lens, tree_mask=None, q_lens=None, tree_lens=None, scale=None,
+                      max_kv_len=None, workspace=None, stream=None):
+    B, Hq, Tq, D = q.shape
+    max_kv_len = block_table.shape[1] * k_pool.shape[2] if max_kv_len is None else int(max_kv_len)
+    if scale is None:
+        scale = D ** -0.5
+    if workspace is None:
+        with _on(stream):
+            workspace = decode_tree_workspace(B, Hq, k_pool.shape[1], D, Tq, max_kv_len, q.device)
+    o = torch.empty_like(q)
+    gqa_attn_decode_tree_paged(q, k_pool, v_pool, block_table, tree_mask, q_lens, tree_lens, kv_lens, o, scale,
+                               workspace, max_kv_len, stream)
     return o
 
 

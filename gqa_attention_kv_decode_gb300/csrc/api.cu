@@ -204,6 +204,51 @@ int run_shared_prefix(SharedPrefixArgs& a, size_t ws_bytes, int dev, void* strea
   return launch_shared_prefix(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
+// Shapes of an attention call over drafted rows.
+int check_tree(int B, int Hq, int Hkv, int D, int Tq, int S_cap, int max_kv_len, float scale) {
+  const int rc = check_decode_shape(B, Hq, Hkv, D, S_cap, max_kv_len, scale);
+  if (rc != GQA_OK) return rc;
+  if (Tq < 1 || Tq > 1024) return GQA_ERR_INVALID_ARG;
+  if (long(B) * Hq * Tq > 0x7fffffffL) return GQA_ERR_INVALID_ARG;  // (rows in 32 bits)
+  if (max_kv_len > (1 << 30)) return GQA_ERR_INVALID_ARG;           // (a length and a tile's rows in 32 bits)
+  return GQA_OK;
+}
+
+// Everything of such a call but its cache; then it runs.
+int run_tree(TreeArgs& a, int dtype, size_t ws_bytes, int dev, void* stream) {
+  if (a.mask == nullptr ? a.W != 0 || a.tree_lens != nullptr : a.W < 1 || a.W > 32) return GQA_ERR_INVALID_ARG;
+  if (a.mask != nullptr && a.tree_lens == nullptr && 32 * a.W < a.Tq) return GQA_ERR_INVALID_ARG;
+  if (dtype != GQA_F32 && dtype != GQA_BF16) return GQA_ERR_INVALID_ARG;
+  if (dtype != GQA_BF16) return GQA_ERR_UNSUPPORTED;
+  int rc = check_ptrs({a.q, a.k, a.v, a.o}, dev, 16);
+  if (rc != GQA_OK) return rc;
+  rc = check_ptrs({a.kv_lens}, dev, 4);
+  if (rc != GQA_OK) return rc;
+  for (const int32_t* n : {a.mask, a.q_lens, a.tree_lens, a.block_table})
+    if (n != nullptr) {
+      rc = check_ptrs({n}, dev, 4);
+      if (rc != GQA_OK) return rc;
+    }
+  if (a.workspace == nullptr) return GQA_ERR_WORKSPACE;
+  rc = check_ptrs({a.workspace}, dev, 256);
+  if (rc == GQA_ERR_INVALID_ARG) return GQA_ERR_WORKSPACE;
+  if (rc != GQA_OK) return rc;
+  if (ws_bytes < tree_workspace_size(a.B, a.Hq, a.Hkv, a.D, a.Tq, a.max_kv_len)) return GQA_ERR_WORKSPACE;
+  return launch_tree(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+// Layers of blocks [n_layers, num_blocks, Hkv, block_size, D].
+int check_layers(int n_layers, int num_blocks, int Hkv, int block_size, int D, int dtype) {
+  if (n_layers < 1 || num_blocks < 1 || Hkv < 1 || block_size < 1) return GQA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return GQA_ERR_INVALID_ARG;
+  if (dtype != GQA_F32 && dtype != GQA_BF16) return GQA_ERR_INVALID_ARG;
+  if (long(n_layers) * Hkv > (1L << 20)) return GQA_ERR_INVALID_ARG;
+  if (long(num_blocks) * Hkv > 0x7fffffffL || long(num_blocks) * Hkv * block_size > 0x7fffffffL)
+    return GQA_ERR_INVALID_ARG;
+  return GQA_OK;
+}
+int row_bytes(int D, int dtype) { return D * (dtype == GQA_F32 ? 4 : 2); }
+
 size_t decode_ws_size(int B, int Hq, int Hkv, int D, int max_kv_len, int tile, int ctas_per_sm = 2) {
   const SplitPlan p = plan_splits(B, Hq, Hkv, max_kv_len, tile, device_sm_count(), ctas_per_sm);
   return workspace_layout(B, Hq, Hkv, p.n_hc, p.n_split, D).total;
@@ -698,6 +743,255 @@ GQA_ATTN_API int gqa_attn_rope_append(const void* q, const void* k, const void* 
   a.status = static_cast<uint32_t*>(workspace);
   if (launch_rope_append(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return GQA_ERR_CUDA;
   return GQA_OK;
+}
+
+GQA_ATTN_API size_t gqa_attn_decode_tree_workspace_size(int B, int Hq, int Hkv, int D, int Tq, int max_kv_len) {
+  if (check_tree(B, Hq, Hkv, D, Tq, max_kv_len, max_kv_len, 1.f) != GQA_OK) return 0;
+  return tree_workspace_size(B, Hq, Hkv, D, Tq, max_kv_len);
+}
+
+GQA_ATTN_API int gqa_attn_decode_tree(const void* q, const void* k, const void* v, const int32_t* tree_mask,
+                                      const int32_t* q_lens, const int32_t* tree_lens, const int32_t* kv_lens,
+                                      void* o, int B, int Hq, int Hkv, int D, int Tq, int mask_words, int S_cap,
+                                      int max_kv_len, float scale, int dtype, void* workspace, size_t ws_bytes,
+                                      void* stream) {
+  const int rc = check_tree(B, Hq, Hkv, D, Tq, S_cap, max_kv_len, scale);
+  if (rc != GQA_OK) return rc;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
+  TreeArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.mask = tree_mask;
+  a.q_lens = q_lens;
+  a.tree_lens = tree_lens;
+  a.kv_lens = kv_lens;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.Tq = Tq;
+  a.W = mask_words;
+  a.S_cap = S_cap;
+  a.max_kv_len = max_kv_len;
+  a.scale = scale;
+  a.workspace = workspace;
+  return run_tree(a, dtype, ws_bytes, dev, stream);
+}
+
+GQA_ATTN_API int gqa_attn_decode_tree_paged(const void* q, const void* k_pool, const void* v_pool,
+                                            const int32_t* block_table, const int32_t* tree_mask,
+                                            const int32_t* q_lens, const int32_t* tree_lens,
+                                            const int32_t* kv_lens, void* o, int B, int Hq, int Hkv, int D, int Tq,
+                                            int mask_words, int block_size, int num_blocks, int max_blocks,
+                                            int max_kv_len, float scale, int dtype, void* workspace, size_t ws_bytes,
+                                            void* stream) {
+  if (block_size < 1 || num_blocks < 1 || max_blocks < 1) return GQA_ERR_INVALID_ARG;
+  if (long(max_kv_len) > long(max_blocks) * block_size) return GQA_ERR_INVALID_ARG;
+  const int rc = check_tree(B, Hq, Hkv, D, Tq, max_kv_len, max_kv_len, scale);
+  if (rc != GQA_OK) return rc;
+  if (long(num_blocks) * Hkv > 0x7fffffffL || long(num_blocks) * Hkv * block_size > 0x7fffffffL)
+    return GQA_ERR_INVALID_ARG;
+  if (block_table == nullptr) return GQA_ERR_INVALID_ARG;
+  if (block_size % 64 != 0) return GQA_ERR_UNSUPPORTED;  // (the kernel copies 64 rows at a time)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
+  TreeArgs a;
+  a.q = q;
+  a.k = k_pool;
+  a.v = v_pool;
+  a.o = o;
+  a.mask = tree_mask;
+  a.q_lens = q_lens;
+  a.tree_lens = tree_lens;
+  a.kv_lens = kv_lens;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.Tq = Tq;
+  a.W = mask_words;
+  a.S_cap = block_size;
+  a.max_kv_len = max_kv_len;
+  a.scale = scale;
+  a.workspace = workspace;
+  a.block_table = block_table;
+  a.block_size = block_size;
+  a.max_blocks = max_blocks;
+  a.num_blocks = num_blocks;
+  return run_tree(a, dtype, ws_bytes, dev, stream);
+}
+
+GQA_ATTN_API int gqa_attn_tree_tables(const int32_t* parents, const int32_t* tree_lens, const int32_t* q_lens,
+                                      const int32_t* kv_lens, const int32_t* q_starts, int32_t* tree_mask,
+                                      int32_t* positions, int B, int N, int Tq, int mask_words, int T,
+                                      void* workspace, size_t ws_bytes, void* stream) {
+  if (B < 1 || B > 65535 || N < 1 || N > 1024 || Tq < 1 || Tq > 1024) return GQA_ERR_INVALID_ARG;
+  if (mask_words != (N + 31) / 32) return GQA_ERR_INVALID_ARG;
+  const bool placed = positions != nullptr;
+  if (placed != (kv_lens != nullptr) || placed != (q_starts != nullptr) || (placed && T < 1)) return GQA_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
+  int rc = check_ptrs({parents, tree_lens, tree_mask}, dev, 4);
+  if (rc != GQA_OK) return rc;
+  if (q_lens != nullptr) {
+    rc = check_ptrs({q_lens}, dev, 4);
+    if (rc != GQA_OK) return rc;
+  }
+  if (placed) {
+    rc = check_ptrs({kv_lens, q_starts, positions}, dev, 4);
+    if (rc != GQA_OK) return rc;
+  }
+  rc = check_status_workspace(workspace, ws_bytes, dev);
+  if (rc != GQA_OK) return rc;
+  TreeTablesArgs a;
+  a.parents = parents;
+  a.tree_lens = tree_lens;
+  a.q_lens = q_lens;
+  a.kv_lens = kv_lens;
+  a.q_starts = q_starts;
+  a.mask = tree_mask;
+  a.positions = positions;
+  a.B = B;
+  a.N = N;
+  a.Tq = Tq;
+  a.W = mask_words;
+  a.T = T;
+  a.status = static_cast<uint32_t*>(workspace);
+  return launch_tree_tables(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+GQA_ATTN_API int gqa_attn_compact_rows(const int32_t* path, const int32_t* n_keep, const int32_t* tree_lens,
+                                       const int32_t* kv_lens, const int32_t* block_table, void* k_cache,
+                                       void* v_cache, int32_t* kv_lens_out, int n_layers, int B, int P, int Hkv,
+                                       int D, int block_size, int num_blocks, int max_blocks, int dtype,
+                                       void* workspace, size_t ws_bytes, void* stream) {
+  constexpr long kMax = 0x7fffffffL;
+  if (B < 1 || B > 65535 || P < 1 || P > 1024) return GQA_ERR_INVALID_ARG;
+  int rc = check_layers(n_layers, num_blocks, Hkv, block_size, D, dtype);
+  if (rc != GQA_OK) return rc;
+  if (block_table != nullptr) {
+    if (max_blocks < 1 || long(B) * max_blocks > kMax || long(max_blocks) * block_size > kMax) return GQA_ERR_INVALID_ARG;
+  } else if (num_blocks != B) {
+    return GQA_ERR_INVALID_ARG;
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
+  rc = check_ptrs({path, n_keep, tree_lens, kv_lens, kv_lens_out}, dev, 4);
+  if (rc != GQA_OK) return rc;
+  if (block_table != nullptr) {
+    rc = check_ptrs({block_table}, dev, 4);
+    if (rc != GQA_OK) return rc;
+  }
+  rc = check_ptrs({k_cache, v_cache}, dev, 16);
+  if (rc != GQA_OK) return rc;
+  rc = check_status_workspace(workspace, ws_bytes, dev);
+  if (rc != GQA_OK) return rc;
+  CompactArgs a;
+  a.path = path;
+  a.n_keep = n_keep;
+  a.tree_lens = tree_lens;
+  a.kv_lens = kv_lens;
+  a.block_table = block_table;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.kv_lens_out = kv_lens_out;
+  a.n_layers = n_layers;
+  a.B = B;
+  a.P = P;
+  a.Hkv = Hkv;
+  a.row_bytes = row_bytes(D, dtype);
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.max_blocks = block_table != nullptr ? max_blocks : 1;
+  a.status = static_cast<uint32_t*>(workspace);
+  return launch_compact(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+GQA_ATTN_API int gqa_attn_fork_tables(const int32_t* src, const int32_t* keep_lens, const int32_t* held_lens,
+                                      const int32_t* block_table, const int32_t* shared, const int32_t* free_blocks,
+                                      const int32_t* free_count, int32_t* block_table_out, int32_t* kv_lens_out,
+                                      int32_t* shared_out, int32_t* free_blocks_out, int32_t* free_count_out,
+                                      int32_t* copy_src, int32_t* copy_dst, int32_t* copy_rows, int B_in, int B,
+                                      int max_blocks, int block_size, int num_blocks, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+  constexpr long kMax = 0x7fffffffL;
+  if (B < 1 || B > 8192 || B_in < 1 || B_in > 8192) return GQA_ERR_INVALID_ARG;
+  if (max_blocks < 1 || block_size < 1 || num_blocks < 1) return GQA_ERR_INVALID_ARG;
+  if (long(std::max(B, B_in)) * max_blocks >= (1L << 30)) return GQA_ERR_INVALID_ARG;
+  if (long(max_blocks) * block_size > kMax || long(num_blocks) * block_size > kMax) return GQA_ERR_INVALID_ARG;
+  if (block_table == block_table_out) return GQA_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
+  int rc = check_ptrs({src, held_lens, block_table, shared, free_blocks, free_count, block_table_out, kv_lens_out,
+                       shared_out, free_blocks_out, free_count_out, copy_src, copy_dst, copy_rows},
+                      dev, 4);
+  if (rc != GQA_OK) return rc;
+  if (keep_lens != nullptr) {
+    rc = check_ptrs({keep_lens}, dev, 4);
+    if (rc != GQA_OK) return rc;
+  }
+  rc = check_status_workspace(workspace, ws_bytes, dev);
+  if (rc != GQA_OK) return rc;
+  ForkArgs a;
+  a.src = src;
+  a.keep_lens = keep_lens;
+  a.held_lens = held_lens;
+  a.table = block_table;
+  a.shared = shared;
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.table_out = block_table_out;
+  a.kv_lens_out = kv_lens_out;
+  a.shared_out = shared_out;
+  a.free_out = free_blocks_out;
+  a.count_out = free_count_out;
+  a.copy_src = copy_src;
+  a.copy_dst = copy_dst;
+  a.copy_rows = copy_rows;
+  a.B_in = B_in;
+  a.B = B;
+  a.max_blocks = max_blocks;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.status = static_cast<uint32_t*>(workspace);
+  return launch_fork(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+GQA_ATTN_API int gqa_attn_copy_blocks(const int32_t* src, const int32_t* dst, const int32_t* rows, void* k_cache,
+                                      void* v_cache, int n_layers, int n, int Hkv, int D, int block_size,
+                                      int num_blocks, int dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (n < 1 || n > 65535) return GQA_ERR_INVALID_ARG;
+  int rc = check_layers(n_layers, num_blocks, Hkv, block_size, D, dtype);
+  if (rc != GQA_OK) return rc;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
+  rc = check_ptrs({src, dst}, dev, 4);
+  if (rc != GQA_OK) return rc;
+  if (rows != nullptr) {
+    rc = check_ptrs({rows}, dev, 4);
+    if (rc != GQA_OK) return rc;
+  }
+  rc = check_ptrs({k_cache, v_cache}, dev, 16);
+  if (rc != GQA_OK) return rc;
+  rc = check_status_workspace(workspace, ws_bytes, dev);
+  if (rc != GQA_OK) return rc;
+  CopyBlocksArgs a;
+  a.src = src;
+  a.dst = dst;
+  a.rows = rows;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.n_layers = n_layers;
+  a.n = n;
+  a.Hkv = Hkv;
+  a.row_bytes = row_bytes(D, dtype);
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.status = static_cast<uint32_t*>(workspace);
+  return launch_copy_blocks(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 GQA_ATTN_API size_t gqa_attn_decode_q4_workspace_size(int B, int Hq, int Hkv, int D,

@@ -227,6 +227,89 @@ struct RopeAppendArgs {
 };
 cudaError_t launch_rope_append(const RopeAppendArgs& a, cudaStream_t stream);
 
+// Attention of drafted rows over the cache (gqa_attn_decode_tree).
+struct TreeArgs {
+  const void* q;
+  const void* k;  // [B][Hkv][S_cap][D], or the pools
+  const void* v;
+  void* o;
+  const int32_t* mask;       // [B][Tq][W], or nullptr: a chain
+  const int32_t* q_lens;     // or nullptr: Tq
+  const int32_t* tree_lens;  // or nullptr: q_lens
+  const int32_t* kv_lens;
+  int B, Hq, Hkv, D, Tq, W, S_cap, max_kv_len;
+  float scale;
+  void* workspace;
+  const int32_t* block_table = nullptr;  // or nullptr: dense
+  int block_size = 0, max_blocks = 0, num_blocks = 0;
+};
+size_t tree_workspace_size(int B, int Hq, int Hkv, int D, int Tq, int max_kv_len);
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
+
+// Tables of a tree of drafted tokens (gqa_attn_tree_tables).
+struct TreeTablesArgs {
+  const int32_t* parents;
+  const int32_t* tree_lens;
+  const int32_t* q_lens;    // or nullptr
+  const int32_t* kv_lens;   // with q_starts and positions, or nullptr
+  const int32_t* q_starts;
+  int32_t* mask;
+  int32_t* positions;
+  int B, N, Tq, W, T;
+  uint32_t* status;
+};
+cudaError_t launch_tree_tables(const TreeTablesArgs& a, cudaStream_t stream);
+
+// Accepted rows moved together (gqa_attn_compact_rows); block_table ==
+// nullptr: a dense cache of block_size rows per request.
+struct CompactArgs {
+  const int32_t* path;
+  const int32_t* n_keep;
+  const int32_t* tree_lens;
+  const int32_t* kv_lens;
+  const int32_t* block_table;
+  void* k_cache;
+  void* v_cache;
+  int32_t* kv_lens_out;
+  int n_layers, B, P, Hkv, row_bytes, block_size, num_blocks, max_blocks;
+  uint32_t* status;
+};
+cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream);
+
+// Block tables of requests that fork, shorten or end (gqa_attn_fork_tables).
+struct ForkArgs {
+  const int32_t* src;
+  const int32_t* keep_lens;  // or nullptr
+  const int32_t* held_lens;
+  const int32_t* table;
+  const int32_t* shared;
+  const int32_t* free_blocks;
+  const int32_t* free_count;
+  int32_t* table_out;
+  int32_t* kv_lens_out;
+  int32_t* shared_out;
+  int32_t* free_out;
+  int32_t* count_out;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t* copy_rows;
+  int B_in, B, max_blocks, block_size, num_blocks;
+  uint32_t* status;
+};
+cudaError_t launch_fork(const ForkArgs& a, cudaStream_t stream);
+
+// Copies of cache blocks (gqa_attn_copy_blocks).
+struct CopyBlocksArgs {
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* rows;  // or nullptr
+  void* k_cache;
+  void* v_cache;
+  int n_layers, n, Hkv, row_bytes, block_size, num_blocks;
+  uint32_t* status;
+};
+cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, cudaStream_t stream);
+
 // Upper bound on the time a kernel waits for one of its own tile copies
 // before it records GQA_DEV_WAIT_TIMEOUT and stops (nanoseconds).
 constexpr uint64_t kWaitLimitNs = 1000000000ull;

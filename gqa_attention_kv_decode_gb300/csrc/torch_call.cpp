@@ -284,6 +284,165 @@ int decode_shared_prefix_paged(PyObject* const* a) {
   return rc;
 }
 
+// Attention of drafted rows; the dense (o at 7) and the paged call (8) differ in
+// the cache, and in the block table before the mask.
+template <bool PAGED>
+int decode_tree(PyObject* const* a) {
+  constexpr int T = PAGED ? 1 : 0;  // (arguments behind the block table)
+  const Tensor *q = tensor(a[0]), *k = tensor(a[1]), *v = tensor(a[2]), *table = PAGED ? tensor(a[3]) : nullptr,
+               *mask = tensor(a[3 + T], true), *q_lens = tensor(a[4 + T], true), *tree_lens = tensor(a[5 + T], true),
+               *lens = tensor(a[6 + T]), *o = tensor(a[7 + T]);
+  rank(q, 4, "q is [B, Hq, Tq, D]");
+  rank(k, 4, PAGED ? "k_pool is [blocks, Hkv, block_size, D]" : "k is [B, Hkv, S_cap, D]");
+  const int64_t B = q->size(0), Hq = q->size(1), Tq = q->size(2), D = q->size(3);
+  if (v->sizes() != k->sizes() || k->size(3) != D || o->sizes() != q->sizes() || (!PAGED && k->size(0) != B))
+    raise(PyExc_ValueError, PAGED ? "k_pool and v_pool are [blocks, Hkv, block_size, D], o as q"
+                                  : "k and v are [B, Hkv, S_cap, D], o as q");
+  one_dtype(q, {k, v, o});
+  int64_t W = 0, max_blocks = 0;
+  if (mask != nullptr) {
+    rank(mask, 3, "tree_mask is [B, Tq, words]");
+    W = mask->size(2);
+    if (!shaped(mask, {B, Tq, W})) raise(PyExc_ValueError, "tree_mask is [B, Tq, words]");
+  }
+  if (PAGED) {
+    rank(table, 2, "block_table is [B, max_blocks]");
+    max_blocks = table->size(1);
+  }
+  const void *pq = dense(q), *pk = dense(k), *pv = dense(v);
+  const int32_t *pt = ints(table, B * max_blocks), *pm = ints(mask, B * Tq * W), *pql = ints(q_lens, B),
+                *ptl = ints(tree_lens, B), *pl = ints(lens, B);
+  void* const po = dense(o);
+  const float scale = number(a[8 + T]);
+  const int b = size(B), hq = size(Hq), hkv = size(k->size(1)), d = size(D), tq = size(Tq), w = size(W),
+            rows = size(k->size(2)), nb = size(k->size(0)), mb = size(max_blocks),
+            mk = bound(a[10 + T], PAGED ? max_blocks * k->size(2) : k->size(2)), dt = dtype_code(q);
+  const Workspace ws(a[9 + T]);
+  void* const stream = stream_of(a[11 + T]);
+  const Pointers known({q, k, v, table, mask, q_lens, tree_lens, lens, o, ws.t});
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = PAGED ? gqa_attn_decode_tree_paged(pq, pk, pv, pt, pm, pql, ptl, pl, po, b, hq, hkv, d, tq, w, rows, nb, mb, mk,
+                                          scale, dt, ws.p, ws.bytes, stream)
+             : gqa_attn_decode_tree(pq, pk, pv, pm, pql, ptl, pl, po, b, hq, hkv, d, tq, w, rows, mk, scale, dt, ws.p,
+                                    ws.bytes, stream);
+  Py_END_ALLOW_THREADS
+  return rc;
+}
+
+int tree_tables(PyObject* const* a) {
+  const Tensor *parents = tensor(a[0]), *tree_lens = tensor(a[1]), *q_lens = tensor(a[2], true),
+               *kv = tensor(a[3], true), *starts = tensor(a[4], true), *mask = tensor(a[5]),
+               *pos = tensor(a[6], true);
+  rank(parents, 2, "parents is [B, N]");
+  rank(mask, 3, "tree_mask is [B, Tq, words]");
+  const int64_t B = parents->size(0), N = parents->size(1), Tq = mask->size(1), W = mask->size(2),
+                T = pos == nullptr ? 0 : pos->numel();
+  if (mask->size(0) != B) raise(PyExc_ValueError, "tree_mask is [B, Tq, words]");
+  const int32_t *pp = ints(parents, B * N), *pn = ints(tree_lens, B), *pq = ints(q_lens, B), *pk = ints(kv, B),
+                *ps = ints(starts, B + 1);
+  int32_t *pm = ints(mask, B * Tq * W), *ppos = ints(pos, T);
+  const int b = size(B), n = size(N), tq = size(Tq), w = size(W), t = size(T);
+  const Workspace ws(a[7]);
+  void* const stream = stream_of(a[8]);
+  const Pointers known({parents, tree_lens, q_lens, kv, starts, mask, pos, ws.t});
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = gqa_attn_tree_tables(pp, pn, pq, pk, ps, pm, ppos, b, n, tq, w, t, ws.p, ws.bytes, stream);
+  Py_END_ALLOW_THREADS
+  return rc;
+}
+
+// K and V of one layer [blocks, Hkv, block_size, D], or of several, stacked.
+struct Layers {
+  int n, blocks, hkv, block_size, d, dtype;
+  void *k, *v;
+  Layers(const Tensor* kc, const Tensor* vc) {
+    const int64_t r = kc->dim();
+    if ((r != 4 && r != 5) || vc->sizes() != kc->sizes())
+      raise(PyExc_ValueError, "k_cache and v_cache are [blocks, Hkv, block_size, D] or [layers, blocks, ...]");
+    one_dtype(kc, {vc});
+    n = r == 5 ? size(kc->size(0)) : 1;
+    blocks = size(kc->size(r - 4));
+    hkv = size(kc->size(r - 3));
+    block_size = size(kc->size(r - 2));
+    d = size(kc->size(r - 1));
+    dtype = dtype_code(kc);
+    k = dense(kc);
+    v = dense(vc);
+  }
+};
+
+int compact_rows(PyObject* const* a) {
+  const Tensor *path = tensor(a[0]), *keep = tensor(a[1]), *tree_lens = tensor(a[2]), *lens = tensor(a[3]),
+               *table = tensor(a[4], true), *kc = tensor(a[5]), *vc = tensor(a[6]), *out = tensor(a[7]);
+  rank(path, 2, "path is [B, P]");
+  const int64_t B = path->size(0), P = path->size(1);
+  int64_t max_blocks = 0;
+  if (table != nullptr) {
+    rank(table, 2, "block_table is [B, max_blocks]");
+    max_blocks = table->size(1);
+  }
+  const Layers c(kc, vc);
+  const int32_t *pp = ints(path, B * P), *pk = ints(keep, B), *pn = ints(tree_lens, B), *pl = ints(lens, B),
+                *pt = ints(table, B * max_blocks);
+  int32_t* const po = ints(out, B);
+  const int b = size(B), w = size(P), mb = size(max_blocks);
+  const Workspace ws(a[8]);
+  void* const stream = stream_of(a[9]);
+  const Pointers known({path, keep, tree_lens, lens, table, kc, vc, out, ws.t});
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = gqa_attn_compact_rows(pp, pk, pn, pl, pt, c.k, c.v, po, c.n, b, w, c.hkv, c.d, c.block_size, c.blocks, mb,
+                             c.dtype, ws.p, ws.bytes, stream);
+  Py_END_ALLOW_THREADS
+  return rc;
+}
+
+int fork_tables(PyObject* const* a) {
+  const Tensor *src = tensor(a[0]), *keep = tensor(a[1], true), *held = tensor(a[2]), *table = tensor(a[3]),
+               *shared = tensor(a[4]), *stack = tensor(a[5]), *count = tensor(a[6]), *table_out = tensor(a[7]),
+               *kv = tensor(a[8]), *shared_out = tensor(a[9]), *stack_out = tensor(a[10]), *count_out = tensor(a[11]),
+               *csrc = tensor(a[12]), *cdst = tensor(a[13]), *crows = tensor(a[14]);
+  rank(table, 2, "block_table is [B_in, max_blocks]");
+  rank(table_out, 2, "block_table_out is [B, max_blocks]");
+  const int64_t B = src->numel(), B_in = held->numel(), mb = table->size(1), nb = stack->numel();
+  if (table_out->size(1) != mb) raise(PyExc_ValueError, "both block tables have max_blocks columns");
+  const int32_t *ps = ints(src, B), *pk = ints(keep, B), *ph = ints(held, B_in), *pt = ints(table, B_in * mb),
+                *psh = ints(shared, nb), *pst = ints(stack, nb), *pc = ints(count, 1);
+  int32_t *pto = ints(table_out, B * mb), *pkv = ints(kv, B), *psho = ints(shared_out, nb), *psto = ints(stack_out, nb),
+          *pco = ints(count_out, 1), *pcs = ints(csrc, B), *pcd = ints(cdst, B), *pcr = ints(crows, B);
+  const int bi = size(B_in), b = size(B), m = size(mb), n = size(nb), bs = size(integer(a[15]));
+  const Workspace ws(a[16]);
+  void* const stream = stream_of(a[17]);
+  const Pointers known({src, keep, held, table, shared, stack, count, table_out, kv, shared_out, stack_out, count_out,
+                        csrc, cdst, crows, ws.t});
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = gqa_attn_fork_tables(ps, pk, ph, pt, psh, pst, pc, pto, pkv, psho, psto, pco, pcs, pcd, pcr, bi, b, m, bs, n,
+                            ws.p, ws.bytes, stream);
+  Py_END_ALLOW_THREADS
+  return rc;
+}
+
+int copy_blocks(PyObject* const* a) {
+  const Tensor *src = tensor(a[0]), *dst = tensor(a[1]), *rows = tensor(a[2], true), *kc = tensor(a[3]),
+               *vc = tensor(a[4]);
+  const int64_t n = src->numel();
+  const Layers c(kc, vc);
+  const int32_t *ps = ints(src, n), *pd = ints(dst, n), *pr = ints(rows, n);
+  const int m = size(n);
+  const Workspace ws(a[5]);
+  void* const stream = stream_of(a[6]);
+  const Pointers known({src, dst, rows, kc, vc, ws.t});
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = gqa_attn_copy_blocks(ps, pd, pr, c.k, c.v, c.n, m, c.hkv, c.d, c.block_size, c.blocks, c.dtype, ws.p, ws.bytes,
+                            stream);
+  Py_END_ALLOW_THREADS
+  return rc;
+}
+
 template <int (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) return PyErr_Format(PyExc_TypeError, "%d arguments are needed, got %zd", N, n);
@@ -305,6 +464,10 @@ PyMethodDef method(const char* name) {
 PyMethodDef methods[] = {method<step_tables, 16>("step_tables"), method<rope_append, 16>("rope_append"),
                          method<decode_shared_prefix, 13>("decode_shared_prefix"),
                          method<decode_shared_prefix_paged, 13>("decode_shared_prefix_paged"),
+                         method<decode_tree<false>, 12>("decode_tree"),
+                         method<decode_tree<true>, 13>("decode_tree_paged"), method<tree_tables, 9>("tree_tables"),
+                         method<compact_rows, 10>("compact_rows"), method<fork_tables, 18>("fork_tables"),
+                         method<copy_blocks, 7>("copy_blocks"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_call", "Native calls of libgqa_attn on torch tensors.", -1,

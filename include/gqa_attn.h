@@ -90,6 +90,7 @@ typedef enum gqa_dtype {
 #define GQA_DEV_OUT_OF_BLOCKS 16u /* too few free blocks: some request got no tokens */
 #define GQA_DEV_BAD_SLOT 32u     /* a slot was past the cache: not written          */
 #define GQA_DEV_BAD_POSITION 64u /* a position outside the angle table: not written */
+#define GQA_DEV_BAD_INDEX 128u   /* a parent, kept node or source request out of range */
 
 /* ---------------------------------------------------------------------------
  * Single-token decode (q_len = 1), split-KV with a log-sum-exp combine.
@@ -358,6 +359,196 @@ GQA_ATTN_API int gqa_attn_rope_append(const void* q, const void* k, const void* 
                                       void* v_cache, int T, int Hq, int Hkv, int D, int rot_dim,
                                       int max_pos, int adjacent, int num_blocks, int block_size,
                                       int q_groups, int q_rows, int dtype, void* workspace,
+                                      size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Verifying drafted tokens: attention of several new rows of each request over
+ * its cache, the new rows seeing one another as a tree (or chain) says.
+ *
+ * A request's new rows are already in the cache, as the last q_lens[b] of its
+ * kv_lens[b] rows (gqa_attn_step_tables and gqa_attn_rope_append put them
+ * there).  Query i belongs to row kv_lens[b] - q_lens[b] + i.  It sees every row
+ * before the request's drafted ones, which are its last tree_lens[b] rows, and
+ * of these the ones whose bit is set in its mask:
+ *   tree_mask     int32 [B, Tq, mask_words] (written by gqa_attn_tree_tables, or
+ *                 by the caller): bit c % 32 of word c / 32 of query i says
+ *                 whether it sees row kv_lens[b] - tree_lens[b] + c.  Any mask will
+ *                 do; a query's own row has no bit by itself.  NULL (mask_words
+ *                 0, tree_lens NULL): a chain, query i sees the rows up to its own
+ *   q_lens        device int32 [B], or NULL: Tq queries in every request;
+ *                 clamped into [0, min(Tq, kv_lens[b])]
+ *   tree_lens     device int32 [B], or NULL: q_lens[b] (mask_words * 32 >= Tq);
+ *                 clamped into [0, min(32 * mask_words, kv_lens[b])].  It is above
+ *                 q_lens[b] where earlier steps drafted the tree's first rows.
+ *   kv_lens       device int32 [B], drafted rows included; clamped into
+ *                 [0, max_kv_len].  Whatever is clamped sets GQA_DEV_KVLEN_CLAMPED.
+ *   q, o          bf16 [B, Hq, Tq, D]; rows of o from q_lens[b] on are not written
+ *   k, v          bf16 [B, Hkv, S_cap, D], or pools and a block_table as for
+ *                 gqa_attn_decode_paged (block_size a multiple of 64; an id outside
+ *                 the pool sets GQA_DEV_BAD_BLOCK)
+ * A query that sees no row at all gets zeros and sets GQA_DEV_EMPTY_REQUEST.
+ * Rows of K and V past kv_lens[b] may hold anything; of a drafted row that a
+ * query does not see, K may hold anything and V finite numbers (its weight is 0
+ * there).  The queries of a request and KV head (Hq / Hkv * q_lens[b] rows) read
+ * its keys together, up to 256 of them at once.
+ * Tq at most 1024, mask_words 1 to 32; B * Hq * Tq < 2^31; dtype must be GQA_BF16
+ * (else GQA_ERR_UNSUPPORTED).  Workspace: gqa_attn_decode_tree_workspace_size, for both
+ * entry points.  Other arguments and errors as for gqa_attn_decode(_paged).
+ * ------------------------------------------------------------------------- */
+GQA_ATTN_API size_t gqa_attn_decode_tree_workspace_size(int B, int Hq, int Hkv, int D, int Tq,
+                                                        int max_kv_len);
+GQA_ATTN_API int gqa_attn_decode_tree(const void* q, const void* k, const void* v,
+                                      const int32_t* tree_mask, const int32_t* q_lens,
+                                      const int32_t* tree_lens, const int32_t* kv_lens, void* o, int B,
+                                      int Hq, int Hkv, int D, int Tq, int mask_words, int S_cap,
+                                      int max_kv_len, float scale, int dtype, void* workspace,
+                                      size_t ws_bytes, void* stream);
+GQA_ATTN_API int gqa_attn_decode_tree_paged(const void* q, const void* k_pool, const void* v_pool,
+                                            const int32_t* block_table, const int32_t* tree_mask,
+                                            const int32_t* q_lens, const int32_t* tree_lens,
+                                            const int32_t* kv_lens, void* o, int B, int Hq, int Hkv,
+                                            int D, int Tq, int mask_words, int block_size,
+                                            int num_blocks, int max_blocks, int max_kv_len, float scale,
+                                            int dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The tables of a tree of drafted tokens, from its parents: once a step, for
+ * every layer's gqa_attn_decode_tree and gqa_attn_rope_append.
+ *
+ *   parents       device int32 [B, N]: parent node of each node of request b, a
+ *                 node before it, or -1 for a node that follows the last row
+ *                 before the tree
+ *   tree_lens     device int32 [B]: nodes of each request, clamped into [0, N]
+ *   q_lens        device int32 [B]: the last so many nodes are this step's
+ *                 queries, clamped into [0, min(Tq, tree_lens[b])]; NULL: as many
+ *                 as there can be
+ *   tree_mask     int32 [B, Tq, mask_words], mask_words = ceil(N / 32) (written):
+ *                 for query i (node tree_lens[b] - q_lens[b] + i) the node and all
+ *                 above it; rows from q_lens[b] on are left as they are
+ *   kv_lens,      device int32 [B] and [B + 1], and int32 [T] (written), or all
+ *   q_starts,     three NULL: the position kv_lens[b] - tree_lens[b] + depth of
+ *   positions     query i goes to positions[q_starts[b] + i] where that is in
+ *                 [0, T), over the consecutive ones of gqa_attn_step_tables; other
+ *                 entries are left as they are.  A tree longer than its request
+ *                 begins at position 0.
+ * Whatever is clamped sets GQA_DEV_KVLEN_CLAMPED.  A parent that is no node before
+ * its node sets GQA_DEV_BAD_INDEX and counts as -1.
+ * 1 <= N <= 1024, 1 <= Tq <= 1024, B <= 65535.
+ *   workspace     as for gqa_attn_step_tables (the status word)
+ * ------------------------------------------------------------------------- */
+GQA_ATTN_API int gqa_attn_tree_tables(const int32_t* parents, const int32_t* tree_lens,
+                                      const int32_t* q_lens, const int32_t* kv_lens,
+                                      const int32_t* q_starts, int32_t* tree_mask, int32_t* positions,
+                                      int B, int N, int Tq, int mask_words, int T, void* workspace,
+                                      size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The accepted rows of a tree, moved together behind the rows before it, in
+ * K and V of every layer.
+ *
+ *   path          device int32 [B, P]: the kept nodes of request b, the first
+ *                 n_keep[b] entries ascending; node c is row
+ *                 kv_lens[b] - tree_lens[b] + c
+ *   n_keep        device int32 [B]: kept nodes, clamped into
+ *                 [0, min(P, tree_lens[b])]
+ *   tree_lens     device int32 [B]: nodes, clamped into [0, kv_lens[b]]
+ *   kv_lens       device int32 [B]: rows with the tree's, clamped into
+ *                 [0, max_blocks * block_size] (dense: block_size)
+ *   block_table   device int32 [B, max_blocks], or NULL: a dense cache
+ *                 (block_size = S_cap, num_blocks = B, max_blocks not used)
+ *   k_cache,      [n_layers, num_blocks, Hkv, block_size, D] dtype (row path[b][i]
+ *   v_cache       of the tree goes to its row i, others stay as they are)
+ *   kv_lens_out   device int32 [B] (written): kv_lens[b] - tree_lens[b] + n_keep[b]
+ * What is clamped sets GQA_DEV_KVLEN_CLAMPED.  A path that does not ascend or leaves
+ * the tree sets GQA_DEV_BAD_INDEX: nothing of that request moves and kv_lens_out[b]
+ * counts the rows before the tree.  A block id outside the pool sets
+ * GQA_DEV_BAD_BLOCK, and rows from or to it do not move.  Blocks of moved rows belong
+ * to one request alone (as gqa_attn_fork_tables leaves them).
+ * D = 64 or 128; 1 <= P <= 1024; n_layers * Hkv <= 2^20; num_blocks * Hkv * block_size
+ * and B * max_blocks < 2^31; no output overlaps another array.
+ *   workspace     as for gqa_attn_step_tables (the status word)
+ * ------------------------------------------------------------------------- */
+GQA_ATTN_API int gqa_attn_compact_rows(const int32_t* path, const int32_t* n_keep,
+                                       const int32_t* tree_lens, const int32_t* kv_lens,
+                                       const int32_t* block_table, void* k_cache, void* v_cache,
+                                       int32_t* kv_lens_out, int n_layers, int B, int P, int Hkv, int D,
+                                       int block_size, int num_blocks, int max_blocks, int dtype,
+                                       void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Requests of a paged cache that continue, fork, shorten or end: the block
+ * tables of a new set of requests, each the first rows of one of the old set.
+ *
+ * Whole blocks are shared between the requests that keep them; `shared` counts
+ * the holders of each block beyond the first (so blocks from gqa_attn_step_tables
+ * need no entry made for them).  A block that is kept in part will be written to, and has one
+ * holder alone: of the new requests with the same source the one that keeps most
+ * rows (of equals the first) is the owner, which stays in the block where nobody
+ * else holds it; every other one, and an owner whose block is shared, gets a
+ * free block and a copy to be made by gqa_attn_copy_blocks.  Blocks that nobody
+ * holds any more go back to the stack.  Ending requests (in no src), rows given
+ * back after a rejected draft (keep_lens), beams and samples are all this call;
+ * a request with shared blocks ends here, not by a negative new_lens of
+ * gqa_attn_step_tables.
+ *
+ *   src           device int32 [B]: source request of each new one, in [0, B_in),
+ *                 or negative: none (an empty new request).  One outside sets
+ *                 GQA_DEV_BAD_INDEX and counts as none.
+ *   keep_lens     device int32 [B]: rows kept, clamped into [0, held_lens[src[b]]];
+ *                 NULL: all
+ *   held_lens     device int32 [B_in]: rows whose blocks each old request holds,
+ *                 clamped into [0, max_blocks * block_size]
+ *   block_table   device int32 [B_in, max_blocks]
+ *   shared        device int32 [num_blocks]: holders beyond the first
+ *   free_blocks   device int32 [num_blocks], free_count device int32 [1]: the stack
+ *                 of gqa_attn_step_tables
+ *   block_table_out  int32 [B, max_blocks] (written): entries past a request's last
+ *                 block are left as they are
+ *   kv_lens_out   int32 [B] (written): rows kept
+ *   shared_out, free_blocks_out, free_count_out (written): holders and stack
+ *                 afterwards; each may be its input itself
+ *   copy_src,     int32 [B] (written): the copy of new request b, copy_rows[b] rows
+ *   copy_dst,     of block copy_src[b] to block copy_dst[b]; -1, -1, 0: none
+ *   copy_rows
+ * Free blocks are taken from the end of the stack, in request order; then those given
+ * back are put on it, in the order of the old tables (so none of these is taken in
+ * the same call).  Where the stack is empty the request keeps its whole blocks
+ * alone: GQA_DEV_OUT_OF_BLOCKS.  What is clamped sets GQA_DEV_KVLEN_CLAMPED.  Block ids
+ * outside [0, num_blocks) in entries that are kept or given back, a *free_count
+ * outside [0, num_blocks] (clamped) and a push past the stack's end (dropped)
+ * set GQA_DEV_BAD_BLOCK; such ids have no holders and are not put on the stack.
+ * B, B_in <= 8192; B * max_blocks, B_in * max_blocks < 2^30; num_blocks * block_size
+ * and max_blocks * block_size < 2^31.  No output overlaps another array but as said.
+ *   workspace     as for gqa_attn_step_tables (the status word)
+ * ------------------------------------------------------------------------- */
+GQA_ATTN_API int gqa_attn_fork_tables(const int32_t* src, const int32_t* keep_lens,
+                                      const int32_t* held_lens, const int32_t* block_table,
+                                      const int32_t* shared, const int32_t* free_blocks,
+                                      const int32_t* free_count, int32_t* block_table_out,
+                                      int32_t* kv_lens_out, int32_t* shared_out,
+                                      int32_t* free_blocks_out, int32_t* free_count_out,
+                                      int32_t* copy_src, int32_t* copy_dst, int32_t* copy_rows, int B_in,
+                                      int B, int max_blocks, int block_size, int num_blocks,
+                                      void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Copies of cache blocks, in K and V of every layer.
+ *
+ *   src, dst      device int32 [n]: copy i goes from block src[i] to dst[i]; a
+ *                 negative src: none
+ *   rows          device int32 [n]: rows copied of each head (the first ones),
+ *                 clamped into [0, block_size] (GQA_DEV_KVLEN_CLAMPED); NULL: all
+ *   k_cache,      [n_layers, num_blocks, Hkv, block_size, D] dtype (modified)
+ *   v_cache
+ * A block is the destination of at most one copy and then the source of none
+ * (otherwise it holds some mix).  Ids past the pool and a negative dst set
+ * GQA_DEV_BAD_BLOCK, and the copy is left out.
+ * D = 64 or 128; n <= 65535; n_layers * Hkv <= 2^20; num_blocks * Hkv * block_size < 2^31.
+ *   workspace     as for gqa_attn_step_tables (the status word)
+ * ------------------------------------------------------------------------- */
+GQA_ATTN_API int gqa_attn_copy_blocks(const int32_t* src, const int32_t* dst, const int32_t* rows,
+                                      void* k_cache, void* v_cache, int n_layers, int n, int Hkv, int D,
+                                      int block_size, int num_blocks, int dtype, void* workspace,
                                       size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
