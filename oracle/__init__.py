@@ -25,3 +25,11 @@ from .step_oracle import (  # noqa: F401
     rope_append,
     attention_shared_prefix,
 )
+from .tree_oracle import (  # noqa: F401
+    tree_tables,
+    tree_visible,
+    attention_tree,
+    compact_rows,
+    fork_tables,
+    copy_blocks,
+)
