@@ -211,6 +211,9 @@ int check_tree(int B, int Hq, int Hkv, int D, int Tq, int S_cap, int max_kv_len,
   if (Tq < 1 || Tq > 1024) return GQA_ERR_INVALID_ARG;
   if (long(B) * Hq * Tq > 0x7fffffffL) return GQA_ERR_INVALID_ARG;  // (rows in 32 bits)
   if (max_kv_len > (1 << 30)) return GQA_ERR_INVALID_ARG;           // (a length and a tile's rows in 32 bits)
+  // (the list of key tiles in 32 bits)
+  const long units = long(B) * Hkv * ((long(Hq / Hkv) * Tq + 255) / 256);
+  if (units * (max_kv_len / 128 + 8L) > 0x7fffffffL) return GQA_ERR_INVALID_ARG;
   return GQA_OK;
 }
 

@@ -47,7 +47,7 @@ namespace gqa {
 namespace {
 
 constexpr int kLead = 2;         // key tiles that the start and the end of a unit count as
-constexpr int kStaged = 1024;    // requests kept in shared memory
+constexpr int kMost = 1024;      // requests of a launch (kept in shared memory)
 constexpr int kMinWork = 3;      // tiles (with kLead) a worker gets at least, where there are few
 
 // Tensor memory, shared memory and registers as in the prefill kernel:
@@ -68,18 +68,19 @@ struct TrCfg {
   static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
   static constexpr int OFF_BAR = OFF_V + NST * TILE_BYTES;
   static constexpr int OFF_WALK = OFF_BAR + 512;             // a Walk per warp
-  static constexpr int OFF_ENT = OFF_WALK + 12 * 64;         // int4 [kStaged]: the live requests
-  static constexpr int SMEM_BYTES = OFF_ENT + kStaged * 16 + 1024;  // + alignment slack
+  static constexpr int OFF_ENT = OFF_WALK + 12 * 64;         // int4 [kMost]: the live requests
+  static constexpr int OFF_OUT = OFF_ENT + kMost * 16;     // 32 rows of 64 bytes for each softmax warp
+  static constexpr int SMEM_BYTES = OFF_OUT + 8 * 2048 + 1024;  // + alignment slack
   // mbarriers, [t] per slot: Q_t loaded / read by its last product; K and V stages
-  // loaded / read; S_t ready; P_t halves stored (4 warps each); P.V of the first
-  // half / of all keys done
+  // loaded / read; S_t ready / read (4 warps); P_t halves stored (4 warps each); P.V
+  // of the first half / of all keys done
   static constexpr int B_QF = 0, B_QE = 2, B_KF = 4, B_VF = B_KF + NST, B_KE = B_VF + NST, B_VE = B_KE + NST,
-                       B_S = B_VE + NST, B_P0 = B_S + 2, B_P1 = B_P0 + 2, B_O0 = B_P1 + 2, B_O1 = B_O0 + 2,
+                       B_S = B_VE + NST, B_SC = B_S + 2, B_P0 = B_SC + 2, B_P1 = B_P0 + 2, B_O0 = B_P1 + 2, B_O1 = B_O0 + 2,
                        B_DRAIN = B_O1 + 2, B_STALL = B_DRAIN + 1, N_BARS = B_STALL + 1;
   static constexpr int OFF_TSLOT = 8 * N_BARS, OFF_ABORT = OFF_TSLOT + 4, OFF_ISSUED = OFF_TSLOT + 8,
-                       OFF_SUMS = OFF_TSLOT + 40;
+                       OFF_START = (OFF_TSLOT + 32 + 15) / 16 * 16, OFF_SUMS = OFF_START + 32;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
-  static_assert(OFF_SUMS % 8 == 0 && OFF_SUMS + 12 * 12 <= 512, "barrier area");
+  static_assert(OFF_SUMS + 12 * 8 <= 512, "barrier area");
   static_assert(128 * REG_CTRL + 256 * REG_SOFTMAX <= NTHR * 168, "register split exceeds the launch allocation");
 };
 
@@ -96,8 +97,10 @@ struct TreeParams {
   float qk_scale_log2;
   __nv_bfloat16* o;
   int4* record;  // [n_workers]: the cut unit that begins in the worker's range (request, unit, its partials or 0)
-  float2* ml;    // [n_workers][2][rows of a unit]; [..][1] of the unit that begins there, [..][0] of one that goes on
-  float* part_o;
+  // partials of a row tile, slots [n_workers][2][row tiles of a unit]: [..][1] of the
+  // unit that begins in the range, [..][0] of one that goes on there
+  float2* ml;     // [slot][128]
+  float* part_o;  // [slot][D / 4][128][4]
   uint32_t* status;
   uint64_t wait_limit_ns, test_stall_ns;
 };
@@ -118,43 +121,36 @@ __device__ __forceinline__ int tiles_of(int L) { return (L + BN - 1) / BN; }
 // A warp's way through its worker's range, a segment (tiles [lo, hi) of unit u of
 // request b) at a time.  In shared memory: kept in registers through the softmax
 // loop, which needs nearly all, it would be spilled there.
-struct Walk {
-  unsigned long long left;  // positions of the range not yet taken
-  int k, next_u, at;        // next: entry of the request, its unit, position in the unit
-  int b, L, ql, t0;         // of the segment
+struct alignas(16) Walk {
+  unsigned left;      // positions of the range not yet taken
+  int k, next_u, at;  // next: entry of the request, its unit, position in the unit
+  int b, L, ql, t0;   // of the segment
   int lo, hi, u;
 };
 static_assert(sizeof(Walk) <= 64, "walk area");
 
-// The live requests: staged ones by number among themselves, others by request.
+// The live requests, in order.
 struct List {
-  const int4* staged;  // or null
+  const int4* ent;
   int n;
 };
-__device__ __forceinline__ int4 entry(const TreeParams& p, const List& list, int& k) {
-  if (list.staged != nullptr) return list.staged[k];
-  uint32_t bits = 0;
-  for (;; ++k) {
-    const int4 e = request(p, k, bits);
-    if (e.z > 0 || k + 1 >= p.B) return e;
-  }
-}
 
 // The next segment; false at the range's end.  Called by a whole warp.
 __device__ __forceinline__ bool next_segment(Walk* w, const TreeParams& p, const List& list) {
-  unsigned long long left = w->left;
+  unsigned left = w->left;
   int k = w->k, u = w->next_u, at = w->at;
   bool found = false;
   int4 e = make_int4(0, 0, 0, 0);
   int lo = 0, hi = 0, seg_u = 0;
+#pragma unroll 1
   while (left > 0 && !found) {
-    if (k >= list.n) {  // (lengths that changed under the call)
+    if (k >= list.n) {  // (not while the list is what it was cut from)
       left = 0;
       break;
     }
-    e = entry(p, list, k);
+    e = list.ent[k];
     const int span = tiles_of(e.y) + kLead;
-    const int take = int(min(left, (unsigned long long)(span - at)));
+    const int take = int(min(left, unsigned(span - at)));
     lo = max(at - kLead, 0);
     hi = max(at + take - kLead, 0);
     seg_u = u;
@@ -183,10 +179,35 @@ __device__ __forceinline__ bool next_segment(Walk* w, const TreeParams& p, const
   return found;
 }
 
-// A wait that a CTA which has given up passes at once.
+// The list cut into n ranges of `size` positions, the first `longer` of them one longer.
+struct Cut {
+  unsigned n, size, longer;
+  __device__ static Cut of(unsigned total, unsigned workers) {
+    Cut c;
+    c.n = min(workers, max(total / kMinWork, 1u));
+    c.size = total / c.n;
+    c.longer = total - c.size * c.n;
+    return c;
+  }
+  __device__ unsigned start(unsigned w) const { return w * size + min(w, longer); }
+  __device__ unsigned holder(unsigned x) const {  // the range with position x
+    const unsigned head = longer * (size + 1);
+    return x < head ? x / (size + 1) : longer + (x - head) / size;
+  }
+};
+
+// A bounded wait shared by the whole CTA: once one thread gives up, the others
+// stop waiting too.  (In few instructions: there are twenty of these, and what the
+// roles run beside one another has to stay in the instruction cache, or the misses,
+// behind the stream of K and V, cost a microsecond each.)
 __device__ __forceinline__ void tile_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
-  if (mbar_test_wait(bar, parity) || *abort_flag) return;
-  cta_wait(bar, parity, abort_flag, limit_ns);
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  do {
+    if (*abort_flag) return;
+    if (global_timer_ns() - t0 > limit_ns) *abort_flag = 1;
+  } while (!mbar_try_wait(bar, parity));
 }
 
 template <int HD, bool PAIR>
@@ -198,7 +219,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   constexpr int NSTR = PAIR ? C::NST : C::NST / 2;  // stages of a ring
   constexpr int OFF_Q = C::OFF_Q, OFF_K = C::OFF_K, OFF_V = C::OFF_V, OFF_BAR = C::OFF_BAR;
   constexpr int B_QF = C::B_QF, B_QE = C::B_QE, B_KF = C::B_KF, B_VF = C::B_VF, B_KE = C::B_KE, B_VE = C::B_VE,
-                B_S = C::B_S, B_P0 = C::B_P0, B_P1 = C::B_P1, B_O0 = C::B_O0, B_O1 = C::B_O1, B_DRAIN = C::B_DRAIN;
+                B_S = C::B_S, B_SC = C::B_SC, B_P0 = C::B_P0, B_P1 = C::B_P1, B_O0 = C::B_O0, B_O1 = C::B_O1, B_DRAIN = C::B_DRAIN;
   constexpr uint32_t TM_S = C::TM_S, TM_O = C::TM_O, TM_P = C::TM_P;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -218,8 +239,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     tmem_relinquish();
   }
   if (tid == 256) {
+#pragma unroll 1
     for (int i = 0; i < C::N_BARS; ++i) {
-      const bool per_warp = i >= B_P0 && i < B_O0;
+      const bool per_warp = i >= B_SC && i < B_O0;
       const bool stage_read = i >= B_KE && i < B_S;  // by the products of each slot on the ring
       mbar_init(&bars[i], per_warp ? 4 : i == B_DRAIN ? 2 : stage_read && PAIR ? 2 : 1);
     }
@@ -230,33 +252,33 @@ __global__ void __launch_bounds__(NTHR, 1)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  if (tid < 12) walks[tid].left = 0;
+  int4* const start_s = reinterpret_cast<int4*>(smem + OFF_BAR + C::OFF_START);  // [2]: how the workers' walks begin
+  if (tid < 2) start_s[tid] = make_int4(0, 0, 0, 0);
   grid_dependency_wait();
 
   // ---- the list of tiles, and the ranges of this CTA's workers ----
-  const bool staged = p.B <= kStaged;
-  unsigned long long total;
-  int n_cut;  // ranges that the list is cut into
-  List list{staged ? ent : nullptr, p.B};
+  List list{ent, 0};
+  Cut cut;
   {
-    unsigned long long* sum_s = reinterpret_cast<unsigned long long*>(smem + OFF_BAR + C::OFF_SUMS);  // [12]
-    int* live_s = reinterpret_cast<int*>(sum_s + 12);                                                  // [12]
+    unsigned* sum_s = reinterpret_cast<unsigned*>(smem + OFF_BAR + C::OFF_SUMS);  // [12]
+    int* live_s = reinterpret_cast<int*>(sum_s + 12);                             // [12]
     const int per = (p.B + NTHR - 1) / NTHR, first = tid * per, last = min(first + per, p.B);
     uint32_t bits = 0;
     int4 e0 = make_int4(0, 0, 0, 0);
-    unsigned long long mine = 0;
+    unsigned mine = 0;
     int live = 0;
+#pragma unroll 1
     for (int b = first; b < last; ++b) {
       const int4 e = request(p, b, bits);
       if (b == first) e0 = e;
-      if (e.z > 0) mine += (unsigned long long)(p.units) * (tiles_of(e.y) + kLead), ++live;
+      if (e.z > 0) mine += unsigned(p.units) * unsigned(tiles_of(e.y) + kLead), ++live;
     }
     if (cta == 0 && bits != 0) atomicOr(p.status, bits);
-    unsigned long long sum = mine;
+    unsigned sum = mine;
     int lsum = live;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const unsigned long long a = __shfl_up_sync(0xffffffffu, sum, d);
+      const unsigned a = __shfl_up_sync(0xffffffffu, sum, d);
       const int c = __shfl_up_sync(0xffffffffu, lsum, d);
       if (lane >= d) sum += a, lsum += c;
     }
@@ -264,37 +286,33 @@ __global__ void __launch_bounds__(NTHR, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    total = 0;
+    unsigned total = 0;
     int n_live = 0;
+#pragma unroll
     for (int w = 0; w < 12; ++w) {
       if (w < warp) sum += sum_s[w], lsum += live_s[w];
       total += sum_s[w];
       n_live += live_s[w];
     }
-    if (staged) list.n = n_live;
-    n_cut = int(min((unsigned long long)(p.n_workers), max(total / kMinWork, 1ull)));
-    unsigned long long base = sum - mine;
+    list.n = n_live;
+    cut = Cut::of(total, p.n_workers);
+    unsigned base = sum - mine;
     int at = lsum - live;
+#pragma unroll 1
     for (int b = first; b < last; ++b) {
       uint32_t again = 0;
       const int4 e = b == first ? e0 : request(p, b, again);
       if (e.z == 0) continue;
-      if (staged) ent[at] = e;
+      ent[at] = e;
       const int span = tiles_of(e.y) + kLead;
-      const unsigned long long cost = (unsigned long long)(p.units) * span;
+      const unsigned cost = unsigned(p.units) * unsigned(span);
 #pragma unroll
       for (int t = 0; t < (PAIR ? 1 : 2); ++t) {
-        const int w = t * p.n_ctas + cta;
-        const unsigned long long s = total * w / n_cut, end = total * (w + 1) / n_cut;
-        if (w < n_cut && s >= base && s < base + cost) {
-          const unsigned long long off = s - base;
-          Walk x;
-          x.left = end - s;
-          x.k = staged ? at : b;
-          x.next_u = int(off / span);
-          x.at = int(off % span);
-          for (int i = 0; i < 12; ++i)  // softmax of slot i / 4; copies 8, 9 and products 10, 11 of slots 0, 1
-            if (PAIR || (i < 8 ? i >> 2 : i & 1) == t) walks[i] = x;
+        const unsigned w = t * p.n_ctas + cta, s = cut.start(w);
+        if (w < cut.n && s >= base && s < base + cost) {
+          const unsigned off = s - base;
+          start_s[t] = make_int4(int(cut.start(w + 1) - s), at, int(off / unsigned(span)),
+                                 int(off % unsigned(span)));
         }
       }
       base += cost;
@@ -304,6 +322,9 @@ __global__ void __launch_bounds__(NTHR, 1)
   }
   const uint32_t tmem = *tslot;
   Walk* const walk = &walks[warp];
+  if (lane == 0)  // softmax of slot warp / 4; copies 8, 9 and products 10, 11 of slots 0, 1
+    *reinterpret_cast<int4*>(walk) = start_s[PAIR ? 0 : warp < 8 ? warp >> 2 : warp & 1];
+  __syncwarp();
 
   if (warp >= 8) {
     set_max_regs_dec<C::REG_CTRL>();
@@ -313,70 +334,73 @@ __global__ void __launch_bounds__(NTHR, 1)
       // ---------------- copies ----------------
       int n = 0, n_seg = 0;
       if (p.test_stall_ns != 0 && lane == 0) stall_test(&bars[C::B_STALL], p.test_stall_ns, abort_flag);
-      const uint64_t once = l2_policy_evict_first();
+      // (rows that other units of the request read too stay in L2)
+      const uint64_t policy = p.np == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+#pragma unroll 1
       while (next_segment(walk, p, list)) {
         const int L = walk->L, b = walk->b, g = walk->u / p.np, part = walk->u % p.np, lo = walk->lo, hi = walk->hi;
         if (lane == 0 && !*abort_flag) {
           const int32_t* const table = p.block_table + (p.block_table != nullptr ? size_t(b) * p.max_blocks : 0);
-          // 64 rows from r0 on: their row in the map, and head
-          auto locate = [&](int r0, int& head) -> int {
-            head = b * p.Hkv + g;
-            if (p.block_table == nullptr || r0 >= L) return r0;
-            int blk = table[r0 / p.block_size];
-            if (blk < 0 || blk >= p.num_blocks) {
-              atomicOr(p.status, GQA_DEV_BAD_BLOCK);
-              blk = 0;
-            }
-            head = blk * p.Hkv + g;
-            return r0 % p.block_size;
-          };
-          int head0, head1, row0 = locate(lo * BN, head0), row1 = locate(lo * BN + 64, head1);
+          // The 64 rows copied next: the block they are in and their place in it, or
+          // their row in a dense cache
+          int blk = 0, in = lo * BN;
+          if (p.block_table != nullptr) blk = in / p.block_size, in -= blk * p.block_size;
+          int row[2] = {0, 0}, head[2] = {0, 0};  // of the tile's halves in the map
 #pragma unroll 1
-          for (int j = lo; j < hi; ++j, ++n) {
-            const int st = ring + n % NSTR;
-            const bool both = j * BN + 64 < L;  // is there a key in the tile's second half?
-            auto copy = [&](int off, const CUtensorMap* map, uint64_t* bar) {
-              mbar_arrive_expect_tx(bar, both ? TILE_BYTES : TILE_BYTES / 2);
-              unsigned char* dst = smem + off + st * TILE_BYTES;
+          for (int j = lo - 1; j < hi; ++j) {
+            // (a tile's blocks are looked up before the wait for its stages)
+            const int j_cur = j, row0 = row[0], row1 = row[1], head0 = head[0], head1 = head[1];
 #pragma unroll
-              for (int bx = 0; bx < NBOX; ++bx) {
-                if (p.np == 1) {  // read by this worker alone
-                  tma_load_3d(dst + bx * BOX_BYTES, map, bx * 64, row0, head0, bar, once);
-                  if (both) tma_load_3d(dst + bx * BOX_BYTES + 8192, map, bx * 64, row1, head1, bar, once);
-                } else {
-                  tma_load_3d(dst + bx * BOX_BYTES, map, bx * 64, row0, head0, bar);
-                  if (both) tma_load_3d(dst + bx * BOX_BYTES + 8192, map, bx * 64, row1, head1, bar);
+            for (int s = 0; s < 2; ++s) {
+              row[s] = in;
+              head[s] = b;
+              if (p.block_table != nullptr && (j + 1) * BN + s * 64 < L) {
+                head[s] = table[blk];
+                if (head[s] < 0 || head[s] >= p.num_blocks) {
+                  atomicOr(p.status, GQA_DEV_BAD_BLOCK);
+                  head[s] = 0;
                 }
               }
-            };
+              head[s] = head[s] * p.Hkv + g;
+              in += 64;
+              if (p.block_table != nullptr && in == p.block_size) in = 0, ++blk;
+            }
+            if (j_cur < lo) continue;
+            const int st = ring + n % NSTR;
+            const bool both = j * BN + 64 < L;  // is there a key in the tile's second half?
             const uint32_t freed = uint32_t(n / NSTR - 1) & 1u;
-            if (n >= NSTR) tile_wait(&bars[B_KE + st], freed, abort_flag, p.wait_limit_ns);
-            if (*abort_flag) break;
-            copy(OFF_K, &tmK, &bars[B_KF + st]);
-            issued[3 * t] = n + 1;
-            if (j == lo) {
-              // the row tiles of the segment (rows past the last one arrive as zeros)
+#pragma unroll 1
+            for (int kind = 0; kind < 2; ++kind) {  // K, then V
+              if (kind == 1 && j == lo) {
+                // the row tiles of the segment (rows past the last one arrive as zeros)
+#pragma unroll 1
+                for (int s = PAIR ? 0 : t; s < (PAIR ? 2 : t + 1); ++s) {
+                  if (n_seg > 0) tile_wait(&bars[B_QE + s], uint32_t(n_seg - 1) & 1u, abort_flag, p.wait_limit_ns);
+                  if (*abort_flag) break;
+                  mbar_arrive_expect_tx(&bars[B_QF + s], TILE_BYTES);
 #pragma unroll
-              for (int s = PAIR ? 0 : t; s < (PAIR ? 2 : t + 1); ++s) {
-                if (n_seg > 0) tile_wait(&bars[B_QE + s], uint32_t(n_seg - 1) & 1u, abort_flag, p.wait_limit_ns);
-                if (*abort_flag) break;
-                mbar_arrive_expect_tx(&bars[B_QF + s], TILE_BYTES);
-#pragma unroll
-                for (int bx = 0; bx < NBOX; ++bx)
-                  tma_load_3d(smem + OFF_Q + s * TILE_BYTES + bx * BOX_BYTES, &tmQ, bx * 64,
-                              (PAIR ? 2 * part + s : part) * BM, b * p.Hkv + g, &bars[B_QF + s]);
-                issued[3 * s + 2] = n_seg + 1;
+                  for (int bx = 0; bx < NBOX; ++bx)
+                    tma_load_3d(smem + OFF_Q + s * TILE_BYTES + bx * BOX_BYTES, &tmQ, bx * 64,
+                                (PAIR ? 2 * part + s : part) * BM, b * p.Hkv + g, &bars[B_QF + s]);
+                  issued[3 * s + 2] = n_seg + 1;
+                }
+                ++n_seg;
               }
-              ++n_seg;
+              if (n >= NSTR) tile_wait(&bars[(kind ? B_VE : B_KE) + st], freed, abort_flag, p.wait_limit_ns);
+              if (*abort_flag) break;
+              uint64_t* const bar = &bars[(kind ? B_VF : B_KF) + st];
+              const CUtensorMap* const map = kind ? &tmV : &tmK;
+              unsigned char* const dst = smem + (kind ? OFF_V : OFF_K) + st * TILE_BYTES;
+              mbar_arrive_expect_tx(bar, both ? TILE_BYTES : TILE_BYTES / 2);
+#pragma unroll
+              for (int bx = 0; bx < NBOX; ++bx) {
+                tma_load_3d(dst + bx * BOX_BYTES, map, bx * 64, row0, head0, bar, policy);
+                if (both) tma_load_3d(dst + bx * BOX_BYTES + 8192, map, bx * 64, row1, head1, bar, policy);
+              }
+              issued[3 * t + kind] = n + 1;
             }
-            if (n >= NSTR) tile_wait(&bars[B_VE + st], freed, abort_flag, p.wait_limit_ns);
             if (*abort_flag) break;
-            copy(OFF_V, &tmV, &bars[B_VF + st]);
-            issued[3 * t + 1] = n + 1;
-            if (j + 1 < hi) {
-              row0 = locate((j + 1) * BN, head0);
-              row1 = locate((j + 1) * BN + 64, head1);
-            }
+            ++n;
           }
         }
         __syncwarp();
@@ -388,21 +412,53 @@ __global__ void __launch_bounds__(NTHR, 1)
       constexpr uint64_t TILE_STEP = TILE_BYTES >> 4, K_KSTEP = 32 >> 4, V_KSTEP = 2048 >> 4, BOX_STEP = BOX_BYTES >> 4;
       const uint32_t dS = tmem + TM_S + t * 128, dO = tmem + TM_O + t * HD, aP = tmem + TM_P + t * C::P_STRIDE;
       int n = 0, n_seg = 0;
+      // O += P V of iteration m: stage st, first tile of the segment or not, rows of V from `rows` on cleared
+      auto pv = [&](int m, bool first, int rows) {
+        const int st = ring + m % NSTR;
+        tile_wait(&bars[B_VF + st], uint32_t(m / NSTR) & 1u, abort_flag, p.wait_limit_ns);
+        if (rows < BN) {  // rows past the keys hold anything (their P is 0, but 0 * NaN is NaN)
+          unsigned char* vt = smem + OFF_V + st * TILE_BYTES;
+          constexpr int LANES = PAIR ? 64 : 32;
+#pragma unroll
+          for (int bx = 0; bx < NBOX; ++bx)  // (whole 128-byte rows: the swizzle stays inside a row)
+#pragma unroll 1
+            for (int at = rows * 128 + ((PAIR ? t * 32 : 0) + lane) * 16; at < BOX_BYTES; at += LANES * 16)
+              *reinterpret_cast<uint4*>(vt + bx * BOX_BYTES + at) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          if (PAIR) named_bar_sync(1, 64);  // both slots' warps are done clearing
+          else __syncwarp();
+        }
+        const uint64_t vd = vdesc + st * TILE_STEP;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          tile_wait(&bars[(half ? B_P1 : B_P0) + t], uint32_t(m) & 1u, abort_flag, p.wait_limit_ns);
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int bx = 0; bx < NBOX; ++bx)
+              mma_bf16_ts_warp(dO + bx * 64, aP + half * 32 + kk * 8, vd + bx * BOX_STEP + (half * 4 + kk) * V_KSTEP,
+                               IDESC_O, (!first || half > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_warp(&bars[(half ? B_O1 : B_O0) + t]);
+        }
+        mma_commit_warp(&bars[B_VE + st]);
+      };
+#pragma unroll 1
       while (next_segment(walk, p, list)) {
         const int L = walk->L, lo = walk->lo, hi = walk->hi;
         tile_wait(&bars[B_QF + t], uint32_t(n_seg) & 1u, abort_flag, p.wait_limit_ns);
         ++n_seg;
-        // rows past L hold anything (their P is 0, but 0 * NaN is NaN): cleared
-        const int j_zero = L % BN != 0 ? L / BN : -1;
+#pragma unroll 1
         for (int j = lo; j < hi; ++j, ++n) {
           const int st = ring + n % NSTR;
-          const uint32_t full = uint32_t(n / NSTR) & 1u;
-          tile_wait(&bars[B_KF + st], full, abort_flag, p.wait_limit_ns);
-          // (S was read before the P that the last P V waited for; P, which may lie over it, by that product)
-          if (C::P_ALIAS && n > 0) tile_wait(&bars[B_O1 + t], uint32_t(n - 1) & 1u, abort_flag, p.wait_limit_ns);
+          tile_wait(&bars[B_KF + st], uint32_t(n / NSTR) & 1u, abort_flag, p.wait_limit_ns);
+          if (n > 0) {  // S has been read, or (where P lies over it) P
+            if (C::P_ALIAS) tile_wait(&bars[B_O1 + t], uint32_t(n - 1) & 1u, abort_flag, p.wait_limit_ns);
+            else tile_wait(&bars[B_SC + t], uint32_t(n - 1) & 1u, abort_flag, p.wait_limit_ns);
+          }
           tc_fence_after();
-          const uint64_t kd = kdesc + st * TILE_STEP, vd = vdesc + st * TILE_STEP;
-#pragma unroll
+          const uint64_t kd = kdesc + st * TILE_STEP;
+#pragma unroll 4
           for (int kk = 0; kk < HD / 16; ++kk) {
             const uint64_t koff = (kk / 4) * BOX_STEP + (kk % 4) * K_KSTEP;
             mma_bf16_warp(dS, qdesc + koff, kd + koff, IDESC_S, kk > 0 ? 1u : 0u);
@@ -410,31 +466,10 @@ __global__ void __launch_bounds__(NTHR, 1)
           mma_commit_warp(&bars[B_S + t]);
           mma_commit_warp(&bars[B_KE + st]);
           if (j + 1 == hi) mma_commit_warp(&bars[B_QE + t]);
-          tile_wait(&bars[B_VF + st], full, abort_flag, p.wait_limit_ns);
-          if (j == j_zero) {
-            unsigned char* vt = smem + OFF_V + st * TILE_BYTES;
-            constexpr int LANES = PAIR ? 64 : 32;
-#pragma unroll
-            for (int bx = 0; bx < NBOX; ++bx)  // (whole 128-byte rows: the swizzle stays inside a row)
-              for (int at = (L % BN) * 128 + ((PAIR ? t * 32 : 0) + lane) * 16; at < BOX_BYTES; at += LANES * 16)
-                *reinterpret_cast<uint4*>(vt + bx * BOX_BYTES + at) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            if (PAIR) named_bar_sync(1, 64);  // both slots' warps are done clearing
-            else __syncwarp();
-          }
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            tile_wait(&bars[(half ? B_P1 : B_P0) + t], uint32_t(n) & 1u, abort_flag, p.wait_limit_ns);
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-              for (int bx = 0; bx < NBOX; ++bx)
-                mma_bf16_ts_warp(dO + bx * 64, aP + half * 32 + kk * 8, vd + bx * BOX_STEP + (half * 4 + kk) * V_KSTEP,
-                                 IDESC_O, (j > lo || half > 0 || kk > 0) ? 1u : 0u);
-            mma_commit_warp(&bars[(half ? B_O1 : B_O0) + t]);
-          }
-          mma_commit_warp(&bars[B_VE + st]);
+          // with P apart from S the next scores run under this tile's softmax
+#pragma unroll 1
+          for (int m = C::P_ALIAS || j == lo ? n : n - 1; m < (C::P_ALIAS || j + 1 == hi ? n + 1 : n); ++m)
+            pv(m, m - n + j == lo, L - (m - n + j) * BN);
         }
       }
     }
@@ -448,13 +483,21 @@ __global__ void __launch_bounds__(NTHR, 1)
     const uint32_t tP = tmem + TM_P + t * C::P_STRIDE + lane_off;
     const float c = p.qk_scale_log2;
     int n = 0;
+#pragma unroll 1
     while (next_segment(walk, p, list)) {
       const int n_it = walk->hi - walk->lo;
       const int masked_from = walk->t0 / BN - walk->lo;  // tiles with drafted rows, or past the keys
       // (rows past the last one are nobody's: a warp that has only such leaves P as it is)
+      // The masks' words are asked for before the scores are there.
+      if (p.mask != nullptr && masked_from < n_it) {
+        const int i = ((PAIR ? 2 * (walk->u % p.np) + t : walk->u % p.np) * BM + (tid & (BM - 1))) % p.Tq;
+        const int32_t* const words = p.mask + (size_t(walk->b) * p.Tq + i) * p.W;
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(words));
+      }
       const bool warp_live = ((PAIR ? 2 * (walk->u % p.np) + t : walk->u % p.np) * 4 + (warp & 3)) * 32 < p.n_rep * p.Tq;
       float m_ref = -INFINITY, lsum = 0.f;
       if (PAIR && t == 1) named_bar_arrive(BAR_TURN_A, 256);  // (slot 0 begins)
+#pragma unroll 1
       for (int j = 0; j < n_it; ++j, ++n) {
         tile_wait(&bars[B_S + t], uint32_t(n) & 1u, abort_flag, p.wait_limit_ns);
         tc_fence_after();
@@ -463,6 +506,12 @@ __global__ void __launch_bounds__(NTHR, 1)
           if (PAIR && (t == 0 || j + 1 < n_it)) named_bar_arrive(t == 0 ? BAR_TURN_B : BAR_TURN_A, 256);
           tc_fence_before();
           __syncwarp();
+          if (!C::P_ALIAS) {
+            if (lane == 0) mbar_arrive(&bars[B_SC + t]);
+            // (S runs ahead of P V: not before the other warps have arrived for the last P)
+            if (n > 0) tile_wait(&bars[B_O1 + t], uint32_t(n - 1) & 1u, abort_flag, p.wait_limit_ns);
+            __syncwarp();
+          }
           if (lane == 0) {
             mbar_arrive(&bars[B_P0 + t]);
             mbar_arrive(&bars[B_P1 + t]);
@@ -476,6 +525,11 @@ __global__ void __launch_bounds__(NTHR, 1)
         tmem_ld32_max(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(s + 64), rmx[2]);
         tmem_ld32_max(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(s + 96), rmx[3]);
         tmem_wait_ld();
+        if (!C::P_ALIAS) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_SC + t]);
+        }
         if (j >= masked_from) {
           const int L = walk->L, t0 = walk->t0, part = walk->u % p.np;
           const int i = ((PAIR ? 2 * part + t : part) * BM + (tid & (BM - 1))) % p.Tq;
@@ -513,7 +567,7 @@ __global__ void __launch_bounds__(NTHR, 1)
             tc_fence_after();
             const float alpha = resc ? fast_exp2(m_ref - tmax) : 1.f;
             if (resc) m_ref = tmax;
-#pragma unroll
+#pragma unroll 1
             for (int cc = 0; cc < HD / 32; ++cc) {
               uint32_t o[32];
               tmem_ld32(tO + cc * 32, o);
@@ -567,30 +621,44 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (whole) {
           const float inv = lsum > 0.f ? 1.f / lsum : lsum == 0.f ? 0.f : lsum;  // (a NaN stays one)
           if (live && lsum == 0.f) atomicOr(p.status, GQA_DEV_EMPTY_REQUEST);
-          uint4* const dst = reinterpret_cast<uint4*>(
-              p.o + ((size_t(walk->b) * p.Hq + g * p.n_rep + h) * p.Tq + i) * HD);
-#pragma unroll
+          const long dst = live ? ((long(walk->b) * p.Hq + g * p.n_rep + h) * p.Tq + i) * HD : -1L;
+          // 32 columns at a time through the warp's staging area, 16-byte chunks XOR-ed
+          // with the row, so that a store covers 64 bytes of a row, not 16
+          unsigned char* const stage = smem + C::OFF_OUT + warp * 2048;
+#pragma unroll 1
           for (int cc = 0; cc < HD / 32; ++cc) {
             uint32_t o[32];
             tmem_ld32(tO + cc * 32, o);
             tmem_wait_ld();
-            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const __nv_bfloat162 pk =
-                  __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-              w[e] = *reinterpret_cast<const uint32_t*>(&pk);
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                const __nv_bfloat162 pk = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * f]) * inv,
+                                                                __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
+                w[f] = *reinterpret_cast<const uint32_t*>(&pk);
+              }
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (live)
+            __syncwarp();
 #pragma unroll
-              for (int e = 0; e < 4; ++e) dst[cc * 4 + e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            for (int it = 0; it < 4; ++it) {
+              const int x = it * 8 + lane / 4, e = lane % 4;
+              const long d = __shfl_sync(0xffffffffu, dst, x);
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + x * 64 + ((e ^ ((x >> 1) & 3)) << 4));
+              if (d >= 0) *reinterpret_cast<uint4*>(p.o + d + cc * 32 + e * 8) = v;
+            }
+            __syncwarp();
           }
         } else {
+          // [columns / 4][128 rows][4]: the lanes of a store are neighbours
           const int worker = PAIR ? cta : t * p.n_ctas + cta;
-          const size_t at = (size_t(worker) * 2 + (begins ? 1 : 0)) * (PAIR ? 2 * BM : BM) + (PAIR ? t * BM : 0) + r;
-          if (live) p.ml[at] = make_float2(m_ref, lsum);
-          float4* const dst = reinterpret_cast<float4*>(p.part_o + at * HD);
-#pragma unroll
+          const size_t slot = (size_t(worker) * 2 + (begins ? 1 : 0)) * (PAIR ? 2 : 1) + (PAIR ? t : 0);
+          if (live) p.ml[slot * BM + r] = make_float2(m_ref, lsum);
+          float4* const dst = reinterpret_cast<float4*>(p.part_o) + slot * (BM * HD / 4) + r;
+#pragma unroll 1
           for (int cc = 0; cc < HD / 32; ++cc) {
             uint32_t o[32];
             tmem_ld32(tO + cc * 32, o);
@@ -598,8 +666,8 @@ __global__ void __launch_bounds__(NTHR, 1)
             if (live)
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                dst[cc * 8 + e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                              __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                dst[(cc * 8 + e) * BM] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                     __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
           }
         }
       }
@@ -607,13 +675,11 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
     // the cut unit that begins in this range, if there is one, and its partials
     if ((warp & 3) == 0 && lane == 0 && !(PAIR && t == 1)) {
-      const int w = PAIR ? cta : t * p.n_ctas + cta;
+      const unsigned w = PAIR ? cta : t * p.n_ctas + cta;
       int4 rec = make_int4(0, 0, 0, 0);
-      if (w < n_cut && n > 0 && walk->lo == 0 && walk->hi > 0 && walk->hi < tiles_of(walk->L)) {
-        const unsigned long long end = total * (w + 1) / n_cut;
-        const unsigned long long tail = end + (tiles_of(walk->L) - walk->hi) - 1;  // the position of its last tile
-        rec = make_int4(walk->b, walk->u, int(((tail + 1) * n_cut - 1) / total) - w + 1, 0);
-      }
+      const int nt = tiles_of(walk->L);
+      if (n > 0 && walk->lo == 0 && walk->hi < nt)  // (the range ends in it)
+        rec = make_int4(walk->b, walk->u, int(cut.holder(cut.start(w + 1) + (nt - walk->hi) - 1) - w) + 1, 0);
       p.record[w] = rec;
     }
   }
@@ -644,13 +710,15 @@ __global__ void __launch_bounds__(NTHR, 1)
 
 // ---- merge -------------------------------------------------------------------
 
-// A block per worker and 8 rows of the cut unit that begins in its range, a warp a
-// row: M = max_s m_s, o = sum_s o_s 2^(m_s - M) / sum_s l_s 2^(m_s - M), in the
-// order of the partials.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
-  constexpr int V = D / 32;
-  const int w = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+// Joins the partials of the cut unit that begins in a worker's range,
+//   M = max_s m_s,   o = sum_s o_s 2^(m_s - M) / sum_s l_s 2^(m_s - M),
+// in their order.  A block has 32 rows, a lane each, and 64 columns, 16 a warp; a
+// load of a warp is 512 bytes in a row, and four partials are asked for at once.
+template <int D, int TILES>
+__global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
+  __shared__ uint4 out_s[32 * 8];  // 32 rows of 128 bytes
+  const int w = blockIdx.x, t = blockIdx.y >> 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = (blockIdx.y & 3) * 32 + lane, chunk = blockIdx.z * 16 + warp * 4;  // (of four columns)
   grid_dependency_wait();
   grid_launch_dependents();
   const int4 rec = __ldcg(&p.record[w]);
@@ -658,40 +726,73 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
   if (n == 0) return;
   uint32_t bits = 0;
   const int4 e = request(p, rec.x, bits);
-  const int row = rec.y % p.np * ROWS + r, g = rec.y / p.np, h = row / p.Tq, i = row % p.Tq;
-  if (h >= p.n_rep || i >= e.z) return;
-  auto at = [&](int s) { return (size_t(w + s) * 2 + (s == 0 ? 1 : 0)) * ROWS + r; };
-  const float2 none = make_float2(-INFINITY, 0.f);
-  const float2 first = lane < n ? __ldcg(&p.ml[at(lane)]) : none;
-  float M = first.x;
-  for (int s = lane + 32; s < n; s += 32) M = fmaxf(M, __ldcg(&p.ml[at(s)]).x);
+  const int row = (rec.y % p.np * TILES + t) * BM + r, g = rec.y / p.np, h = row / p.Tq, i = row % p.Tq;
+  const bool live = h < p.n_rep && i < e.z;
+  if (!__any_sync(0xffffffffu, live)) return;  // (the same rows in every warp)
+  float M = -INFINITY, den = 0.f, acc[4][4] = {};
+  constexpr int AHEAD = 4;
+  for (int s0 = 0; s0 < n; s0 += AHEAD) {
+    float2 ml[AHEAD];
+    float4 x[AHEAD][4];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  float den = 0.f, acc[V] = {};
-  for (int s0 = 0; s0 < n; s0 += 32) {
-    const float2 x = s0 == 0 ? first : s0 + lane < n ? __ldcg(&p.ml[at(s0 + lane)]) : none;
-    const float wt = x.x == -INFINITY ? 0.f : fast_exp2(x.x - M);
-    den += x.y * wt;
-    const int m = min(32, n - s0);
-#pragma unroll 4
-    for (int s = 0; s < m; ++s) {
-      const float ws = __shfl_sync(0xffffffffu, wt, s);
-      const float* const src = p.part_o + at(s0 + s) * D + lane * V;
-      float x4[V];
-      if constexpr (V == 4) *reinterpret_cast<float4*>(x4) = __ldcg(reinterpret_cast<const float4*>(src));
-      else *reinterpret_cast<float2*>(x4) = __ldcg(reinterpret_cast<const float2*>(src));
+    for (int k = 0; k < AHEAD; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (s0 + k < n && live) {
+        const size_t slot = (size_t(w + s0 + k) * 2 + (s0 + k == 0 ? 1 : 0)) * TILES + t;
+        ml[k] = __ldcg(&p.ml[slot * BM + r]);
+        const float4* const src = reinterpret_cast<const float4*>(p.part_o) + (slot * (D / 4) + chunk) * BM + r;
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = fmaf(x4[v], ws, acc[v]);
+        for (int c = 0; c < 4; ++c) x[k][c] = __ldcg(src + c * BM);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[k][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) m = fmaxf(m, ml[k].x);
+    const float a = M == -INFINITY ? 0.f : fast_exp2(M - m);
+    M = m;
+    den *= a;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[c][v] *= a;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const float wt = ml[k].x == -INFINITY ? 0.f : fast_exp2(ml[k].x - M);
+      den = fmaf(ml[k].y, wt, den);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[c][0] = fmaf(x[k][c].x, wt, acc[c][0]);
+        acc[c][1] = fmaf(x[k][c].y, wt, acc[c][1]);
+        acc[c][2] = fmaf(x[k][c].z, wt, acc[c][2]);
+        acc[c][3] = fmaf(x[k][c].w, wt, acc[c][3]);
+      }
     }
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
-  if (den == 0.f && lane == 0) atomicOr(p.status, GQA_DEV_EMPTY_REQUEST);
+  if (live && den == 0.f) atomicOr(p.status, GQA_DEV_EMPTY_REQUEST);
   const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;
-  __nv_bfloat16* const dst = p.o + ((size_t(rec.x) * p.Hq + g * p.n_rep + h) * p.Tq + i) * D + lane * V;
 #pragma unroll
-  for (int v = 0; v < V; v += 2)
-    *reinterpret_cast<__nv_bfloat162*>(dst + v) = __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
+  for (int c = 0; c < 4; c += 2) {
+    uint32_t u[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const __nv_bfloat162 pk =
+          __floats2bfloat162_rn(acc[c + f / 2][2 * (f % 2)] * inv, acc[c + f / 2][2 * (f % 2) + 1] * inv);
+      u[f] = *reinterpret_cast<const uint32_t*>(&pk);
+    }
+    out_s[lane * 8 + ((warp * 2 + c / 2) ^ (lane & 7))] = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  __syncthreads();
+  const long dst = live ? ((long(rec.x) * p.Hq + g * p.n_rep + h) * p.Tq + i) * D + blockIdx.z * 64 : -1L;
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {  // (a warp stores 8 of the rows, each of them whole)
+    const int x = warp * 8 + it * 4 + lane / 8, c = lane % 8;
+    const long d = __shfl_sync(0xffffffffu, dst, x);
+    const uint4 v = out_s[x * 8 + (c ^ (x & 7))];
+    if (d >= 0) *reinterpret_cast<uint4*>(p.o + d + c * 8) = v;
+  }
 }
 
 // ---- plan ----------------------------------------------------------------------
@@ -719,7 +820,8 @@ TreePlan tree_plan(int B, int Hq, int Hkv, int D, int Tq, int max_kv_len) {
 }
 
 template <int HD, bool PAIR>
-cudaError_t launch_tree_as(const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
+cudaError_t launch_tree_as(const TreeArgs& a, cudaStream_t stream) {
+  const TreePlan plan = tree_plan(a.B, a.Hq, a.Hkv, a.D, a.Tq, a.max_kv_len);
   using C = TrCfg<HD>;
   const int n_rep = a.Hq / a.Hkv;
   const bool paged = a.block_table != nullptr;
@@ -766,21 +868,42 @@ cudaError_t launch_tree_as(const TreeArgs& a, const TreePlan& plan, cudaStream_t
   e = launch_pdl(tree_kernel<HD, PAIR>, dim3(plan.n_ctas), dim3(NTHR), C::SMEM_BYTES, stream, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
   if (a.max_kv_len <= BN) return cudaSuccess;  // (no unit has a second tile: none is cut)
-  constexpr int ROWS = PAIR ? 2 * BM : BM;
-  const int live = std::min(ROWS, n_rep * a.Tq);
-  return launch_pdl(tree_merge_kernel<HD, ROWS>, dim3(plan.n_workers, (live + 7) / 8), dim3(256), 0, stream, p);
+  constexpr int TILES = PAIR ? 2 : 1;
+  const int live = std::min(TILES * BM, n_rep * a.Tq);
+  return launch_pdl(tree_merge_kernel<HD, TILES>, dim3(plan.n_workers, (live + 31) / 32, HD / 64), dim3(128), 0, stream,
+                    p);
 }
 
 }  // namespace
 
 size_t tree_workspace_size(int B, int Hq, int Hkv, int D, int Tq, int max_kv_len) {
-  return tree_plan(B, Hq, Hkv, D, Tq, max_kv_len).total;
+  return tree_plan(std::min(B, kMost), Hq, Hkv, D, Tq, max_kv_len).total;
 }
 
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
-  const TreePlan plan = tree_plan(a.B, a.Hq, a.Hkv, a.D, a.Tq, a.max_kv_len);
-  if (a.D == 64) return plan.pair ? launch_tree_as<64, true>(a, plan, stream) : launch_tree_as<64, false>(a, plan, stream);
-  return plan.pair ? launch_tree_as<128, true>(a, plan, stream) : launch_tree_as<128, false>(a, plan, stream);
+  // (a launch's list fits its shared memory; that many requests fill the GPU)
+  for (int b = 0; b < a.B; b += kMost) {
+    TreeArgs s = a;
+    const size_t rows = size_t(b) * a.Hq * a.Tq * a.D * 2, keys = size_t(b) * a.Hkv * a.S_cap * a.D * 2;
+    s.B = std::min(kMost, a.B - b);
+    s.q = static_cast<const unsigned char*>(a.q) + rows;
+    s.o = static_cast<unsigned char*>(a.o) + rows;
+    if (a.block_table == nullptr) {
+      s.k = static_cast<const unsigned char*>(a.k) + keys;
+      s.v = static_cast<const unsigned char*>(a.v) + keys;
+    } else {
+      s.block_table = a.block_table + size_t(b) * a.max_blocks;
+    }
+    if (a.mask != nullptr) s.mask = a.mask + size_t(b) * a.Tq * a.W;
+    if (a.q_lens != nullptr) s.q_lens = a.q_lens + b;
+    if (a.tree_lens != nullptr) s.tree_lens = a.tree_lens + b;
+    s.kv_lens = a.kv_lens + b;
+    const bool pair = long(a.Hq / a.Hkv) * a.Tq > BM;
+    const cudaError_t e = a.D == 64 ? (pair ? launch_tree_as<64, true>(s, stream) : launch_tree_as<64, false>(s, stream))
+                                    : (pair ? launch_tree_as<128, true>(s, stream) : launch_tree_as<128, false>(s, stream));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace gqa

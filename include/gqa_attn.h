@@ -391,7 +391,8 @@ GQA_ATTN_API int gqa_attn_rope_append(const void* q, const void* k, const void* 
  * query does not see, K may hold anything and V finite numbers (its weight is 0
  * there).  The queries of a request and KV head (Hq / Hkv * q_lens[b] rows) read
  * its keys together, up to 256 of them at once.
- * Tq at most 1024, mask_words 1 to 32; B * Hq * Tq < 2^31; dtype must be GQA_BF16
+ * Tq at most 1024, mask_words 1 to 32; B * Hq * Tq < 2^31, and B * Hkv *
+ * ceil(Hq / Hkv * Tq / 256) * (max_kv_len / 128 + 8) < 2^31; dtype must be GQA_BF16
  * (else GQA_ERR_UNSUPPORTED).  Workspace: gqa_attn_decode_tree_workspace_size, for both
  * entry points.  Other arguments and errors as for gqa_attn_decode(_paged).
  * ------------------------------------------------------------------------- */
