@@ -25,9 +25,21 @@
 //   !PAIR   a worker is a slot, with a ring of K and V stages of its own, and the two
 //           know nothing of each other: one's start and end run under the other's
 //           products.
-// Roles as in the prefill kernel: warps 0 to 3 and 4 to 7 the softmax of slots 0 and
-// 1, a row a thread; warps 8 and 9 the copies; warps 10 and 11 the products of slots
-// 0 and 1.  S, P and O are in tensor memory, Q, K and V in shared memory.
+// Roles: warps 0 to 3 and 4 to 7 the softmax of slots 0 and 1, a row a thread; with
+// PAIR warp 8 the copies, 9 S of both slots, 10 and 11 P V of slots 0 and 1; without,
+// 8 and 9 the copies and 10 and 11 both products of slots 0 and 1 (a wait or a product
+// costs its warp a hundred cycles or two: where the products are the bound, three warps
+// issue them, 4 x 61 queries over 16,385 keys 64.8 us with two, 62.0 with three).  S, P and O are in
+// tensor memory, Q, K and V in shared memory.
+//
+// What bounds it: up to 128 rows a unit the stream of K and V (32/8 x 128, 4 rows,
+// 32,768 keys: 6.2 TB/s; x 64: 6.7).  With two row tiles the exponentials and products of a
+// key tile take as long as its bytes: 1.63 us where 1.5 would be the copy's.  Key tiles of
+// 64 with two score buffers a slot, so that scores never wait for P V, were slower
+// (65.2, 124.2 us for 32 x 64 queries over up to 8,192 keys, against 62.0 and 120.3; D = 64
+// 51.5 against 44.1): a tile has some 500 cycles of waits and hand-overs
+// whatever its size.  Asking for tiles in L2 ahead of their copies was slower too (chains of
+// 128 x 5 over up to 2,048: 83.9 us without, 92.9 one tile ahead, 99.5 four).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -46,9 +58,12 @@
 namespace gqa {
 namespace {
 
-constexpr int kLead = 2;         // key tiles that the start and the end of a unit count as
 constexpr int kMost = 1024;      // requests of a launch (kept in shared memory)
-constexpr int kMinWork = 3;      // tiles (with kLead) a worker gets at least, where there are few
+// Key tiles that the start and the end of a unit count as, with PAIR and without
+// (4 x 61 queries over 16,385 keys: 1 63.2 us, 2 61.8, 4 60.7; chains of 128 x 5 over up
+// to 2,048: 1 83.5, 2 83.5, 4 86.5).
+template <bool PAIR>
+constexpr int kLead = PAIR ? 4 : 2;
 
 // Tensor memory, shared memory and registers as in the prefill kernel:
 //   HD = 64:  S_0 [0,128) S_1 [128,256) O_0 [256,320) O_1 [320,384) P_0 [384,448) P_1 [448,512)
@@ -68,7 +83,7 @@ struct TrCfg {
   static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
   static constexpr int OFF_BAR = OFF_V + NST * TILE_BYTES;
   static constexpr int OFF_WALK = OFF_BAR + 512;             // a Walk per warp
-  static constexpr int OFF_ENT = OFF_WALK + 12 * 64;         // int4 [kMost]: the live requests
+  static constexpr int OFF_ENT = OFF_WALK + 12 * 64;         // int4 [kMost]: the requests
   static constexpr int OFF_OUT = OFF_ENT + kMost * 16;     // 32 rows of 64 bytes for each softmax warp
   static constexpr int SMEM_BYTES = OFF_OUT + 8 * 2048 + 1024;  // + alignment slack
   // mbarriers, [t] per slot: Q_t loaded / read by its last product; K and V stages
@@ -78,9 +93,9 @@ struct TrCfg {
                        B_S = B_VE + NST, B_SC = B_S + 2, B_P0 = B_SC + 2, B_P1 = B_P0 + 2, B_O0 = B_P1 + 2, B_O1 = B_O0 + 2,
                        B_DRAIN = B_O1 + 2, B_STALL = B_DRAIN + 1, N_BARS = B_STALL + 1;
   static constexpr int OFF_TSLOT = 8 * N_BARS, OFF_ABORT = OFF_TSLOT + 4, OFF_ISSUED = OFF_TSLOT + 8,
-                       OFF_START = (OFF_TSLOT + 32 + 15) / 16 * 16, OFF_SUMS = OFF_START + 32;
+                       OFF_START = (OFF_TSLOT + 32 + 15) / 16 * 16, OFF_SUMS = OFF_START + 64;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
-  static_assert(OFF_SUMS + 12 * 8 <= 512, "barrier area");
+  static_assert(OFF_SUMS + 12 * 4 <= 512, "barrier area");
   static_assert(128 * REG_CTRL + 256 * REG_SOFTMAX <= NTHR * 168, "register split exceeds the launch allocation");
 };
 
@@ -92,7 +107,7 @@ struct TreeParams {
   const int32_t* block_table;  // or null: rows of a dense cache
   int B, Hq, Hkv, n_rep, Tq, W, max_kv_len;
   int block_size, max_blocks, num_blocks;
-  int np, units;  // units of a KV head, of a request
+  int np, units;  // units of a KV head (1 without PAIR), of a request
   int n_ctas, n_workers;
   float qk_scale_log2;
   __nv_bfloat16* o;
@@ -123,36 +138,37 @@ __device__ __forceinline__ int tiles_of(int L) { return (L + BN - 1) / BN; }
 // loop, which needs nearly all, it would be spilled there.
 struct alignas(16) Walk {
   unsigned left;      // positions of the range not yet taken
-  int k, next_u, at;  // next: entry of the request, its unit, position in the unit
+  int k, next_u, at;  // next: request, its unit, position in the unit
   int b, L, ql, t0;   // of the segment
   int lo, hi, u;
 };
 static_assert(sizeof(Walk) <= 64, "walk area");
 
-// The live requests, in order.
-struct List {
-  const int4* ent;
-  int n;
-};
+// The row tile or pair of them that a unit is, and its KV head.
+template <bool PAIR>
+__device__ __forceinline__ int part_of(int u, const TreeParams& p) { return PAIR ? u % p.np : 0; }
+template <bool PAIR>
+__device__ __forceinline__ int head_of(int u, const TreeParams& p) { return PAIR ? u / p.np : u; }
 
 // The next segment; false at the range's end.  Called by a whole warp.
-__device__ __forceinline__ bool next_segment(Walk* w, const TreeParams& p, const List& list) {
+template <int LEAD>
+__device__ __forceinline__ bool next_segment(Walk* w, const TreeParams& p, const int4* ent) {
   unsigned left = w->left;
   int k = w->k, u = w->next_u, at = w->at;
   bool found = false;
   int4 e = make_int4(0, 0, 0, 0);
   int lo = 0, hi = 0, seg_u = 0;
 #pragma unroll 1
-  while (left > 0 && !found) {
-    if (k >= list.n) {  // (not while the list is what it was cut from)
-      left = 0;
-      break;
+  while (left > 0 && k < p.B && !found) {
+    e = ent[k];
+    if (e.z == 0) {  // idle
+      ++k;
+      continue;
     }
-    e = list.ent[k];
-    const int span = tiles_of(e.y) + kLead;
+    const int span = tiles_of(e.y) + LEAD;
     const int take = int(min(left, unsigned(span - at)));
-    lo = max(at - kLead, 0);
-    hi = max(at + take - kLead, 0);
+    lo = max(at - LEAD, 0);
+    hi = max(at + take - LEAD, 0);
     seg_u = u;
     left -= take;
     at = 0;
@@ -184,12 +200,12 @@ struct Cut {
   unsigned n, size, longer;
   __device__ static Cut of(unsigned total, unsigned workers) {
     Cut c;
-    c.n = min(workers, max(total / kMinWork, 1u));
+    c.n = min(workers, max(total, 1u));
     c.size = total / c.n;
     c.longer = total - c.size * c.n;
     return c;
   }
-  __device__ unsigned start(unsigned w) const { return w * size + min(w, longer); }
+  __device__ unsigned start(unsigned w) const { return w >= n ? n * size + longer : w * size + min(w, longer); }
   __device__ unsigned holder(unsigned x) const {  // the range with position x
     const unsigned head = longer * (size + 1);
     return x < head ? x / (size + 1) : longer + (x - head) / size;
@@ -224,7 +240,10 @@ __global__ void __launch_bounds__(NTHR, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (Without PAIR the warp's number comes from a shuffle: the compiler then knows that
+  // the lanes agree, which saves code, 1 to 8 % of a call of short requests.  With it
+  // the score loop came out 3 % slower that way.)
+  const int tid = threadIdx.x, warp = PAIR ? tid >> 5 : __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int cta = blockIdx.x;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + OFF_BAR + C::OFF_TSLOT);
@@ -242,8 +261,8 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll 1
     for (int i = 0; i < C::N_BARS; ++i) {
       const bool per_warp = i >= B_SC && i < B_O0;
-      const bool stage_read = i >= B_KE && i < B_S;  // by the products of each slot on the ring
-      mbar_init(&bars[i], per_warp ? 4 : i == B_DRAIN ? 2 : stage_read && PAIR ? 2 : 1);
+      const bool by_slots = PAIR && i >= B_VE && i < B_S;  // V is read by the products of both slots
+      mbar_init(&bars[i], per_warp ? 4 : i == B_DRAIN ? (PAIR ? 3 : 2) : by_slots ? 2 : 1);
     }
     *abort_flag = 0;
     for (int i = 0; i < 6; ++i) issued[i] = 0;
@@ -252,78 +271,68 @@ __global__ void __launch_bounds__(NTHR, 1)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  int4* const start_s = reinterpret_cast<int4*>(smem + OFF_BAR + C::OFF_START);  // [2]: how the workers' walks begin
-  if (tid < 2) start_s[tid] = make_int4(0, 0, 0, 0);
+  // where the ranges of this CTA's workers begin and end: request, unit, place in the unit
+  int4* const border_s = reinterpret_cast<int4*>(smem + OFF_BAR + C::OFF_START);  // [2][2]
   grid_dependency_wait();
 
   // ---- the list of tiles, and the ranges of this CTA's workers ----
-  List list{ent, 0};
+  constexpr int LEAD = kLead<PAIR>;
   Cut cut;
   {
     unsigned* sum_s = reinterpret_cast<unsigned*>(smem + OFF_BAR + C::OFF_SUMS);  // [12]
-    int* live_s = reinterpret_cast<int*>(sum_s + 12);                             // [12]
     const int per = (p.B + NTHR - 1) / NTHR, first = tid * per, last = min(first + per, p.B);
     uint32_t bits = 0;
-    int4 e0 = make_int4(0, 0, 0, 0);
     unsigned mine = 0;
-    int live = 0;
 #pragma unroll 1
     for (int b = first; b < last; ++b) {
       const int4 e = request(p, b, bits);
-      if (b == first) e0 = e;
-      if (e.z > 0) mine += unsigned(p.units) * unsigned(tiles_of(e.y) + kLead), ++live;
+      ent[b] = e;
+      if (e.z > 0) mine += unsigned(p.units) * unsigned(tiles_of(e.y) + LEAD);
     }
     if (cta == 0 && bits != 0) atomicOr(p.status, bits);
     unsigned sum = mine;
-    int lsum = live;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const unsigned a = __shfl_up_sync(0xffffffffu, sum, d);
-      const int c = __shfl_up_sync(0xffffffffu, lsum, d);
-      if (lane >= d) sum += a, lsum += c;
+      if (lane >= d) sum += a;
     }
-    if (lane == 31) sum_s[warp] = sum, live_s[warp] = lsum;
+    if (lane == 31) sum_s[warp] = sum;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     unsigned total = 0;
-    int n_live = 0;
 #pragma unroll
     for (int w = 0; w < 12; ++w) {
-      if (w < warp) sum += sum_s[w], lsum += live_s[w];
-      total += sum_s[w];
-      n_live += live_s[w];
+      const unsigned x = sum_s[w];
+      if (w < warp) sum += x;
+      total += x;
     }
-    list.n = n_live;
     cut = Cut::of(total, p.n_workers);
     unsigned base = sum - mine;
-    int at = lsum - live;
 #pragma unroll 1
     for (int b = first; b < last; ++b) {
-      uint32_t again = 0;
-      const int4 e = b == first ? e0 : request(p, b, again);
+      const int4 e = ent[b];
       if (e.z == 0) continue;
-      ent[at] = e;
-      const int span = tiles_of(e.y) + kLead;
-      const unsigned cost = unsigned(p.units) * unsigned(span);
-#pragma unroll
-      for (int t = 0; t < (PAIR ? 1 : 2); ++t) {
-        const unsigned w = t * p.n_ctas + cta, s = cut.start(w);
-        if (w < cut.n && s >= base && s < base + cost) {
-          const unsigned off = s - base;
-          start_s[t] = make_int4(int(cut.start(w + 1) - s), at, int(off / unsigned(span)),
-                                 int(off % unsigned(span)));
-        }
+      const unsigned span = tiles_of(e.y) + LEAD, cost = unsigned(p.units) * span;
+#pragma unroll 1
+      for (int q = 0; q < (PAIR ? 2 : 4); ++q) {
+        const unsigned off = cut.start((q >> 1) * p.n_ctas + cta + (q & 1)) - base;
+        if (off < cost) border_s[q] = make_int4(b, off / span, off % span, 0);
       }
       base += cost;
-      ++at;
     }
     __syncthreads();
   }
   const uint32_t tmem = *tslot;
   Walk* const walk = &walks[warp];
-  if (lane == 0)  // softmax of slot warp / 4; copies 8, 9 and products 10, 11 of slots 0, 1
-    *reinterpret_cast<int4*>(walk) = start_s[PAIR ? 0 : warp < 8 ? warp >> 2 : warp & 1];
+  // the slot whose worker this warp serves (softmax of slot warp / 4; the others in pairs)
+  const int slot = PAIR ? 0 : warp < 8 ? warp >> 2 : warp & 1;
+  const unsigned worker = slot * p.n_ctas + cta;
+  if (lane == 0) {
+    const int4 s = border_s[2 * slot];
+    *reinterpret_cast<int4*>(walk) =
+        make_int4(worker < cut.n ? int(cut.start(worker + 1) - cut.start(worker)) : 0, s.x, s.y, s.z);
+  }
   __syncwarp();
 
   if (warp >= 8) {
@@ -337,8 +346,9 @@ __global__ void __launch_bounds__(NTHR, 1)
       // (rows that other units of the request read too stay in L2)
       const uint64_t policy = p.np == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
 #pragma unroll 1
-      while (next_segment(walk, p, list)) {
-        const int L = walk->L, b = walk->b, g = walk->u / p.np, part = walk->u % p.np, lo = walk->lo, hi = walk->hi;
+      while (next_segment<kLead<PAIR>>(walk, p, ent)) {
+        const int L = walk->L, b = walk->b, g = head_of<PAIR>(walk->u, p), part = part_of<PAIR>(walk->u, p), lo = walk->lo,
+                  hi = walk->hi;
         if (lane == 0 && !*abort_flag) {
           const int32_t* const table = p.block_table + (p.block_table != nullptr ? size_t(b) * p.max_blocks : 0);
           // The 64 rows copied next: the block they are in and their place in it, or
@@ -405,12 +415,13 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
         __syncwarp();
       }
-    } else if (warp >= 10) {
-      // ---------------- products of slot t: S = Q K^T, O += P V ----------------
-      const uint64_t qdesc = sdesc_sw128(smem_u32(smem + OFF_Q + t * TILE_BYTES));
+    } else {
+      // ---------------- products: S = Q K^T, O += P V ----------------
+      const uint64_t qdesc = sdesc_sw128(smem_u32(smem + OFF_Q));
       const uint64_t kdesc = sdesc_sw128(smem_u32(smem + OFF_K)), vdesc = sdesc_sw128(smem_u32(smem + OFF_V));
       constexpr uint64_t TILE_STEP = TILE_BYTES >> 4, K_KSTEP = 32 >> 4, V_KSTEP = 2048 >> 4, BOX_STEP = BOX_BYTES >> 4;
-      const uint32_t dS = tmem + TM_S + t * 128, dO = tmem + TM_O + t * HD, aP = tmem + TM_P + t * C::P_STRIDE;
+      const uint32_t dO = tmem + TM_O + t * HD, aP = tmem + TM_P + t * C::P_STRIDE;
+      const bool scores = !PAIR || warp == 9, adds = !PAIR || warp >= 10;  // what this warp issues
       int n = 0, n_seg = 0;
       // O += P V of iteration m: stage st, first tile of the segment or not, rows of V from `rows` on cleared
       auto pv = [&](int m, bool first, int rows) {
@@ -444,32 +455,42 @@ __global__ void __launch_bounds__(NTHR, 1)
         mma_commit_warp(&bars[B_VE + st]);
       };
 #pragma unroll 1
-      while (next_segment(walk, p, list)) {
+      while (next_segment<kLead<PAIR>>(walk, p, ent)) {
         const int L = walk->L, lo = walk->lo, hi = walk->hi;
-        tile_wait(&bars[B_QF + t], uint32_t(n_seg) & 1u, abort_flag, p.wait_limit_ns);
+#pragma unroll 1
+        for (int s = PAIR ? 0 : t; scores && s < (PAIR ? 2 : t + 1); ++s)
+          tile_wait(&bars[B_QF + s], uint32_t(n_seg) & 1u, abort_flag, p.wait_limit_ns);
         ++n_seg;
 #pragma unroll 1
         for (int j = lo; j < hi; ++j, ++n) {
-          const int st = ring + n % NSTR;
-          tile_wait(&bars[B_KF + st], uint32_t(n / NSTR) & 1u, abort_flag, p.wait_limit_ns);
-          if (n > 0) {  // S has been read, or (where P lies over it) P
-            if (C::P_ALIAS) tile_wait(&bars[B_O1 + t], uint32_t(n - 1) & 1u, abort_flag, p.wait_limit_ns);
-            else tile_wait(&bars[B_SC + t], uint32_t(n - 1) & 1u, abort_flag, p.wait_limit_ns);
-          }
-          tc_fence_after();
-          const uint64_t kd = kdesc + st * TILE_STEP;
-#pragma unroll 4
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint64_t koff = (kk / 4) * BOX_STEP + (kk % 4) * K_KSTEP;
-            mma_bf16_warp(dS, qdesc + koff, kd + koff, IDESC_S, kk > 0 ? 1u : 0u);
-          }
-          mma_commit_warp(&bars[B_S + t]);
-          mma_commit_warp(&bars[B_KE + st]);
-          if (j + 1 == hi) mma_commit_warp(&bars[B_QE + t]);
-          // with P apart from S the next scores run under this tile's softmax
+          if (scores) {
+            const int st = ring + n % NSTR;
+            tile_wait(&bars[B_KF + st], uint32_t(n / NSTR) & 1u, abort_flag, p.wait_limit_ns);
+            const uint64_t kd = kdesc + st * TILE_STEP;
 #pragma unroll 1
-          for (int m = C::P_ALIAS || j == lo ? n : n - 1; m < (C::P_ALIAS || j + 1 == hi ? n + 1 : n); ++m)
-            pv(m, m - n + j == lo, L - (m - n + j) * BN);
+            for (int s = PAIR ? 0 : t; s < (PAIR ? 2 : t + 1); ++s) {
+              // S has been read, or (where P lies over it) P
+              if (n > 0) tile_wait(&bars[(C::P_ALIAS ? B_O1 : B_SC) + s], uint32_t(n - 1) & 1u, abort_flag, p.wait_limit_ns);
+              tc_fence_after();
+              const uint64_t qd = qdesc + s * TILE_STEP;
+#pragma unroll
+              for (int kk = 0; kk < HD / 16; ++kk) {
+                const uint64_t koff = (kk / 4) * BOX_STEP + (kk % 4) * K_KSTEP;
+                mma_bf16_warp(tmem + TM_S + s * 128, qd + koff, kd + koff, IDESC_S, kk > 0 ? 1u : 0u);
+              }
+              mma_commit_warp(&bars[B_S + s]);
+              if (j + 1 == hi) mma_commit_warp(&bars[B_QE + s]);
+            }
+            mma_commit_warp(&bars[B_KE + st]);
+          }
+          if (PAIR) {
+            if (adds) pv(n, j == lo, L - j * BN);
+          } else {
+            // with P apart from S the next scores run under this tile's softmax
+#pragma unroll 1
+            for (int m = C::P_ALIAS || j == lo ? n : n - 1; m < (C::P_ALIAS || j + 1 == hi ? n + 1 : n); ++m)
+              pv(m, m - n + j == lo, L - (m - n + j) * BN);
+          }
         }
       }
     }
@@ -482,19 +503,33 @@ __global__ void __launch_bounds__(NTHR, 1)
     const uint32_t tO = tmem + TM_O + t * HD + lane_off;
     const uint32_t tP = tmem + TM_P + t * C::P_STRIDE + lane_off;
     const float c = p.qk_scale_log2;
+    if ((warp & 3) == 0 && lane == 0 && !(PAIR && t == 1)) {
+      // The unit that the range ends in, where it begins there too (a tile of it at least
+      // is this worker's and one another's): its partials are this worker's and those
+      // of the workers up to the one with its last tile.
+      int4 rec = make_int4(0, 0, 0, 0);
+      const unsigned s = cut.start(worker), end = cut.start(worker + 1);
+      if (worker + 1 < cut.n) {
+        const int4 x = border_s[2 * slot + 1], e = ent[x.x];
+        const unsigned begin = end - x.z;
+        if (x.z > LEAD && (begin >= s || s - begin <= LEAD))
+          rec = make_int4(e.x, x.y, int(cut.holder(begin + tiles_of(e.y) + LEAD - 1) - worker) + 1, 0);
+      }
+      p.record[worker] = rec;
+    }
     int n = 0;
 #pragma unroll 1
-    while (next_segment(walk, p, list)) {
+    while (next_segment<kLead<PAIR>>(walk, p, ent)) {
       const int n_it = walk->hi - walk->lo;
       const int masked_from = walk->t0 / BN - walk->lo;  // tiles with drafted rows, or past the keys
       // (rows past the last one are nobody's: a warp that has only such leaves P as it is)
       // The masks' words are asked for before the scores are there.
       if (p.mask != nullptr && masked_from < n_it) {
-        const int i = ((PAIR ? 2 * (walk->u % p.np) + t : walk->u % p.np) * BM + (tid & (BM - 1))) % p.Tq;
+        const int i = ((PAIR ? 2 * part_of<PAIR>(walk->u, p) + t : 0) * BM + (tid & (BM - 1))) % p.Tq;
         const int32_t* const words = p.mask + (size_t(walk->b) * p.Tq + i) * p.W;
         asm volatile("prefetch.global.L1 [%0];" ::"l"(words));
       }
-      const bool warp_live = ((PAIR ? 2 * (walk->u % p.np) + t : walk->u % p.np) * 4 + (warp & 3)) * 32 < p.n_rep * p.Tq;
+      const bool warp_live = ((PAIR ? 2 * part_of<PAIR>(walk->u, p) + t : 0) * 4 + (warp & 3)) * 32 < p.n_rep * p.Tq;
       float m_ref = -INFINITY, lsum = 0.f;
       if (PAIR && t == 1) named_bar_arrive(BAR_TURN_A, 256);  // (slot 0 begins)
 #pragma unroll 1
@@ -531,8 +566,8 @@ __global__ void __launch_bounds__(NTHR, 1)
           if (lane == 0) mbar_arrive(&bars[B_SC + t]);
         }
         if (j >= masked_from) {
-          const int L = walk->L, t0 = walk->t0, part = walk->u % p.np;
-          const int i = ((PAIR ? 2 * part + t : part) * BM + (tid & (BM - 1))) % p.Tq;
+          const int L = walk->L, t0 = walk->t0;
+          const int i = ((PAIR ? 2 * part_of<PAIR>(walk->u, p) + t : 0) * BM + (tid & (BM - 1))) % p.Tq;
           const int32_t* const words = p.mask + (p.mask != nullptr ? (size_t(walk->b) * p.Tq + i) * p.W : 0);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -614,7 +649,7 @@ __global__ void __launch_bounds__(NTHR, 1)
 
       // ---- the segment's rows: finished, or partials ----
       if (warp_live) {
-        const int part = walk->u % p.np, g = walk->u / p.np, r = tid & (BM - 1);
+        const int part = part_of<PAIR>(walk->u, p), g = head_of<PAIR>(walk->u, p), r = tid & (BM - 1);
         const int row = (PAIR ? 2 * part + t : part) * BM + r, h = row / p.Tq, i = row % p.Tq;
         const bool live = h < p.n_rep && i < walk->ql && !*abort_flag;
         const bool begins = walk->lo == 0, whole = begins && walk->hi == tiles_of(walk->L);
@@ -654,7 +689,6 @@ __global__ void __launch_bounds__(NTHR, 1)
           }
         } else {
           // [columns / 4][128 rows][4]: the lanes of a store are neighbours
-          const int worker = PAIR ? cta : t * p.n_ctas + cta;
           const size_t slot = (size_t(worker) * 2 + (begins ? 1 : 0)) * (PAIR ? 2 : 1) + (PAIR ? t : 0);
           if (live) p.ml[slot * BM + r] = make_float2(m_ref, lsum);
           float4* const dst = reinterpret_cast<float4*>(p.part_o) + slot * (BM * HD / 4) + r;
@@ -673,20 +707,11 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       tc_fence_before();
     }
-    // the cut unit that begins in this range, if there is one, and its partials
-    if ((warp & 3) == 0 && lane == 0 && !(PAIR && t == 1)) {
-      const unsigned w = PAIR ? cta : t * p.n_ctas + cta;
-      int4 rec = make_int4(0, 0, 0, 0);
-      const int nt = tiles_of(walk->L);
-      if (n > 0 && walk->lo == 0 && walk->hi < nt)  // (the range ends in it)
-        rec = make_int4(walk->b, walk->u, int(cut.holder(cut.start(w + 1) + (nt - walk->hi) - 1) - w) + 1, 0);
-      p.record[w] = rec;
-    }
   }
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) {  // let the work in flight end before the memories are released (as in prefill)
-    if (warp >= 10) {
+    if (warp >= (PAIR ? 9 : 10)) {
       mma_commit_warp(&bars[B_DRAIN]);
       mbar_wait_bounded(&bars[B_DRAIN], 0, p.wait_limit_ns);
     }
@@ -726,7 +751,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
   if (n == 0) return;
   uint32_t bits = 0;
   const int4 e = request(p, rec.x, bits);
-  const int row = (rec.y % p.np * TILES + t) * BM + r, g = rec.y / p.np, h = row / p.Tq, i = row % p.Tq;
+  const int row = (part_of<TILES == 2>(rec.y, p) * TILES + t) * BM + r, g = head_of<TILES == 2>(rec.y, p), h = row / p.Tq, i = row % p.Tq;
   const bool live = h < p.n_rep && i < e.z;
   if (!__any_sync(0xffffffffu, live)) return;  // (the same rows in every warp)
   float M = -INFINITY, den = 0.f, acc[4][4] = {};
