@@ -15,56 +15,98 @@
 namespace gqa {
 namespace {
 
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 load_once(const uint4* src) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(src));
+  return v;
+}
+
 // ---- accepted rows ------------------------------------------------------------
 
-// A thread owns 16 bytes of a head row (one layer, K or V, one KV head) and
-// moves them for every kept node in ascending order.  Node path[i] >= i, so a
-// row is written only after every read of what it held.
+// A block has a request and a share of its (layer, K or V, KV head) rows.  It first
+// looks up where the kept nodes stand and go to, a node a thread; then a thread owns
+// 16 bytes of a head row, of two heads at once, and moves them for all nodes, four at a
+// time: the loads of a batch before its stores.  path[i] >= i, ascending, so the nodes
+// that stay where they are come first, and what a batch writes is behind every
+// later batch's sources.
+//
+// The moves are few rows here and there: the time is four dependent round trips and
+// what the scattered rows' 128-byte pieces get out of HBM.
+constexpr int kMostKept = 1024;
+constexpr int kBatch = 4;
+
 __global__ void __launch_bounds__(256) compact_kernel(const CompactArgs p) {
+  __shared__ int2 move_s[kMostKept];  // rows of KV head 0, from and to
   const int b = blockIdx.x, tid = threadIdx.x;
   grid_launch_dependents();
   grid_dependency_wait();
   const bool paged = p.block_table != nullptr;
   const int cap = paged ? p.max_blocks * p.block_size : p.block_size;
   uint32_t bits = 0;
+  const int32_t* const path = p.path + size_t(b) * p.P;
   const int raw_len = p.kv_lens[b], raw_n = p.tree_lens[b], raw_keep = p.n_keep[b];
+  int node = tid < p.P ? path[tid] : 0, before = tid > 0 && tid < p.P ? path[tid - 1] : -1;
   const int len = min(max(raw_len, 0), cap), n = min(max(raw_n, 0), len), keep = min(max(raw_keep, 0), min(p.P, n));
   if (len != raw_len || n != raw_n || keep != raw_keep) bits |= GQA_DEV_KVLEN_CLAMPED;
-  const int32_t* const path = p.path + size_t(b) * p.P;
-  bool bad = false;
-  for (int i = tid; i < keep; i += blockDim.x) {
-    const int c = path[i], before = i > 0 ? path[i - 1] : -1;
-    bad |= c <= before || c >= n;
-  }
-  bad = __syncthreads_or(bad);
-  if (bad) bits |= GQA_DEV_BAD_INDEX;
   const int base = len - n;
-  if (blockIdx.y == 0 && tid == 0) p.kv_lens_out[b] = bad ? base : base + keep;
-  if (!bad) {
-    const int cols = p.row_bytes / 16;
-    const long unit = long(blockIdx.y) * (blockDim.x / cols) + tid / cols;  // (layer, K or V, KV head)
-    if (unit < 2L * p.n_layers * p.Hkv) {
-      const int h = int(unit % p.Hkv), which = int(unit / p.Hkv % 2), layer = int(unit / p.Hkv / 2);
-      uint4* const cache = static_cast<uint4*>(which ? p.v_cache : p.k_cache) +
-                           size_t(layer) * p.num_blocks * p.Hkv * p.block_size * cols + tid % cols;
-      auto row_of = [&](int r) -> uint4* {
-        int blk = b, in = r;
+  bool bad = false;
+  int stay = 0;  // nodes that are where they belong, the first ones
+  for (int i0 = 0; i0 < keep; i0 += 256) {
+    const int i = i0 + tid;
+    if (i0 > 0 && i < keep) node = path[i], before = path[i - 1];
+    const bool here = i < keep;
+    bad |= __syncthreads_or(here && (node <= before || node >= n));
+    stay += __syncthreads_count(here && node == i);
+    int2 m = make_int2(-1, -1);
+    if (here && !bad && node != i) {
+      int row[2] = {base + node, base + i};
+      bool ok = true;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
         if (paged) {
-          blk = p.block_table[size_t(b) * p.max_blocks + r / p.block_size];
-          in = r % p.block_size;
-          if (blk < 0 || blk >= p.num_blocks) {
-            bits |= GQA_DEV_BAD_BLOCK;
-            return nullptr;
-          }
+          const int j = row[x] / p.block_size, blk = p.block_table[size_t(b) * p.max_blocks + j];
+          const bool there = blk >= 0 && blk < p.num_blocks;
+          if (!there) bits |= GQA_DEV_BAD_BLOCK;
+          ok &= there;
+          row[x] = blk * p.Hkv * p.block_size + row[x] - j * p.block_size;
+        } else {
+          row[x] += b * p.Hkv * p.block_size;
         }
-        return cache + ((size_t(blk) * p.Hkv + h) * p.block_size + in) * cols;
-      };
-      for (int i = 0; i < keep; ++i) {
-        const int c = path[i];
-        if (c == i) continue;
-        const uint4* const from = row_of(base + c);
-        uint4* const to = row_of(base + i);
-        if (from != nullptr && to != nullptr) *to = *from;
+      }
+      if (ok) m = make_int2(row[0], row[1]);
+    }
+    if (here) move_s[i] = m;
+  }
+  if (bad) bits |= GQA_DEV_BAD_INDEX;
+  if (blockIdx.y == 0 && tid == 0) p.kv_lens_out[b] = bad ? base : base + keep;
+  __syncthreads();
+  if (!bad && stay < keep) {
+    const int cols = p.row_bytes / 16, per = 256 / cols, units = 2 * p.n_layers * p.Hkv, step = int(gridDim.y) * per;
+    auto place = [&](int unit) {  // (layer, K or V, KV head): its row 0
+      const int h = unit % p.Hkv, which = unit / p.Hkv % 2, layer = unit / p.Hkv / 2;
+      return static_cast<uint4*>(which ? p.v_cache : p.k_cache) +
+             (size_t(layer) * p.num_blocks * p.Hkv + h) * p.block_size * cols + tid % cols;
+    };
+    for (int u = int(blockIdx.y) * per + tid / cols; u < units; u += 2 * step) {
+      uint4* const cache[2] = {place(u), u + step < units ? place(u + step) : nullptr};
+      for (int i0 = stay; i0 < keep; i0 += kBatch) {
+        uint4 x[2][kBatch];
+        int2 m[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          m[k] = i0 + k < keep ? move_s[i0 + k] : make_int2(-1, -1);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (m[k].x >= 0 && cache[q] != nullptr) x[q][k] = load_once(cache[q] + size_t(m[k].x) * cols);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (m[k].x >= 0 && cache[q] != nullptr) cache[q][size_t(m[k].y) * cols] = x[q][k];
       }
     }
   }
@@ -73,27 +115,36 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactArgs p) {
 
 // ---- copies of pages ------------------------------------------------------------
 
-// The copied rows of a head are contiguous in a block.  One block of threads a
-// (copy, K or V, layer and head).
-__global__ void __launch_bounds__(256) copy_blocks_kernel(const CopyBlocksArgs p) {
+// The copied rows of a head are contiguous in a block of the cache.  One block of
+// threads a (copy, K or V, layer) and `heads` of its heads, four loads a thread under
+// way at once.
+__global__ void __launch_bounds__(256) copy_blocks_kernel(const CopyBlocksArgs p, int heads, int groups) {
   const int i = blockIdx.y;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int src = p.src[i];
+  const int src = p.src[i], dst = p.dst[i], raw = p.rows != nullptr ? p.rows[i] : p.block_size;
   if (src < 0) return;
-  const int dst = p.dst[i], raw = p.rows != nullptr ? p.rows[i] : p.block_size;
   const int rows = min(max(raw, 0), p.block_size);
   uint32_t bits = rows != raw ? GQA_DEV_KVLEN_CLAMPED : 0u;
   const bool ok = src < p.num_blocks && dst >= 0 && dst < p.num_blocks;
   if (!ok) bits |= GQA_DEV_BAD_BLOCK;
   if (ok && src != dst) {
-    const int unit = blockIdx.x, h = unit % p.Hkv, which = unit / p.Hkv % 2, layer = unit / p.Hkv / 2;
-    const int cols = p.row_bytes / 16;
-    uint4* const cache = static_cast<uint4*>(which ? p.v_cache : p.k_cache) +
-                         size_t(layer) * p.num_blocks * p.Hkv * p.block_size * cols;
-    const uint4* const from = cache + (size_t(src) * p.Hkv + h) * p.block_size * cols;
-    uint4* const to = cache + (size_t(dst) * p.Hkv + h) * p.block_size * cols;
-    for (int x = threadIdx.x; x < rows * cols; x += blockDim.x) to[x] = from[x];
+    const int h0 = int(blockIdx.x % groups) * heads, which = blockIdx.x / groups % 2, layer = blockIdx.x / groups / 2;
+    const int cols = p.row_bytes / 16, n = rows * cols, pitch = p.block_size * cols;
+    uint4* const cache = static_cast<uint4*>(which ? p.v_cache : p.k_cache) + size_t(layer) * p.num_blocks * p.Hkv * pitch;
+    for (int h = h0; h < min(h0 + heads, p.Hkv); ++h) {
+      const uint4* const from = cache + (size_t(src) * p.Hkv + h) * pitch;
+      uint4* const to = cache + (size_t(dst) * p.Hkv + h) * pitch;
+      for (int x0 = threadIdx.x; x0 < n; x0 += 4 * 256) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (x0 + k * 256 < n) v[k] = load_once(from + x0 + k * 256);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (x0 + k * 256 < n) to[x0 + k * 256] = v[k];
+      }
+    }
   }
   if (bits != 0 && threadIdx.x == 0) atomicOr(p.status, bits);
 }
@@ -101,7 +152,7 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(const CopyBlocksArgs p
 // ---- tables of requests that fork, shorten or end ---------------------------------
 
 constexpr int NT = 1024, NWARP = NT / 32;
-constexpr int kMostRequests = 8192;  // 12 bytes of shared memory each
+constexpr int kMostRequests = 8192;  // 16 bytes of shared memory for each old one, 12 for each new one
 
 // Sum over the block's threads before this one, and over all.  (part: 32 ints,
 // free again after the caller's next __syncthreads)
@@ -132,63 +183,118 @@ struct Fork {
   int src, keep;  // src < 0: none
 };
 
-// One block.  Whole numbers on a few hundred kilobytes at most: first the owner
-// of every old request, then what each new one keeps and which need a block,
-// then tables and holders, and at last the blocks without a holder, each of
-// which is put on the stack by the first entry, in the order of the old tables,
-// that gave it back.
+// Requests, old and new, from which on a cluster of eight blocks does the work (of up
+// to 128 blocks each: 16 in one block 11.5 us, in a cluster 14.7; 64 15.7, 19.0; 128 19.7
+// either way; 600 of up to 16 28.2, 14.0).
+constexpr int kClusterRequests = 128;
+constexpr unsigned kCluster = 8;
+
+// First the owner of every old request, then what each new one keeps and which need a
+// block: every block works all of that out for itself, in shared memory.  Then
+// tables and holders, a warp a request, over all blocks; and at last the blocks
+// without a holder, each of which is put on the stack by the first entry, in the
+// order of the old tables, that gave it back.
+//
+// Whole numbers on a few hundred kilobytes at most, so the time is a chain of eight
+// dependent round trips and of barriers.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
   extern __shared__ unsigned long long best[];          // [B_in]: (rows kept + 1, ~b) of the owner
   int* const kept = reinterpret_cast<int*>(best + p.B_in);  // [B_in]: blocks that the owner stays in
+  int* const held = kept + p.B_in;                          // [B_in]: rows
+  Fork* const fork_s = reinterpret_cast<Fork*>(held + p.B_in);  // [B]
+  int* const stack_s = reinterpret_cast<int*>(fork_s + p.B);    // [B]: the top of the stack, from the end
   __shared__ int part[NWARP];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cap = p.max_blocks * p.block_size;
+  unsigned rank = 0;
+  if (CLUSTER) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int cap = p.max_blocks * p.block_size, n_thr = CLUSTER ? int(kCluster) * NT : NT;
   uint32_t bits = 0;
-  grid_launch_dependents();
-  grid_dependency_wait();
-  for (int s = tid; s < p.B_in; s += NT) best[s] = 0, kept[s] = 0;
-  if (p.shared_out != p.shared)
-    for (int i = tid; i < p.num_blocks; i += NT) p.shared_out[i] = p.shared[i];
-  if (p.free_out != p.free_blocks)
-    for (int i = tid; i < p.num_blocks; i += NT) p.free_out[i] = p.free_blocks[i];
-  const int raw_count = *p.free_count, count = min(max(raw_count, 0), p.num_blocks);
-  if (raw_count != count) bits |= GQA_DEV_BAD_BLOCK;
-  __syncthreads();
-
-  auto held_of = [&](int s) { return min(max(p.held_lens[s], 0), cap); };
+  auto barrier = [&] {  // of all threads; what they wrote and added before is seen after it
+    if (CLUSTER) {
+      asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    } else {
+      __syncthreads();
+    }
+  };
   auto blocks_of = [&](int n) { return int((unsigned(n) + unsigned(p.block_size) - 1u) / unsigned(p.block_size)); };
   auto valid = [&](int id) { return id >= 0 && id < p.num_blocks; };
-  auto ask = [&](int b) {
-    Fork f{p.src[b], 0};
+  auto key = [&](const Fork& f, int b) { return (unsigned long long)(f.keep + 1) << 32 | unsigned(~b); };
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  // ---- what is asked for ----
+  const int raw_count = *p.free_count, count = min(max(raw_count, 0), p.num_blocks);
+  for (int s = tid; s < p.B_in; s += NT) {
+    const int raw = p.held_lens[s], n = min(max(raw, 0), cap);
+    if (raw != n) bits |= GQA_DEV_KVLEN_CLAMPED;
+    held[s] = n;
+    best[s] = 0;
+    kept[s] = 0;
+  }
+  for (int b = tid; b < p.B; b += NT) {
+    Fork f{p.src[b], p.keep_lens != nullptr ? p.keep_lens[b] : -1};
     if (f.src >= p.B_in) {
       bits |= GQA_DEV_BAD_INDEX;
       f.src = -1;
     }
-    if (f.src >= 0) {
-      const int held = held_of(f.src), raw = p.keep_lens != nullptr ? p.keep_lens[b] : held;
-      f.keep = min(max(raw, 0), held);
-      if (f.keep != raw) bits |= GQA_DEV_KVLEN_CLAMPED;
-    }
-    return f;
-  };
-  auto key = [&](const Fork& f, int b) { return (unsigned long long)(f.keep + 1) << 32 | unsigned(~b); };
-
-  for (int b = tid; b < p.B; b += NT) {
-    const Fork f = ask(b);
-    if (f.src >= 0) atomicMax(&best[f.src], key(f, b));
+    fork_s[b] = f;
   }
-  for (int s = tid; s < p.B_in; s += NT) {
-    const int raw = p.held_lens[s];
-    if (raw < 0 || raw > cap) bits |= GQA_DEV_KVLEN_CLAMPED;
+  if (raw_count != count) bits |= GQA_DEV_BAD_BLOCK;
+  for (int i = tid; i < min(p.B, count); i += NT) stack_s[i] = p.free_blocks[count - 1 - i];
+  // (what is not changed in place is copied meanwhile)
+  auto copy = [&](const int32_t* from, int32_t* to) {
+    if (from == to) return;
+    int i = int(rank) * NT + tid;
+    if (((reinterpret_cast<uintptr_t>(from) | reinterpret_cast<uintptr_t>(to)) & 15) == 0) {
+      const int n4 = p.num_blocks / 4;
+#pragma unroll 2
+      for (int q = i; q < n4; q += n_thr) reinterpret_cast<int4*>(to)[q] = reinterpret_cast<const int4*>(from)[q];
+      i += 4 * n4;
+    }
+    for (; i < p.num_blocks; i += 4 * n_thr) {
+      int v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k * n_thr < p.num_blocks) v[k] = from[i + k * n_thr];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k * n_thr < p.num_blocks) to[i + k * n_thr] = v[k];
+    }
+  };
+  copy(p.shared, p.shared_out);
+  copy(p.free_blocks, p.free_out);
+  __syncthreads();
+
+  // ---- owners ----
+  for (int b = tid; b < p.B; b += NT) {
+    Fork f = fork_s[b];
+    if (f.src >= 0) {
+      const int most = held[f.src], raw = p.keep_lens != nullptr ? f.keep : most;
+      f.keep = min(max(raw, 0), most);
+      if (f.keep != raw) bits |= GQA_DEV_KVLEN_CLAMPED;
+      atomicMax(&best[f.src], key(f, b));
+    } else {
+      f.keep = 0;
+    }
+    fork_s[b] = f;
   }
   __syncthreads();
 
   // ---- what each new request keeps, and the blocks taken ----
+  const int gw = int(rank) * NWARP + warp, n_warps = n_thr / 32;
+  // (the tables that this warp reads next are asked for meanwhile)
+  auto ask = [&](int s, int n) {
+    if (lane * 32 < n) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.table + size_t(s) * p.max_blocks + lane * 32));
+  };
+  if (gw < p.B && fork_s[gw].src >= 0) ask(fork_s[gw].src, fork_s[gw].keep / p.block_size);
+  if (gw < p.B_in) ask(gw, blocks_of(held[gw]));
   int taken = 0;
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     const int b = b0 + tid;
     Fork f{-1, 0};
-    if (b < p.B) f = ask(b);
+    if (b < p.B) f = fork_s[b];
     const int whole = f.keep / p.block_size, rest = f.keep % p.block_size;
     const bool owner = f.src >= 0 && best[f.src] == key(f, b);
     int last = -1;
@@ -203,67 +309,107 @@ __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
     const int nth = taken + block_exclusive(wants ? 1 : 0, part, total);
     const bool copies = wants && nth < count;
     if (b < p.B) {
-      if (wants && !copies) bits |= GQA_DEV_OUT_OF_BLOCKS;
-      const int id = copies ? p.free_blocks[count - 1 - nth] : last;
-      if (copies && !valid(id)) bits |= GQA_DEV_BAD_BLOCK;
-      if (stays || copies) p.table_out[size_t(b) * p.max_blocks + whole] = id;
-      p.kv_lens_out[b] = whole * p.block_size + (stays || copies ? rest : 0);
-      p.copy_src[b] = copies ? last : -1;
-      p.copy_dst[b] = copies ? id : -1;
-      p.copy_rows[b] = copies ? rest : 0;
       if (owner) kept[f.src] = whole + (stays ? 1 : 0);
+      if (rank == 0) {
+        if (wants && !copies) bits |= GQA_DEV_OUT_OF_BLOCKS;
+        const int id = copies ? stack_s[nth] : last;
+        if (copies && !valid(id)) bits |= GQA_DEV_BAD_BLOCK;
+        if (stays || copies) p.table_out[size_t(b) * p.max_blocks + whole] = id;
+        p.kv_lens_out[b] = whole * p.block_size + (stays || copies ? rest : 0);
+        p.copy_src[b] = copies ? last : -1;
+        p.copy_dst[b] = copies ? id : -1;
+        p.copy_rows[b] = copies ? rest : 0;
+      }
     }
     taken = min(taken + total, count);
     __syncthreads();
   }
+  // Every block has read holders and stack as they were, and the copies are made.
+  barrier();
 
   // ---- whole blocks into the tables; holders ----
-  for (int b = warp; b < p.B; b += NWARP) {
-    const Fork f = ask(b);
+  for (int b = gw; b < p.B; b += n_warps) {
+    const Fork f = fork_s[b];
     if (f.src < 0) continue;
     const bool owner = best[f.src] == key(f, b);
     const int whole = f.keep / p.block_size;
+    const int32_t* const from = p.table + size_t(f.src) * p.max_blocks;
+    int32_t* const to = p.table_out + size_t(b) * p.max_blocks;
+#pragma unroll 4
     for (int j = lane; j < whole; j += 32) {
-      const int id = p.table[size_t(f.src) * p.max_blocks + j];
-      p.table_out[size_t(b) * p.max_blocks + j] = id;
+      const int id = from[j];
+      to[j] = id;
       if (!valid(id)) bits |= GQA_DEV_BAD_BLOCK;
       else if (!owner) atomicAdd(&p.shared_out[id], 1);
     }
   }
-  for (int s = warp; s < p.B_in; s += NWARP) {
-    const int have = blocks_of(held_of(s));
+  bool gives = false;
+  for (int s = gw; s < p.B_in; s += n_warps) {
+    const int have = blocks_of(held[s]);
+    const int32_t* const from = p.table + size_t(s) * p.max_blocks;
+#pragma unroll 4
     for (int j = kept[s] + lane; j < have; j += 32) {
-      const int id = p.table[size_t(s) * p.max_blocks + j];
+      const int id = from[j];
+      gives = true;
       if (!valid(id)) bits |= GQA_DEV_BAD_BLOCK;
       else atomicSub(&p.shared_out[id], 1);
     }
   }
-  __threadfence();
-  __syncthreads();
+  gives = __any_sync(0xffffffffu, gives);
+  barrier();
 
   // ---- blocks that nobody holds: the first entry that gave one back claims it ----
   constexpr int kClaim = INT32_MIN;  // + the entry's number (below 2^30)
-  for (int s = warp; s < p.B_in; s += NWARP) {
-    const int have = blocks_of(held_of(s));
-    for (int j = kept[s] + lane; j < have; j += 32) {
-      const int id = p.table[size_t(s) * p.max_blocks + j];
-      if (valid(id) && __ldcg(&p.shared_out[id]) < 0) atomicMin(&p.shared_out[id], kClaim + s * p.max_blocks + j);
+  if (gives)
+    for (int s = gw; s < p.B_in; s += n_warps) {
+      const int have = blocks_of(held[s]);
+      const int32_t* const from = p.table + size_t(s) * p.max_blocks;
+#pragma unroll 4
+      for (int j = kept[s] + lane; j < have; j += 32) {
+        const int id = from[j];
+        if (valid(id) && __ldcg(&p.shared_out[id]) < 0) atomicMin(&p.shared_out[id], kClaim + s * p.max_blocks + j);
+      }
     }
-  }
-  __threadfence();
-  __syncthreads();
-  int* const won = reinterpret_cast<int*>(best);  // [B_in]: blocks that each old request puts on the stack
-  for (int s = warp; s < p.B_in; s += NWARP) {
-    const int have = blocks_of(held_of(s));
+  barrier();
+  // Which of the entries j0 + 32 k + lane of old request s put a block on the stack (bit
+  // k): 256 at once, so that one round trip finds them.
+  auto winners = [&](int s, int j0, int have, int (&id)[8]) {
+    unsigned mine = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int j = j0 + 32 * k + lane;
+      id[k] = j < have ? p.table[size_t(s) * p.max_blocks + j] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (valid(id[k]) && __ldcg(&p.shared_out[id[k]]) == kClaim + s * p.max_blocks + j0 + 32 * k + lane) mine |= 1u << k;
+    return mine;
+  };
+  // Blocks that each old request puts on the stack, told to every block of the cluster
+  // (best is not needed any more).
+  int* const won = reinterpret_cast<int*>(best);
+  for (int s = gw; s < p.B_in; s += n_warps) {
     int n = 0;
-    for (int j = kept[s] + lane; j < have; j += 32) {
-      const int id = p.table[size_t(s) * p.max_blocks + j];
-      n += valid(id) && __ldcg(&p.shared_out[id]) == kClaim + s * p.max_blocks + j;
+    if (gives) {
+      const int have = blocks_of(held[s]);
+      for (int j0 = kept[s]; j0 < have; j0 += 256) {
+        int id[8];
+        n += __popc(winners(s, j0, have, id));
+      }
+      n = __reduce_add_sync(0xffffffffu, n);
     }
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) won[s] = n;
+    if (!CLUSTER) {
+      if (lane == 0) won[s] = n;
+    } else if (lane < int(kCluster)) {
+      asm volatile(
+          "{\n\t.reg .b32 a;\n\t"
+          "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+          "st.shared::cluster.u32 [a], %2;\n\t}" ::"r"(smem_u32(won) + 4 * s),
+          "r"(lane), "r"(n)
+          : "memory");
+    }
   }
-  __syncthreads();
+  barrier();
   int top = count - taken;
   for (int s0 = 0; s0 < p.B_in; s0 += NT) {
     const int s = s0 + tid;
@@ -273,28 +419,27 @@ __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
     top += total;
     __syncthreads();
   }
-  for (int s = warp; s < p.B_in; s += NWARP) {
-    const int have = blocks_of(held_of(s));
-    int at = won[s];
-    for (int j0 = kept[s]; j0 < have; j0 += 32) {
-      const int j = j0 + lane;
-      bool mine = false;
-      int id = -1;
-      if (j < have) {
-        id = p.table[size_t(s) * p.max_blocks + j];
-        mine = valid(id) && __ldcg(&p.shared_out[id]) == kClaim + s * p.max_blocks + j;
+  if (gives)
+    for (int s = gw; s < p.B_in; s += n_warps) {
+      const int have = blocks_of(held[s]);
+      int at = won[s];
+      for (int j0 = kept[s]; j0 < have; j0 += 256) {
+        int id[8];
+        const unsigned mine = winners(s, j0, have, id);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const unsigned all = __ballot_sync(0xffffffffu, mine >> k & 1u);
+          if (mine >> k & 1u) {
+            const long to = long(at) + __popc(all & ((1u << lane) - 1u));
+            if (to < p.num_blocks) p.free_out[to] = id[k];
+            else bits |= GQA_DEV_BAD_BLOCK;
+            p.shared_out[id[k]] = 0;
+          }
+          at += __popc(all);
+        }
       }
-      const unsigned all = __ballot_sync(0xffffffffu, mine);
-      if (mine) {
-        const long to = long(at) + __popc(all & ((1u << lane) - 1u));
-        if (to < p.num_blocks) p.free_out[to] = id;
-        else bits |= GQA_DEV_BAD_BLOCK;
-        p.shared_out[id] = 0;
-      }
-      at += __popc(all);
     }
-  }
-  if (tid == 0) *p.count_out = min(top, p.num_blocks);
+  if (rank == 0 && tid == 0) *p.count_out = min(top, p.num_blocks);
   if (bits != 0) atomicOr(p.status, bits);
 }
 
@@ -302,23 +447,34 @@ __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
 
 cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream) {
   const long units = 2L * a.n_layers * a.Hkv;
-  const int per = 256 / (a.row_bytes / 16);
-  const long ny = (units + per - 1) / per;
-  return launch_pdl(compact_kernel, dim3(a.B, unsigned(ny)), dim3(256), 0, stream, a);
+  const long per = 256 / (a.row_bytes / 16);
+  // one wave of blocks, eight an SM, where that leaves every block a step
+  const long ny = std::min((units + per - 1) / per, std::max(1L, 8L * device_sm_count() / a.B));
+  return launch_pdl(compact_kernel, dim3(a.B, unsigned(std::min(ny, 65535L))), dim3(256), 0, stream, a);
 }
 
 cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, cudaStream_t stream) {
-  return launch_pdl(copy_blocks_kernel, dim3(2u * a.n_layers * a.Hkv, a.n), dim3(256), 0, stream, a);
+  // A block of threads takes several heads where there are blocks enough all the same.
+  int heads = 1;
+  while (heads < a.Hkv && 2L * a.n_layers * ((a.Hkv + 2 * heads - 1) / (2 * heads)) * a.n >= 16L * device_sm_count())
+    heads *= 2;
+  const int groups = (a.Hkv + heads - 1) / heads;
+  return launch_pdl(copy_blocks_kernel, dim3(2u * a.n_layers * groups, a.n), dim3(256), 0, stream, a, heads, groups);
 }
 
 cudaError_t launch_fork(const ForkArgs& a, cudaStream_t stream) {
   static DeviceOnce once;
   const cudaError_t e = once.run([&] {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(fork_kernel),
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMostRequests * 12);
+    cudaError_t r = cudaSuccess;
+    for (const void* k : {reinterpret_cast<const void*>(fork_kernel<false>), reinterpret_cast<const void*>(fork_kernel<true>)})
+      if (r == cudaSuccess) r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostRequests * 28);
+    return r;
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(fork_kernel, dim3(1), dim3(NT), size_t(a.B_in) * 12, stream, a);
+  const size_t smem = size_t(a.B_in) * 16 + size_t(a.B) * 12;
+  if (a.B + a.B_in < kClusterRequests)
+    return launch_pdl(fork_kernel<false>, dim3(1), dim3(NT), smem, stream, a);
+  return launch_pdl_cluster(fork_kernel<true>, kCluster, dim3(kCluster), dim3(NT), smem, stream, a);
 }
 
 }  // namespace gqa
