@@ -115,38 +115,161 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactArgs p) {
 
 // ---- copies of pages ------------------------------------------------------------
 
-// The copied rows of a head are contiguous in a block of the cache.  One block of
-// threads a (copy, K or V, layer) and `heads` of its heads, four loads a thread under
-// way at once.
-__global__ void __launch_bounds__(256) copy_blocks_kernel(const CopyBlocksArgs p, int heads, int groups) {
-  const int i = blockIdx.y;
+// The copied rows of a head are contiguous in a block of the cache: a piece of work.
+// Every block of threads finds the copies that are to be made (1,024 entries of the
+// list at a time, most of which may be idle) and its warps take their shares of the
+// pieces, neighbours neighbouring heads.  A warp moves a chunk at a time through
+// shared memory with bulk copies, two loads under way while the third chunk is stored:
+// nothing passes through registers.  Chunks of 16 KB by four warps, and more warps with
+// smaller ones where no piece is longer (pieces of up to 2 KB, 90 copies in 8 layers of
+// 8 heads: 11.7 us by four warps, 7.8 by eight).
+//
+// What bounds it is HBM, half of it writing: 64 pages of 8 x 64 x 128 in 16 layers 42.8 us, 6.4 TB/s
+// (registers, four 16-byte loads a thread: 44.8; with an evict-first policy on the
+// loads 47.1); six live copies in a list of 256 5.0 us (a block of threads for every entry and
+// head: 12.9).
+constexpr int kListed = 1024;
+constexpr int kCopyStages = 3;
+template <int WARPS>
+constexpr int kChunk = 65536 / WARPS;
+constexpr int kCopySmem = kCopyStages * 65536;
+
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src_smem, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(dst),
+               "r"(smem_u32(src_smem)), "r"(bytes)
+               : "memory");
+}
+
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) copy_blocks_kernel(const CopyBlocksArgs p, uint64_t wait_limit_ns,
+                                                                uint64_t test_stall_ns) {
+  extern __shared__ __align__(128) unsigned char stage_s[];
+  __shared__ int src_s[kListed], dst_s[kListed], rows_s[kListed], warp_s[WARPS];
+  __shared__ uint64_t bars[WARPS * kCopyStages + 1];  // (nothing arrives on the last one)
+  constexpr int NTC = WARPS * 32, EACH = kListed / NTC, CHUNK = kChunk<WARPS>;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned units = 2u * p.n_layers * p.Hkv;
+  uint32_t bits = 0;
+  if (tid < WARPS * kCopyStages + 1) mbar_init(&bars[tid], 1);
+  fence_barrier_init();
   grid_launch_dependents();
   grid_dependency_wait();
-  const int src = p.src[i], dst = p.dst[i], raw = p.rows != nullptr ? p.rows[i] : p.block_size;
-  if (src < 0) return;
-  const int rows = min(max(raw, 0), p.block_size);
-  uint32_t bits = rows != raw ? GQA_DEV_KVLEN_CLAMPED : 0u;
-  const bool ok = src < p.num_blocks && dst >= 0 && dst < p.num_blocks;
-  if (!ok) bits |= GQA_DEV_BAD_BLOCK;
-  if (ok && src != dst) {
-    const int h0 = int(blockIdx.x % groups) * heads, which = blockIdx.x / groups % 2, layer = blockIdx.x / groups / 2;
-    const int cols = p.row_bytes / 16, n = rows * cols, pitch = p.block_size * cols;
-    uint4* const cache = static_cast<uint4*>(which ? p.v_cache : p.k_cache) + size_t(layer) * p.num_blocks * p.Hkv * pitch;
-    for (int h = h0; h < min(h0 + heads, p.Hkv); ++h) {
-      const uint4* const from = cache + (size_t(src) * p.Hkv + h) * pitch;
-      uint4* const to = cache + (size_t(dst) * p.Hkv + h) * pitch;
-      for (int x0 = threadIdx.x; x0 < n; x0 += 4 * 256) {
-        uint4 v[4];
+  const uint64_t policy = l2_policy_evict_normal();
+  unsigned char* const stage = stage_s + warp * kCopyStages * CHUNK;
+  uint64_t* const bar = bars + warp * kCopyStages;
+  unsigned n_loads = 0, n_stores = 0;  // of this warp (lane 0)
+  bool lost = false;
+  for (int c0 = 0; c0 < p.n; c0 += kListed) {
+    int src[EACH], dst[EACH], rows[EACH], mine = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (x0 + k * 256 < n) v[k] = load_once(from + x0 + k * 256);
+    for (int k = 0; k < EACH; ++k) {
+      const int i = c0 + k * NTC + tid;
+      src[k] = i < p.n ? p.src[i] : -1;
+      dst[k] = i < p.n ? p.dst[i] : -1;
+      rows[k] = i < p.n && p.rows != nullptr ? p.rows[i] : p.block_size;
+    }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (x0 + k * 256 < n) to[x0 + k * 256] = v[k];
+    for (int k = 0; k < EACH; ++k) {
+      if (src[k] < 0) continue;
+      const int raw = rows[k];
+      rows[k] = min(max(raw, 0), p.block_size);
+      if (rows[k] != raw) bits |= GQA_DEV_KVLEN_CLAMPED;
+      if (src[k] >= p.num_blocks || dst[k] < 0 || dst[k] >= p.num_blocks) {
+        bits |= GQA_DEV_BAD_BLOCK;
+        src[k] = -1;
+      } else if (src[k] == dst[k] || rows[k] == 0) {
+        src[k] = -1;
+      }
+      mine += src[k] >= 0;
+    }
+    int sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += u;
+    }
+    if (lane == 31) warp_s[warp] = sum;
+    __syncthreads();
+    int at = sum - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) at += warp_s[w];
+      total += warp_s[w];
+    }
+#pragma unroll
+    for (int k = 0; k < EACH; ++k)
+      if (src[k] >= 0) {
+        src_s[at] = src[k];
+        dst_s[at] = dst[k];
+        rows_s[at] = rows[k];
+        ++at;
+      }
+    __syncthreads();
+    if (lane == 0 && !lost) {
+      const unsigned pieces = unsigned(total) * units;  // (below 2^31)
+      unsigned x = blockIdx.x * WARPS + warp;
+      size_t left = 0;  // bytes of the piece not yet asked for
+      const unsigned char* from = nullptr;
+      unsigned char* to = nullptr;
+      unsigned char* to_of[kCopyStages];  // of the chunks under way
+      uint32_t bytes_of[kCopyStages];
+      const unsigned first = n_loads;
+      bool more = true;
+      // step i asks for chunk i and stores chunk i - 2
+      for (unsigned i = first; more || n_stores != n_loads; ++i) {
+        if (more && left == 0) {
+          more = x < pieces;
+          if (more) {
+            const unsigned c = x / units, u = x % units, h = u % p.Hkv, which = u / p.Hkv % 2, layer = u / p.Hkv / 2;
+            const size_t pitch = size_t(p.block_size) * p.row_bytes;
+            unsigned char* const cache = static_cast<unsigned char*>(which ? p.v_cache : p.k_cache) +
+                                         (size_t(layer) * p.num_blocks * p.Hkv + h) * pitch;
+            from = cache + size_t(src_s[c]) * p.Hkv * pitch;
+            to = cache + size_t(dst_s[c]) * p.Hkv * pitch;
+            left = size_t(rows_s[c]) * p.row_bytes;
+            x += gridDim.x * WARPS;
+          }
+        }
+        if (more) {
+          const int st = int(n_loads % kCopyStages);
+          const uint32_t bytes = uint32_t(left < size_t(CHUNK) ? left : size_t(CHUNK));
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // (the store out of this stage has read it)
+          mbar_arrive_expect_tx(&bar[st], bytes);
+          bulk_g2s(stage + st * CHUNK, from, bytes, &bar[st], policy);
+#pragma unroll
+          for (int k = 0; k < kCopyStages; ++k)
+            if (k == st) to_of[k] = to, bytes_of[k] = bytes;
+          from += bytes;
+          to += bytes;
+          left -= bytes;
+          ++n_loads;
+          if (test_stall_ns != 0 && !mbar_wait_bounded(&bars[WARPS * kCopyStages], 0, test_stall_ns)) {
+            lost = true;
+            break;
+          }
+        }
+        if (n_loads - n_stores > kCopyStages - 1 || (!more && n_stores != n_loads)) {
+          const int st = int(n_stores % kCopyStages);
+          if (!mbar_wait_bounded(&bar[st], n_stores / kCopyStages & 1u, wait_limit_ns)) {
+            lost = true;
+            break;
+          }
+#pragma unroll
+          for (int k = 0; k < kCopyStages; ++k)
+            if (k == st) bulk_s2g(to_of[k], stage + st * CHUNK, bytes_of[k]);
+          ++n_stores;
+        }
       }
     }
+    __syncthreads();  // (the list is made again)
   }
-  if (bits != 0 && threadIdx.x == 0) atomicOr(p.status, bits);
+  if (lost) {  // a copy that never came: those under way end before the memory is given away
+    atomicOr(p.status, GQA_DEV_WAIT_TIMEOUT);
+    for (; n_stores != n_loads; ++n_stores)
+      mbar_wait_bounded(&bar[n_stores % kCopyStages], n_stores / kCopyStages & 1u, wait_limit_ns);
+  }
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (blockIdx.x == 0 && bits != 0) atomicOr(p.status, bits);
 }
 
 // ---- tables of requests that fork, shorten or end ---------------------------------
@@ -328,31 +451,44 @@ __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
   barrier();
 
   // ---- whole blocks into the tables; holders ----
+  // Entries j0 + 32 k + lane of an old table up to `end` (-1 past it): 256 at once,
+  // so that one round trip brings them.
+  auto entries = [&](int s, int j0, int end, int (&id)[8]) {
+    const int32_t* const from = p.table + size_t(s) * p.max_blocks;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int j = j0 + 32 * k + lane;
+      id[k] = j < end ? from[j] : -1;
+      if (j < end && !valid(id[k])) bits |= GQA_DEV_BAD_BLOCK;
+    }
+  };
   for (int b = gw; b < p.B; b += n_warps) {
     const Fork f = fork_s[b];
     if (f.src < 0) continue;
     const bool owner = best[f.src] == key(f, b);
     const int whole = f.keep / p.block_size;
-    const int32_t* const from = p.table + size_t(f.src) * p.max_blocks;
     int32_t* const to = p.table_out + size_t(b) * p.max_blocks;
-#pragma unroll 4
-    for (int j = lane; j < whole; j += 32) {
-      const int id = from[j];
-      to[j] = id;
-      if (!valid(id)) bits |= GQA_DEV_BAD_BLOCK;
-      else if (!owner) atomicAdd(&p.shared_out[id], 1);
+    for (int j0 = 0; j0 < whole; j0 += 256) {
+      int id[8];
+      entries(f.src, j0, whole, id);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int j = j0 + 32 * k + lane;
+        if (j < whole) to[j] = id[k];
+        if (!owner && valid(id[k])) atomicAdd(&p.shared_out[id[k]], 1);
+      }
     }
   }
   bool gives = false;
   for (int s = gw; s < p.B_in; s += n_warps) {
     const int have = blocks_of(held[s]);
-    const int32_t* const from = p.table + size_t(s) * p.max_blocks;
-#pragma unroll 4
-    for (int j = kept[s] + lane; j < have; j += 32) {
-      const int id = from[j];
+    for (int j0 = kept[s]; j0 < have; j0 += 256) {
+      int id[8];
+      entries(s, j0, have, id);
       gives = true;
-      if (!valid(id)) bits |= GQA_DEV_BAD_BLOCK;
-      else atomicSub(&p.shared_out[id], 1);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (valid(id[k])) atomicSub(&p.shared_out[id[k]], 1);
     }
   }
   gives = __any_sync(0xffffffffu, gives);
@@ -363,26 +499,25 @@ __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
   if (gives)
     for (int s = gw; s < p.B_in; s += n_warps) {
       const int have = blocks_of(held[s]);
-      const int32_t* const from = p.table + size_t(s) * p.max_blocks;
-#pragma unroll 4
-      for (int j = kept[s] + lane; j < have; j += 32) {
-        const int id = from[j];
-        if (valid(id) && __ldcg(&p.shared_out[id]) < 0) atomicMin(&p.shared_out[id], kClaim + s * p.max_blocks + j);
+      for (int j0 = kept[s]; j0 < have; j0 += 256) {
+        int id[8];
+        unsigned none = 0;
+        entries(s, j0, have, id);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) none |= unsigned(valid(id[k]) && __ldcg(&p.shared_out[id[k]]) < 0) << k;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (none >> k & 1u) atomicMin(&p.shared_out[id[k]], kClaim + s * p.max_blocks + j0 + 32 * k + lane);
       }
     }
   barrier();
-  // Which of the entries j0 + 32 k + lane of old request s put a block on the stack (bit
-  // k): 256 at once, so that one round trip finds them.
+  // Which of these put a block on the stack (bit k).
   auto winners = [&](int s, int j0, int have, int (&id)[8]) {
     unsigned mine = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int j = j0 + 32 * k + lane;
-      id[k] = j < have ? p.table[size_t(s) * p.max_blocks + j] : -1;
-    }
+    entries(s, j0, have, id);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (valid(id[k]) && __ldcg(&p.shared_out[id[k]]) == kClaim + s * p.max_blocks + j0 + 32 * k + lane) mine |= 1u << k;
+      mine |= unsigned(valid(id[k]) && __ldcg(&p.shared_out[id[k]]) == kClaim + s * p.max_blocks + j0 + 32 * k + lane) << k;
     return mine;
   };
   // Blocks that each old request puts on the stack, told to every block of the cluster
@@ -454,12 +589,21 @@ cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, cudaStream_t stream) {
-  // A block of threads takes several heads where there are blocks enough all the same.
-  int heads = 1;
-  while (heads < a.Hkv && 2L * a.n_layers * ((a.Hkv + 2 * heads - 1) / (2 * heads)) * a.n >= 16L * device_sm_count())
-    heads *= 2;
-  const int groups = (a.Hkv + heads - 1) / heads;
-  return launch_pdl(copy_blocks_kernel, dim3(2u * a.n_layers * groups, a.n), dim3(256), 0, stream, a, heads, groups);
+  const long pieces = 2L * a.n_layers * a.Hkv * a.n, longest = long(a.block_size) * a.row_bytes;
+  const dim3 grid(unsigned(std::min(pieces, long(std::max(1, device_sm_count())))));
+  auto go = [&](auto kern, DeviceOnce& once, int warps) {
+    const cudaError_t e = once.run([&] {
+      return cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  kCopySmem);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, grid, dim3(warps * 32), kCopySmem, stream, a, uint64_t(kWaitLimitNs),
+                      wait_test_ns());
+  };
+  static DeviceOnce once4, once8, once16;
+  if (longest > kChunk<8>) return go(copy_blocks_kernel<4>, once4, 4);
+  if (longest > kChunk<16>) return go(copy_blocks_kernel<8>, once8, 8);
+  return go(copy_blocks_kernel<16>, once16, 16);
 }
 
 cudaError_t launch_fork(const ForkArgs& a, cudaStream_t stream) {

@@ -543,7 +543,8 @@ GQA_ATTN_API int gqa_attn_fork_tables(const int32_t* src, const int32_t* keep_le
  *   v_cache
  * A block is the destination of at most one copy and then the source of none
  * (otherwise it holds some mix).  Ids past the pool and a negative dst set
- * GQA_DEV_BAD_BLOCK, and the copy is left out.
+ * GQA_DEV_BAD_BLOCK, and the copy is left out.  A piece that does not come within the
+ * kernel's bounded wait sets GQA_DEV_WAIT_TIMEOUT and is not written.
  * D = 64 or 128; n <= 65535; n_layers * Hkv <= 2^20; num_blocks * Hkv * block_size < 2^31.
  *   workspace     as for gqa_attn_step_tables (the status word)
  * ------------------------------------------------------------------------- */
@@ -683,7 +684,7 @@ GQA_ATTN_API int gqa_attn_set_prefill_interleave_override(int from_pair);
  * output rows as NaN and sets GQA_DEV_WAIT_TIMEOUT in the prefill status word.
  * With stall_ns > 0 every later launch of gqa_attn_decode, _decode_paged,
  * _decode_layers, _decode_q4, _decode_q4_residual, _decode_shared_prefix(_paged),
- * _prefill and _prefill_varlen makes the thread that issues a CTA's copies, once it has
+ * _decode_tree(_paged), _copy_blocks, _prefill and _prefill_varlen makes the thread that issues a CTA's copies, once it has
  * issued its first ones, wait stall_ns on a barrier that nothing arrives on
  * and give up, so that this path runs deterministically: the call reports
  * GQA_DEV_WAIT_TIMEOUT and its outputs are unspecified (a prefill CTA whose
