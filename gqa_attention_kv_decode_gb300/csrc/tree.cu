@@ -93,7 +93,7 @@ struct TrCfg {
                        B_S = B_VE + NST, B_SC = B_S + 2, B_P0 = B_SC + 2, B_P1 = B_P0 + 2, B_O0 = B_P1 + 2, B_O1 = B_O0 + 2,
                        B_DRAIN = B_O1 + 2, B_STALL = B_DRAIN + 1, N_BARS = B_STALL + 1;
   static constexpr int OFF_TSLOT = 8 * N_BARS, OFF_ABORT = OFF_TSLOT + 4, OFF_ISSUED = OFF_TSLOT + 8,
-                       OFF_START = (OFF_TSLOT + 32 + 15) / 16 * 16, OFF_SUMS = OFF_START + 64;
+                       OFF_SUMS = OFF_TSLOT + 32;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
   static_assert(OFF_SUMS + 12 * 4 <= 512, "barrier area");
   static_assert(128 * REG_CTRL + 256 * REG_SOFTMAX <= NTHR * 168, "register split exceeds the launch allocation");
@@ -111,7 +111,7 @@ struct TreeParams {
   int n_ctas, n_workers;
   float qk_scale_log2;
   __nv_bfloat16* o;
-  int4* record;  // [n_workers]: the cut unit that begins in the worker's range (request, unit, its partials or 0)
+  int4* record;  // [n_workers]: the cut unit that begins in the worker's range (request, unit, its partials or 0, queries)
   // partials of a row tile, slots [n_workers][2][row tiles of a unit]: [..][1] of the
   // unit that begins in the range, [..][0] of one that goes on there
   float2* ml;     // [slot][128]
@@ -120,15 +120,15 @@ struct TreeParams {
   uint64_t wait_limit_ns, test_stall_ns;
 };
 
-// A request: number, keys, queries (0: idle) and first drafted row (in a chain
-// the first query's).
+// A request: (place for where it begins in the list,) keys, queries (0: idle) and first
+// drafted row (in a chain the first query's).
 __device__ __forceinline__ int4 request(const TreeParams& p, int b, uint32_t& bits) {
   const int raw_L = p.kv_lens[b], L = min(max(raw_L, 0), p.max_kv_len);
   const int raw_q = p.q_lens != nullptr ? p.q_lens[b] : p.Tq, ql = min(max(raw_q, 0), min(p.Tq, L));
   const int raw_n = p.mask == nullptr || p.tree_lens == nullptr ? ql : p.tree_lens[b];
   const int n = p.mask == nullptr ? ql : min(max(raw_n, 0), min(32 * p.W, L));
   if (raw_L != L || raw_q != ql || raw_n != n) bits |= GQA_DEV_KVLEN_CLAMPED;
-  return make_int4(b, L, ql, L - n);
+  return make_int4(0, L, ql, L - n);
 }
 
 __device__ __forceinline__ int tiles_of(int L) { return (L + BN - 1) / BN; }
@@ -157,7 +157,7 @@ __device__ __forceinline__ bool next_segment(Walk* w, const TreeParams& p, const
   int k = w->k, u = w->next_u, at = w->at;
   bool found = false;
   int4 e = make_int4(0, 0, 0, 0);
-  int lo = 0, hi = 0, seg_u = 0;
+  int lo = 0, hi = 0, seg_u = 0, seg_k = 0;
 #pragma unroll 1
   while (left > 0 && k < p.B && !found) {
     e = ent[k];
@@ -170,6 +170,7 @@ __device__ __forceinline__ bool next_segment(Walk* w, const TreeParams& p, const
     lo = max(at - LEAD, 0);
     hi = max(at + take - LEAD, 0);
     seg_u = u;
+    seg_k = k;
     left -= take;
     at = 0;
     if (++u == p.units) u = 0, ++k;
@@ -182,7 +183,7 @@ __device__ __forceinline__ bool next_segment(Walk* w, const TreeParams& p, const
       w->k = k;
       w->next_u = u;
       w->at = at;
-      w->b = e.x;
+      w->b = seg_k;
       w->L = e.y;
       w->ql = e.z;
       w->t0 = e.w;
@@ -271,8 +272,6 @@ __global__ void __launch_bounds__(NTHR, 1)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  // where the ranges of this CTA's workers begin and end: request, unit, place in the unit
-  int4* const border_s = reinterpret_cast<int4*>(smem + OFF_BAR + C::OFF_START);  // [2][2]
   grid_dependency_wait();
 
   // ---- the list of tiles, and the ranges of this CTA's workers ----
@@ -312,27 +311,32 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll 1
     for (int b = first; b < last; ++b) {
       const int4 e = ent[b];
-      if (e.z == 0) continue;
-      const unsigned span = tiles_of(e.y) + LEAD, cost = unsigned(p.units) * span;
-#pragma unroll 1
-      for (int q = 0; q < (PAIR ? 2 : 4); ++q) {
-        const unsigned off = cut.start((q >> 1) * p.n_ctas + cta + (q & 1)) - base;
-        if (off < cost) border_s[q] = make_int4(b, off / span, off % span, 0);
-      }
-      base += cost;
+      ent[b].x = int(base);
+      if (e.z > 0) base += unsigned(p.units) * unsigned(tiles_of(e.y) + LEAD);
     }
     __syncthreads();
   }
   const uint32_t tmem = *tslot;
   Walk* const walk = &walks[warp];
-  // the slot whose worker this warp serves (softmax of slot warp / 4; the others in pairs)
-  const int slot = PAIR ? 0 : warp < 8 ? warp >> 2 : warp & 1;
-  const unsigned worker = slot * p.n_ctas + cta;
-  if (lane == 0) {
-    const int4 s = border_s[2 * slot];
-    *reinterpret_cast<int4*>(walk) =
-        make_int4(worker < cut.n ? int(cut.start(worker + 1) - cut.start(worker)) : 0, s.x, s.y, s.z);
+  // the worker that this warp serves (softmax of slot warp / 4; the others in pairs)
+  const unsigned worker = PAIR ? cta : (warp < 8 ? warp >> 2 : warp & 1) * p.n_ctas + cta;
+  // Where its range begins (lane 0) and ends (lane 1): request, unit and place in the unit.
+  int at_k = 0, at_unit = 0, at_place = 0;
+  if (lane < 2) {
+    const unsigned pos = cut.start(worker + lane);
+    int hi = p.B;  // the last request that begins at or before pos
+#pragma unroll 1
+    while (hi - at_k > 1) {
+      const int mid = (at_k + hi) >> 1;
+      if (unsigned(ent[mid].x) <= pos) at_k = mid; else hi = mid;
+    }
+    const unsigned span = tiles_of(ent[at_k].y) + LEAD, off = pos - unsigned(ent[at_k].x);
+    at_unit = off / span;
+    at_place = off - at_unit * span;
   }
+  if (lane == 0)
+    *reinterpret_cast<int4*>(walk) =
+        make_int4(worker < cut.n ? int(cut.start(worker + 1) - cut.start(worker)) : 0, at_k, at_unit, at_place);
   __syncwarp();
 
   if (warp >= 8) {
@@ -503,17 +507,15 @@ __global__ void __launch_bounds__(NTHR, 1)
     const uint32_t tO = tmem + TM_O + t * HD + lane_off;
     const uint32_t tP = tmem + TM_P + t * C::P_STRIDE + lane_off;
     const float c = p.qk_scale_log2;
-    if ((warp & 3) == 0 && lane == 0 && !(PAIR && t == 1)) {
+    if ((warp & 3) == 0 && lane == 1 && !(PAIR && t == 1)) {
       // The unit that the range ends in, where it begins there too (a tile of it at least
       // is this worker's and one another's): its partials are this worker's and those
       // of the workers up to the one with its last tile.
       int4 rec = make_int4(0, 0, 0, 0);
-      const unsigned s = cut.start(worker), end = cut.start(worker + 1);
-      if (worker + 1 < cut.n) {
-        const int4 x = border_s[2 * slot + 1], e = ent[x.x];
-        const unsigned begin = end - x.z;
-        if (x.z > LEAD && (begin >= s || s - begin <= LEAD))
-          rec = make_int4(e.x, x.y, int(cut.holder(begin + tiles_of(e.y) + LEAD - 1) - worker) + 1, 0);
+      const unsigned s = cut.start(worker), begin = cut.start(worker + 1) - at_place;
+      if (worker + 1 < cut.n && at_place > LEAD && (begin >= s || s - begin <= LEAD)) {
+        const int4 e = ent[at_k];
+        rec = make_int4(at_k, at_unit, int(cut.holder(begin + tiles_of(e.y) + LEAD - 1) - worker) + 1, e.z);
       }
       p.record[worker] = rec;
     }
@@ -744,15 +746,13 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
   __shared__ uint4 out_s[32 * 8];  // 32 rows of 128 bytes
   const int w = blockIdx.x, t = blockIdx.y >> 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = (blockIdx.y & 3) * 32 + lane, chunk = blockIdx.z * 16 + warp * 4;  // (of four columns)
-  grid_dependency_wait();
   grid_launch_dependents();
+  grid_dependency_wait();
   const int4 rec = __ldcg(&p.record[w]);
   const int n = rec.z;
   if (n == 0) return;
-  uint32_t bits = 0;
-  const int4 e = request(p, rec.x, bits);
   const int row = (part_of<TILES == 2>(rec.y, p) * TILES + t) * BM + r, g = head_of<TILES == 2>(rec.y, p), h = row / p.Tq, i = row % p.Tq;
-  const bool live = h < p.n_rep && i < e.z;
+  const bool live = h < p.n_rep && i < rec.w;
   if (!__any_sync(0xffffffffu, live)) return;  // (the same rows in every warp)
   float M = -INFINITY, den = 0.f, acc[4][4] = {};
   constexpr int AHEAD = 4;
