@@ -250,6 +250,17 @@ int check_layers(int n_layers, int num_blocks, int Hkv, int block_size, int D, i
     return GQA_ERR_INVALID_ARG;
   return GQA_OK;
 }
+// Whether one of the written arrays begins where another array of the call does.
+// (Where the pages' calls allow it, the pair is left out by the caller.)
+bool same_array(std::initializer_list<const void*> written, std::initializer_list<const void*> read) {
+  for (auto w = written.begin(); w != written.end(); ++w) {
+    for (auto x = written.begin(); x != w; ++x)
+      if (*w == *x) return true;
+    for (const void* r : read)
+      if (*w == r) return true;
+  }
+  return false;
+}
 int row_bytes(int D, int dtype) { return D * (dtype == GQA_F32 ? 4 : 2); }
 
 size_t decode_ws_size(int B, int Hq, int Hkv, int D, int max_kv_len, int tile, int ctas_per_sm = 2) {
@@ -890,6 +901,7 @@ GQA_ATTN_API int gqa_attn_compact_rows(const int32_t* path, const int32_t* n_kee
   }
   rc = check_ptrs({k_cache, v_cache}, dev, 16);
   if (rc != GQA_OK) return rc;
+  if (same_array({kv_lens_out, k_cache, v_cache}, {path, n_keep, tree_lens, kv_lens, block_table})) return GQA_ERR_INVALID_ARG;
   rc = check_status_workspace(workspace, ws_bytes, dev);
   if (rc != GQA_OK) return rc;
   CompactArgs a;
@@ -925,7 +937,10 @@ GQA_ATTN_API int gqa_attn_fork_tables(const int32_t* src, const int32_t* keep_le
   if (max_blocks < 1 || block_size < 1 || num_blocks < 1) return GQA_ERR_INVALID_ARG;
   if (long(std::max(B, B_in)) * max_blocks >= (1L << 30)) return GQA_ERR_INVALID_ARG;
   if (long(max_blocks) * block_size > kMax || long(num_blocks) * block_size > kMax) return GQA_ERR_INVALID_ARG;
-  if (block_table == block_table_out) return GQA_ERR_INVALID_ARG;
+  if (same_array({block_table_out, kv_lens_out, copy_src, copy_dst, copy_rows, shared_out, free_blocks_out, free_count_out},
+                 {src, keep_lens, held_lens, block_table}) ||
+      same_array({block_table_out, kv_lens_out, copy_src, copy_dst, copy_rows}, {shared, free_blocks, free_count}))
+    return GQA_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
   int rc = check_ptrs({src, held_lens, block_table, shared, free_blocks, free_count, block_table_out, kv_lens_out,
@@ -979,6 +994,7 @@ GQA_ATTN_API int gqa_attn_copy_blocks(const int32_t* src, const int32_t* dst, co
   }
   rc = check_ptrs({k_cache, v_cache}, dev, 16);
   if (rc != GQA_OK) return rc;
+  if (same_array({k_cache, v_cache}, {src, dst, rows})) return GQA_ERR_INVALID_ARG;
   rc = check_status_workspace(workspace, ws_bytes, dev);
   if (rc != GQA_OK) return rc;
   CopyBlocksArgs a;

@@ -171,14 +171,29 @@ def test_compact_is_checked_on_the_host(lib, bad):
     assert compact(lib, **bad) == INVALID
 
 
+FORK = ("src", "keep", "held", "table", "shared", "stack", "count", "out", "kv", "shared_out", "stack_out", "count_out",
+        "csrc", "cdst", "crows")
+AT = {name: ctypes.c_void_p(256 * (i + 2)) for i, name in enumerate(FORK)}
+REACHES_THE_DEVICE = (binding.GQA_ERR_CUDA, binding.GQA_ERR_NOT_DEVICE_PTR)  # (without one, and with these pointers)
+
+
 def fork(lib, **change):
-    a = dict(B_in=3, B=4, mb=5, bs=16, nb=20, table=P, out=ctypes.c_void_p(512)) | change
-    return lib.gqa_attn_fork_tables(P, P, P, a["table"], P, P, P, a["out"], P, P, P, P, P, P, P, a["B_in"], a["B"],
-                                    a["mb"], a["bs"], a["nb"], P, 256, None)
+    a = dict(B_in=3, B=4, mb=5, bs=16, nb=20) | AT | change
+    return lib.gqa_attn_fork_tables(*(a[x] for x in FORK), a["B_in"], a["B"], a["mb"], a["bs"], a["nb"], P, 256, None)
+
+
+def test_fork_arrays_that_may_not_be_one(lib):
+    for now, before in (("shared_out", "shared"), ("stack_out", "stack"), ("count_out", "count")):
+        assert fork(lib, **{now: AT[before]}) in REACHES_THE_DEVICE
+    assert fork(lib, keep=None) in REACHES_THE_DEVICE
+    for now, before in (("out", "table"), ("kv", "held"), ("kv", "keep"), ("kv", "src"), ("csrc", "src"), ("cdst", "csrc"),
+                        ("crows", "keep"), ("shared_out", "stack_out"), ("count_out", "kv"), ("out", "stack"), ("crows", "count"),
+                        ("stack_out", "table")):
+        assert fork(lib, **{now: AT[before]}) == INVALID
 
 
 @pytest.mark.parametrize("bad", [
-    dict(B=0), dict(B=8193), dict(B_in=0), dict(B_in=8193), dict(mb=0), dict(bs=0), dict(nb=0), dict(out=P),
+    dict(B=0), dict(B=8193), dict(B_in=0), dict(B_in=8193), dict(mb=0), dict(bs=0), dict(nb=0),
     dict(B=8192, mb=1 << 17, bs=1), dict(mb=1 << 20, bs=1 << 12), dict(nb=1 << 28),
 ])
 def test_fork_is_checked_on_the_host(lib, bad):
