@@ -17,7 +17,8 @@
 // any lengths balance, a long one is shared by many workers, and of many short ones
 // a worker takes several.  A unit inside one range is finished there.  One that is
 // cut leaves partials (max, sum, unnormalised O), at most two per worker, and
-// tree_merge_kernel joins them.
+// tree_merge_kernel joins them.  Few units get a cluster of CTAs each instead, which
+// joins its partials through distributed shared memory (cluster_size has the choice).
 //
 // A CTA (one an SM) has two slots, each with the softmax of a 128-row tile:
 //   PAIR    (more than 128 rows a unit) a worker is the CTA; both slots work on the
@@ -45,6 +46,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "attn_tile.cuh"
@@ -95,6 +97,7 @@ struct TrCfg {
   static constexpr int OFF_TSLOT = 8 * N_BARS, OFF_ABORT = OFF_TSLOT + 4, OFF_ISSUED = OFF_TSLOT + 8,
                        OFF_SUMS = OFF_TSLOT + 32;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+  static_assert(2 * BM * HD * 4 <= OFF_BAR - OFF_K && 2 * BM * 8 <= kMost * 16, "partials of a cluster's rows");
   static_assert(OFF_SUMS + 12 * 4 <= 512, "barrier area");
   static_assert(128 * REG_CTRL + 256 * REG_SOFTMAX <= NTHR * 168, "register split exceeds the launch allocation");
 };
@@ -109,6 +112,7 @@ struct TreeParams {
   int block_size, max_blocks, num_blocks;
   int np, units;  // units of a KV head (1 without PAIR), of a request
   int n_ctas, n_workers;
+  int cluster;  // CTAs of a unit (CLUSTERED)
   float qk_scale_log2;
   __nv_bfloat16* o;
   int4* record;  // [n_workers]: the cut unit that begins in the worker's range (request, unit, its partials or 0, queries)
@@ -196,6 +200,20 @@ __device__ __forceinline__ bool next_segment(Walk* w, const TreeParams& p, const
   return found;
 }
 
+// The next segment, or the only one.
+template <bool CLUSTERED, int LEAD>
+__device__ __forceinline__ bool segment(Walk* w, const TreeParams& p, const int4* ent) {
+  if constexpr (CLUSTERED) {
+    const bool found = w->left != 0;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) w->left = 0;
+    __syncwarp();
+    return found;
+  } else {
+    return next_segment<LEAD>(w, p, ent);
+  }
+}
+
 // The list cut into n ranges of `size` positions, the first `longer` of them one longer.
 struct Cut {
   unsigned n, size, longer;
@@ -227,7 +245,20 @@ __device__ __forceinline__ void tile_wait(uint64_t* bar, uint32_t parity, volati
   } while (!mbar_try_wait(bar, parity));
 }
 
-template <int HD, bool PAIR>
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t shared_of(const void* at, uint32_t rank) {  // the same place in another CTA
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+  return a;
+}
+
+// CLUSTERED: a cluster of p.cluster CTAs has one unit.  Its tiles are shared out
+// evenly, and the partials are joined through distributed shared memory, each CTA
+// a part of the rows: no list, no partials in memory, no second kernel.
+template <int HD, bool PAIR, bool CLUSTERED>
 __global__ void __launch_bounds__(NTHR, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const TreeParams p) {
@@ -276,8 +307,8 @@ __global__ void __launch_bounds__(NTHR, 1)
 
   // ---- the list of tiles, and the ranges of this CTA's workers ----
   constexpr int LEAD = kLead<PAIR>;
-  Cut cut;
-  {
+  Cut cut = {};
+  if constexpr (!CLUSTERED) {
     unsigned* sum_s = reinterpret_cast<unsigned*>(smem + OFF_BAR + C::OFF_SUMS);  // [12]
     const int per = (p.B + NTHR - 1) / NTHR, first = tid * per, last = min(first + per, p.B);
     uint32_t bits = 0;
@@ -316,28 +347,56 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
     __syncthreads();
   }
+  if constexpr (CLUSTERED) {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
   const uint32_t tmem = *tslot;
   Walk* const walk = &walks[warp];
-  // the worker that this warp serves (softmax of slot warp / 4; the others in pairs)
-  const unsigned worker = PAIR ? cta : (warp < 8 ? warp >> 2 : warp & 1) * p.n_ctas + cta;
-  // Where its range begins (lane 0) and ends (lane 1): request, unit and place in the unit.
+  // the worker that this warp serves (softmax of slot warp / 4; the others in pairs),
+  // in the list or among those of the unit
+  const unsigned in_slot = PAIR ? 0 : warp < 8 ? warp >> 2 : warp & 1;
+  const unsigned rank = CLUSTERED ? cta % p.cluster : 0;
+  const unsigned worker = CLUSTERED ? in_slot * p.cluster + rank : in_slot * p.n_ctas + cta;
   int at_k = 0, at_unit = 0, at_place = 0;
-  if (lane < 2) {
-    const unsigned pos = cut.start(worker + lane);
-    int hi = p.B;  // the last request that begins at or before pos
-#pragma unroll 1
-    while (hi - at_k > 1) {
-      const int mid = (at_k + hi) >> 1;
-      if (unsigned(ent[mid].x) <= pos) at_k = mid; else hi = mid;
+  if constexpr (CLUSTERED) {
+    if (lane == 0) {
+      const int unit = cta / p.cluster, b = unit / p.units, n = (PAIR ? 1 : 2) * p.cluster;
+      uint32_t bits = 0;
+      const int4 e = request(p, b, bits);
+      if (tid == 0 && rank == 0 && bits != 0) atomicOr(p.status, bits);
+      const unsigned tiles = e.z > 0 ? tiles_of(e.y) : 0;
+      walk->b = b;
+      walk->u = unit - b * p.units;
+      walk->L = e.y;
+      walk->ql = e.z;
+      walk->t0 = e.w;
+      walk->lo = int(tiles * worker / n);
+      walk->hi = int(tiles * (worker + 1) / n);
+      walk->left = walk->hi > walk->lo;
     }
-    const unsigned span = tiles_of(ent[at_k].y) + LEAD, off = pos - unsigned(ent[at_k].x);
-    at_unit = off / span;
-    at_place = off - at_unit * span;
+    __syncwarp();
+  } else {
+    // Where its range begins (lane 0) and ends (lane 1): request, unit and place in the unit.
+    if (lane < 2) {
+      const unsigned pos = cut.start(worker + lane);
+      int hi = p.B;  // the last request that begins at or before pos
+#pragma unroll 1
+      while (hi - at_k > 1) {
+        const int mid = (at_k + hi) >> 1;
+        if (unsigned(ent[mid].x) <= pos) at_k = mid; else hi = mid;
+      }
+      const unsigned span = tiles_of(ent[at_k].y) + LEAD, off = pos - unsigned(ent[at_k].x);
+      at_unit = off / span;
+      at_place = off - at_unit * span;
+    }
+    if (lane == 0)
+      *reinterpret_cast<int4*>(walk) =
+          make_int4(worker < cut.n ? int(cut.start(worker + 1) - cut.start(worker)) : 0, at_k, at_unit, at_place);
+    __syncwarp();
   }
-  if (lane == 0)
-    *reinterpret_cast<int4*>(walk) =
-        make_int4(worker < cut.n ? int(cut.start(worker + 1) - cut.start(worker)) : 0, at_k, at_unit, at_place);
-  __syncwarp();
+  float m_ref = -INFINITY, lsum = 0.f;  // of a softmax thread's row
 
   if (warp >= 8) {
     set_max_regs_dec<C::REG_CTRL>();
@@ -350,7 +409,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       // (rows that other units of the request read too stay in L2)
       const uint64_t policy = p.np == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
 #pragma unroll 1
-      while (next_segment<kLead<PAIR>>(walk, p, ent)) {
+      while (segment<CLUSTERED, kLead<PAIR>>(walk, p, ent)) {
         const int L = walk->L, b = walk->b, g = head_of<PAIR>(walk->u, p), part = part_of<PAIR>(walk->u, p), lo = walk->lo,
                   hi = walk->hi;
         if (lane == 0 && !*abort_flag) {
@@ -459,7 +518,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         mma_commit_warp(&bars[B_VE + st]);
       };
 #pragma unroll 1
-      while (next_segment<kLead<PAIR>>(walk, p, ent)) {
+      while (segment<CLUSTERED, kLead<PAIR>>(walk, p, ent)) {
         const int L = walk->L, lo = walk->lo, hi = walk->hi;
 #pragma unroll 1
         for (int s = PAIR ? 0 : t; scores && s < (PAIR ? 2 : t + 1); ++s)
@@ -507,7 +566,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     const uint32_t tO = tmem + TM_O + t * HD + lane_off;
     const uint32_t tP = tmem + TM_P + t * C::P_STRIDE + lane_off;
     const float c = p.qk_scale_log2;
-    if ((warp & 3) == 0 && lane == 1 && !(PAIR && t == 1)) {
+    if (!CLUSTERED && (warp & 3) == 0 && lane == 1 && !(PAIR && t == 1)) {
       // The unit that the range ends in, where it begins there too (a tile of it at least
       // is this worker's and one another's): its partials are this worker's and those
       // of the workers up to the one with its last tile.
@@ -521,7 +580,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
     int n = 0;
 #pragma unroll 1
-    while (next_segment<kLead<PAIR>>(walk, p, ent)) {
+    while (segment<CLUSTERED, kLead<PAIR>>(walk, p, ent)) {
       const int n_it = walk->hi - walk->lo;
       const int masked_from = walk->t0 / BN - walk->lo;  // tiles with drafted rows, or past the keys
       // (rows past the last one are nobody's: a warp that has only such leaves P as it is)
@@ -532,7 +591,8 @@ __global__ void __launch_bounds__(NTHR, 1)
         asm volatile("prefetch.global.L1 [%0];" ::"l"(words));
       }
       const bool warp_live = ((PAIR ? 2 * part_of<PAIR>(walk->u, p) + t : 0) * 4 + (warp & 3)) * 32 < p.n_rep * p.Tq;
-      float m_ref = -INFINITY, lsum = 0.f;
+      m_ref = -INFINITY;
+      lsum = 0.f;
       if (PAIR && t == 1) named_bar_arrive(BAR_TURN_A, 256);  // (slot 0 begins)
 #pragma unroll 1
       for (int j = 0; j < n_it; ++j, ++n) {
@@ -650,7 +710,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       tc_fence_after();
 
       // ---- the segment's rows: finished, or partials ----
-      if (warp_live) {
+      if (!CLUSTERED && warp_live) {
         const int part = part_of<PAIR>(walk->u, p), g = head_of<PAIR>(walk->u, p), r = tid & (BM - 1);
         const int row = (PAIR ? 2 * part + t : part) * BM + r, h = row / p.Tq, i = row % p.Tq;
         const bool live = h < p.n_rep && i < walk->ql && !*abort_flag;
@@ -731,6 +791,70 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (tid == 0) atomicOr(p.status, GQA_DEV_WAIT_TIMEOUT);
     tc_fence_before();
     __syncthreads();
+  }
+  if constexpr (CLUSTERED) {
+    // Row R of the unit is joined by CTA R / share.  There, over the stages of K and V:
+    // O as [worker][D / 4][share][4], and (m, l) as [worker][share] where the list would be.
+    // (The cluster's size divides 128, so workers * share <= 256 rows of D floats.)
+    const int n = (PAIR ? 1 : 2) * p.cluster, part = part_of<PAIR>(walk->u, p), g = head_of<PAIR>(walk->u, p);
+    const int rows = min(PAIR ? 2 * BM : BM, p.n_rep * p.Tq - part * 2 * BM), share = (rows + p.cluster - 1) / p.cluster;
+    cluster_barrier();  // every CTA is done with its stages
+    if (warp < 8) {
+      const int R = (PAIR ? (warp >> 2) * BM : 0) + (tid & (BM - 1)), to = R / share, at = R - to * share;
+      const bool any = walk->hi > walk->lo && !*abort_flag, live = R < rows;
+      const uint32_t tO = tmem + TM_O + (warp >> 2) * HD + (uint32_t((warp & 3) * 32) << 16);
+      if (live) {
+        const uint32_t dst = shared_of(ent, to) + (worker * share + at) * 8;
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(any ? m_ref : -INFINITY),
+                     "f"(any ? lsum : 0.f)
+                     : "memory");
+      }
+      if (any && __any_sync(0xffffffffu, live)) {
+        const uint32_t dst = live ? shared_of(smem + OFF_K, to) + (worker * (HD / 4) * share + at) * 16 : 0u;
+#pragma unroll 1
+        for (int cc = 0; cc < HD / 32; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(tO + cc * 32, o);
+          tmem_wait_ld();
+          if (live)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (cc * 8 + e) * share * 16),
+                           "r"(o[4 * e]), "r"(o[4 * e + 1]), "r"(o[4 * e + 2]), "r"(o[4 * e + 3])
+                           : "memory");
+        }
+      }
+    }
+    cluster_barrier();
+    const float2* const ml = reinterpret_cast<const float2*>(ent);
+    const float4* const part_o = reinterpret_cast<const float4*>(smem + OFF_K);
+    const int mine = min(share, rows - int(rank) * share);
+    for (int x = tid; x < mine * (HD / 4); x += NTHR) {
+      const int chunk = x / mine, at = x - chunk * mine;
+      const int row = part * 2 * BM + int(rank) * share + at, h = row / p.Tq, i = row - h * p.Tq;
+      if (i >= walk->ql) continue;
+      float M = -INFINITY;
+      for (int v = 0; v < n; ++v) M = fmaxf(M, ml[v * share + at].x);
+      float den = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int v = 0; v < n; ++v) {
+        const float2 s = ml[v * share + at];
+        if (s.x == -INFINITY) continue;  // (no O was sent, or zeros)
+        const float w = fast_exp2(s.x - M);
+        const float4 o = part_o[(v * (HD / 4) + chunk) * share + at];
+        den = fmaf(s.y, w, den);
+        acc.x = fmaf(o.x, w, acc.x);
+        acc.y = fmaf(o.y, w, acc.y);
+        acc.z = fmaf(o.z, w, acc.z);
+        acc.w = fmaf(o.w, w, acc.w);
+      }
+      if (den == 0.f) atomicOr(p.status, GQA_DEV_EMPTY_REQUEST);
+      const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                           hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(p.o + ((size_t(walk->b) * p.Hq + g * p.n_rep + h) * p.Tq + i) * HD + chunk * 4) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
   }
   if (warp == 9) tmem_dealloc(tmem, TMEM_COLS);
 }
@@ -822,6 +946,27 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
 
 // ---- plan ----------------------------------------------------------------------
 
+// CTAs in the cluster of a unit, or 0: the list.  Estimated times in us: what comes
+// before and behind the tiles (with the list a tenth for each partial of a unit), and
+// the tiles of the longest request by its cluster or (three quarters of) all by all SMs,
+// where a tile takes its exponentials and products or its share of HBM.  Measured, list and clusters of 2, 4, 8 (D = 128, rows x units x keys
+// of each, *: a pair of row tiles): 64 x 8 x 2,048 14.0, 16.6, 12.9, 10.9; 64 x 32 x
+// 4,096 22.3, 23.8, 19.1, 38.2 (not one wave); 128 x 8 x 32,768 40.8, 130, 70.9,
+// 42.8; 182* x 32 x 4,097 29.3, 40.7, 28.5, 63.1; 427* x 16 x 16,385 61.0, 110, 64.6, 116.
+// `fits`: clusters of 2, 4 and 8 that run at once.
+int cluster_size(bool pair, int D, int B, long units, long tiles, int sms, const int (&fits)[3]) {
+  const double tile = D / 128.0 * (pair ? 1.65 : 1.0), hbm = D / 128.0 * 1.53;
+  const double partials = std::min(double(tiles), double(pair ? sms : 2 * sms) / double(units));
+  double best = (pair ? 18.0 : 11.5) + 0.1 * partials + (B > 1 ? 0.75 : 1.0) * double(units) * tiles / sms * std::max(tile, hbm);
+  int size = 0;
+  for (int i = 0, c = 2; i < 3; ++i, c *= 2) {
+    if (units > fits[i] || c > std::max(2L, 2 * tiles)) continue;
+    const double t = (pair ? 13.0 : 8.7) + double((tiles + c - 1) / c) * std::max(tile, hbm * double(units) * c / sms);
+    if (t < best) best = t, size = c;
+  }
+  return size;
+}
+
 struct TreePlan {
   bool pair;
   int np, n_ctas, n_workers;
@@ -842,6 +987,40 @@ TreePlan tree_plan(int B, int Hq, int Hkv, int D, int Tq, int max_kv_len) {
   q.off_o = align256(q.off_ml + sizeof(float2) * slots);
   q.total = q.off_o + sizeof(float) * slots * D;
   return q;
+}
+
+// How many clusters of 2, 4 and 8 CTAs the current device runs at once (asked once a
+// device and kernel; a device that cannot say has none).
+template <typename Kern>
+void clusters_at_once(Kern kern, size_t smem, int (&fits)[3]) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> kept[kDevices][3];  // the answer + 1; 0: not asked yet
+  int dev = 0;
+  const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices;
+  for (int i = 0; i < 3; ++i) {
+    const int have = known ? kept[dev][i].load(std::memory_order_relaxed) : 0;
+    if (have > 0) {
+      fits[i] = have - 1;
+      continue;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2u << i;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2u << i);
+    cfg.blockDim = dim3(NTHR);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    fits[i] = n;
+    if (known) kept[dev][i].store(n + 1, std::memory_order_relaxed);
+  }
 }
 
 template <int HD, bool PAIR>
@@ -886,11 +1065,23 @@ cudaError_t launch_tree_as(const TreeArgs& a, cudaStream_t stream) {
   p.test_stall_ns = wait_test_ns();
   static DeviceOnce once;
   cudaError_t e = once.run([&] {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(tree_kernel<HD, PAIR>),
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    cudaError_t r = cudaSuccess;
+    for (const void* k : {reinterpret_cast<const void*>(tree_kernel<HD, PAIR, false>),
+                          reinterpret_cast<const void*>(tree_kernel<HD, PAIR, true>)})
+      if (r == cudaSuccess) r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    return r;
   });
   if (e != cudaSuccess) return e;
-  e = launch_pdl(tree_kernel<HD, PAIR>, dim3(plan.n_ctas), dim3(NTHR), C::SMEM_BYTES, stream, tq, tk, tv, p);
+  const long units = long(a.B) * p.units, tiles = (long(a.max_kv_len) + BN - 1) / BN;
+  int fits[3];
+  clusters_at_once(tree_kernel<HD, PAIR, true>, C::SMEM_BYTES, fits);
+  p.cluster = cluster_size(PAIR, HD, a.B, units, tiles, std::max(1, device_sm_count()), fits);
+  // (a power of two: what the CTAs of a cluster send each other then fits the stages)
+  if (const int c = prefill_kv_split_override(); c > 0) p.cluster = c >= 8 ? 8 : c >= 4 ? 4 : c >= 2 ? 2 : 0;
+  if (p.cluster > 0)
+    return launch_pdl_cluster(tree_kernel<HD, PAIR, true>, unsigned(p.cluster), dim3(unsigned(units * p.cluster)), dim3(NTHR),
+                              C::SMEM_BYTES, stream, tq, tk, tv, p);
+  e = launch_pdl(tree_kernel<HD, PAIR, false>, dim3(plan.n_ctas), dim3(NTHR), C::SMEM_BYTES, stream, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
   if (a.max_kv_len <= BN) return cudaSuccess;  // (no unit has a second tile: none is cut)
   constexpr int TILES = PAIR ? 2 : 1;

@@ -654,7 +654,9 @@ GQA_ATTN_API int gqa_attn_quantize_q4(const void* src, int64_t src_head_rows, ui
  * splits instead of the planner's count (a split still holds at least one
  * tile, and there are at most 1024).  prefill_kv_split in [1, 8] forces the
  * size of the thread-block cluster that shares one query-tile pair's keys in
- * prefill (1 = no split).  0 restores the planner's choice for either.  The
+ * prefill (1 = no split), and of the one that shares the keys of a unit of
+ * gqa_attn_decode_tree (1 = the list of all units, cut evenly; else rounded down
+ * to a power of two).  0 restores the planner's choice for either.  The
  * setting is process-wide and starts at 0; nothing else (no environment
  * variable) changes a plan.  Change it only while no other thread is calling
  * the library, and size workspaces after changing it.

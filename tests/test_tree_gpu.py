@@ -119,10 +119,14 @@ class Case:
         return o, binding.gqa_attn_read_device_status(ws)
 
     def check(self, bs=None):
+        """As planned, as one list over all SMs, and in clusters of two and of eight a unit."""
         ref, status = self.oracle()
-        o, seen = self.dense()
-        parity.check(f64(o), ref, "bf16", "dense")
-        assert seen == status
+        units = self.B * self.Hkv * -(-self.q.shape[1] // self.Hkv * self.q.shape[2] // 256)
+        for split in (0, 1, 2, 8) if units <= 600 else (0, 1):
+            with binding.plan_override(prefill_kv_split=split):
+                o, seen = self.dense()
+            parity.check(f64(o), ref, "bf16", f"dense, {split}")
+            assert seen == status
         if bs is not None:
             o, seen = self.paged(bs)
             parity.check(f64(o), ref, "bf16", "paged")
