@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(WARPS * 32) copy_blocks_kernel(const CopyBlock
 
 // ---- tables of requests that fork, shorten or end ---------------------------------
 
-constexpr int NT = 1024, NWARP = NT / 32;
+constexpr int NT = 512, NWARP = NT / 32;
 constexpr int kMostRequests = 8192;  // 16 bytes of shared memory for each old one, 12 for each new one
 
 // Sum over the block's threads before this one, and over all.  (part: 32 ints,
@@ -289,7 +289,7 @@ __device__ __forceinline__ int block_exclusive(int v, int* part, int& total) {
   }
   if (lane == 31) part[warp] = s;
   __syncthreads();
-  int w = part[lane];
+  int w = lane < NWARP ? part[lane] : 0;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, w, d);
@@ -299,28 +299,38 @@ __device__ __forceinline__ int block_exclusive(int v, int* part, int& total) {
   const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
   return s - v + (warp > 0 ? before : 0);
 }
-static_assert(NWARP == 32, "block_exclusive reads one warp's sum per lane");
+static_assert(NWARP <= 32, "block_exclusive reads one warp's sum per lane");
 
 // What new request b asks for.
 struct Fork {
   int src, keep;  // src < 0: none
 };
 
-// Requests, old and new, from which on a cluster of eight blocks does the work (of up
-// to 128 blocks each: 16 in one block 11.5 us, in a cluster 14.7; 64 15.7, 19.0; 128 19.7
-// either way; 600 of up to 16 28.2, 14.0).
-constexpr int kClusterRequests = 128;
-constexpr unsigned kCluster = 8;
+// Entries of a table that a lane has at once (256 requests of 128 blocks with 2, 4, 8:
+// 15.4, 13.8, 15.3 us: of 8 more than half are past the end of a table of this length,
+// and cost their instructions all the same).
+constexpr int kPer = 4;
+
+// One block does the work where every request has a warp there and the tables are
+// short: this many times kPer * 32 entries, of all requests.  Past that it is a cluster
+// of 16, whose barriers cost 1.5 us (8 requests of 128 blocks in one block 6.6 us, in a
+// cluster 8.1; 16 of 128 7.6, 8.8; 24 of 128 11.1, 8.8; 256 of 128 66, 11.3; 8 of 3,750 51,
+// 12.6; a cluster of 8 with 256 of 128 15.7).
+constexpr int kOneBlock = 48;
+constexpr unsigned kCluster = 16;
+constexpr int kForkSmem = kMostRequests * 28 + int(kCluster) * NWARP * 4;
 
 // First the owner of every old request, then what each new one keeps and which need a
 // block: every block works all of that out for itself, in shared memory.  Then
-// tables and holders, a warp a request, over all blocks; and at last the blocks
-// without a holder, each of which is put on the stack by the first entry, in the
-// order of the old tables, that gave it back.
+// tables and holders, over all blocks, a warp a request or as many warps as there are
+// for each; and at last the blocks without a holder, each of which is put on the stack
+// by the first entry, in the order of the old tables, that gave it back.
 //
 // Whole numbers on a few hundred kilobytes at most, so the time is a chain of eight
-// dependent round trips and of barriers.
-template <bool CLUSTER>
+// dependent round trips, of barriers, and of instructions: loops whose body is rarely
+// entered twice are not unrolled (60 KB of code became 32, and 16.4 us of 256 requests 13.3), and 512
+// threads do with the few requests of a block what 1,024 did (9.0 us became 6.6).
+template <int CLUSTER>
 __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
   extern __shared__ unsigned long long best[];          // [B_in]: (rows kept + 1, ~b) of the owner
   int* const kept = reinterpret_cast<int*>(best + p.B_in);  // [B_in]: blocks that the owner stays in
@@ -328,13 +338,13 @@ __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
   Fork* const fork_s = reinterpret_cast<Fork*>(held + p.B_in);  // [B]
   int* const stack_s = reinterpret_cast<int*>(fork_s + p.B);    // [B]: the top of the stack, from the end
   __shared__ int part[NWARP];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, back = NT - 1 - tid;
   unsigned rank = 0;
-  if (CLUSTER) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  const int cap = p.max_blocks * p.block_size, n_thr = CLUSTER ? int(kCluster) * NT : NT;
+  if (CLUSTER > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int cap = p.max_blocks * p.block_size, n_thr = CLUSTER * NT;
   uint32_t bits = 0;
   auto barrier = [&] {  // of all threads; what they wrote and added before is seen after it
-    if (CLUSTER) {
+    if (CLUSTER > 1) {
       asm volatile("barrier.cluster.arrive.release;" ::: "memory");
       asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     } else {
@@ -349,6 +359,7 @@ __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
 
   // ---- what is asked for ----
   const int raw_count = *p.free_count, count = min(max(raw_count, 0), p.num_blocks);
+#pragma unroll 1
   for (int s = tid; s < p.B_in; s += NT) {
     const int raw = p.held_lens[s], n = min(max(raw, 0), cap);
     if (raw != n) bits |= GQA_DEV_KVLEN_CLAMPED;
@@ -356,6 +367,7 @@ __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
     best[s] = 0;
     kept[s] = 0;
   }
+#pragma unroll 1
   for (int b = tid; b < p.B; b += NT) {
     Fork f{p.src[b], p.keep_lens != nullptr ? p.keep_lens[b] : -1};
     if (f.src >= p.B_in) {
@@ -365,32 +377,10 @@ __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
     fork_s[b] = f;
   }
   if (raw_count != count) bits |= GQA_DEV_BAD_BLOCK;
-  for (int i = tid; i < min(p.B, count); i += NT) stack_s[i] = p.free_blocks[count - 1 - i];
-  // (what is not changed in place is copied meanwhile)
-  auto copy = [&](const int32_t* from, int32_t* to) {
-    if (from == to) return;
-    int i = int(rank) * NT + tid;
-    if (((reinterpret_cast<uintptr_t>(from) | reinterpret_cast<uintptr_t>(to)) & 15) == 0) {
-      const int n4 = p.num_blocks / 4;
-#pragma unroll 2
-      for (int q = i; q < n4; q += n_thr) reinterpret_cast<int4*>(to)[q] = reinterpret_cast<const int4*>(from)[q];
-      i += 4 * n4;
-    }
-    for (; i < p.num_blocks; i += 4 * n_thr) {
-      int v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i + k * n_thr < p.num_blocks) v[k] = from[i + k * n_thr];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i + k * n_thr < p.num_blocks) to[i + k * n_thr] = v[k];
-    }
-  };
-  copy(p.shared, p.shared_out);
-  copy(p.free_blocks, p.free_out);
   __syncthreads();
 
   // ---- owners ----
+#pragma unroll 1
   for (int b = tid; b < p.B; b += NT) {
     Fork f = fork_s[b];
     if (f.src >= 0) {
@@ -406,14 +396,65 @@ __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
   __syncthreads();
 
   // ---- what each new request keeps, and the blocks taken ----
-  const int gw = int(rank) * NWARP + warp, n_warps = n_thr / 32;
-  // (the tables that this warp reads next are asked for meanwhile)
-  auto ask = [&](int s, int n) {
-    if (lane * 32 < n) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.table + size_t(s) * p.max_blocks + lane * 32));
+  // The warps that see to a request's entries, a run of them each: a power of two, as
+  // many as there are for the larger number of requests.
+  const int n_warps = CLUSTER * NWARP, most = max(p.B, p.B_in);
+  const int log_parts = most < n_warps ? 31 - __clz(n_warps / most) : 0, parts = 1 << log_parts;
+  const int gw = int(rank) * NWARP + warp, mine_0 = gw >> log_parts, part_no = gw & (parts - 1), n_mine = n_warps >> log_parts;
+  auto run = [&](int n) { return ((n + parts - 1 >> log_parts) + 31) & ~31; };  // entries of each, of n
+  // Entries j0 + 32 k + lane of an old table up to `end` (-1 past it), so that one
+  // round trip brings them all.
+  auto entries = [&](int s, int j0, int end, int (&id)[kPer]) {
+    const int32_t* const from = p.table + size_t(s) * p.max_blocks;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int j = j0 + 32 * k + lane;
+      id[k] = j < end ? from[j] : -1;
+    }
   };
-  if (gw < p.B && fork_s[gw].src >= 0) ask(fork_s[gw].src, fork_s[gw].keep / p.block_size);
-  if (gw < p.B_in) ask(gw, blocks_of(held[gw]));
+  // The first ones of the first new and old request that this warp has: the new one's
+  // whole blocks, and all that the old one holds.
+  int new_ids[kPer], old_ids[kPer];
+  {
+    const Fork f = mine_0 < p.B ? fork_s[mine_0] : Fork{-1, 0};
+    const int whole = f.src >= 0 ? f.keep / p.block_size : 0, r = run(whole);
+    entries(max(f.src, 0), part_no * r, min(whole, part_no * r + r), new_ids);
+    const int have = mine_0 < p.B_in ? blocks_of(held[mine_0]) : 0, r_old = run(have);
+    entries(min(mine_0, p.B_in - 1), part_no * r_old, min(have, part_no * r_old + r_old), old_ids);
+  }
+  // What is not changed in place is copied, and the top of the stack looked at, by the
+  // threads from the last one on, while the first ones see to the requests.  One round
+  // trip: the loads go out before anything is written.
+  {
+    const int n_top = min(p.B, count);
+    auto top_at = [&](int i) { return p.free_blocks[count - 1 - i]; };
+    const int top0 = back < n_top ? top_at(back) : 0;
+    const bool c0 = p.shared != p.shared_out, c1 = p.free_blocks != p.free_out;
+    auto copy = [&](auto unit, int first, int end) {
+      using U = decltype(unit);
+#pragma unroll 1
+      for (int q = first; q < end; q += n_thr) {
+        U a{}, b{};
+        if (c0) a = reinterpret_cast<const U*>(p.shared)[q];
+        if (c1) b = reinterpret_cast<const U*>(p.free_blocks)[q];
+        if (c0) reinterpret_cast<U*>(p.shared_out)[q] = a;
+        if (c1) reinterpret_cast<U*>(p.free_out)[q] = b;
+      }
+    };
+    const int first = int(rank) * NT + back;
+    int done = 0;
+    if (((reinterpret_cast<uintptr_t>(p.shared) | reinterpret_cast<uintptr_t>(p.shared_out) |
+          reinterpret_cast<uintptr_t>(p.free_blocks) | reinterpret_cast<uintptr_t>(p.free_out)) & 15) == 0) {
+      copy(int4{}, first, p.num_blocks / 4);
+      done = p.num_blocks & ~3;
+    }
+    copy(int{}, done + first, p.num_blocks);
+    if (back < n_top) stack_s[back] = top0;
+#pragma unroll 1
+    for (int i = back + NT; i < n_top; i += NT) stack_s[i] = top_at(i);
+  }
   int taken = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     const int b = b0 + tid;
     Fork f{-1, 0};
@@ -451,129 +492,128 @@ __global__ void __launch_bounds__(NT, 1) fork_kernel(const ForkArgs p) {
   barrier();
 
   // ---- whole blocks into the tables; holders ----
-  // Entries j0 + 32 k + lane of an old table up to `end` (-1 past it): 256 at once,
-  // so that one round trip brings them.
-  auto entries = [&](int s, int j0, int end, int (&id)[8]) {
-    const int32_t* const from = p.table + size_t(s) * p.max_blocks;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int j = j0 + 32 * k + lane;
-      id[k] = j < end ? from[j] : -1;
-      if (j < end && !valid(id[k])) bits |= GQA_DEV_BAD_BLOCK;
-    }
-  };
-  for (int b = gw; b < p.B; b += n_warps) {
+#pragma unroll 1
+  for (int b = mine_0; b < p.B; b += n_mine) {
     const Fork f = fork_s[b];
     if (f.src < 0) continue;
     const bool owner = best[f.src] == key(f, b);
-    const int whole = f.keep / p.block_size;
+    const int whole = f.keep / p.block_size, r = run(whole), lo = part_no * r, hi = min(whole, lo + r);
     int32_t* const to = p.table_out + size_t(b) * p.max_blocks;
-    for (int j0 = 0; j0 < whole; j0 += 256) {
-      int id[8];
-      entries(f.src, j0, whole, id);
+#pragma unroll 1
+    for (int j0 = lo; j0 < hi; j0 += 32 * kPer) {
+      if (b != mine_0 || j0 > lo) entries(f.src, j0, hi, new_ids);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < kPer; ++k) {
         const int j = j0 + 32 * k + lane;
-        if (j < whole) to[j] = id[k];
-        if (!owner && valid(id[k])) atomicAdd(&p.shared_out[id[k]], 1);
+        if (j >= hi) continue;
+        to[j] = new_ids[k];
+        if (!valid(new_ids[k])) bits |= GQA_DEV_BAD_BLOCK;
+        else if (!owner) atomicAdd(&p.shared_out[new_ids[k]], 1);
       }
     }
   }
-  bool gives = false;
-  for (int s = gw; s < p.B_in; s += n_warps) {
-    const int have = blocks_of(held[s]);
-    for (int j0 = kept[s]; j0 < have; j0 += 256) {
-      int id[8];
-      entries(s, j0, have, id);
-      gives = true;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (valid(id[k])) atomicSub(&p.shared_out[id[k]], 1);
-    }
-  }
-  gives = __any_sync(0xffffffffu, gives);
-  barrier();
-
-  // ---- blocks that nobody holds: the first entry that gave one back claims it ----
-  constexpr int kClaim = INT32_MIN;  // + the entry's number (below 2^30)
-  if (gives)
-    for (int s = gw; s < p.B_in; s += n_warps) {
-      const int have = blocks_of(held[s]);
-      for (int j0 = kept[s]; j0 < have; j0 += 256) {
-        int id[8];
-        unsigned none = 0;
-        entries(s, j0, have, id);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) none |= unsigned(valid(id[k]) && __ldcg(&p.shared_out[id[k]]) < 0) << k;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (none >> k & 1u) atomicMin(&p.shared_out[id[k]], kClaim + s * p.max_blocks + j0 + 32 * k + lane);
-      }
-    }
-  barrier();
-  // Which of these put a block on the stack (bit k).
-  auto winners = [&](int s, int j0, int have, int (&id)[8]) {
-    unsigned mine = 0;
-    entries(s, j0, have, id);
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      mine |= unsigned(valid(id[k]) && __ldcg(&p.shared_out[id[k]]) == kClaim + s * p.max_blocks + j0 + 32 * k + lane) << k;
-    return mine;
-  };
-  // Blocks that each old request puts on the stack, told to every block of the cluster
-  // (best is not needed any more).
-  int* const won = reinterpret_cast<int*>(best);
-  for (int s = gw; s < p.B_in; s += n_warps) {
-    int n = 0;
-    if (gives) {
-      const int have = blocks_of(held[s]);
-      for (int j0 = kept[s]; j0 < have; j0 += 256) {
-        int id[8];
-        n += __popc(winners(s, j0, have, id));
-      }
-      n = __reduce_add_sync(0xffffffffu, n);
-    }
-    if (!CLUSTER) {
-      if (lane == 0) won[s] = n;
-    } else if (lane < int(kCluster)) {
-      asm volatile(
-          "{\n\t.reg .b32 a;\n\t"
-          "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-          "st.shared::cluster.u32 [a], %2;\n\t}" ::"r"(smem_u32(won) + 4 * s),
-          "r"(lane), "r"(n)
-          : "memory");
-    }
-  }
-  barrier();
+  // What the old requests give back, in four steps over the same entries: a holder less
+  // for each; blocks that nobody holds now, claimed by the first entry that gave one
+  // back; how many of them each old request gave; and they, in its order, onto the
+  // stack.
+  constexpr int kClaim = INT32_MIN;               // + the entry's number (below 2^30)
+  // [B_in][parts] (n_warps at most where there are parts; best is not needed any more)
+  int* const won = parts > 1 ? stack_s + p.B : reinterpret_cast<int*>(best);
   int top = count - taken;
-  for (int s0 = 0; s0 < p.B_in; s0 += NT) {
-    const int s = s0 + tid;
-    int total;
-    const int before = block_exclusive(s < p.B_in ? won[s] : 0, part, total);
-    if (s < p.B_in) won[s] = top + before;
-    top += total;
-    __syncthreads();
-  }
-  if (gives)
-    for (int s = gw; s < p.B_in; s += n_warps) {
-      const int have = blocks_of(held[s]);
-      int at = won[s];
-      for (int j0 = kept[s]; j0 < have; j0 += 256) {
-        int id[8];
-        const unsigned mine = winners(s, j0, have, id);
+  bool gives = false;
+  unsigned first_winners = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const unsigned all = __ballot_sync(0xffffffffu, mine >> k & 1u);
-          if (mine >> k & 1u) {
-            const long to = long(at) + __popc(all & ((1u << lane) - 1u));
-            if (to < p.num_blocks) p.free_out[to] = id[k];
-            else bits |= GQA_DEV_BAD_BLOCK;
-            p.shared_out[id[k]] = 0;
+  for (int step = 0; step < 4; ++step) {
+#pragma unroll 1
+    for (int s = mine_0; s < p.B_in && (step == 0 || gives || step == 2); s += n_mine) {
+      const int have = blocks_of(held[s]), from = kept[s], r = run(have), lo = part_no * r, hi = min(have, lo + r);
+      const int unit = s * parts + part_no;
+      int n_won = 0, at = step == 3 ? won[unit] : 0;
+#pragma unroll 1
+      for (int j0 = lo + (max(from - lo, 0) & ~(32 * kPer - 1)); j0 < hi; j0 += 32 * kPer) {
+        const bool first = s == mine_0 && j0 == lo;
+        int ids[kPer], holders[kPer];
+        if (first) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) ids[k] = old_ids[k];
+        } else {
+          entries(s, j0, hi, ids);
+        }
+        unsigned which = 0;  // (bit k: entry j0 + 32 k + lane)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int j = j0 + 32 * k + lane;
+          if (j < from || j >= hi) continue;
+          if (valid(ids[k])) which |= 1u << k;
+          else bits |= GQA_DEV_BAD_BLOCK;
+        }
+        if (step == 0) {
+          gives |= which != 0;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k)
+            if (which >> k & 1u) atomicSub(&p.shared_out[ids[k]], 1);
+          continue;
+        }
+        // Entries that put their block on the stack: those whose claim stands.
+        const int claim = kClaim + s * p.max_blocks + j0 + lane;
+        unsigned mine = 0;
+        if (step == 3 && first) {
+          mine = first_winners;
+        } else {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) holders[k] = which >> k & 1u ? __ldcg(&p.shared_out[ids[k]]) : 0;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            if (step == 1 && holders[k] < 0) atomicMin(&p.shared_out[ids[k]], claim + 32 * k);
+            mine |= unsigned(holders[k] == claim + 32 * k) << k;
           }
-          at += __popc(all);
+        }
+        if (step == 2) {
+          if (first) first_winners = mine;
+          n_won += __popc(mine);
+        }
+        if (step == 3) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const unsigned all = __ballot_sync(0xffffffffu, mine >> k & 1u);
+            if (mine >> k & 1u) {
+              const long to = long(at) + __popc(all & ((1u << lane) - 1u));
+              if (to < p.num_blocks) p.free_out[to] = ids[k];
+              else bits |= GQA_DEV_BAD_BLOCK;
+              p.shared_out[ids[k]] = 0;
+            }
+            at += __popc(all);
+          }
+        }
+      }
+      if (step == 2) {  // told to every block of the cluster
+        n_won = __reduce_add_sync(0xffffffffu, n_won);
+        if (CLUSTER == 1) {
+          if (lane == 0) won[unit] = n_won;
+        } else if (lane < CLUSTER) {
+          asm volatile(
+              "{\n\t.reg .b32 a;\n\t"
+              "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+              "st.shared::cluster.u32 [a], %2;\n\t}" ::"r"(smem_u32(won) + 4 * unit),
+              "r"(lane), "r"(n_won)
+              : "memory");
         }
       }
     }
+    if (step == 0) gives = __any_sync(0xffffffffu, gives);
+    if (step < 3) barrier();
+    if (step == 2) {
+#pragma unroll 1
+      for (int u0 = 0; u0 < p.B_in << log_parts; u0 += NT) {
+        const int u = u0 + tid;
+        int total;
+        const int before = block_exclusive(u < p.B_in << log_parts ? won[u] : 0, part, total);
+        if (u < p.B_in << log_parts) won[u] = top + before;
+        top += total;
+        __syncthreads();
+      }
+    }
+  }
   if (rank == 0 && tid == 0) *p.count_out = min(top, p.num_blocks);
   if (bits != 0) atomicOr(p.status, bits);
 }
@@ -607,18 +647,21 @@ cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_fork(const ForkArgs& a, cudaStream_t stream) {
-  static DeviceOnce once;
-  const cudaError_t e = once.run([&] {
-    cudaError_t r = cudaSuccess;
-    for (const void* k : {reinterpret_cast<const void*>(fork_kernel<false>), reinterpret_cast<const void*>(fork_kernel<true>)})
-      if (r == cudaSuccess) r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostRequests * 28);
-    return r;
-  });
-  if (e != cudaSuccess) return e;
-  const size_t smem = size_t(a.B_in) * 16 + size_t(a.B) * 12;
-  if (a.B + a.B_in < kClusterRequests)
-    return launch_pdl(fork_kernel<false>, dim3(1), dim3(NT), smem, stream, a);
-  return launch_pdl_cluster(fork_kernel<true>, kCluster, dim3(kCluster), dim3(NT), smem, stream, a);
+  auto go = [&](auto kern, DeviceOnce& once, unsigned cluster) {
+    const size_t smem = size_t(a.B_in) * 16 + size_t(a.B) * 12 + cluster * NWARP * 4;
+    const cudaError_t e = once.run([&] {
+      const void* const k = reinterpret_cast<const void*>(kern);
+      const cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kForkSmem);
+      return r != cudaSuccess || cluster <= 8 ? r : cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
+    if (e != cudaSuccess) return e;
+    return cluster == 1 ? launch_pdl(kern, dim3(1), dim3(NT), smem, stream, a)
+                        : launch_pdl_cluster(kern, cluster, dim3(cluster), dim3(NT), smem, stream, a);
+  };
+  static DeviceOnce once1, once16;
+  const long chunks = (a.max_blocks + 32 * kPer - 1) / (32 * kPer);
+  const long most = std::max(a.B, a.B_in);
+  return most <= NWARP && most * chunks <= kOneBlock ? go(fork_kernel<1>, once1, 1) : go(fork_kernel<kCluster>, once16, kCluster);
 }
 
 }  // namespace gqa

@@ -218,7 +218,8 @@ def run_fork(ws, src, keep, held, table, shared, stack, count, bs, in_place=Fals
 
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("B_in,B,bs,mb", [(1, 1, 16, 3), (1, 9, 64, 5), (8, 8, 16, 40), (33, 20, 1, 12), (100, 150, 4, 33),
-                                          (257, 300, 16, 6), (1100, 1030, 2, 3), (3, 2000, 8, 70)])
+                                          (257, 300, 16, 6), (1100, 1030, 2, 3), (3, 2000, 8, 70), (2, 3, 1, 4100), (16, 15, 2, 384),
+                                          (17, 16, 1, 130), (40, 5, 1, 900), (1, 1, 2, 129), (128, 100, 3, 200), (8192, 8192, 1, 2)])
 def test_forks(ws, B_in, B, bs, mb, in_place):
     r = np.random.default_rng(B_in + B)
     held, table, shared, stack, count = pool_of_requests(r, B_in, bs, mb, B + 5)
