@@ -933,6 +933,63 @@ def _case_inputs(name, device):
         nbytes = 4 * (n * 2 + n * 7 + 2)  # (lengths read; six arrays and a block id of each written)
         return (lambda st: binding_mod().gqa_attn_step_tables(lens, one, table, stack, count, kv, ql, starts, pos, slots,
                                                               rows, left, bs, 1, ws, stream=st)), nbytes, "bytes"
+    if name in ("decode-tree-B8-T64-S8192", "decode-chain-B64-T5-S2048"):
+        # drafted rows over a paged cache: trees of 64, each node's parent any before it, or chains of 5
+        chain = "chain" in name
+        n, tq, S, bs = (64, 5, 2048, 64) if chain else (8, 64, 8192, 64)
+        rng = np.random.default_rng(0)
+        table = torch.from_numpy(rng.permutation(n * S // bs).astype(np.int32).reshape(n, S // bs)).to(device)
+        kp, vp = (inputs.randn((n * S // bs, 8, bs, 128), inputs.tensor_seed(0, i), torch.bfloat16, device) for i in (1, 2))
+        q = inputs.randn((n, 32, tq, 128), inputs.tensor_seed(0, 0), torch.bfloat16, device)
+        o = torch.empty_like(q)
+        lens, nodes = (torch.full((n,), x, dtype=torch.int32, device=device) for x in (S, tq))
+        ws = binding_mod().decode_tree_workspace(n, 32, 8, 128, tq, S, device)
+        mask = None
+        if not chain:
+            parents = np.floor(rng.random((n, tq)) * np.arange(tq)).astype(np.int32)
+            parents[:, 0] = -1
+            mask = torch.empty((n, tq, 2), dtype=torch.int32, device=device)
+            binding_mod().gqa_attn_tree_tables(torch.from_numpy(parents).to(device), nodes, None, None, None, mask, None, ws)
+        nbytes = metrics.decode_bytes(32 * tq, 8, 128, [S] * n, 2)
+        return (lambda st: binding_mod().gqa_attn_decode_tree_paged(q, kp, vp, table, mask, None, None, lens, o, 128 ** -0.5,
+                                                                    ws, S, stream=st)), nbytes, "bytes"
+    if name == "decode-compact-rows-B128":
+        # of 64 drafted rows of each request every sixth is kept, in 16 layers' caches
+        n, layers, S, bs = 128, 16, 256, 64
+        path = torch.arange(0, 64, 6, device=device).int().repeat(n, 1)
+        keep, nodes, lens = (torch.full((n,), x, dtype=torch.int32, device=device) for x in (path.shape[1], 64, S))
+        table = torch.from_numpy(np.random.default_rng(0).permutation(n * S // bs).astype(np.int32).reshape(n, S // bs)).to(device)
+        kc, vc = (torch.zeros((layers, n * S // bs, 8, bs, 128), dtype=torch.bfloat16, device=device) for _ in range(2))
+        left, ws = torch.empty_like(lens), torch.zeros(256, dtype=torch.uint8, device=device)
+        nbytes = 2 * 2 * n * (path.shape[1] - 1) * layers * 8 * 128 * 2
+        return (lambda st: binding_mod().gqa_attn_compact_rows(path, keep, nodes, lens, table, kc, vc, left, ws,
+                                                               stream=st)), nbytes, "bytes"
+    if name == "decode-fork-tables-B256":
+        # 256 beams of up to 128 blocks, each from a random one of the last step's
+        n, bs, mb = 256, 64, 128
+        rng = np.random.default_rng(0)
+        n_pool = n * mb + n
+        held = rng.integers(1, mb * bs + 1, n).astype(np.int32)
+        src = torch.from_numpy(rng.integers(0, n, n).astype(np.int32)).to(device)
+        table = torch.arange(n * mb, dtype=torch.int32, device=device).reshape(n, mb)
+        lens = torch.from_numpy(held).to(device)
+        shared = torch.zeros(n_pool, dtype=torch.int32, device=device)
+        stack = torch.zeros(n_pool, dtype=torch.int32, device=device)
+        stack[:n] = torch.arange(n * mb, n_pool, device=device)
+        count = torch.full((1,), n, dtype=torch.int32, device=device)
+        out = [torch.empty_like(x) for x in (table, lens, shared, stack, count, lens, lens, lens)]
+        ws = torch.zeros(256, dtype=torch.uint8, device=device)
+        blocks = -(-held // bs)
+        nbytes = 4 * int(blocks.sum() + blocks[src.cpu().numpy()].sum() + 4 * n_pool + 6 * n)
+        return (lambda st: binding_mod().gqa_attn_fork_tables(src, None, lens, table, shared, stack, count, *out, bs, ws,
+                                                              stream=st)), nbytes, "bytes"
+    if name == "decode-copy-blocks-n64":
+        n, layers, bs = 64, 16, 64
+        ids = torch.from_numpy(np.random.default_rng(0).permutation(2 * n).astype(np.int32)).to(device)
+        kc, vc = (torch.zeros((layers, 2 * n, 8, bs, 128), dtype=torch.bfloat16, device=device) for _ in range(2))
+        ws = torch.zeros(256, dtype=torch.uint8, device=device)
+        nbytes = kc.numel() * 2 * 2
+        return (lambda st: binding_mod().gqa_attn_copy_blocks(ids[:n], ids[n:], None, kc, vc, ws, stream=st)), nbytes, "bytes"
     if name.startswith("prefill-"):
         # prefill-T4097, prefill-q512-kv4096 (Qwen2.5-0.5B heads, D=64) or
         # prefill-d128-T4097 (Qwen2.5-7B heads, D=128)
@@ -960,7 +1017,8 @@ KERNEL_CASES = ("decode-f32-S32768", "decode-bf16-S32768", "decode-bf16-ragged-B
                 "prefill-d128-T4097", "prefill-d128-T16384",
                 "decode-f32-layers8-S32768",
                 "decode-shared-prefix-B64-P32768", "decode-shared-prefix-B256-P16384", "prefill-rope-append-T16384",
-                "decode-step-tables-B256")
+                "decode-step-tables-B256", "decode-tree-B8-T64-S8192", "decode-chain-B64-T5-S2048", "decode-compact-rows-B128",
+                "decode-fork-tables-B256", "decode-copy-blocks-n64")
 
 
 def binding_mod():
