@@ -144,15 +144,12 @@ struct alignas(16) Walk {
   unsigned left;      // positions of the range not yet taken
   int k, next_u, at;  // next: request, its unit, position in the unit
   int b, L, ql, t0;   // of the segment
-  int lo, hi, u;
+  int lo, hi, part, g;  // (part: the row tile or pair of them, g: the KV head)
 };
 static_assert(sizeof(Walk) <= 64, "walk area");
 
-// The row tile or pair of them that a unit is, and its KV head.
-template <bool PAIR>
-__device__ __forceinline__ int part_of(int u, const TreeParams& p) { return PAIR ? u % p.np : 0; }
-template <bool PAIR>
-__device__ __forceinline__ int head_of(int u, const TreeParams& p) { return PAIR ? u / p.np : u; }
+// The KV head of a unit, whose row tile or pair of them is u - head * p.np.
+__device__ __forceinline__ int head_of(int u, const TreeParams& p) { return p.np == 1 ? u : u / p.np; }
 
 // The next segment; false at the range's end.  Called by a whole warp.
 template <int LEAD>
@@ -193,7 +190,8 @@ __device__ __forceinline__ bool next_segment(Walk* w, const TreeParams& p, const
       w->t0 = e.w;
       w->lo = lo;
       w->hi = hi;
-      w->u = seg_u;
+      w->g = head_of(seg_u, p);
+      w->part = seg_u - w->g * p.np;
     }
   }
   __syncwarp();
@@ -368,7 +366,8 @@ __global__ void __launch_bounds__(NTHR, 1)
       if (tid == 0 && rank == 0 && bits != 0) atomicOr(p.status, bits);
       const unsigned tiles = e.z > 0 ? tiles_of(e.y) : 0;
       walk->b = b;
-      walk->u = unit - b * p.units;
+      walk->g = head_of(unit - b * p.units, p);
+      walk->part = unit - b * p.units - walk->g * p.np;
       walk->L = e.y;
       walk->ql = e.z;
       walk->t0 = e.w;
@@ -410,7 +409,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       const uint64_t policy = p.np == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
 #pragma unroll 1
       while (segment<CLUSTERED, kLead<PAIR>>(walk, p, ent)) {
-        const int L = walk->L, b = walk->b, g = head_of<PAIR>(walk->u, p), part = part_of<PAIR>(walk->u, p), lo = walk->lo,
+        const int L = walk->L, b = walk->b, g = walk->g, part = walk->part, lo = walk->lo,
                   hi = walk->hi;
         if (lane == 0 && !*abort_flag) {
           const int32_t* const table = p.block_table + (p.block_table != nullptr ? size_t(b) * p.max_blocks : 0);
@@ -566,6 +565,8 @@ __global__ void __launch_bounds__(NTHR, 1)
     const uint32_t tO = tmem + TM_O + t * HD + lane_off;
     const uint32_t tP = tmem + TM_P + t * C::P_STRIDE + lane_off;
     const float c = p.qk_scale_log2;
+    unsigned char* const stage = smem + C::OFF_OUT + warp * 2048;
+    uint4* const sees = reinterpret_cast<uint4*>(stage);  // (each lane's own)
     if (!CLUSTERED && (warp & 3) == 0 && lane == 1 && !(PAIR && t == 1)) {
       // The unit that the range ends in, where it begins there too (a tile of it at least
       // is this worker's and one another's): its partials are this worker's and those
@@ -584,18 +585,39 @@ __global__ void __launch_bounds__(NTHR, 1)
       const int n_it = walk->hi - walk->lo;
       const int masked_from = walk->t0 / BN - walk->lo;  // tiles with drafted rows, or past the keys
       // (rows past the last one are nobody's: a warp that has only such leaves P as it is)
-      // The masks' words are asked for before the scores are there.
-      if (p.mask != nullptr && masked_from < n_it) {
-        const int i = ((PAIR ? 2 * part_of<PAIR>(walk->u, p) + t : 0) * BM + (tid & (BM - 1))) % p.Tq;
-        const int32_t* const words = p.mask + (size_t(walk->b) * p.Tq + i) * p.W;
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(words));
-      }
-      const bool warp_live = ((PAIR ? 2 * part_of<PAIR>(walk->u, p) + t : 0) * 4 + (warp & 3)) * 32 < p.n_rep * p.Tq;
+      const bool warp_live = ((PAIR ? 2 * walk->part + t : 0) * 4 + (warp & 3)) * 32 < p.n_rep * p.Tq;
       m_ref = -INFINITY;
       lsum = 0.f;
       if (PAIR && t == 1) named_bar_arrive(BAR_TURN_A, 256);  // (slot 0 begins)
 #pragma unroll 1
       for (int j = 0; j < n_it; ++j, ++n) {
+        if (j >= masked_from && warp_live) {
+          // Which keys of the tile the row sees: all words of the mask are asked for at
+          // once, before the scores are there, and 32 keys are a word of `see`.
+          const int L = walk->L, t0 = walk->t0, k0 = (walk->lo + j) * BN;
+          const int i = ((PAIR ? 2 * walk->part + t : 0) * BM + (tid & (BM - 1))) % p.Tq;
+          uint32_t word[5];
+          if (p.mask != nullptr) {
+            const int32_t* const words = p.mask + (size_t(walk->b) * p.Tq + i) * p.W;
+            const int x0 = (k0 - t0) >> 5;
+#pragma unroll
+            for (int x = 0; x < 5; ++x) word[x] = uint32_t(words[min(max(x0 + x, 0), p.W - 1)]);
+#pragma unroll
+            for (int x = 0; x < 5; ++x) word[x] = x0 + x < 0 ? 0xffffffffu : x0 + x < p.W ? word[x] : 0u;
+          } else {
+#pragma unroll
+            for (int x = 0; x < 5; ++x) word[x] = 0xffffffffu;
+          }
+          const int end = p.mask != nullptr ? L : min(L, t0 + i + 1);
+          uint32_t see[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int keys = end - k0 - 32 * q;  // of these 32
+            see[q] = __funnelshift_r(word[q], word[q + 1], (k0 - t0) & 31);
+            if (keys < 32) see[q] &= keys > 0 ? (1u << keys) - 1u : 0u;
+          }
+          sees[lane] = make_uint4(see[0], see[1], see[2], see[3]);
+        }
         tile_wait(&bars[B_S + t], uint32_t(n) & 1u, abort_flag, p.wait_limit_ns);
         tc_fence_after();
         if (!warp_live) {
@@ -628,22 +650,9 @@ __global__ void __launch_bounds__(NTHR, 1)
           if (lane == 0) mbar_arrive(&bars[B_SC + t]);
         }
         if (j >= masked_from) {
-          const int L = walk->L, t0 = walk->t0;
-          const int i = ((PAIR ? 2 * part_of<PAIR>(walk->u, p) + t : 0) * BM + (tid & (BM - 1))) % p.Tq;
-          const int32_t* const words = p.mask + (p.mask != nullptr ? (size_t(walk->b) * p.Tq + i) * p.W : 0);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int ks = (walk->lo + j) * BN + 32 * q;  // the first of these 32 keys
-            int keys = L - ks;                            // of them that there are
-            uint32_t see = 0xffffffffu;
-            if (p.mask == nullptr) {
-              keys = min(keys, t0 + i + 1 - ks);
-            } else {
-              const int c0 = ks - t0;
-              auto word = [&](int x) { return x < 0 ? 0xffffffffu : x < p.W ? uint32_t(words[x]) : 0u; };
-              see = __funnelshift_r(word(c0 >> 5), word((c0 >> 5) + 1), c0 & 31);
-            }
-            if (keys < 32) see &= keys > 0 ? (1u << keys) - 1u : 0u;
+            const uint32_t see = reinterpret_cast<const uint32_t*>(&sees[lane])[q];
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!((see >> e) & 1u)) s[32 * q + e] = 0xff800000u;
@@ -711,7 +720,7 @@ __global__ void __launch_bounds__(NTHR, 1)
 
       // ---- the segment's rows: finished, or partials ----
       if (!CLUSTERED && warp_live) {
-        const int part = part_of<PAIR>(walk->u, p), g = head_of<PAIR>(walk->u, p), r = tid & (BM - 1);
+        const int part = walk->part, g = walk->g, r = tid & (BM - 1);
         const int row = (PAIR ? 2 * part + t : part) * BM + r, h = row / p.Tq, i = row % p.Tq;
         const bool live = h < p.n_rep && i < walk->ql && !*abort_flag;
         const bool begins = walk->lo == 0, whole = begins && walk->hi == tiles_of(walk->L);
@@ -721,7 +730,13 @@ __global__ void __launch_bounds__(NTHR, 1)
           const long dst = live ? ((long(walk->b) * p.Hq + g * p.n_rep + h) * p.Tq + i) * HD : -1L;
           // 32 columns at a time through the warp's staging area, 16-byte chunks XOR-ed
           // with the row, so that a store covers 64 bytes of a row, not 16
-          unsigned char* const stage = smem + C::OFF_OUT + warp * 2048;
+          __nv_bfloat16* to[4];  // of the row that this lane stores a part of, in each of four stores
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const long d = __shfl_sync(0xffffffffu, dst, it * 8 + lane / 4);
+            to[it] = d >= 0 ? p.o + d + lane % 4 * 8 : nullptr;
+          }
+          __syncwarp();  // (the lanes are done with `sees`)
 #pragma unroll 1
           for (int cc = 0; cc < HD / 32; ++cc) {
             uint32_t o[32];
@@ -743,9 +758,8 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
               const int x = it * 8 + lane / 4, e = lane % 4;
-              const long d = __shfl_sync(0xffffffffu, dst, x);
               const uint4 v = *reinterpret_cast<const uint4*>(stage + x * 64 + ((e ^ ((x >> 1) & 3)) << 4));
-              if (d >= 0) *reinterpret_cast<uint4*>(p.o + d + cc * 32 + e * 8) = v;
+              if (to[it] != nullptr) *reinterpret_cast<uint4*>(to[it] + cc * 32) = v;
             }
             __syncwarp();
           }
@@ -796,7 +810,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     // Row R of the unit is joined by CTA R / share.  There, over the stages of K and V:
     // O as [worker][D / 4][share][4], and (m, l) as [worker][share] where the list would be.
     // (The cluster's size divides 128, so workers * share <= 256 rows of D floats.)
-    const int n = (PAIR ? 1 : 2) * p.cluster, part = part_of<PAIR>(walk->u, p), g = head_of<PAIR>(walk->u, p);
+    const int n = (PAIR ? 1 : 2) * p.cluster, part = walk->part, g = walk->g;
     const int rows = min(PAIR ? 2 * BM : BM, p.n_rep * p.Tq - part * 2 * BM), share = (rows + p.cluster - 1) / p.cluster;
     cluster_barrier();  // every CTA is done with its stages
     if (warp < 8) {
@@ -875,7 +889,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
   const int4 rec = __ldcg(&p.record[w]);
   const int n = rec.z;
   if (n == 0) return;
-  const int row = (part_of<TILES == 2>(rec.y, p) * TILES + t) * BM + r, g = head_of<TILES == 2>(rec.y, p), h = row / p.Tq, i = row % p.Tq;
+  const int g = head_of(rec.y, p), row = ((rec.y - g * p.np) * TILES + t) * BM + r, h = row / p.Tq, i = row % p.Tq;
   const bool live = h < p.n_rep && i < rec.w;
   if (!__any_sync(0xffffffffu, live)) return;  // (the same rows in every warp)
   float M = -INFINITY, den = 0.f, acc[4][4] = {};
