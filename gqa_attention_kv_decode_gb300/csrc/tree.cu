@@ -61,11 +61,11 @@ namespace gqa {
 namespace {
 
 constexpr int kMost = 1024;      // requests of a launch (kept in shared memory)
-// Key tiles that the start and the end of a unit count as, with PAIR and without
-// (4 x 61 queries over 16,385 keys: 1 63.2 us, 2 61.8, 4 60.7; chains of 128 x 5 over up
-// to 2,048: 1 83.5, 2 83.5, 4 86.5).
+// Key tiles that the start and the end of a unit count as, with PAIR and without (2 and 1,
+// 3 and 1, 4 and 2: 20 x 40 queries over up to 3,000 keys 40.6, 41.0, 42.6 us; 4 x 61
+// over 16,385 60.2, 60.4, 59.3; chains of 128 x 5 over up to 2,048 82.4, 82.4, 82.9).
 template <bool PAIR>
-constexpr int kLead = PAIR ? 4 : 2;
+constexpr int kLead = PAIR ? 2 : 1;
 
 // Tensor memory, shared memory and registers as in the prefill kernel:
 //   HD = 64:  S_0 [0,128) S_1 [128,256) O_0 [256,320) O_1 [320,384) P_0 [384,448) P_1 [448,512)
@@ -85,7 +85,7 @@ struct TrCfg {
   static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
   static constexpr int OFF_BAR = OFF_V + NST * TILE_BYTES;
   static constexpr int OFF_WALK = OFF_BAR + 512;             // a Walk per warp
-  static constexpr int OFF_ENT = OFF_WALK + 12 * 64;         // int4 [kMost]: the requests
+  static constexpr int OFF_ENT = OFF_WALK + 12 * 80;         // int4 [kMost]: the requests
   static constexpr int OFF_OUT = OFF_ENT + kMost * 16;     // 32 rows of 64 bytes for each softmax warp
   static constexpr int SMEM_BYTES = OFF_OUT + 8 * 2048 + 1024;  // + alignment slack
   // mbarriers, [t] per slot: Q_t loaded / read by its last product; K and V stages
@@ -137,23 +137,28 @@ __device__ __forceinline__ int4 request(const TreeParams& p, int b, uint32_t& bi
 
 __device__ __forceinline__ int tiles_of(int L) { return (L + BN - 1) / BN; }
 
-// A warp's way through its worker's range, a segment (tiles [lo, hi) of unit u of
-// request b) at a time.  In shared memory: kept in registers through the softmax
-// loop, which needs nearly all, it would be spilled there.
+// Tiles [lo, hi) of a unit of request b: of KV head g, row tile or pair of them `part`.
+struct Segment {
+  int b, L, ql, t0;
+  int lo, hi, part, g;
+};
+
+// A warp's way through its worker's range, a segment at a time.  In shared memory:
+// kept in registers through the softmax loop, which needs nearly all, it would be
+// spilled there.
 struct alignas(16) Walk {
   unsigned left;      // positions of the range not yet taken
   int k, next_u, at;  // next: request, its unit, position in the unit
-  int b, L, ql, t0;   // of the segment
-  int lo, hi, part, g;  // (part: the row tile or pair of them, g: the KV head)
+  Segment seg[2];
 };
-static_assert(sizeof(Walk) <= 64, "walk area");
+static_assert(sizeof(Walk) == 80, "walk area");
 
 // The KV head of a unit, whose row tile or pair of them is u - head * p.np.
 __device__ __forceinline__ int head_of(int u, const TreeParams& p) { return p.np == 1 ? u : u / p.np; }
 
-// The next segment; false at the range's end.  Called by a whole warp.
+// The next segment into w->seg[to]; false at the range's end.  Called by a whole warp.
 template <int LEAD>
-__device__ __forceinline__ bool next_segment(Walk* w, const TreeParams& p, const int4* ent) {
+__device__ __forceinline__ bool next_segment(Walk* w, int to, const TreeParams& p, const int4* ent) {
   unsigned left = w->left;
   int k = w->k, u = w->next_u, at = w->at;
   bool found = false;
@@ -184,14 +189,8 @@ __device__ __forceinline__ bool next_segment(Walk* w, const TreeParams& p, const
       w->k = k;
       w->next_u = u;
       w->at = at;
-      w->b = seg_k;
-      w->L = e.y;
-      w->ql = e.z;
-      w->t0 = e.w;
-      w->lo = lo;
-      w->hi = hi;
-      w->g = head_of(seg_u, p);
-      w->part = seg_u - w->g * p.np;
+      const int g = head_of(seg_u, p);
+      w->seg[to] = Segment{seg_k, e.y, e.z, e.w, lo, hi, seg_u - g * p.np, g};
     }
   }
   __syncwarp();
@@ -200,7 +199,7 @@ __device__ __forceinline__ bool next_segment(Walk* w, const TreeParams& p, const
 
 // The next segment, or the only one.
 template <bool CLUSTERED, int LEAD>
-__device__ __forceinline__ bool segment(Walk* w, const TreeParams& p, const int4* ent) {
+__device__ __forceinline__ bool segment(Walk* w, int to, const TreeParams& p, const int4* ent) {
   if constexpr (CLUSTERED) {
     const bool found = w->left != 0;
     __syncwarp();
@@ -208,7 +207,7 @@ __device__ __forceinline__ bool segment(Walk* w, const TreeParams& p, const int4
     __syncwarp();
     return found;
   } else {
-    return next_segment<LEAD>(w, p, ent);
+    return next_segment<LEAD>(w, to, p, ent);
   }
 }
 
@@ -365,15 +364,9 @@ __global__ void __launch_bounds__(NTHR, 1)
       const int4 e = request(p, b, bits);
       if (tid == 0 && rank == 0 && bits != 0) atomicOr(p.status, bits);
       const unsigned tiles = e.z > 0 ? tiles_of(e.y) : 0;
-      walk->b = b;
-      walk->g = head_of(unit - b * p.units, p);
-      walk->part = unit - b * p.units - walk->g * p.np;
-      walk->L = e.y;
-      walk->ql = e.z;
-      walk->t0 = e.w;
-      walk->lo = int(tiles * worker / n);
-      walk->hi = int(tiles * (worker + 1) / n);
-      walk->left = walk->hi > walk->lo;
+      const int u = unit - b * p.units, g = head_of(u, p);
+      walk->seg[0] = Segment{b, e.y, e.z, e.w, int(tiles * worker / n), int(tiles * (worker + 1) / n), u - g * p.np, g};
+      walk->left = walk->seg[0].hi > walk->seg[0].lo;
     }
     __syncwarp();
   } else {
@@ -395,6 +388,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           make_int4(worker < cut.n ? int(cut.start(worker + 1) - cut.start(worker)) : 0, at_k, at_unit, at_place);
     __syncwarp();
   }
+  const Segment* const seg = &walk->seg[0];
   float m_ref = -INFINITY, lsum = 0.f;  // of a softmax thread's row
 
   if (warp >= 8) {
@@ -408,9 +402,9 @@ __global__ void __launch_bounds__(NTHR, 1)
       // (rows that other units of the request read too stay in L2)
       const uint64_t policy = p.np == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
 #pragma unroll 1
-      while (segment<CLUSTERED, kLead<PAIR>>(walk, p, ent)) {
-        const int L = walk->L, b = walk->b, g = walk->g, part = walk->part, lo = walk->lo,
-                  hi = walk->hi;
+      while (segment<CLUSTERED, kLead<PAIR>>(walk, 0, p, ent)) {
+        const int L = seg->L, b = seg->b, g = seg->g, part = seg->part, lo = seg->lo,
+                  hi = seg->hi;
         if (lane == 0 && !*abort_flag) {
           const int32_t* const table = p.block_table + (p.block_table != nullptr ? size_t(b) * p.max_blocks : 0);
           // The 64 rows copied next: the block they are in and their place in it, or
@@ -517,8 +511,8 @@ __global__ void __launch_bounds__(NTHR, 1)
         mma_commit_warp(&bars[B_VE + st]);
       };
 #pragma unroll 1
-      while (segment<CLUSTERED, kLead<PAIR>>(walk, p, ent)) {
-        const int L = walk->L, lo = walk->lo, hi = walk->hi;
+      while (segment<CLUSTERED, kLead<PAIR>>(walk, 0, p, ent)) {
+        const int L = seg->L, lo = seg->lo, hi = seg->hi;
 #pragma unroll 1
         for (int s = PAIR ? 0 : t; scores && s < (PAIR ? 2 : t + 1); ++s)
           tile_wait(&bars[B_QF + s], uint32_t(n_seg) & 1u, abort_flag, p.wait_limit_ns);
@@ -580,25 +574,33 @@ __global__ void __launch_bounds__(NTHR, 1)
       p.record[worker] = rec;
     }
     int n = 0;
+    // With D = 128 the next segment is looked for while the last scores of one are waited
+    // for (4 x 61 queries over 16,385 keys 60.1 us, behind the segment's end 60.5); with
+    // D = 64 that costs the loop more than it saves (8 x 64 45.2, 43.4).
+    constexpr bool EARLY = HD == 128;
+    int cur = 0;
+    bool more = segment<CLUSTERED, kLead<PAIR>>(walk, 0, p, ent);
 #pragma unroll 1
-    while (segment<CLUSTERED, kLead<PAIR>>(walk, p, ent)) {
-      const int n_it = walk->hi - walk->lo;
-      const int masked_from = walk->t0 / BN - walk->lo;  // tiles with drafted rows, or past the keys
+    for (; more; cur ^= 1) {
+      const Segment* const seg = &walk->seg[cur];
+      const int n_it = seg->hi - seg->lo;
+      const int masked_from = seg->t0 / BN - seg->lo;  // tiles with drafted rows, or past the keys
       // (rows past the last one are nobody's: a warp that has only such leaves P as it is)
-      const bool warp_live = ((PAIR ? 2 * walk->part + t : 0) * 4 + (warp & 3)) * 32 < p.n_rep * p.Tq;
+      const bool warp_live = ((PAIR ? 2 * seg->part + t : 0) * 4 + (warp & 3)) * 32 < p.n_rep * p.Tq;
       m_ref = -INFINITY;
       lsum = 0.f;
       if (PAIR && t == 1) named_bar_arrive(BAR_TURN_A, 256);  // (slot 0 begins)
 #pragma unroll 1
       for (int j = 0; j < n_it; ++j, ++n) {
+        if (EARLY && j + 1 == n_it) more = segment<CLUSTERED, kLead<PAIR>>(walk, cur ^ 1, p, ent);
         if (j >= masked_from && warp_live) {
           // Which keys of the tile the row sees: all words of the mask are asked for at
           // once, before the scores are there, and 32 keys are a word of `see`.
-          const int L = walk->L, t0 = walk->t0, k0 = (walk->lo + j) * BN;
-          const int i = ((PAIR ? 2 * walk->part + t : 0) * BM + (tid & (BM - 1))) % p.Tq;
+          const int L = seg->L, t0 = seg->t0, k0 = (seg->lo + j) * BN;
+          const int i = ((PAIR ? 2 * seg->part + t : 0) * BM + (tid & (BM - 1))) % p.Tq;
           uint32_t word[5];
           if (p.mask != nullptr) {
-            const int32_t* const words = p.mask + (size_t(walk->b) * p.Tq + i) * p.W;
+            const int32_t* const words = p.mask + (size_t(seg->b) * p.Tq + i) * p.W;
             const int x0 = (k0 - t0) >> 5;
 #pragma unroll
             for (int x = 0; x < 5; ++x) word[x] = uint32_t(words[min(max(x0 + x, 0), p.W - 1)]);
@@ -715,19 +717,21 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
         lsum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y) + (acc[2].x + acc[2].y) + (acc[3].x + acc[3].y);
       }
-      tile_wait(&bars[B_O1 + t], uint32_t(n - 1) & 1u, abort_flag, p.wait_limit_ns);
-      tc_fence_after();
 
       // ---- the segment's rows: finished, or partials ----
+      const int part = seg->part, r = tid & (BM - 1);
+      const int row = (PAIR ? 2 * part + t : part) * BM + r, h = row / p.Tq, i = row - h * p.Tq;
+      const bool mine = h < p.n_rep && i < seg->ql;
+      const long at = mine ? ((long(seg->b) * p.Hq + seg->g * p.n_rep + h) * p.Tq + i) * HD : -1L;
+      tile_wait(&bars[B_O1 + t], uint32_t(n - 1) & 1u, abort_flag, p.wait_limit_ns);
+      tc_fence_after();
       if (!CLUSTERED && warp_live) {
-        const int part = walk->part, g = walk->g, r = tid & (BM - 1);
-        const int row = (PAIR ? 2 * part + t : part) * BM + r, h = row / p.Tq, i = row % p.Tq;
-        const bool live = h < p.n_rep && i < walk->ql && !*abort_flag;
-        const bool begins = walk->lo == 0, whole = begins && walk->hi == tiles_of(walk->L);
+        const bool live = mine && !*abort_flag;
+        const bool begins = seg->lo == 0, whole = begins && seg->hi == tiles_of(seg->L);
         if (whole) {
           const float inv = lsum > 0.f ? 1.f / lsum : lsum == 0.f ? 0.f : lsum;  // (a NaN stays one)
           if (live && lsum == 0.f) atomicOr(p.status, GQA_DEV_EMPTY_REQUEST);
-          const long dst = live ? ((long(walk->b) * p.Hq + g * p.n_rep + h) * p.Tq + i) * HD : -1L;
+          const long dst = live ? at : -1L;
           // 32 columns at a time through the warp's staging area, 16-byte chunks XOR-ed
           // with the row, so that a store covers 64 bytes of a row, not 16
           __nv_bfloat16* to[4];  // of the row that this lane stores a part of, in each of four stores
@@ -755,12 +759,15 @@ __global__ void __launch_bounds__(NTHR, 1)
                   make_uint4(w[0], w[1], w[2], w[3]);
             }
             __syncwarp();
+            uint4 v[4];
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
               const int x = it * 8 + lane / 4, e = lane % 4;
-              const uint4 v = *reinterpret_cast<const uint4*>(stage + x * 64 + ((e ^ ((x >> 1) & 3)) << 4));
-              if (to[it] != nullptr) *reinterpret_cast<uint4*>(to[it] + cc * 32) = v;
+              v[it] = *reinterpret_cast<const uint4*>(stage + x * 64 + ((e ^ ((x >> 1) & 3)) << 4));
             }
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+              if (to[it] != nullptr) *reinterpret_cast<uint4*>(to[it] + cc * 32) = v[it];
             __syncwarp();
           }
         } else {
@@ -781,6 +788,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           }
         }
       }
+      if (!EARLY) more = segment<CLUSTERED, kLead<PAIR>>(walk, cur ^ 1, p, ent);
       tc_fence_before();
     }
   }
@@ -810,12 +818,12 @@ __global__ void __launch_bounds__(NTHR, 1)
     // Row R of the unit is joined by CTA R / share.  There, over the stages of K and V:
     // O as [worker][D / 4][share][4], and (m, l) as [worker][share] where the list would be.
     // (The cluster's size divides 128, so workers * share <= 256 rows of D floats.)
-    const int n = (PAIR ? 1 : 2) * p.cluster, part = walk->part, g = walk->g;
+    const int n = (PAIR ? 1 : 2) * p.cluster, part = seg->part, g = seg->g;
     const int rows = min(PAIR ? 2 * BM : BM, p.n_rep * p.Tq - part * 2 * BM), share = (rows + p.cluster - 1) / p.cluster;
     cluster_barrier();  // every CTA is done with its stages
     if (warp < 8) {
       const int R = (PAIR ? (warp >> 2) * BM : 0) + (tid & (BM - 1)), to = R / share, at = R - to * share;
-      const bool any = walk->hi > walk->lo && !*abort_flag, live = R < rows;
+      const bool any = seg->hi > seg->lo && !*abort_flag, live = R < rows;
       const uint32_t tO = tmem + TM_O + (warp >> 2) * HD + (uint32_t((warp & 3) * 32) << 16);
       if (live) {
         const uint32_t dst = shared_of(ent, to) + (worker * share + at) * 8;
@@ -846,7 +854,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     for (int x = tid; x < mine * (HD / 4); x += NTHR) {
       const int chunk = x / mine, at = x - chunk * mine;
       const int row = part * 2 * BM + int(rank) * share + at, h = row / p.Tq, i = row - h * p.Tq;
-      if (i >= walk->ql) continue;
+      if (i >= seg->ql) continue;
       float M = -INFINITY;
       for (int v = 0; v < n; ++v) M = fmaxf(M, ml[v * share + at].x);
       float den = 0.f;
@@ -866,7 +874,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;
       const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
                            hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-      *reinterpret_cast<uint2*>(p.o + ((size_t(walk->b) * p.Hq + g * p.n_rep + h) * p.Tq + i) * HD + chunk * 4) =
+      *reinterpret_cast<uint2*>(p.o + ((size_t(seg->b) * p.Hq + g * p.n_rep + h) * p.Tq + i) * HD + chunk * 4) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
   }
