@@ -968,22 +968,34 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
 
 // ---- plan ----------------------------------------------------------------------
 
-// CTAs in the cluster of a unit, or 0: the list.  Estimated times in us: what comes
-// before and behind the tiles (with the list a tenth for each partial of a unit), and
-// the tiles of the longest request by its cluster or (three quarters of) all by all SMs,
-// where a tile takes its exponentials and products or its share of HBM.  Measured, list and clusters of 2, 4, 8 (D = 128, rows x units x keys
-// of each, *: a pair of row tiles): 64 x 8 x 2,048 14.0, 16.6, 12.9, 10.9; 64 x 32 x
-// 4,096 22.3, 23.8, 19.1, 38.2 (not one wave); 128 x 8 x 32,768 40.8, 130, 70.9,
-// 42.8; 182* x 32 x 4,097 29.3, 40.7, 28.5, 63.1; 427* x 16 x 16,385 61.0, 110, 64.6, 116.
+// CTAs in the cluster of a unit, or 0: the list.  Estimated times in us, with what was
+// fitted to 356 calls (1 to 72 units of 1 to 256 key tiles, D = 64 and 128, one and two
+// row tiles), each with the list and clusters of 2, 4 and 8: what it chooses is 0.7 %
+// slower than the best of them in the mean, 14 % at most.  A tile takes its time or its
+// share of HBM; the requests of a call are taken to have nine tenths of the longest
+// one's keys.  Measured, list and clusters of 2, 4, 8 (D = 128, rows x units x keys, *: a
+// pair of row tiles): 64 x 8 x 2,048 13.3, 16.7, 12.8, 10.8; 64 x 32 x 4,097 22.7, 26.7,
+// 21.8, 45.2 (not one wave); 256* x 8 x 256 12.0, 17.2, 15.1, 13.9; 256* x 1 x 100 9.0,
+// 16.9, 14.7, 13.5; 256* x 16 x 8,192 27.4, 64.0, 38.8, 51.3.
 // `fits`: clusters of 2, 4 and 8 that run at once.
 int cluster_size(bool pair, int D, int B, long units, long tiles, int sms, const int (&fits)[3]) {
-  const double tile = D / 128.0 * (pair ? 1.65 : 1.0), hbm = D / 128.0 * 1.53;
-  const double partials = std::min(double(tiles), double(pair ? sms : 2 * sms) / double(units));
-  double best = (pair ? 18.0 : 11.5) + 0.1 * partials + (B > 1 ? 0.75 : 1.0) * double(units) * tiles / sms * std::max(tile, hbm);
+  struct Times {
+    double list, merge, partial, tile;  // the list: start and end, merge and each of a unit's partials, a tile
+    double cluster, rows, its_tile;     // a cluster: start and end, rows joined by one CTA, a tile
+  };
+  constexpr Times times[2][2] = {{{7.6, 1.5, 0.14, 0.0, 7.3, 0.9, 1.20}, {8.3, 1.7, 0.14, 0.0, 8.1, 2.4, 1.73}},
+                                 {{7.5, 3.5, 0.14, 1.29, 9.3, 5.5, 1.16}, {7.6, 4.6, 0.17, 1.92, 11.5, 9.8, 1.53}}};
+  const Times& x = times[pair][D == 128];
+  const int slots = pair ? 1 : 2;  // workers of a CTA
+  const double hbm = 0.0099 * D / 128, share = (B > 1 ? 0.9 : 1.0) * double(units) * tiles, workers = double(slots) * sms;
+  if (tiles < 2) return 0;
+  double best = x.list + x.merge + x.partial * std::min(double(tiles), workers / double(units)) +
+                std::max(std::max(1.0, share / workers) * x.tile, share * hbm);
   int size = 0;
   for (int i = 0, c = 2; i < 3; ++i, c *= 2) {
-    if (units > fits[i] || c > std::max(2L, 2 * tiles)) continue;
-    const double t = (pair ? 13.0 : 8.7) + double((tiles + c - 1) / c) * std::max(tile, hbm * double(units) * c / sms);
+    if (units > fits[i] || c > 2 * tiles) continue;
+    const double at_once = double(units) * std::min(long(c) * slots, tiles);
+    const double t = x.cluster + x.rows / c + double((tiles + c * slots - 1) / (c * slots)) * std::max(x.its_tile, at_once * hbm);
     if (t < best) best = t, size = c;
   }
   return size;
