@@ -286,16 +286,18 @@ __global__ void __launch_bounds__(NTHR, 1)
     tmem_alloc(tslot, TMEM_COLS);
     tmem_relinquish();
   }
-  if (tid == 256) {
+  if (warp == 8) {
 #pragma unroll 1
-    for (int i = 0; i < C::N_BARS; ++i) {
+    for (int i = lane; i < C::N_BARS; i += 32) {
       const bool per_warp = i >= B_SC && i < B_O0;
       const bool by_slots = PAIR && i >= B_VE && i < B_S;  // V is read by the products of both slots
       mbar_init(&bars[i], per_warp ? 4 : i == B_DRAIN ? (PAIR ? 3 : 2) : by_slots ? 2 : 1);
     }
-    *abort_flag = 0;
-    for (int i = 0; i < 6; ++i) issued[i] = 0;
+    if (lane < 6) issued[lane] = 0;
+    if (lane == 6) *abort_flag = 0;
     fence_barrier_init();
+  }
+  if (tid == 320) {
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
