@@ -408,32 +408,37 @@ __global__ void __launch_bounds__(NTHR, 1)
         const int L = seg->L, b = seg->b, g = seg->g, part = seg->part, lo = seg->lo,
                   hi = seg->hi;
         if (lane == 0 && !*abort_flag) {
-          const int32_t* const table = p.block_table + (p.block_table != nullptr ? size_t(b) * p.max_blocks : 0);
+          const bool paged = p.block_table != nullptr;
+          const int32_t* const table = p.block_table + (paged ? size_t(b) * p.max_blocks : 0);
           // The 64 rows copied next: the block they are in and their place in it, or
           // their row in a dense cache
           int blk = 0, in = lo * BN;
-          if (p.block_table != nullptr) blk = in / p.block_size, in -= blk * p.block_size;
-          int row[2] = {0, 0}, head[2] = {0, 0};  // of the tile's halves in the map
-#pragma unroll 1
-          for (int j = lo - 1; j < hi; ++j) {
-            // (a tile's blocks are looked up before the wait for its stages)
-            const int j_cur = j, row0 = row[0], row1 = row[1], head0 = head[0], head1 = head[1];
+          if (paged) blk = in / p.block_size, in -= blk * p.block_size;
+          // Of a tile's halves the row in the map and the block, which is asked for while the
+          // tile before is copied and looked at when it is needed.
+          int row[2], id[2];
+          auto look_up = [&](int j) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
               row[s] = in;
-              head[s] = b;
-              if (p.block_table != nullptr && (j + 1) * BN + s * 64 < L) {
-                head[s] = table[blk];
-                if (head[s] < 0 || head[s] >= p.num_blocks) {
-                  atomicOr(p.status, GQA_DEV_BAD_BLOCK);
-                  head[s] = 0;
-                }
-              }
-              head[s] = head[s] * p.Hkv + g;
+              id[s] = paged ? (j * BN + s * 64 < L ? table[blk] : 0) : b;
               in += 64;
-              if (p.block_table != nullptr && in == p.block_size) in = 0, ++blk;
+              if (paged && in == p.block_size) in = 0, ++blk;
             }
-            if (j_cur < lo) continue;
+          };
+          look_up(lo);
+#pragma unroll 1
+          for (int j = lo; j < hi; ++j) {
+            const int row0 = row[0], row1 = row[1];
+            int head0 = id[0], head1 = id[1];
+            if (paged && (unsigned(head0) >= unsigned(p.num_blocks) || unsigned(head1) >= unsigned(p.num_blocks))) {
+              atomicOr(p.status, GQA_DEV_BAD_BLOCK);
+              if (unsigned(head0) >= unsigned(p.num_blocks)) head0 = 0;
+              if (unsigned(head1) >= unsigned(p.num_blocks)) head1 = 0;
+            }
+            head0 = head0 * p.Hkv + g;
+            head1 = head1 * p.Hkv + g;
+            if (j + 1 < hi) look_up(j + 1);
             const int st = ring + n % NSTR;
             const bool both = j * BN + 64 < L;  // is there a key in the tile's second half?
             const uint32_t freed = uint32_t(n / NSTR - 1) & 1u;
