@@ -34,7 +34,9 @@ __device__ __forceinline__ uint4 load_once(const uint4* src) {
 // later batch's sources.
 //
 // The moves are few rows here and there: the time is four dependent round trips and
-// what the scattered rows' 128-byte pieces get out of HBM.
+// what the scattered rows' 128-byte pieces get out of HBM (a request in 28 layers of 4 x
+// 128 2.5 us; 128 requests with 3 rows in the mean to move, 16 layers of 8 x 128, 9.8, of
+// which their 38 MB would be 5.6; with 10 rows to move 168 MB, 27.5 us).
 constexpr int kMostKept = 1024;
 constexpr int kBatch = 4;
 

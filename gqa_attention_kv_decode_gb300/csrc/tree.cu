@@ -30,17 +30,23 @@
 // PAIR warp 8 the copies, 9 S of both slots, 10 and 11 P V of slots 0 and 1; without,
 // 8 and 9 the copies and 10 and 11 both products of slots 0 and 1 (a wait or a product
 // costs its warp a hundred cycles or two: where the products are the bound, three warps
-// issue them, 4 x 61 queries over 16,385 keys 64.8 us with two, 62.0 with three).  S, P and O are in
-// tensor memory, Q, K and V in shared memory.
+// issue them, 4 x 61 queries over 16,385 keys 64.8 us with two, 62.0 with three).  S, P
+// and O are in tensor memory, Q, K and V in shared memory.
 //
-// What bounds it: up to 128 rows a unit the stream of K and V (32/8 x 128, 4 rows,
-// 32,768 keys: 6.2 TB/s; x 64: 6.7).  With two row tiles the exponentials and products of a
-// key tile take as long as its bytes: 1.63 us where 1.5 would be the copy's.  Key tiles of
-// 64 with two score buffers a slot, so that scores never wait for P V, were slower
-// (65.2, 124.2 us for 32 x 64 queries over up to 8,192 keys, against 62.0 and 120.3; D = 64
-// 51.5 against 44.1): a tile has some 500 cycles of waits and hand-overs
-// whatever its size.  Asking for tiles in L2 ahead of their copies was slower too (chains of
-// 128 x 5 over up to 2,048: 83.9 us without, 92.9 one tile ahead, 99.5 four).
+// What bounds it: up to 128 rows a unit the stream of K and V (chains of 128 x 5 rows over
+// up to 2,048 keys, 32/8 x 128: 6.6 TB/s, 99 % of a copy's rate).  With two row tiles a
+// key tile is a chain of some 3,100 cycles in each slot, the two half a chain apart: S
+// 350, its softmax 1,400, P V 650, and 700 until S is issued again, which P lies over
+// (512 columns of tensor memory are two S and two O).  A tile takes 1.45 us from L2, 1.65
+// from HBM (1.5 would be the copy's), and a unit's start and end 3 us more.  Measured
+// and slower, against 62.0 us for 4 x 61 queries over 16,385 keys and 120.3 for 32 x 64
+// over up to 8,192: key tiles of 64 with two score buffers a slot, so that scores never
+// wait for P V (65.2, 124.2; a tile has 500 cycles of hand-overs whatever its size);
+// against 60.1 and 116.8: the scores of a tile's upper half, which P does not cover,
+// issued as soon as the softmax has read them (64.8, 122.0; a product of 64 columns reads
+// Q as often as one of 128); against 58.2 and 111.3: slots that do not take turns at
+// the exponentials (59.7, 113.2).  Asking for tiles in L2 ahead of their copies: chains of
+// 128 x 5 over up to 2,048 83.9 us without, 92.9 one tile ahead, 99.5 four.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
