@@ -35,7 +35,7 @@ __device__ __forceinline__ uint4 load_once(const uint4* src) {
 //
 // The moves are few rows here and there: the time is four dependent round trips and
 // what the scattered rows' 128-byte pieces get out of HBM (a request in 28 layers of 4 x
-// 128 2.5 us; 128 requests with 3 rows in the mean to move, 16 layers of 8 x 128, 9.8, of
+// 128 2.5 us; 128 requests with 2 or 3 rows to move, 16 layers of 8 x 128, 9.8, of
 // which their 38 MB would be 5.6; with 10 rows to move 168 MB, 27.5 us).
 constexpr int kMostKept = 1024;
 constexpr int kBatch = 4;
