@@ -314,11 +314,11 @@ struct Fork {
 constexpr int kPer = 4;
 
 // One block does the work where every request has a warp there and the tables are
-// short: this many times kPer * 32 entries, of all requests.  Past that it is a cluster
-// of 16, whose barriers cost 1.5 us (8 requests of 128 blocks in one block 6.6 us, in a
-// cluster 8.1; 16 of 128 7.6, 8.8; 24 of 128 11.1, 8.8; 256 of 128 66, 11.3; 8 of 3,750 51,
-// 12.6; a cluster of 8 with 256 of 128 15.7).
-constexpr int kOneBlock = 48;
+// short: so many entries, of all requests.  Past that it is a cluster of 16, whose
+// barriers cost 1.5 us (requests x blocks each, one block and cluster: 8 x 130 6.9, 8.3 us;
+// 8 x 300 7.9, 8.2; 8 x 500 11.0, 9.3; 12 x 130 7.5, 8.6; 12 x 200 10.1, 8.7; 24 x 128
+// 11.1, 8.8; 256 x 128 66, 11.3; a cluster of 8 15.7).
+constexpr long kOneBlock = 2560;
 constexpr unsigned kCluster = 16;
 constexpr int kForkSmem = kMostRequests * 28 + int(kCluster) * NWARP * 4;
 
@@ -661,9 +661,8 @@ cudaError_t launch_fork(const ForkArgs& a, cudaStream_t stream) {
                         : launch_pdl_cluster(kern, cluster, dim3(cluster), dim3(NT), smem, stream, a);
   };
   static DeviceOnce once1, once16;
-  const long chunks = (a.max_blocks + 32 * kPer - 1) / (32 * kPer);
   const long most = std::max(a.B, a.B_in);
-  return most <= NWARP && most * chunks <= kOneBlock ? go(fork_kernel<1>, once1, 1) : go(fork_kernel<kCluster>, once16, kCluster);
+  return most <= NWARP && most * a.max_blocks <= kOneBlock ? go(fork_kernel<1>, once1, 1) : go(fork_kernel<kCluster>, once16, kCluster);
 }
 
 }  // namespace gqa
