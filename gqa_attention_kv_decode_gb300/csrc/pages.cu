@@ -318,7 +318,7 @@ constexpr int kPer = 4;
 // barriers cost 1.5 us (requests x blocks each, one block and cluster: 8 x 130 6.9, 8.3 us;
 // 8 x 300 7.9, 8.2; 8 x 500 11.0, 9.3; 12 x 130 7.5, 8.6; 12 x 200 10.1, 8.7; 24 x 128
 // 11.1, 8.8; 256 x 128 66, 11.3; a cluster of 8 15.7).
-constexpr long kOneBlock = 2560;
+constexpr long kOneBlock = 2300;
 constexpr unsigned kCluster = 16;
 constexpr int kForkSmem = kMostRequests * 28 + int(kCluster) * NWARP * 4;
 
