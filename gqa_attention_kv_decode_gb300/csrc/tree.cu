@@ -17,8 +17,9 @@
 // any lengths balance, a long one is shared by many workers, and of many short ones
 // a worker takes several.  A unit inside one range is finished there.  One that is
 // cut leaves partials (max, sum, unnormalised O), at most two per worker, and
-// tree_merge_kernel joins them.  Few units get a cluster of CTAs each instead, which
-// joins its partials through distributed shared memory (cluster_size has the choice).
+// tree_merge_kernel joins them (where a unit may have many, tree_merge_units_kernel).
+// Few units of a middling length get a cluster of CTAs each instead, which joins its
+// partials through distributed shared memory (cluster_size has the choice).
 //
 // A CTA (one an SM) has two slots, each with the softmax of a 128-row tile:
 //   PAIR    (more than 128 rows a unit) a worker is the CTA; both slots work on the
@@ -121,7 +122,10 @@ struct TreeParams {
   int cluster;  // CTAs of a unit (CLUSTERED)
   float qk_scale_log2;
   __nv_bfloat16* o;
-  int4* record;  // [n_workers]: the cut unit that begins in the worker's range (request, unit, its partials or 0, queries)
+  // [n_workers]: the cut unit that begins in the worker's range (request, unit, its partials or 0, queries),
+  // or, by_unit, [units of all requests]: where the unit was cut (.., .., first worker + (partials << 16), ..)
+  int4* record;
+  bool by_unit;
   // partials of a row tile, slots [n_workers][2][row tiles of a unit]: [..][1] of the
   // unit that begins in the range, [..][0] of one that goes on there
   float2* ml;     // [slot][128]
@@ -351,6 +355,17 @@ __global__ void __launch_bounds__(NTHR, 1)
       if (e.z > 0) base += unsigned(p.units) * unsigned(tiles_of(e.y) + LEAD);
     }
     __syncthreads();
+    if (p.by_unit && tid == NTHR - 1 && cta < p.B * p.units) {  // (there are at least eight workers a unit)
+      const int k = cta / p.units, u = cta - k * p.units;
+      const int4 e = ent[k];
+      int cuts = 0;
+      if (e.z > 0) {
+        const unsigned span = tiles_of(e.y) + LEAD, begin = unsigned(e.x) + u * span;
+        const unsigned w0 = cut.holder(begin + LEAD), w1 = cut.holder(begin + span - 1);
+        if (w1 > w0) cuts = int(w0 | (w1 - w0 + 1) << 16);
+      }
+      p.record[cta] = make_int4(k, u, cuts, e.z);
+    }
   }
   if constexpr (CLUSTERED) {
     tc_fence_before();
@@ -574,7 +589,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     const float c = p.qk_scale_log2;
     unsigned char* const stage = smem + C::OFF_OUT + warp * 2048;
     uint4* const sees = reinterpret_cast<uint4*>(stage);  // (each lane's own)
-    if (!CLUSTERED && (warp & 3) == 0 && lane == 1 && !(PAIR && t == 1)) {
+    if (!CLUSTERED && !p.by_unit && (warp & 3) == 0 && lane == 1 && !(PAIR && t == 1)) {
       // The unit that the range ends in, where it begins there too (a tile of it at least
       // is this worker's and one another's): its partials are this worker's and those
       // of the workers up to the one with its last tile.
@@ -979,25 +994,109 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
   }
 }
 
+// The same for few units of many partials each (grid.x: the units): a block has 32
+// rows and 16 columns, and each of its WARPS takes every WARPS-th pair of partials; then
+// four warps join four of the columns each.  (One unit of 64 rows x 32,768 keys, 128 partials,
+// with tree_merge_kernel 46.9 us, with 4 warps 40.0, 8 26.5, 16 21.8.)
+template <int D, int TILES, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) tree_merge_units_kernel(const TreeParams p) {
+  __shared__ float part_s[WARPS][18][32];  // [warp][16 columns, max, sum][row]
+  __shared__ uint2 out_s[32][4];
+  const int t = blockIdx.y >> 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r0 = (blockIdx.y & 3) * 32;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int4 rec = __ldcg(&p.record[blockIdx.x]);
+  const int n = rec.z >> 16, w0 = rec.z & 0xffff;
+  if (n == 0) return;
+  const int g = head_of(rec.y, p), first = ((rec.y - g * p.np) * TILES + t) * BM + r0;
+  auto live = [&](int row) { return row / p.Tq < p.n_rep && row % p.Tq < rec.w; };
+  const bool mine = live(first + lane);
+  if (!__any_sync(0xffffffffu, mine)) return;  // (the same rows in every warp)
+  float M = -INFINITY, den = 0.f, acc[16] = {};
+  constexpr int AHEAD = 2;
+  for (int s0 = warp * AHEAD; s0 < n; s0 += WARPS * AHEAD) {
+    float2 ml[AHEAD];
+    float4 x[AHEAD][4];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[k][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s0 + k < n && mine) {
+        const size_t slot = (size_t(w0 + s0 + k) * 2 + (s0 + k == 0 ? 1 : 0)) * TILES + t;
+        ml[k] = __ldcg(&p.ml[slot * BM + r0 + lane]);
+        const float4* const src = reinterpret_cast<const float4*>(p.part_o) + (slot * (D / 4) + blockIdx.z * 4) * BM + r0 + lane;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[k][c] = __ldcg(src + c * BM);
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) m = fmaxf(m, ml[k].x);
+    const float a = M == -INFINITY ? 0.f : fast_exp2(M - m);
+    M = m;
+    den *= a;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[v] *= a;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const float wt = ml[k].x == -INFINITY ? 0.f : fast_exp2(ml[k].x - M);
+      den = fmaf(ml[k].y, wt, den);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[4 * c] = fmaf(x[k][c].x, wt, acc[4 * c]);
+        acc[4 * c + 1] = fmaf(x[k][c].y, wt, acc[4 * c + 1]);
+        acc[4 * c + 2] = fmaf(x[k][c].z, wt, acc[4 * c + 2]);
+        acc[4 * c + 3] = fmaf(x[k][c].w, wt, acc[4 * c + 3]);
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < 16; ++v) part_s[warp][v][lane] = acc[v];
+  part_s[warp][16][lane] = M;
+  part_s[warp][17][lane] = den;
+  __syncthreads();
+  if (warp >= 4) return;
+  float m = -INFINITY, sum = 0.f, o[4] = {};
+#pragma unroll
+  for (int k = 0; k < WARPS; ++k) m = fmaxf(m, part_s[k][16][lane]);
+#pragma unroll
+  for (int k = 0; k < WARPS; ++k) {
+    const float mk = part_s[k][16][lane], wt = mk == -INFINITY ? 0.f : fast_exp2(mk - m);
+    sum = fmaf(part_s[k][17][lane], wt, sum);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) o[v] = fmaf(part_s[k][4 * warp + v][lane], wt, o[v]);
+  }
+  if (mine && sum == 0.f) atomicOr(p.status, GQA_DEV_EMPTY_REQUEST);
+  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0] * inv, o[1] * inv), hi = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
+  out_s[lane][warp] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  named_bar_sync(1, 128);
+  const int x = threadIdx.x >> 2, c = threadIdx.x & 3, row = first + x;  // (four threads store a row's 32 bytes)
+  if (live(row))
+    *reinterpret_cast<uint2*>(p.o + ((size_t(rec.x) * p.Hq + g * p.n_rep + row / p.Tq) * p.Tq + row % p.Tq) * D +
+                              blockIdx.z * 16 + c * 4) = out_s[x][c];
+}
+
 // ---- plan ----------------------------------------------------------------------
 
 // CTAs in the cluster of a unit, or 0: the list.  Estimated times in us, with what was
 // fitted to 356 calls (1 to 72 units of 1 to 256 key tiles, D = 64 and 128, one and two
 // row tiles), each with the list and clusters of 2, 4 and 8: what it chooses is 0.7 %
-// slower than the best of them in the mean, 14 % at most.  A tile takes its time or its
+// slower than the best of them in the mean, 19 % at most.  A tile takes its time or its
 // share of HBM; the requests of a call are taken to have nine tenths of the longest
 // one's keys.  Measured, list and clusters of 2, 4, 8 (D = 128, rows x units x keys, *: a
-// pair of row tiles): 64 x 8 x 2,048 13.3, 16.7, 12.8, 10.8; 64 x 32 x 4,097 22.7, 26.7,
-// 21.8, 45.2 (not one wave); 256* x 8 x 256 12.0, 17.2, 15.1, 13.9; 256* x 1 x 100 9.0,
-// 16.9, 14.7, 13.5; 256* x 16 x 8,192 27.4, 64.0, 38.8, 51.3.
+// pair of row tiles): 64 x 8 x 2,048 11.9, 16.4, 12.5, 10.3; 64 x 32 x 4,097 21.4, 26.2,
+// 21.4, 43.0 (not one wave); 256* x 8 x 256 11.3, 16.1, 13.8, 12.8; 256* x 1 x 100 8.6,
+// 15.9, 13.6, 12.6; 256* x 16 x 8,192 26.4, 60.3, 37.0, 48.2.
 // `fits`: clusters of 2, 4 and 8 that run at once.
 int cluster_size(bool pair, int D, int B, long units, long tiles, int sms, const int (&fits)[3]) {
   struct Times {
     double list, merge, partial, tile;  // the list: start and end, merge and each of a unit's partials, a tile
     double cluster, rows, its_tile;     // a cluster: start and end, rows joined by one CTA, a tile
   };
-  constexpr Times times[2][2] = {{{7.6, 1.5, 0.14, 0.0, 7.3, 0.9, 1.20}, {8.3, 1.7, 0.14, 0.0, 8.1, 2.4, 1.73}},
-                                 {{7.5, 3.5, 0.14, 1.29, 9.3, 5.5, 1.16}, {7.6, 4.6, 0.17, 1.92, 11.5, 9.8, 1.53}}};
+  constexpr Times times[2][2] = {{{7.2, 2.1, 0.03, 0.0, 6.9, 0.9, 1.14}, {8.0, 2.0, 0.03, 0.0, 7.7, 2.5, 1.70}},
+                                 {{6.9, 3.8, 0.03, 1.22, 8.6, 5.1, 1.09}, {7.0, 4.8, 0.03, 1.88, 10.7, 9.2, 1.45}}};
   const Times& x = times[pair][D == 128];
   const int slots = pair ? 1 : 2;  // workers of a CTA
   const double hbm = 0.0099 * D / 128, share = (B > 1 ? 0.9 : 1.0) * double(units) * tiles, workers = double(slots) * sms;
@@ -1013,6 +1112,9 @@ int cluster_size(bool pair, int D, int B, long units, long tiles, int sms, const
   }
   return size;
 }
+
+// Partials of a unit from which on many warps share them.
+constexpr long kManyPartials = 8;
 
 struct TreePlan {
   bool pair;
@@ -1108,6 +1210,7 @@ cudaError_t launch_tree_as(const TreeArgs& a, cudaStream_t stream) {
   p.ml = reinterpret_cast<float2*>(ws + plan.off_ml);
   p.part_o = reinterpret_cast<float*>(ws + plan.off_o);
   p.status = reinterpret_cast<uint32_t*>(ws);
+  p.by_unit = false;
   p.wait_limit_ns = kWaitLimitNs;
   p.test_stall_ns = wait_test_ns();
   static DeviceOnce once;
@@ -1128,11 +1231,20 @@ cudaError_t launch_tree_as(const TreeArgs& a, cudaStream_t stream) {
   if (p.cluster > 0)
     return launch_pdl_cluster(tree_kernel<HD, PAIR, true>, unsigned(p.cluster), dim3(unsigned(units * p.cluster)), dim3(NTHR),
                               C::SMEM_BYTES, stream, tq, tk, tv, p);
+  p.by_unit = units * kManyPartials <= plan.n_workers && tiles > kManyPartials;
   e = launch_pdl(tree_kernel<HD, PAIR, false>, dim3(plan.n_ctas), dim3(NTHR), C::SMEM_BYTES, stream, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
   if (a.max_kv_len <= BN) return cudaSuccess;  // (no unit has a second tile: none is cut)
   constexpr int TILES = PAIR ? 2 : 1;
   const int live = std::min(TILES * BM, n_rep * a.Tq);
+  if (p.by_unit) {
+    // sixteen warps a block where the blocks are on the SMs two by two at most, else eight
+    // (8 x 256 rows x 8,192 keys 21.7 us with sixteen, 20.1 with eight; 4 x 256 16.2, 18.3)
+    const dim3 blocks(unsigned(units), (live + 31) / 32, HD / 16);
+    return long(units) * blocks.y * blocks.z <= 2L * device_sm_count()
+               ? launch_pdl(tree_merge_units_kernel<HD, TILES, 16>, blocks, dim3(512), 0, stream, p)
+               : launch_pdl(tree_merge_units_kernel<HD, TILES, 8>, blocks, dim3(256), 0, stream, p);
+  }
   return launch_pdl(tree_merge_kernel<HD, TILES>, dim3(plan.n_workers, (live + 31) / 32, HD / 64), dim3(128), 0, stream,
                     p);
 }

@@ -162,6 +162,16 @@ def test_row_tiles(rows, D):
     Case(1, 2, 2, D, rows, [rows + 200], seed=rows).check()
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,Tq", [(4, 1, 64, 3), (4, 1, 128, 16), (8, 2, 64, 50), (4, 1, 128, 64), (6, 1, 128, 70),
+                                         (16, 1, 64, 40)])
+@pytest.mark.parametrize("lens", [[9000], [5000, 70, 1153, 0, 130], [1025, 1100], [33000]])
+def test_few_long_units(Hq, Hkv, D, Tq, lens):
+    """Many partials of a unit, joined by many warps; beside them units of one tile, of two and of none."""
+    q_lens = [min(Tq, n) for n in lens]
+    q_lens[-1] = min(q_lens[-1], max(1, Tq - 2))
+    Case(len(lens), Hq, Hkv, D, Tq, lens, q_lens, seed=Tq).check(64)
+
+
 @pytest.mark.parametrize("bs", [64, 128, 192, 448])
 @pytest.mark.parametrize("D", [64, 128])
 def test_block_sizes(bs, D):
