@@ -119,7 +119,7 @@ struct TreeParams {
   int block_size, max_blocks, num_blocks;
   int np, units;  // units of a KV head (1 without PAIR), of a request
   int n_ctas, n_workers;
-  int cluster;  // CTAs of a unit (CLUSTERED)
+  int cluster, cluster_log;  // CTAs of a unit (CLUSTERED), a power of two
   float qk_scale_log2;
   __nv_bfloat16* o;
   // [n_workers]: the cut unit that begins in the worker's range (request, unit, its partials or 0, queries),
@@ -377,18 +377,18 @@ __global__ void __launch_bounds__(NTHR, 1)
   // the worker that this warp serves (softmax of slot warp / 4; the others in pairs),
   // in the list or among those of the unit
   const unsigned in_slot = PAIR ? 0 : warp < 8 ? warp >> 2 : warp & 1;
-  const unsigned rank = CLUSTERED ? cta % p.cluster : 0;
+  const unsigned rank = CLUSTERED ? cta & (p.cluster - 1) : 0;
   const unsigned worker = CLUSTERED ? in_slot * p.cluster + rank : in_slot * p.n_ctas + cta;
   int at_k = 0, at_unit = 0, at_place = 0;
   if constexpr (CLUSTERED) {
     if (lane == 0) {
-      const int unit = cta / p.cluster, b = unit / p.units, n = (PAIR ? 1 : 2) * p.cluster;
+      const int unit = cta >> p.cluster_log, b = unit / p.units, log_n = p.cluster_log + (PAIR ? 0 : 1);  // (2^log_n workers)
       uint32_t bits = 0;
       const int4 e = request(p, b, bits);
       if (tid == 0 && rank == 0 && bits != 0) atomicOr(p.status, bits);
       const unsigned tiles = e.z > 0 ? tiles_of(e.y) : 0;
       const int u = unit - b * p.units, g = head_of(u, p);
-      walk->seg[0] = Segment{b, e.y, e.z, e.w, int(tiles * worker / n), int(tiles * (worker + 1) / n), u - g * p.np, g};
+      walk->seg[0] = Segment{b, e.y, e.z, e.w, int(tiles * worker >> log_n), int(tiles * (worker + 1) >> log_n), u - g * p.np, g};
       walk->left = walk->seg[0].hi > walk->seg[0].lo;
     }
     __syncwarp();
@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     // O as [worker][D / 4][share][4], and (m, l) as [worker][share] where the list would be.
     // (The cluster's size divides 128, so workers * share <= 256 rows of D floats.)
     const int n = (PAIR ? 1 : 2) * p.cluster, part = seg->part, g = seg->g;
-    const int rows = min(PAIR ? 2 * BM : BM, p.n_rep * p.Tq - part * 2 * BM), share = (rows + p.cluster - 1) / p.cluster;
+    const int rows = min(PAIR ? 2 * BM : BM, p.n_rep * p.Tq - part * 2 * BM), share = (rows + p.cluster - 1) >> p.cluster_log;
     cluster_barrier();  // every CTA is done with its stages
     if (warp < 8) {
       const int R = (PAIR ? (warp >> 2) * BM : 0) + (tid & (BM - 1)), to = R / share, at = R - to * share;
@@ -1231,6 +1231,7 @@ cudaError_t launch_tree_as(const TreeArgs& a, cudaStream_t stream) {
   p.cluster = cluster_size(PAIR, HD, a.B, units, tiles, std::max(1, device_sm_count()), fits);
   // (a power of two: what the CTAs of a cluster send each other then fits the stages)
   if (const int c = prefill_kv_split_override(); c > 0) p.cluster = c >= 8 ? 8 : c >= 4 ? 4 : c >= 2 ? 2 : 0;
+  p.cluster_log = p.cluster >= 8 ? 3 : p.cluster >= 4 ? 2 : 1;
   if (p.cluster > 0)
     return launch_pdl_cluster(tree_kernel<HD, PAIR, true>, unsigned(p.cluster), dim3(unsigned(units * p.cluster)), dim3(NTHR),
                               C::SMEM_BYTES, stream, tq, tk, tv, p);
