@@ -172,6 +172,14 @@ def test_few_long_units(Hq, Hkv, D, Tq, lens):
     Case(len(lens), Hq, Hkv, D, Tq, lens, q_lens, seed=Tq).check(64)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,Tq,lens", [(2, 1, 64, 1024, [1024, 1500]), (4, 2, 128, 700, [701, 2000]),
+                                              (8, 1, 128, 333, [333, 900, 400]), (3, 1, 64, 1000, [5000])])
+@pytest.mark.parametrize("kind", ["tree", None])
+def test_large_trees(Hq, Hkv, D, Tq, lens, kind):
+    """Masks over many key tiles, from every place in a tile, alone and behind other rows; chains as long."""
+    Case(len(lens), Hq, Hkv, D, Tq, lens, mask=kind, seed=Tq).check(64)
+
+
 @pytest.mark.parametrize("bs", [64, 128, 192, 448])
 @pytest.mark.parametrize("D", [64, 128])
 def test_block_sizes(bs, D):
