@@ -857,10 +857,10 @@ __global__ void __launch_bounds__(NTHR, 1)
       const bool any = seg->hi > seg->lo && !*abort_flag, live = R < rows;
       const uint32_t tO = tmem + TM_O + (warp >> 2) * HD + (uint32_t((warp & 3) * 32) << 16);
       if (live) {
+        // (of a CTA that gave up waiting: rows of NaN, nothing plausible)
+        const float l = *abort_flag ? __int_as_float(0x7fffffff) : any ? lsum : 0.f;
         const uint32_t dst = shared_of(ent, to) + (worker * share + at) * 8;
-        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(any ? m_ref : -INFINITY),
-                     "f"(any ? lsum : 0.f)
-                     : "memory");
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(any ? m_ref : -INFINITY), "f"(l) : "memory");
       }
       if (any && __any_sync(0xffffffffu, live)) {
         const uint32_t dst = live ? shared_of(smem + OFF_K, to) + (worker * (HD / 4) * share + at) * 16 : 0u;
@@ -892,7 +892,10 @@ __global__ void __launch_bounds__(NTHR, 1)
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int v = 0; v < n; ++v) {
         const float2 s = ml[v * share + at];
-        if (s.x == -INFINITY) continue;  // (no O was sent, or zeros)
+        if (s.x == -INFINITY) {  // no O was sent, or zeros, or (with l, of scores that were all NaN) NaN
+          den += s.y;
+          continue;
+        }
         const float w = fast_exp2(s.x - M);
         const float4 o = part_o[(v * (HD / 4) + chunk) * share + at];
         den = fmaf(s.y, w, den);
