@@ -939,7 +939,10 @@ GQA_ATTN_API int gqa_attn_fork_tables(const int32_t* src, const int32_t* keep_le
   if (long(max_blocks) * block_size > kMax || long(num_blocks) * block_size > kMax) return GQA_ERR_INVALID_ARG;
   if (same_array({block_table_out, kv_lens_out, copy_src, copy_dst, copy_rows, shared_out, free_blocks_out, free_count_out},
                  {src, keep_lens, held_lens, block_table}) ||
-      same_array({block_table_out, kv_lens_out, copy_src, copy_dst, copy_rows}, {shared, free_blocks, free_count}))
+      same_array({block_table_out, kv_lens_out, copy_src, copy_dst, copy_rows}, {shared, free_blocks, free_count}) ||
+      // (each of these three may be its own input)
+      same_array({shared_out}, {free_blocks, free_count}) || same_array({free_blocks_out}, {shared, free_count}) ||
+      same_array({free_count_out}, {shared, free_blocks}))
     return GQA_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
