@@ -251,9 +251,10 @@ int check_layers(int n_layers, int num_blocks, int Hkv, int block_size, int D, i
   return GQA_OK;
 }
 // Whether one of the written arrays begins where another array of the call does.
-// (Where the pages' calls allow it, the pair is left out by the caller.)
+// (Where the pages' calls allow it, the pair is left out by the caller; nullptr is no array.)
 bool same_array(std::initializer_list<const void*> written, std::initializer_list<const void*> read) {
   for (auto w = written.begin(); w != written.end(); ++w) {
+    if (*w == nullptr) continue;
     for (auto x = written.begin(); x != w; ++x)
       if (*w == *x) return true;
     for (const void* r : read)
@@ -846,6 +847,7 @@ GQA_ATTN_API int gqa_attn_tree_tables(const int32_t* parents, const int32_t* tre
   if (mask_words != (N + 31) / 32) return GQA_ERR_INVALID_ARG;
   const bool placed = positions != nullptr;
   if (placed != (kv_lens != nullptr) || placed != (q_starts != nullptr) || (placed && T < 1)) return GQA_ERR_INVALID_ARG;
+  if (same_array({tree_mask, positions}, {parents, tree_lens, q_lens, kv_lens, q_starts})) return GQA_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
   int rc = check_ptrs({parents, tree_lens, tree_mask}, dev, 4);

@@ -434,7 +434,7 @@ GQA_ATTN_API int gqa_attn_decode_tree_paged(const void* q, const void* k_pool, c
  *                 begins at position 0.
  * Whatever is clamped sets GQA_DEV_KVLEN_CLAMPED.  A parent that is no node before
  * its node sets GQA_DEV_BAD_INDEX and counts as -1.
- * 1 <= N <= 1024, 1 <= Tq <= 1024, B <= 65535.
+ * 1 <= N <= 1024, 1 <= Tq <= 1024, B <= 65535.  No output overlaps another array.
  *   workspace     as for gqa_attn_step_tables (the status word)
  * ------------------------------------------------------------------------- */
 GQA_ATTN_API int gqa_attn_tree_tables(const int32_t* parents, const int32_t* tree_lens,
