@@ -1,4 +1,5 @@
-// device_once.h -- setup that belongs to a device, done once on each.
+// device_once.h -- setup that belongs to a device, done once on each, and numbers
+// that a device is asked for, once each.
 //
 // A kernel's attributes (its dynamic shared memory above 48 KB, its carveout)
 // are set for the current device only, so a process that calls the library on
@@ -34,6 +35,30 @@ class DeviceOnce {
   static constexpr int kDevices = 64;
   std::mutex mu_;
   std::atomic<bool> done_[kDevices] = {};
+};
+
+// N numbers (of 0 or more) that depend on the device and on what the owner of the object
+// asks: one object a kernel.  What could not be answered counts as 0 and is asked again.
+template <int N>
+class DeviceAnswers {
+ public:
+  // ask(int&) -> cudaError_t, unless number i of the current device is known.
+  template <typename Ask>
+  int get(int i, Ask ask) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const bool kept = dev >= 0 && dev < kDevices;
+    if (kept)
+      if (const int known = known_[dev][i].load(std::memory_order_relaxed); known > 0) return known - 1;
+    int n = 0;
+    if (ask(n) != cudaSuccess) return 0;
+    if (kept) known_[dev][i].store(n + 1, std::memory_order_relaxed);
+    return n;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  std::atomic<int> known_[kDevices][N] = {};  // the number + 1; 0: not known yet
 };
 
 }  // namespace gqa

@@ -53,7 +53,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
 #include "attn_tile.cuh"
@@ -1144,38 +1143,26 @@ TreePlan tree_plan(int B, int Hq, int Hkv, int D, int Tq, int max_kv_len) {
   return q;
 }
 
-// How many clusters of 2, 4 and 8 CTAs the current device runs at once (asked once a
-// device and kernel; a device that cannot say has none).
+// How many clusters of 2, 4 and 8 CTAs of a kernel the current device runs at once (`kept` is
+// that kernel's; a device that cannot say has none).
 template <typename Kern>
-void clusters_at_once(Kern kern, size_t smem, int (&fits)[3]) {
-  constexpr int kDevices = 64;
-  static std::atomic<int> kept[kDevices][3];  // the answer + 1; 0: not asked yet
-  int dev = 0;
-  const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices;
-  for (int i = 0; i < 3; ++i) {
-    const int have = known ? kept[dev][i].load(std::memory_order_relaxed) : 0;
-    if (have > 0) {
-      fits[i] = have - 1;
-      continue;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2u << i;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(2u << i);
-    cfg.blockDim = dim3(NTHR);
-    cfg.dynamicSmemBytes = smem;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
-      cudaGetLastError();
-      n = 0;
-    }
-    fits[i] = n;
-    if (known) kept[dev][i].store(n + 1, std::memory_order_relaxed);
-  }
+void clusters_at_once(Kern kern, size_t smem, DeviceAnswers<3>& kept, int (&fits)[3]) {
+  for (int i = 0; i < 3; ++i)
+    fits[i] = kept.get(i, [&](int& n) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = 2u << i;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.gridDim = dim3(2u << i);
+      cfg.blockDim = dim3(NTHR);
+      cfg.dynamicSmemBytes = smem;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      if (e != cudaSuccess) cudaGetLastError();
+      return e;
+    });
 }
 
 template <int HD, bool PAIR>
@@ -1230,7 +1217,8 @@ cudaError_t launch_tree_as(const TreeArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const long units = long(a.B) * p.units, tiles = (long(a.max_kv_len) + BN - 1) / BN;
   int fits[3];
-  clusters_at_once(tree_kernel<HD, PAIR, true>, C::SMEM_BYTES, fits);
+  static DeviceAnswers<3> kept;
+  clusters_at_once(tree_kernel<HD, PAIR, true>, C::SMEM_BYTES, kept, fits);
   p.cluster = cluster_size(PAIR, HD, a.B, units, tiles, std::max(1, device_sm_count()), fits);
   // (a power of two: what the CTAs of a cluster send each other then fits the stages)
   if (const int c = prefill_kv_split_override(); c > 0) p.cluster = c >= 8 ? 8 : c >= 4 ? 4 : c >= 2 ? 2 : 0;
