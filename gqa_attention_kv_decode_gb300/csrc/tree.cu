@@ -7,8 +7,11 @@
 // and K and V are read once for them, not once per query or per query head.  Rows
 // come in tiles of 128, keys in tiles of 128.  A key before the request's drafted
 // rows is visible to every query; of the drafted rows, the last ones, each query's
-// bit mask says which are (or, in a chain, those up to its own): only the last one
-// or two key tiles are masked, a word of the mask per 32 keys.
+// bit mask says which are (or, in a chain, those up to its own): only the last key
+// tiles are masked, a word of the mask per 32 keys.  All n_rep * Tq rows are worked on,
+// whatever a request's q_lens is, and every row tile of a chain goes over all keys
+// of the request (32 x 64 queries over 8,192 keys, 32/8 x 128, 203 us; with 32 of the 64
+// queries 197, as a call of Tq = 32 180).
 //
 // The work is one list of key tiles, request after request, and in a request KV
 // head after KV head (the units; several where the rows fill more than the tiles
@@ -1005,7 +1008,8 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
 // The same for few units of many partials each (grid.x: the units): a block has 32
 // rows and 16 columns, and each of its WARPS takes every WARPS-th pair of partials; then
 // four warps join four of the columns each.  (One unit of 64 rows x 32,768 keys, 128 partials,
-// with tree_merge_kernel 46.9 us, with 4 warps 40.0, 8 26.5, 16 21.8.)
+// with tree_merge_kernel 46.9 us, with 4 warps 40.0, 8 26.5, 16 21.8; 17.7 since the merge's
+// blocks start when all CTAs are done.)
 template <int D, int TILES, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) tree_merge_units_kernel(const TreeParams p) {
   __shared__ float part_s[WARPS][18][32];  // [warp][16 columns, max, sum][row]
@@ -1090,13 +1094,16 @@ __global__ void __launch_bounds__(WARPS * 32) tree_merge_units_kernel(const Tree
 
 // CTAs in the cluster of a unit, or 0: the list.  Estimated times in us, with what was
 // fitted to 356 calls (1 to 72 units of 1 to 256 key tiles, D = 64 and 128, one and two
-// row tiles), each with the list and clusters of 2, 4 and 8: what it chooses is 0.7 %
-// slower than the best of them in the mean, 19 % at most.  A tile takes its time or its
-// share of HBM; the requests of a call are taken to have nine tenths of the longest
-// one's keys.  Measured, list and clusters of 2, 4, 8 (D = 128, rows x units x keys, *: a
-// pair of row tiles): 64 x 8 x 2,048 11.9, 16.4, 12.5, 10.3; 64 x 32 x 4,097 21.4, 26.2,
-// 21.4, 43.0 (not one wave); 256* x 8 x 256 11.3, 16.1, 13.8, 12.8; 256* x 1 x 100 8.6,
-// 15.9, 13.6, 12.6; 256* x 16 x 8,192 26.4, 60.3, 37.0, 48.2.
+// row tiles), each with the list and clusters of 2, 4 and 8: what it chooses is 1 %
+// slower than the best of them in the mean, 17 % at most (a unit of 64 rows x 4,097 keys,
+// D = 64: the list 9.2, a cluster of eight 10.5), measured again after the kernels' last
+// changes.  A tile takes its time or its share of HBM; the requests of a call are taken
+// to have nine tenths of the longest one's keys, and the longest one max_kv_len of them
+// (8 rows over 513 keys, 14/2 x 64, 7.5 us; under a bound of 32,768 9.3, by the list).
+// Measured, list and clusters of 2, 4, 8 (D = 128, rows x units x keys, *: a pair of row
+// tiles): 64 x 8 x 2,048 11.4, 16.1, 12.4, 10.2; 64 x 32 x 4,097 21.2, 25.9, 21.4, 42.4 (not
+// one wave); 256* x 8 x 256 11.2, 16.1, 13.9, 12.8; 256* x 1 x 100 8.4, 15.9, 13.6, 12.5;
+// 256* x 16 x 8,192 26.1, 61.6, 37.4, 48.4.
 // `fits`: clusters of 2, 4 and 8 that run at once.
 int cluster_size(bool pair, int D, int B, long units, long tiles, int sms, const int (&fits)[3]) {
   struct Times {

@@ -389,8 +389,11 @@ GQA_ATTN_API int gqa_attn_rope_append(const void* q, const void* k, const void* 
  * A query that sees no row at all gets zeros and sets GQA_DEV_EMPTY_REQUEST.
  * Rows of K and V past kv_lens[b] may hold anything; of a drafted row that a
  * query does not see, K may hold anything and V finite numbers (its weight is 0
- * there).  The queries of a request and KV head (Hq / Hkv * q_lens[b] rows) read
- * its keys together, up to 256 of them at once.
+ * there).  A row with a NaN among the scores that it sees is NaN.  The Tq queries of
+ * the query heads of a KV head (Hq / Hkv * Tq rows) read a request's keys together, up
+ * to 256 rows at once; rows from q_lens[b] on take part without being written, so a call
+ * takes about the time of its Tq.  A chain's rows go over all keys of the request, also
+ * the drafted ones behind their own.
  * Tq at most 1024, mask_words 1 to 32; B * Hq * Tq < 2^31, and B * Hkv *
  * ceil(Hq / Hkv * Tq / 256) * (max_kv_len / 128 + 8) < 2^31; dtype must be GQA_BF16
  * (else GQA_ERR_UNSUPPORTED).  Workspace: gqa_attn_decode_tree_workspace_size, for both
@@ -682,7 +685,8 @@ GQA_ATTN_API int gqa_attn_set_prefill_interleave_override(int from_pair);
  * on a copy or a product gives up after 1 s; the CTA then lets the copies it
  * issued land (waiting with the same 1 s limit) and returns, leaving the
  * context usable: a decode CTA writes no partials and sets
- * GQA_DEV_WAIT_TIMEOUT in the workspace status word, a prefill CTA writes its
+ * GQA_DEV_WAIT_TIMEOUT in the workspace status word (of a unit that a cluster of
+ * CTAs shares in gqa_attn_decode_tree, the rows are NaN), a prefill CTA writes its
  * output rows as NaN and sets GQA_DEV_WAIT_TIMEOUT in the prefill status word.
  * With stall_ns > 0 every later launch of gqa_attn_decode, _decode_paged,
  * _decode_layers, _decode_q4, _decode_q4_residual, _decode_shared_prefix(_paged),
