@@ -627,15 +627,22 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+@contextlib.contextmanager
 def _zeros_like(q, stream):
     """An output of which a call writes some rows, the others zeros: filled on the
-    call's stream, whose kernels follow.  (Should the call be refused, the fill
-    may still run when the memory is given back.)"""
+    call's stream, whose kernels follow.  Where the call is refused the current
+    stream, which the memory goes back to, waits for the fill."""
     o = torch.empty_like(q)
     with _on(stream):
-        if stream is not None and o.is_cuda:
-            o.record_stream(torch.cuda.current_stream())
-        return o.zero_()
+        o.zero_()
+    try:
+        yield o
+    except Exception:
+        if stream is not None:
+            with _on(stream):
+                used = torch.cuda.current_stream()
+            torch.cuda.current_stream().wait_stream(used)
+        raise
 
 
 def rope_table(max_pos, rot_dim, base=10000.0, device="cuda") -> torch.Tensor:
@@ -765,8 +772,8 @@ def decode_tree(q, k, v, kv_lens, tree_mask=None, q_lens=None, tree_lens=None, s
     if workspace is None:
         with _on(stream):
             workspace = decode_tree_workspace(B, Hq, k.shape[1], D, Tq, max_kv_len, q.device)
-    o = _zeros_like(q, stream)
-    gqa_attn_decode_tree(q, k, v, tree_mask, q_lens, tree_lens, kv_lens, o, scale, workspace, max_kv_len, stream)
+    with _zeros_like(q, stream) as o:
+        gqa_attn_decode_tree(q, k, v, tree_mask, q_lens, tree_lens, kv_lens, o, scale, workspace, max_kv_len, stream)
     return o
 
 
@@ -779,9 +786,9 @@ def decode_tree_paged(q, k_pool, v_pool, block_table, kv_lens, tree_mask=None, q
     if workspace is None:
         with _on(stream):
             workspace = decode_tree_workspace(B, Hq, k_pool.shape[1], D, Tq, max_kv_len, q.device)
-    o = _zeros_like(q, stream)
-    gqa_attn_decode_tree_paged(q, k_pool, v_pool, block_table, tree_mask, q_lens, tree_lens, kv_lens, o, scale,
-                               workspace, max_kv_len, stream)
+    with _zeros_like(q, stream) as o:
+        gqa_attn_decode_tree_paged(q, k_pool, v_pool, block_table, tree_mask, q_lens, tree_lens, kv_lens, o, scale,
+                                   workspace, max_kv_len, stream)
     return o
 
 
