@@ -389,11 +389,12 @@ GQA_ATTN_API int gqa_attn_rope_append(const void* q, const void* k, const void* 
  * A query that sees no row at all gets zeros and sets GQA_DEV_EMPTY_REQUEST.
  * Rows of K and V past kv_lens[b] may hold anything; of a drafted row that a
  * query does not see, K may hold anything and V finite numbers (its weight is 0
- * there).  A row with a NaN among the scores that it sees is NaN.  The Tq queries of
- * the query heads of a KV head (Hq / Hkv * Tq rows) read a request's keys together, up
- * to 256 rows at once; rows from q_lens[b] on take part without being written, so a call
- * takes about the time of its Tq.  A chain's rows go over all keys of the request, also
- * the drafted ones behind their own.
+ * there).  A row with a NaN or a +inf among the scores that it sees is NaN; a score of
+ * -inf has no weight, and a row with no other ones is as one that sees nothing.
+ * The Tq queries of the query heads of a KV head (Hq / Hkv * Tq rows) read a request's
+ * keys together, up to 256 rows at once; rows from q_lens[b] on take part without being
+ * written, so a call takes about the time of its Tq.  A chain's rows go over all keys
+ * of the request, also the drafted ones behind their own.
  * Tq at most 1024, mask_words 1 to 32; B * Hq * Tq < 2^31, and B * Hkv *
  * ceil(Hq / Hkv * Tq / 256) * (max_kv_len / 128 + 8) < 2^31; dtype must be GQA_BF16
  * (else GQA_ERR_UNSUPPORTED).  Workspace: gqa_attn_decode_tree_workspace_size, for both
